@@ -281,6 +281,136 @@ ssm_status ssm_ssd_state_update(const ssm_ssd_params* p, float* state, const voi
                                 const float* dt_bias, const float* A, const void* B, const void* C, const float* Dskip,
                                 const void* z, void* y, void* stream);
 
+/*
+ * ---- Packed sequences: the Mamba-2 block's operators over tokens ----
+ *
+ * The rows of x, u, y, z (and of the gradients) are tokens, channels innermost, and the sequences of a batch lie one
+ * behind the other: sequence s has the tokens cu_seqlens[s] .. cu_seqlens[s+1]-1 (int32, on the device, non-decreasing,
+ * cu_seqlens[0] >= 0, cu_seqlens[nseqs] <= ntokens; a sequence may be empty).  Rows outside every sequence are neither
+ * used nor written.  A row stride is the number of elements from one row to the next (0: the rows are dense), so that
+ * slices of a wider row (the parts of a layer's projected input) are taken as they are.
+ *
+ * Recurrent states live in pools of nslots slots.  Sequence (or row) s uses slot state_idx[s] (int32, on the device;
+ * NULL: slot s); an index outside [0, nslots) means that it has none: it starts from zeros and its last state is not
+ * kept.  Each slot may be named once per call.  has_state (one byte per sequence, on the device, or NULL: all) says
+ * whether a sequence starts from its slot or from zeros.  state and state_out may be the same pool, which updates it in
+ * place; the other slots are left as they are.  The last state of an empty sequence is the state it starts from.
+ * None of this is read on the host: the same call can be captured into a graph and replayed with other lengths.
+ */
+typedef struct {
+  int64_t ntokens;   /* rows, >= 1 (below 2^30; ssm_conv1d_slot_update: at most 65535) */
+  int64_t nseqs;     /* sequences, >= 1 (ignored by ssm_conv1d_slot_update) */
+  int64_t dim;       /* channels */
+  int64_t nslots;    /* slots of state and state_out */
+  int64_t x_stride, u_stride, du_stride, dx_stride;   /* row strides; 0 = dim */
+  int32_t width;     /* 1 <= width <= 4 */
+  int32_t activation;/* 1: SiLU after the convolution; 0: none */
+  int32_t io_dtype;  /* ssm_dtype of x, u, du, dx */
+  int32_t reserved;  /* must be 0 */
+} ssm_conv_packed_params;
+
+/*
+ * Causal depthwise convolution (+ SiLU), channels last: u_t = act(bias + sum_k weight[k] x_{t-(width-1)+k}), with the
+ * inputs before a sequence from its window.  x, u [ntokens][dim] io_dtype; weight [dim][width], bias [dim] or NULL fp32;
+ * state, state_out [nslots][dim][width-1] fp32 or NULL: the width-1 inputs before the sequence, oldest first, and its
+ * last ones.  u must not overlap x.  Rows that are 16-byte aligned (base, stride and dim) run fastest.
+ */
+ssm_status ssm_conv1d_packed_fwd(const ssm_conv_packed_params* p, const void* x, const float* weight, const float* bias,
+                                 const int32_t* cu_seqlens, const float* state, const int32_t* state_idx,
+                                 const uint8_t* has_state, float* state_out, void* u, void* stream);
+
+/* One token per row: x, u [ntokens][dim]; row r shifts the window in slot state_idx[r] in place. */
+ssm_status ssm_conv1d_slot_update(const ssm_conv_packed_params* p, const void* x, const float* weight, const float* bias,
+                                  float* state, const int32_t* state_idx, void* u, void* stream);
+
+/* Bytes of device workspace ssm_conv1d_packed_bwd needs (0 for invalid parameters). */
+size_t ssm_conv1d_packed_bwd_workspace_bytes(const ssm_conv_packed_params* p);
+
+/*
+ * Backward of ssm_conv1d_packed_fwd for du = dL/du [ntokens][dim] and, optionally, dstate_out = dL/d(last window)
+ * [nseqs][dim][width-1] fp32 (by sequence, not by slot).  Outputs, overwritten: dx [ntokens][dim]; dweight [dim][width]
+ * fp32 (required); dbias [dim] and dstate [nseqs][dim][width-1] fp32 (the gradient of each sequence's first window, at
+ * zero where it has none), each optional.  state is the pool as it was before the forward.  Deterministic.
+ */
+ssm_status ssm_conv1d_packed_bwd(const ssm_conv_packed_params* p, const void* x, const float* weight, const float* bias,
+                                 const int32_t* cu_seqlens, const float* state, const int32_t* state_idx,
+                                 const uint8_t* has_state, const void* du, const float* dstate_out, void* dx,
+                                 float* dweight, float* dbias, float* dstate, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+typedef struct {
+  int64_t ntokens;   /* rows, >= 1 and below 2^30 */
+  int64_t nseqs;     /* sequences, >= 1 (ignored by ssm_ssd_slot_update) */
+  int64_t nheads;    /* H, a multiple of ngroups */
+  int64_t headdim;   /* P: must be 64 */
+  int64_t ngroups;   /* G */
+  int64_t dstate;    /* N: 64, 128 or 256 */
+  int64_t nslots;    /* slots of state and state_out */
+  int64_t x_stride, dt_stride, b_stride, c_stride, y_stride;      /* row strides; 0 = dense; below 2^24 */
+  int64_t dy_stride, dx_stride, ddt_stride, db_stride, dc_stride; /* of the backward's arrays */
+  int32_t io_dtype;  /* must be SSM_BF16 (x, dt, B, C, y and their gradients) */
+  int32_t disc;      /* ssm_disc */
+  int32_t dt_softplus;
+  int32_t segment_chunks;  /* 0: the library picks how many 64-step chunks of a sequence run one after the other before
+                              the rest runs beside them; k > 0 forces k; results agree within rounding */
+  int32_t reserved;  /* must be 0 */
+} ssm_ssd_packed_params;
+
+/* Bytes of device workspace ssm_ssd_packed_fwd needs (0 when it needs none, and for invalid parameters). */
+size_t ssm_ssd_packed_fwd_workspace_bytes(const ssm_ssd_packed_params* p);
+
+/*
+ * The SSD layer (see ssm_ssd_fwd) over packed sequences, without the gate (which belongs to the norm behind it):
+ *   S_t = exp(Delta_t A) S_{t-1} + phi_t x_t B_t^T,  y_t = S_t C_t + Dskip x_t
+ * x, y [ntokens][nheads][headdim]; dt [ntokens][nheads]; B, C [ntokens][ngroups][dstate], bf16; A, dt_bias, Dskip [nheads]
+ * fp32 (dt_bias, Dskip NULL = 0); state, state_out [nslots][nheads][headdim][dstate] fp32 or NULL.  Rows of x, B, C and
+ * y, the states and the workspace must be 16-byte aligned.  y must not overlap an input.
+ */
+ssm_status ssm_ssd_packed_fwd(const ssm_ssd_packed_params* p, const void* x, const void* dt, const float* dt_bias,
+                              const float* A, const void* B, const void* C, const float* Dskip,
+                              const int32_t* cu_seqlens, const float* state, const int32_t* state_idx,
+                              const uint8_t* has_state, float* state_out, void* y, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* One step per row: x, y [ntokens][nheads][headdim], dt [ntokens][nheads], B, C [ntokens][ngroups][dstate] (rows 8-byte
+ * aligned); the state in slot state_idx[r] is updated in place (16-byte aligned). */
+ssm_status ssm_ssd_slot_update(const ssm_ssd_packed_params* p, float* state, const void* x, const void* dt,
+                               const float* dt_bias, const float* A, const void* B, const void* C, const float* Dskip,
+                               const int32_t* state_idx, void* y, void* stream);
+
+typedef struct {
+  int64_t ntokens;   /* rows, >= 1 */
+  int64_t dim;       /* channels of a row, a multiple of ngroups */
+  int64_t ngroups;   /* groups of dim / ngroups (at most 16384) consecutive channels, each with its own statistics */
+  int64_t x_stride, z_stride, y_stride, dy_stride, dx_stride, dz_stride;   /* row strides; 0 = dim */
+  float eps;         /* >= 0 */
+  int32_t io_dtype;  /* ssm_dtype of x, z, y, dy, dx, dz */
+  int32_t gate_first;/* with z: 1 = the norm of x silu(z), 0 = the norm of x, times silu(z) */
+  int32_t center;    /* 1: the mean is taken off (layer norm of each group), 0: root mean square only */
+  int32_t reserved;  /* must be 0 */
+} ssm_gated_norm_params;
+
+/*
+ * Group norm of each row with an optional SiLU gate: h = x silu(z) (gate_first) or x; per group of channels
+ * m = mean(h) (center) or 0, r = 1 / sqrt(mean((h - m)^2) + eps); y = (h - m) r weight + bias, times silu(z) without
+ * gate_first.  x, z (or NULL: no gate), y [ntokens][dim] io_dtype; weight [dim], bias [dim] or NULL fp32.  y may be x
+ * or z.  Rows that are 16-byte aligned (base, stride and group) run fastest.
+ */
+ssm_status ssm_gated_norm_fwd(const ssm_gated_norm_params* p, const void* x, const void* z, const float* weight,
+                              const float* bias, void* y, void* stream);
+
+/* Bytes of device workspace ssm_gated_norm_bwd needs (0 for invalid parameters). */
+size_t ssm_gated_norm_bwd_workspace_bytes(const ssm_gated_norm_params* p);
+
+/*
+ * Backward of ssm_gated_norm_fwd for dy = dL/dy, statistics recomputed.  Outputs, overwritten: dx and dz [ntokens][dim]
+ * (dz exactly when z is given); dweight [dim] fp32; dbias [dim] fp32 or NULL (at zero where bias is NULL).
+ * dx may be x or dy, dz may be z.  Deterministic.
+ */
+ssm_status ssm_gated_norm_bwd(const ssm_gated_norm_params* p, const void* x, const void* z, const float* weight,
+                              const float* bias, const void* dy, void* dx, void* dz, float* dweight, float* dbias,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* ssm_status_str(ssm_status s);
 

@@ -3,7 +3,10 @@
 ``scan_fwd``, ``scan_bwd`` and ``state_update`` call the C ABI of libssm57.so (include/ssm_scan.h) on PyTorch device
 tensors; ``conv_scan_fwd`` and ``conv_state_update`` do the same with the block's causal depthwise convolution + SiLU
 applied to x inside the kernels; ``complex_scan_fwd`` and ``complex_state_update`` run the complex-A variant;
-``ssd_fwd`` and ``ssd_state_update`` run the Mamba-2 SSD layer (scalar A per head, bf16 matrix cores).  The
+``ssd_fwd`` and ``ssd_state_update`` run the Mamba-2 SSD layer (scalar A per head, bf16 matrix cores).  The Mamba-2
+block over packed tokens (sequences of uneven length one behind the other, states in slots) is
+``conv1d_packed_fwd`` / ``conv1d_slot_update`` / ``conv1d_packed_bwd``, ``ssd_packed_fwd`` / ``ssd_slot_update`` /
+``ssd_packed_bwd`` and ``gated_norm_fwd`` / ``gated_norm_bwd`` (module ``packed``).  The
 arithmetic runs entirely in the HIP kernels.  ``inputs`` generates the seeded
 synthetic workloads.
 """
@@ -14,7 +17,9 @@ from ._abi import (EULER_B, ZOH, SSM_BF16, SSM_F32, SSMError, Params, make_param
                    bwd_workspace_bytes)
 
 __all__ = ["scan_fwd", "scan_bwd", "state_update", "conv_scan_fwd", "conv_state_update", "complex_scan_fwd",
-           "complex_state_update", "conv1d_fwd", "conv1d_bwd", "ssd_fwd", "ssd_state_update", "ssd_workspace_bytes", "EULER_B", "ZOH", "SSMError",
+           "complex_state_update", "conv1d_fwd", "conv1d_bwd", "ssd_fwd", "ssd_state_update", "ssd_workspace_bytes",
+           "conv1d_packed_fwd", "conv1d_slot_update", "conv1d_packed_bwd", "ssd_packed_fwd", "ssd_slot_update",
+           "gated_norm_fwd", "gated_norm_bwd", "EULER_B", "ZOH", "SSMError",
            "Params", "make_params", "workspace_bytes", "bwd_workspace_bytes", "plan_segments", "io_code"]
 
 
@@ -426,3 +431,7 @@ def ssd_state_update(state, x, dt, A, B, C, dt_bias=None, Dskip=None, z=None, *,
                                    _addr(C), _addr(Dskip), _addr(z), _addr(y), _stream_handle(stream, dev))
     _abi.check(st)
     return y
+
+
+from .packed import (conv1d_packed_fwd, conv1d_slot_update, conv1d_packed_bwd, ssd_packed_fwd, ssd_slot_update,  # noqa: E402
+                     gated_norm_fwd, gated_norm_bwd)

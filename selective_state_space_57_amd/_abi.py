@@ -19,7 +19,10 @@ EXPORTS = ["ssm_scan_fwd_workspace_bytes", "ssm_scan_fwd", "ssm_state_update", "
            "ssm_abi_version", "ssm_scan_fwd_plan_segments", "ssm_scan_bwd_workspace_bytes", "ssm_scan_bwd",
            "ssm_conv_scan_fwd", "ssm_conv_state_update", "ssm_complex_scan_fwd", "ssm_complex_state_update",
            "ssm_ssd_fwd", "ssm_ssd_state_update", "ssm_ssd_fwd_workspace_bytes", "ssm_ssd_fwd_plan_segments",
-           "ssm_conv1d_fwd", "ssm_conv1d_bwd", "ssm_scan_fwd_noalloc"]
+           "ssm_conv1d_fwd", "ssm_conv1d_bwd", "ssm_scan_fwd_noalloc", "ssm_conv1d_packed_fwd", "ssm_conv1d_slot_update",
+           "ssm_conv1d_packed_bwd", "ssm_conv1d_packed_bwd_workspace_bytes", "ssm_ssd_packed_fwd",
+           "ssm_ssd_packed_fwd_workspace_bytes", "ssm_ssd_slot_update", "ssm_gated_norm_fwd", "ssm_gated_norm_bwd",
+           "ssm_gated_norm_bwd_workspace_bytes"]
 
 
 class Params(ctypes.Structure):
@@ -39,6 +42,26 @@ class SsdParams(ctypes.Structure):
                 ("headdim", ctypes.c_int64), ("ngroups", ctypes.c_int64), ("dstate", ctypes.c_int64),
                 ("io_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("disc", ctypes.c_int32),
                 ("dt_softplus", ctypes.c_int32), ("segments", ctypes.c_int32)]
+
+
+class ConvPackedParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("ntokens", "nseqs", "dim", "nslots", "x_stride", "u_stride", "du_stride",
+                                              "dx_stride")] + \
+               [(n, ctypes.c_int32) for n in ("width", "activation", "io_dtype", "reserved")]
+
+
+class SsdPackedParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("ntokens", "nseqs", "nheads", "headdim", "ngroups", "dstate", "nslots",
+                                              "x_stride", "dt_stride", "b_stride", "c_stride", "y_stride", "dy_stride",
+                                              "dx_stride", "ddt_stride", "db_stride", "dc_stride")] + \
+               [(n, ctypes.c_int32) for n in ("io_dtype", "disc", "dt_softplus", "segment_chunks", "reserved")]
+
+
+class GatedNormParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("ntokens", "dim", "ngroups", "x_stride", "z_stride", "y_stride",
+                                              "dy_stride", "dx_stride", "dz_stride")] + \
+               [("eps", ctypes.c_float)] + \
+               [(n, ctypes.c_int32) for n in ("io_dtype", "gate_first", "center", "reserved")]
 
 
 class SSMError(RuntimeError):
@@ -97,6 +120,27 @@ def lib():
         L.ssm_ssd_fwd_plan_segments.restype = ctypes.c_int
         L.ssm_ssd_state_update.argtypes = [SP] + [P] * 11
         L.ssm_ssd_state_update.restype = ctypes.c_int
+        KP, QP, NP = (ctypes.POINTER(c) for c in (ConvPackedParams, SsdPackedParams, GatedNormParams))
+        L.ssm_conv1d_packed_fwd.argtypes = [KP] + [P] * 10
+        L.ssm_conv1d_packed_fwd.restype = ctypes.c_int
+        L.ssm_conv1d_slot_update.argtypes = [KP] + [P] * 7
+        L.ssm_conv1d_slot_update.restype = ctypes.c_int
+        L.ssm_conv1d_packed_bwd_workspace_bytes.argtypes = [KP]
+        L.ssm_conv1d_packed_bwd_workspace_bytes.restype = S
+        L.ssm_conv1d_packed_bwd.argtypes = [KP] + [P] * 13 + [P, S, P]
+        L.ssm_conv1d_packed_bwd.restype = ctypes.c_int
+        L.ssm_ssd_packed_fwd_workspace_bytes.argtypes = [QP]
+        L.ssm_ssd_packed_fwd_workspace_bytes.restype = S
+        L.ssm_ssd_packed_fwd.argtypes = [QP] + [P] * 13 + [P, S, P]
+        L.ssm_ssd_packed_fwd.restype = ctypes.c_int
+        L.ssm_ssd_slot_update.argtypes = [QP] + [P] * 11
+        L.ssm_ssd_slot_update.restype = ctypes.c_int
+        L.ssm_gated_norm_fwd.argtypes = [NP] + [P] * 6
+        L.ssm_gated_norm_fwd.restype = ctypes.c_int
+        L.ssm_gated_norm_bwd_workspace_bytes.argtypes = [NP]
+        L.ssm_gated_norm_bwd_workspace_bytes.restype = S
+        L.ssm_gated_norm_bwd.argtypes = [NP] + [P] * 9 + [P, S, P]
+        L.ssm_gated_norm_bwd.restype = ctypes.c_int
         L.ssm_status_str.argtypes = [ctypes.c_int]
         L.ssm_status_str.restype = ctypes.c_char_p
         L.ssm_last_error.argtypes = []

@@ -1,0 +1,231 @@
+// Device helpers of the SSD kernels over packed sequences (ssm_packed_ssd.hip, ssm_packed_ssd_bwd.hip): matrix-core
+// operands, the chunk copies into LDS, per-step scalars, and the segments that sequences are cut into.
+//
+// v_mfma_f32_16x16x32_bf16: lane l holds A[l%16][8(l/16)+q] and B[8(l/16)+q][l%16], q = 0..7, and the result
+// D[4(l/16)+c][l%16] in register c.  Which rows, columns or k a lane's index stands for is free as long as the operands
+// agree, so accumulator tiles become operands without moving data between lanes, and two 16-row tiles 2i, 2i + 1 are
+// numbered 32 i + 8 (r / 4) + 4 (tile & 1) + r % 4: a lane's four values of each then stand for eight consecutive
+// rows, which is one 16-byte access to memory or LDS.
+#pragma once
+
+#include "packed.hpp"
+
+namespace ssm57 {
+
+typedef __bf16 pb8 __attribute__((ext_vector_type(8)));
+typedef short pv4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) pv4s lds_pv4s;
+typedef __attribute__((address_space(3))) void lds_pvoid;
+
+constexpr int kChunk = 64;   // steps per chunk
+constexpr int kHead = 64;    // head width
+
+__device__ __forceinline__ pf4 mma(pu4 a, pu4 b, pf4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(pb8, a), __builtin_bit_cast(pb8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ pu2 bf16x4(float a, float b, float c, float d) { return pu2{pack_bf16(a, b), pack_bf16(c, d)}; }
+__device__ __forceinline__ pu4 join(pu2 a, pu2 b) { return pu4{a[0], a[1], b[0], b[1]}; }
+// v = hi + lo, each in bf16 (hi rounded to nearest, lo the rounded rest): 16 significant bits, off by at most 2^-18 v
+__device__ __forceinline__ void split_bf16x4(float a, float b, float c, float d, pu2& hi, pu2& lo) {
+  hi = bf16x4(a, b, c, d);
+  lo = bf16x4(a - lo_f32(hi[0]), b - hi_f32(hi[0]), c - lo_f32(hi[1]), d - hi_f32(hi[1]));
+}
+
+// Rows of a chunk in LDS: U 16-byte units each, unit u of row r at u ^ swz(r).  16-byte reads go 8 lanes at a time over
+// 128 bytes of banks: 8 consecutive rows of one unit need 8 different places (the low three bits).  Transposing reads
+// go 32 lanes over 256 bytes: 8 consecutive rows x 4 consecutive units, one 8-byte half of each, spread over all 16
+// places by bit 3.
+template <int U>
+__device__ __forceinline__ int swz_unit(int r, int u) {
+  return u ^ (((r & 7) | ((r & 2) << 2)) & (U - 1));
+}
+// byte address of unit u of row r
+template <int U>
+__device__ __forceinline__ int unit_at(int r, int u) {
+  return (r * U + swz_unit<U>(r, u)) * 16;
+}
+__device__ __forceinline__ pu4 lds_u4(const void* base, int byte) {
+  return *reinterpret_cast<const pu4*>(static_cast<const char*>(base) + byte);
+}
+// ds_read_b64_tr_b16: within each 16 lanes, lane i receives element i%4 of the 8-byte pieces that lanes 4q + i/4
+// (q = 0..3) point at.  Lane j points at row k0 + j/4, columns 4(j%4).. of tile `tile` (16 columns, numbered as above):
+// lane i receives column i of the tile at rows k0 .. k0+3.
+template <int U>
+__device__ __forceinline__ pu2 lds_tr(const void* base, int k0, int tile, int l16) {
+  const int byte = unit_at<U>(k0 + (l16 >> 2), 4 * (tile >> 1) + (l16 & 3)) + 8 * (tile & 1);
+  return __builtin_bit_cast(pu2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                     (lds_pv4s*)(static_cast<const char*>(base) + byte)));
+}
+// operand over 32 rows (the k index) of a tile's 16 columns; the lane's k: rows 32 kk + 4 g4 + c and 16 more
+template <int U>
+__device__ __forceinline__ pu4 lds_tr_operand(const void* base, int kk, int tile, int l16, int g4) {
+  return join(lds_tr<U>(base, 32 * kk + 4 * g4, tile, l16), lds_tr<U>(base, 32 * kk + 16 + 4 * g4, tile, l16));
+}
+// operand whose row (or column) index is a row of LDS and whose k are 32 consecutive columns from 32 kk
+template <int U>
+__device__ __forceinline__ pu4 lds_row_operand(const void* base, int row, int kk, int g4) {
+  return lds_u4(base, unit_at<U>(row, 4 * kk + g4));
+}
+
+// A chunk's rows of one tensor: a buffer range that starts at the chunk's first row and ends with its last valid one,
+// so that rows behind it read as zeros and are not written.  The base is 64-bit; only offsets inside a chunk are 32-bit.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rsrc(const uint16_t* base, int64_t row, int64_t stride, int rows,
+                                                             int width) {
+  return make_rsrc(base + row * stride, rows > 0 ? int64_t(rows - 1) * stride + width : 0);
+}
+
+// Copy of a chunk's 64 rows x U units into LDS by NW waves.
+template <int U, int NW>
+__device__ __forceinline__ void copy_rows(void* dst, __amdgpu_buffer_rsrc_t rsrc, int wave, int lane,
+                                          uint32_t row_bytes) {
+  constexpr int kInstr = kChunk * U / (64 * NW);
+  constexpr int kStep = 64 * NW / U;   // rows between a lane's copies
+  static_assert(kInstr >= 1 && kStep % 8 == 0, "a lane's copies share their place in the row");
+  const int place = 64 * wave + lane;
+  const int r = place / U;
+  const uint32_t base = static_cast<uint32_t>(r) * row_bytes + 16u * static_cast<uint32_t>(swz_unit<U>(r, place % U));
+#pragma unroll
+  for (int i = 0; i < kInstr; ++i)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rsrc, (lds_pvoid*)(static_cast<char*>(dst) + 1024 * (wave + NW * i)), 16,
+        static_cast<int>(base + static_cast<uint32_t>(i * kStep) * row_bytes), 0, 0, 0);
+}
+
+__device__ __forceinline__ void wait_memory() { __builtin_amdgcn_s_waitcnt(0x0F70); }   // vmcnt(0)
+// Keeps the parts of a chunk apart for the compiler: operands read from LDS for one are not kept in registers for the
+// next (they are read again), nor read ahead of it, so that the parts' registers do not add up.
+__device__ __forceinline__ void part_ends() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+// Waits for this wave's LDS operations: what it read is in registers before anything that follows is issued.
+__device__ __forceinline__ void wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+}
+// Barrier for LDS written by ds_write: waits for this wave's LDS operations only.  (The empty asm keeps the compiler
+// from moving memory accesses across it.)
+__device__ __forceinline__ void barrier_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <int K>
+__device__ __forceinline__ float lanes_shr(float v) {   // lane i of a 16-lane row reads lane i - K, 0 before the row
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x110 + K, 0xf, 0xf,
+                                                               false));
+}
+template <int K>
+__device__ __forceinline__ float lanes_shl(float v) {   // lane i + K, 0 behind the row
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x100 + K, 0xf, 0xf,
+                                                               false));
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+// sum over lanes 0..lane
+__device__ __forceinline__ float wave_prefix(float v, int lane) {
+  v += lanes_shr<1>(v);
+  v += lanes_shr<2>(v);
+  v += lanes_shr<4>(v);
+  v += lanes_shr<8>(v);
+  const float r0 = lane_value(v, 15), r1 = lane_value(v, 31), r2 = lane_value(v, 47);
+  const int row = lane >> 4;
+  return v + (row >= 1 ? r0 : 0.0f) + (row >= 2 ? r1 : 0.0f) + (row >= 3 ? r2 : 0.0f);
+}
+// sum over lanes lane..63
+__device__ __forceinline__ float wave_suffix(float v, int lane) {
+  v += lanes_shl<1>(v);
+  v += lanes_shl<2>(v);
+  v += lanes_shl<4>(v);
+  v += lanes_shl<8>(v);
+  const float r1 = lane_value(v, 16), r2 = lane_value(v, 32), r3 = lane_value(v, 48);
+  const int row = lane >> 4;
+  return v + (row <= 2 ? r3 : 0.0f) + (row <= 1 ? r2 : 0.0f) + (row <= 0 ? r1 : 0.0f);
+}
+
+// Segments: sequence s is cut into max(1, ceil(chunks / cps)) segments of cps chunks, numbered over all sequences.
+struct Segment {
+  int seq, begin, end;   // sequence and its tokens
+  int index, count;      // segment within the sequence, and how many it has
+  int first;             // number of the sequence's first segment
+};
+__device__ __forceinline__ int segments_of(int tokens, int cps) {
+  const int chunks = (tokens + kChunk - 1) / kChunk;
+  return chunks > cps ? (chunks + cps - 1) / cps : 1;
+}
+// Segment `want` over all sequences; false past the last.  Every lane of the wave takes part and gets the answer.
+__device__ __forceinline__ bool find_segment(const int32_t* cu, int nseqs, int ntokens, int cps, int want, int lane,
+                                             Segment& out) {
+  int before = 0;
+  for (int s0 = 0; s0 < nseqs; s0 += 64) {
+    const int s = s0 + lane;
+    int begin = 0, end = 0, n = 0;
+    if (s < nseqs) {
+      seq_range(cu, s, ntokens, begin, end);
+      n = segments_of(end - begin, cps);
+    }
+    int sum = n;   // inclusive sum over the lanes
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) {
+      const int v = __shfl_up(sum, m);
+      if (lane >= m) sum += v;
+    }
+    const uint64_t hit = __ballot(n > 0 && want >= before + sum - n && want < before + sum);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      out.seq = s0 + l;
+      out.begin = __builtin_amdgcn_readlane(begin, l);
+      out.end = __builtin_amdgcn_readlane(end, l);
+      out.count = __builtin_amdgcn_readlane(n, l);
+      out.first = before + __builtin_amdgcn_readlane(sum, l) - out.count;
+      out.index = want - out.first;
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(sum, 63);
+  }
+  return false;
+}
+
+// Step size, its weight and the decay's logarithm (base 2) of one step; zeros behind the sequence.
+__device__ __forceinline__ void step_scalars(float dt, float bias, float A, bool use_softplus, bool zoh, bool live,
+                                             float& delta, float& phi, float& la) {
+  const float u = dt + bias;
+  delta = use_softplus ? softplus(u) : u;
+  delta = live ? delta : 0.0f;
+  la = delta * A * kLog2e;
+  phi = delta;
+  if (zoh && A != 0.0f) {
+    const float e = delta * A;
+    phi = expm1_from(e, hw_exp2(e * kLog2e)) / A;
+  }
+}
+
+// Workgroups are dealt to the 8 XCDs in turn: give each XCD a run of consecutive items (the grid is a multiple of 8).
+__device__ __forceinline__ int xcd_item() {
+  const int per = static_cast<int>(gridDim.x) / 8;
+  return (static_cast<int>(blockIdx.x) % 8) * per + static_cast<int>(blockIdx.x) / 8;
+}
+
+// ---------------------------------------------------------------------------------------------------------------
+// host side
+
+ssm_status check_packed_ssd(const ssm_ssd_packed_params* p, bool step);
+
+// Heads a workgroup of 8 waves takes: a wave holds the state of one for N <= 128, of half of one for N = 256.
+inline int heads_per_group(const ssm_ssd_packed_params* p) { return p->dstate == 256 ? 4 : 8; }
+
+struct PackedPlan {
+  int hblocks;    // workgroups per group of heads
+  int cps;        // chunks per segment
+  int64_t nseg;   // segments at most, over all sequences
+  bool split;     // whether a sequence can have more than one
+};
+PackedPlan packed_plan(const ssm_ssd_packed_params* p);
+
+inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace ssm57

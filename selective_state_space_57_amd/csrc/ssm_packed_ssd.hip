@@ -1,0 +1,620 @@
+// The Mamba-2 SSD layer over packed sequences on gfx950: prompts (chunked matrix form on the bf16 matrix cores) and
+// single tokens, with the recurrent state of each sequence in a slot of a pool.
+//
+//   Delta_t = softplus(dt + bias);  a_t = exp(Delta_t A);  phi_t = Delta_t or expm1(Delta_t A) / A
+//   S_t[p][n] = a_t S_{t-1}[p][n] + phi_t x_t[p] B_t[n];   y_t[p] = sum_n S_t[p][n] C_t[n] + D x_t[p]
+// In chunks of 64 steps, with c_t the running sum of Delta A inside a chunk and S the state entering it:
+//   y_t = exp(c_t) S C_t + sum_{s<=t} M[t][s] x_s + D x_t,   M[t][s] = (C_t . B_s) exp(c_t - c_s) phi_s
+//   S  <- exp(c_63) S + sum_s (phi_s exp(c_63 - c_s) x_s) B_s^T
+//
+// A workgroup takes 8 heads of one group over one segment of a sequence and walks its chunks, one wave to a head, with
+// the state in registers (N x 64 fp32 = N VGPRs a lane; for N = 256 a wave takes half of a head's columns, which do not
+// meet, and the workgroup 4 heads).  What heads share is done once: B and C are copied to LDS for all of them, a chunk
+// ahead, and the 10 lower tiles of C B^T are shared out over the waves.  Everything else belongs to one wave, so a chunk
+// has two barriers only, and every operand is read from LDS once per wave for all of its columns.
+// Sequences longer than a segment: a first pass runs the state recurrence of each segment from zero, a second joins
+// the segments' states in order, and the full pass starts every segment from its state.
+//
+// Precision: fp32 state and accumulation; x, B and C enter the matrix cores as they are.  The weighted x of the state
+// update is split into two bf16 parts (2^-18 relative), so the state keeps fp32 quality over long sequences.  M and the
+// state's copy that meets C are rounded once to bf16 (2^-9 relative, as the output is): they only reach y, which is
+// rounded to bf16 itself.
+#include "packed_ssd.hpp"
+
+namespace ssm57 {
+namespace {
+
+struct PSsdArgs {
+  const uint16_t* x;
+  const uint16_t* dt;
+  const uint16_t* B;
+  const uint16_t* C;
+  const float* dt_bias;
+  const float* A;
+  const float* Dskip;
+  const int32_t* cu;
+  const float* state;
+  const int32_t* idx;
+  const uint8_t* has;
+  float* state_out;
+  uint16_t* y;
+  float* ws_state;   // [segments][H][64][N]
+  float* ws_decay;   // [segments][H]
+  int64_t xs, dts, bs, cs, ys, nslots;
+  int T, S, H, G, hpg, hblocks;   // hblocks: workgroups per group
+  int cps, nseg, nwork;
+  int softplus, zoh;
+};
+
+constexpr int kWaves = 8;
+
+// scalars of one chunk, per wave
+struct alignas(16) HeadScalars {
+  float c[kChunk];     // c_t, base 2
+  float phi[kChunk];
+  float w[kChunk];     // phi_s exp(c_63 - c_s)
+};
+
+// STATES: the first pass (the state recurrence alone, from zero)
+template <int N, bool STATES>
+__global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
+packed_ssd_fwd_kernel(PSsdArgs a) {
+  constexpr int NW = kWaves;
+  constexpr int PT = N == 256 ? 2 : 4;   // 16-column tiles of a wave
+  constexpr int kParts = 4 / PT;         // waves of a head
+  constexpr int UX = 2 * PT;             // 16-byte units of its columns
+  constexpr int U = N / 8;
+  constexpr int NT = N / 16;   // 16-row tiles of the state
+  constexpr int NK = N / 32;
+  constexpr bool kOneC = N == 256;       // (two copies of C would not fit the LDS)
+  __shared__ alignas(16) uint16_t sB0[kChunk * N], sB1[kChunk * N];
+  __shared__ alignas(16) uint16_t sC0[STATES ? 8 : kChunk * N], sC1[STATES || kOneC ? 8 : kChunk * N];
+  __shared__ alignas(16) uint16_t sX[NW][kChunk * 16 * PT];
+  __shared__ pf4 sCB[STATES ? 1 : 10][64];
+  __shared__ HeadScalars sS[NW];
+
+  const int item = xcd_item();
+  if (item >= a.nwork) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, g4 = lane >> 4;
+  const int hb = item % (a.G * a.hblocks);
+  Segment seg;
+  if (!find_segment(a.cu, a.S, a.T, a.cps, item / (a.G * a.hblocks), lane, seg)) return;
+  if (STATES && seg.index == seg.count - 1) return;   // nothing starts from the last segment's end
+  const int g = hb / a.hblocks;
+  const int hg = (hb % a.hblocks) * (NW / kParts) + wave / kParts;   // head within the group
+  const int p0 = (wave % kParts) * 16 * PT;            // first column of this wave
+  const bool on = hg < a.hpg;                          // (a wave without a head computes the last one's, unstored)
+  const int h = g * a.hpg + (on ? hg : a.hpg - 1);
+
+  const int t_begin = seg.begin + seg.index * a.cps * kChunk;
+  const int t_end = min(seg.end, seg.index == seg.count - 1 ? seg.end : t_begin + a.cps * kChunk);
+  const int nchunks = (t_end - t_begin + kChunk - 1) / kChunk;
+
+  const float Ah = a.A[h];
+  const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+  const float Dh = a.Dskip ? a.Dskip[h] : 0.0f;
+  const uint16_t* xh = a.x + int64_t(h) * kHead + p0;
+  const uint16_t* Bg = a.B + int64_t(g) * N;
+  const uint16_t* Cg = a.C + int64_t(g) * N;
+  const uint32_t xrow = static_cast<uint32_t>(a.xs) * 2u, brow = static_cast<uint32_t>(a.bs) * 2u,
+                 crow = static_cast<uint32_t>(a.cs) * 2u, yrow = static_cast<uint32_t>(a.ys) * 2u;
+
+  auto rows_of = [&](int ck) { return min(max(t_end - (t_begin + ck * kChunk), 0), kChunk); };
+  auto copy_group = [&](int ck, uint16_t* dst, const uint16_t* src, int64_t stride, uint32_t row_bytes)
+                        __attribute__((always_inline)) {
+    const int64_t t0 = t_begin + int64_t(ck) * kChunk;
+    const int rows = rows_of(ck);
+    copy_rows<U, NW>(dst, chunk_rsrc(src, rows ? t0 : 0, stride, rows, N), wave, lane, row_bytes);
+  };
+  auto copy_x = [&](int ck) __attribute__((always_inline)) {
+    const int64_t t0 = t_begin + int64_t(ck) * kChunk;
+    const int rows = rows_of(ck);
+    copy_rows<UX, 1>(sX[wave], chunk_rsrc(xh, rows ? t0 : 0, a.xs, rows, 16 * PT), 0, lane, xrow);
+  };
+  auto load_dt = [&](int ck) __attribute__((always_inline)) -> uint32_t {
+    const int64_t t = t_begin + int64_t(ck) * kChunk + lane;
+    return a.dt[(t < t_end ? t : (t_begin < a.T ? t_begin : 0)) * a.dts + h];
+  };
+
+  // state tiles: S[nt][pt][c] = S[p][n], n = 32 (nt/2) + 8 g4 + 4 (nt%2) + c, p = p0 + 32 (pt/2) + 8 (l16/4) + 4 (pt%2) + l16%4
+  pf4 S[NT][PT];
+  const int64_t head_size = int64_t(kHead) * N;
+  const int lane_entry = (p0 + 8 * (l16 >> 2) + (l16 & 3)) * N + 8 * g4;
+  auto entry = [&](int nt, int pt) __attribute__((always_inline)) {
+    return lane_entry + (32 * (pt >> 1) + 4 * (pt & 1)) * N + 32 * (nt >> 1) + 4 * (nt & 1);
+  };
+  {
+    const float* from = nullptr;
+    if constexpr (!STATES) {
+      if (seg.count > 1) {
+        from = a.ws_state + (int64_t(seg.first + seg.index) * a.H + h) * head_size;
+      } else if (a.state && (!a.has || a.has[seg.seq])) {
+        const int64_t slot = slot_of(a.idx, seg.seq, a.nslots);
+        if (slot >= 0) from = a.state + (slot * a.H + h) * head_size;
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+        S[nt][pt] = from ? *reinterpret_cast<const pf4*>(from + entry(nt, pt)) : pf4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  float decay = 0.0f;   // sum of log2 decays over the segment (first pass)
+
+  HeadScalars& sc = sS[wave];
+  const uint16_t* X = sX[wave];
+
+  auto chunk = [&](const int ck, const uint16_t* B, const uint16_t* C, uint16_t* Bn, uint16_t* Cn, const uint32_t dtv)
+                   __attribute__((always_inline)) -> uint32_t {
+    wait_memory();    // this wave's copies of the chunk
+    barrier_lds();    // everyone's, and the previous chunk's readers are done
+    copy_group(ck + 1, Bn, Bg, a.bs, brow);
+    if constexpr (!STATES && !kOneC) copy_group(ck + 1, Cn, Cg, a.cs, crow);
+    const uint32_t dt_next = load_dt(ck + 1);
+    const int rows = rows_of(ck);
+    {
+      float delta, phi, la;
+      step_scalars(lo_f32(dtv), bias, Ah, a.softplus, a.zoh, lane < rows, delta, phi, la);
+      const float c = wave_prefix(la, lane);
+      // exp(c_63 - c_s) from the sum behind step s: no difference of two large sums
+      const float behind = wave_suffix(la, lane) - la;
+      sc.c[lane] = c;
+      sc.phi[lane] = phi;
+      sc.w[lane] = phi * hw_exp2(behind);
+    }
+    wave_lds_sync();
+    const float total = sc.c[kChunk - 1];
+    if constexpr (!STATES) {
+      // C B^T, tile i = (tb, sb), sb <= tb: rows s, columns t
+#pragma unroll
+      for (int i = 0; i < 10; ++i) {
+        if (i % NW != wave) continue;
+        const int tb = i >= 6 ? 3 : (i >= 3 ? 2 : (i >= 1 ? 1 : 0)), sb = i - tb * (tb + 1) / 2;
+        pf4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk)
+          v = mma(lds_row_operand<U>(B, 16 * sb + l16, kk, g4), lds_row_operand<U>(C, 16 * tb + l16, kk, g4), v);
+        sCB[i][lane] = v;
+      }
+      barrier_lds();
+      // M[t][s] of this head, operand over s: (tb, kk) = (0,0) (1,0) (2,0) (2,1) (3,0) (3,1)
+      pu4 M[4][2];
+      float ct[4];
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) {
+        ct[tb] = sc.c[16 * tb + l16];
+#pragma unroll
+        for (int kk = 0; kk <= tb / 2; ++kk) {
+          pu2 half[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int sb = 2 * kk + e;
+            if (sb > tb) {
+              half[e] = pu2{0u, 0u};
+              continue;
+            }
+            const pf4 cb = sCB[tb * (tb + 1) / 2 + sb][lane];
+            const pf4 cs = *reinterpret_cast<const pf4*>(&sc.c[16 * sb + 4 * g4]);
+            const pf4 ph = *reinterpret_cast<const pf4*>(&sc.phi[16 * sb + 4 * g4]);
+            float m[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              // (above the diagonal the difference can be large and positive: masked after the fact)
+              m[c] = cb[c] * (hw_exp2(ct[tb] - cs[c]) * ph[c]);
+              if (sb == tb) m[c] = 4 * g4 + c <= l16 ? m[c] : 0.0f;
+            }
+            half[e] = bf16x4(m[0], m[1], m[2], m[3]);
+          }
+          M[tb][kk] = join(half[0], half[1]);
+        }
+      }
+      const int64_t t0 = t_begin + int64_t(ck) * kChunk;
+      const auto ry = chunk_rsrc(a.y + int64_t(h) * kHead + p0, t0, a.ys, on ? rows : 0, 16 * PT);
+      // a pair of column tiles at a time: Y^T[p][t = 16 tb + l16]
+#pragma unroll
+      for (int pp = 0; pp < PT / 2; ++pp) {
+        part_ends();
+        pf4 acc[2][4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int tb = 0; tb < 4; ++tb) acc[e][tb] = pf4{0.0f, 0.0f, 0.0f, 0.0f};
+        // what the entering state gives: S C_t, scaled by exp(c_t)
+#pragma unroll
+        for (int kn = 0; kn < NK; ++kn) {
+          pu4 c[4];
+#pragma unroll
+          for (int tb = 0; tb < 4; ++tb) c[tb] = lds_row_operand<U>(C, 16 * tb + l16, kn, g4);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const pf4 s0 = S[2 * kn][2 * pp + e], s1 = S[2 * kn + 1][2 * pp + e];
+            const pu4 s = join(bf16x4(s0[0], s0[1], s0[2], s0[3]), bf16x4(s1[0], s1[1], s1[2], s1[3]));
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) acc[e][tb] = mma(s, c[tb], acc[e][tb]);
+          }
+        }
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+          const float f = hw_exp2(ct[tb]);
+          acc[0][tb] *= f;
+          acc[1][tb] *= f;
+        }
+        // inside the chunk: sum_{s<=t} x_s M[t][s]
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const pu4 xt = lds_tr_operand<UX>(X, kk, 2 * pp + e, l16, g4);
+#pragma unroll
+            for (int tb = 2 * kk; tb < 4; ++tb) acc[e][tb] = mma(xt, M[tb][kk], acc[e][tb]);
+          }
+        // a lane's two tiles of the pair are eight consecutive columns of step 16 tb + l16
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) {
+          const pu4 xv = lds_u4(X, unit_at<UX>(16 * tb + l16, 4 * pp + g4));
+          const pf4 y0 = acc[0][tb], y1 = acc[1][tb];
+          const pu4 o = {pack_bf16(fmaf(Dh, lo_f32(xv[0]), y0[0]), fmaf(Dh, hi_f32(xv[0]), y0[1])),
+                         pack_bf16(fmaf(Dh, lo_f32(xv[1]), y0[2]), fmaf(Dh, hi_f32(xv[1]), y0[3])),
+                         pack_bf16(fmaf(Dh, lo_f32(xv[2]), y1[0]), fmaf(Dh, hi_f32(xv[2]), y1[1])),
+                         pack_bf16(fmaf(Dh, lo_f32(xv[3]), y1[2]), fmaf(Dh, hi_f32(xv[3]), y1[3]))};
+          __builtin_amdgcn_raw_buffer_store_b128(
+              o, ry, static_cast<int>(static_cast<uint32_t>(16 * tb + l16) * yrow + (32u * pp + 8u * g4) * 2u), 0, 0);
+        }
+      }
+      if constexpr (kOneC) {
+        barrier_lds();   // everyone is done with C
+        copy_group(ck + 1, Cn, Cg, a.cs, crow);
+      }
+    }
+    part_ends();
+    // state update
+    pu4 wh[PT][2], wl[PT][2];   // phi_s exp(c_63 - c_s) x_s, in two parts
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const pf4 w0 = *reinterpret_cast<const pf4*>(&sc.w[32 * kk + 4 * g4]);
+      const pf4 w1 = *reinterpret_cast<const pf4*>(&sc.w[32 * kk + 16 + 4 * g4]);
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+        const pu4 v = lds_tr_operand<UX>(X, kk, pt, l16, g4);
+        pu2 h0, l0, h1, l1;
+        split_bf16x4(lo_f32(v[0]) * w0[0], hi_f32(v[0]) * w0[1], lo_f32(v[1]) * w0[2], hi_f32(v[1]) * w0[3], h0, l0);
+        split_bf16x4(lo_f32(v[2]) * w1[0], hi_f32(v[2]) * w1[1], lo_f32(v[3]) * w1[2], hi_f32(v[3]) * w1[3], h1, l1);
+        wh[pt][kk] = join(h0, h1);
+        wl[pt][kk] = join(l0, l1);
+      }
+    }
+    wait_lds();
+    copy_x(ck + 1);   // every read of this chunk's x has its value
+    const float fade = hw_exp2(total);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const pu4 b0 = lds_tr_operand<U>(B, 0, nt, l16, g4), b1 = lds_tr_operand<U>(B, 1, nt, l16, g4);
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+        pf4 v = S[nt][pt] * fade;
+        v = mma(b0, wh[pt][0], v);
+        v = mma(b0, wl[pt][0], v);
+        v = mma(b1, wh[pt][1], v);
+        S[nt][pt] = mma(b1, wl[pt][1], v);
+      }
+    }
+    if constexpr (STATES) decay += total;
+    return dt_next;
+  };
+
+  uint32_t dtv = load_dt(0);
+  copy_group(0, sB0, Bg, a.bs, brow);
+  if constexpr (!STATES) copy_group(0, sC0, Cg, a.cs, crow);
+  copy_x(0);
+  for (int ck = 0; ck < nchunks; ck += 2) {
+    dtv = chunk(ck, sB0, sC0, sB1, kOneC ? sC0 : sC1, dtv);
+    if (ck + 1 < nchunks) dtv = chunk(ck + 1, sB1, kOneC ? sC0 : sC1, sB0, sC0, dtv);
+  }
+  wait_memory();   // (the copies issued past the last chunk)
+
+  float* to = nullptr;
+  if constexpr (STATES) {
+    to = a.ws_state + (int64_t(seg.first + seg.index) * a.H + h) * head_size;
+    if (on && p0 == 0 && lane == 0) a.ws_decay[int64_t(seg.first + seg.index) * a.H + h] = decay;
+  } else if (a.state_out && seg.index == seg.count - 1) {
+    const int64_t slot = slot_of(a.idx, seg.seq, a.nslots);
+    if (slot >= 0) to = a.state_out + (slot * a.H + h) * head_size;
+  }
+  if (to && on) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) *reinterpret_cast<pf4*>(to + entry(nt, pt)) = S[nt][pt];
+  }
+}
+
+// Joins the segments of a sequence in order: the end state that the first pass left for segment j (from zero) gives
+// way to the state entering segment j.  A thread owns four entries; nothing to do for one segment.
+__global__ void __launch_bounds__(256) packed_ssd_join_kernel(PSsdArgs a, int entries) {
+  const int lane = threadIdx.x & 63;
+  int begin, end;
+  seq_range(a.cu, blockIdx.x, a.T, begin, end);
+  int count = segments_of(end - begin, a.cps);
+  if (count <= 1) return;
+  int before = 0;   // segments of the sequences before this one
+  for (int s0 = 0; s0 < static_cast<int>(blockIdx.x); s0 += 64) {
+    const int s = s0 + lane;
+    int n = 0;
+    if (s < static_cast<int>(blockIdx.x)) {
+      int b, e;
+      seq_range(a.cu, s, a.T, b, e);
+      n = segments_of(e - b, a.cps);
+    }
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) n += __shfl_xor(n, m);
+    before += n;
+  }
+  count = min(count, a.nseg - before);   // (only a cu_seqlens that is not ordered reaches this bound)
+  const int64_t e = (int64_t(blockIdx.y) * 256 + threadIdx.x) * 4;
+  const int64_t per = int64_t(a.H) * entries;   // entries of a head
+  if (e >= per) return;
+  const int h = static_cast<int>(e / entries);
+  pf4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (a.state && (!a.has || a.has[blockIdx.x])) {
+    const int64_t slot = slot_of(a.idx, blockIdx.x, a.nslots);
+    if (slot >= 0) s = *reinterpret_cast<const pf4*>(a.state + slot * per + e);
+  }
+  for (int j = 0; j < count; ++j) {
+    float* at = a.ws_state + int64_t(before + j) * per + e;
+    const bool more = j + 1 < count;
+    const pf4 own = more ? *reinterpret_cast<const pf4*>(at) : pf4{0.0f, 0.0f, 0.0f, 0.0f};
+    const float d = more ? hw_exp2(a.ws_decay[int64_t(before + j) * a.H + h]) : 0.0f;
+    *reinterpret_cast<pf4*>(at) = s;
+    s = s * d + own;
+  }
+}
+
+// One step for each row: 16 lanes own a state row, so a load instruction of theirs covers 256 contiguous bytes; the state
+// is read and written once, and everything else is small beside it.
+template <int N>
+__global__ void __launch_bounds__(256) packed_ssd_step_kernel(PSsdArgs a) {
+  constexpr int kV = N / 64;   // 16-byte pieces a lane holds of a row
+  const int64_t row = int64_t(blockIdx.x) * 16 + threadIdx.x / 16;   // (token, head, p); 64 rows a head: all in range
+  const int q = threadIdx.x % 16;
+  const int64_t th = row / kHead;
+  const int p = static_cast<int>(row % kHead);
+  const int h = static_cast<int>(th % a.H);
+  const int t = static_cast<int>(th / a.H);
+  const int g = h / a.hpg;
+  const int64_t slot = slot_of(a.idx, t, a.nslots);
+  float* st = a.state_out + ((max(slot, int64_t(0)) * a.H + h) * kHead + p) * N;
+  const uint16_t* Bt = a.B + t * a.bs + int64_t(g) * N;
+  const uint16_t* Ct = a.C + t * a.cs + int64_t(g) * N;
+  pf4 s[kV];
+  pu2 bw[kV], cw[kV];
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    const int n = 4 * (q + 16 * i);
+    s[i] = *reinterpret_cast<const pf4*>(st + n);
+    bw[i] = *reinterpret_cast<const pu2*>(Bt + n);
+    cw[i] = *reinterpret_cast<const pu2*>(Ct + n);
+  }
+  const float xv = lo_f32(a.x[t * a.xs + int64_t(h) * kHead + p]);
+  const float Dh = a.Dskip ? a.Dskip[h] : 0.0f;
+  float delta, phi, la;
+  step_scalars(lo_f32(a.dt[t * a.dts + h]), a.dt_bias ? a.dt_bias[h] : 0.0f, a.A[h], a.softplus, a.zoh, true, delta, phi,
+               la);
+  const float fade = slot >= 0 ? hw_exp2(la) : 0.0f;
+  const float in = phi * xv;
+  float acc = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kV; ++i) {
+    const float bv[4] = {lo_f32(bw[i][0]), hi_f32(bw[i][0]), lo_f32(bw[i][1]), hi_f32(bw[i][1])};
+    const float cv[4] = {lo_f32(cw[i][0]), hi_f32(cw[i][0]), lo_f32(cw[i][1]), hi_f32(cw[i][1])};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      // (without a state the row starts from zero, whatever the place read in its stead holds)
+      s[i][c] = fmaf(fade, slot >= 0 ? s[i][c] : 0.0f, in * bv[c]);
+      acc = fmaf(cv[c], s[i][c], acc);
+    }
+    if (slot >= 0) *reinterpret_cast<pf4*>(st + 4 * (q + 16 * i)) = s[i];
+  }
+  acc += row_ror<8>(acc);
+  acc += row_ror<4>(acc);
+  acc += row_ror<2>(acc);
+  acc += row_ror<1>(acc);
+  if (q == 0) Elem<uint16_t>::st(a.y, t * a.ys + int64_t(h) * kHead + p, fmaf(Dh, xv, acc));
+}
+
+template <int N>
+ssm_status launch_fwd(const PSsdArgs& args, const PackedPlan& pl, hipStream_t st) {
+  PSsdArgs a = args;
+  a.nwork = static_cast<int>(pl.nseg * a.G * a.hblocks);
+  const dim3 grid((a.nwork + 7) / 8 * 8), block(kWaves * 64);
+  if (pl.split) {
+    hipLaunchKernelGGL((packed_ssd_fwd_kernel<N, true>), grid, block, 0, st, a);
+    const int64_t entries = int64_t(kHead) * N;
+    const int64_t blocks = (a.H * entries / 4 + 255) / 256;
+    hipLaunchKernelGGL(packed_ssd_join_kernel, dim3(a.S, static_cast<uint32_t>(blocks)), dim3(256), 0, st, a,
+                       static_cast<int>(entries));
+  }
+  hipLaunchKernelGGL((packed_ssd_fwd_kernel<N, false>), grid, block, 0, st, a);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? SSM_OK : fail(SSM_ERR_HIP, "packed SSD launch: %s", hipGetErrorString(e));
+}
+
+template <int N>
+ssm_status launch_step(const PSsdArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((packed_ssd_step_kernel<N>), dim3(static_cast<uint32_t>(int64_t(a.T) * a.H * (kHead / 16))),
+                     dim3(256), 0, st, a);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? SSM_OK : fail(SSM_ERR_HIP, "packed SSD step launch: %s", hipGetErrorString(e));
+}
+
+size_t fwd_workspace(const ssm_ssd_packed_params* p) {
+  const PackedPlan pl = packed_plan(p);
+  if (!pl.split) return 0;
+  return up256(size_t(pl.nseg) * p->nheads * kHead * p->dstate * 4) + up256(size_t(pl.nseg) * p->nheads * 4);
+}
+
+PSsdArgs ssd_args(const ssm_ssd_packed_params* p) {
+  PSsdArgs a{};
+  a.T = static_cast<int>(p->ntokens);
+  a.S = static_cast<int>(p->nseqs);
+  a.H = static_cast<int>(p->nheads);
+  a.G = static_cast<int>(p->ngroups);
+  a.hpg = a.H / a.G;
+  a.nslots = p->nslots;
+  a.xs = p->x_stride ? p->x_stride : p->nheads * kHead;
+  a.ys = p->y_stride ? p->y_stride : p->nheads * kHead;
+  a.dts = p->dt_stride ? p->dt_stride : p->nheads;
+  a.bs = p->b_stride ? p->b_stride : p->ngroups * p->dstate;
+  a.cs = p->c_stride ? p->c_stride : p->ngroups * p->dstate;
+  a.softplus = p->dt_softplus;
+  a.zoh = p->disc == SSM_DISC_ZOH;
+  return a;
+}
+
+}  // namespace
+
+ssm_status check_packed_ssd(const ssm_ssd_packed_params* p, bool step) {
+  if (!p) return fail(SSM_ERR_NULL, "params is NULL");
+  if (p->reserved != 0) return fail(SSM_ERR_UNSUPPORTED, "reserved must be 0");
+  if (p->ntokens < 1 || p->nheads < 1 || p->ngroups < 1 || (!step && p->nseqs < 1) || p->nslots < 0)
+    return fail(SSM_ERR_SHAPE, "ntokens, nseqs, nheads and ngroups must be >= 1, nslots >= 0");
+  if (p->nheads % p->ngroups) return fail(SSM_ERR_SHAPE, "nheads (%lld) must be a multiple of ngroups (%lld)",
+                                          (long long)p->nheads, (long long)p->ngroups);
+  if (p->headdim != kHead) return fail(SSM_ERR_UNSUPPORTED, "headdim must be %d (got %lld)", kHead, (long long)p->headdim);
+  if (p->dstate != 64 && p->dstate != 128 && p->dstate != 256)
+    return fail(SSM_ERR_UNSUPPORTED, "dstate must be 64, 128 or 256 (got %lld)", (long long)p->dstate);
+  if (p->ntokens >= (int64_t(1) << 30) || p->nheads > (int64_t(1) << 20) ||
+      (!step && (p->nseqs > (int64_t(1) << 20))))
+    return fail(SSM_ERR_SHAPE, "ntokens must be below 2^30, nheads and nseqs at most 2^20");
+  if (p->io_dtype != SSM_BF16)
+    return fail(SSM_ERR_DTYPE, "the SSD path takes bf16 x, dt, B and C (io_dtype must be SSM_BF16)");
+  if (p->disc != SSM_DISC_EULER_B && p->disc != SSM_DISC_ZOH) return fail(SSM_ERR_UNSUPPORTED, "unknown disc %d", p->disc);
+  if (p->dt_softplus != 0 && p->dt_softplus != 1)
+    return fail(SSM_ERR_UNSUPPORTED, "dt_softplus must be 0 or 1 (got %d)", p->dt_softplus);
+  if (p->segment_chunks < 0) return fail(SSM_ERR_UNSUPPORTED, "segment_chunks must be >= 0 (got %d)", p->segment_chunks);
+  const int64_t head = p->nheads * kHead, grp = p->ngroups * p->dstate;
+  const struct { int64_t s, row; } rows[] = {{p->x_stride, head}, {p->y_stride, head}, {p->dt_stride, p->nheads},
+                                             {p->b_stride, grp}, {p->c_stride, grp}, {p->dy_stride, head},
+                                             {p->dx_stride, head}, {p->ddt_stride, p->nheads}, {p->db_stride, grp},
+                                             {p->dc_stride, grp}};
+  // a chunk of 64 rows is addressed with 32-bit byte offsets
+  const int64_t most = int64_t(1) << 24;
+  for (const auto& r : rows) {
+    if (r.s != 0 && r.s < r.row)
+      return fail(SSM_ERR_SHAPE, "a row stride of %lld is shorter than a row of %lld", (long long)r.s, (long long)r.row);
+    if (r.s >= most || r.row >= most)
+      return fail(SSM_ERR_SHAPE, "rows and row strides must stay below 2^24 elements");
+  }
+  if (step && p->ntokens * p->nheads >= (int64_t(1) << 29)) return fail(SSM_ERR_SHAPE, "too many rows for one launch");
+  if (!step) {
+    const PackedPlan pl = packed_plan(p);
+    if (pl.nseg * p->ngroups * pl.hblocks >= (int64_t(1) << 31) - 8) return fail(SSM_ERR_SHAPE, "too many work items");
+    if (p->nheads * kHead * p->dstate / 1024 >= 65535) return fail(SSM_ERR_SHAPE, "nheads is too large");
+  }
+  return SSM_OK;
+}
+
+PackedPlan packed_plan(const ssm_ssd_packed_params* p) {
+  PackedPlan pl{};
+  const int64_t hpg = p->nheads / p->ngroups, per = heads_per_group(p);
+  pl.hblocks = static_cast<int>((hpg + per - 1) / per);
+  const int64_t longest = (p->ntokens + kChunk - 1) / kChunk;      // chunks of one sequence, at most
+  const int64_t chunks = p->ntokens / kChunk + p->nseqs;           // and of all
+  int64_t cps = p->segment_chunks;
+  if (cps == 0) {
+    // one workgroup for each of the 256 CUs; a segment's state costs as much memory traffic as four chunks
+    cps = (chunks * p->ngroups * pl.hblocks + 255) / 256;
+    if (cps < 8) cps = 8;
+  }
+  if (cps > longest) cps = longest;
+  pl.cps = static_cast<int>(cps);
+  pl.split = longest > cps;
+  pl.nseg = pl.split ? p->nseqs + chunks / cps : p->nseqs;
+  return pl;
+}
+
+}  // namespace ssm57
+
+using namespace ssm57;
+
+extern "C" size_t ssm_ssd_packed_fwd_workspace_bytes(const ssm_ssd_packed_params* p) {
+  return check_packed_ssd(p, false) == SSM_OK ? fwd_workspace(p) : 0;
+}
+
+extern "C" ssm_status ssm_ssd_packed_fwd(const ssm_ssd_packed_params* p, const void* x, const void* dt,
+                                         const float* dt_bias, const float* A, const void* B, const void* C,
+                                         const float* Dskip, const int32_t* cu_seqlens, const float* state,
+                                         const int32_t* state_idx, const uint8_t* has_state, float* state_out, void* y,
+                                         void* workspace, size_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  if (ssm_status s = check_packed_ssd(p, false); s != SSM_OK) return s;
+  if (!x || !dt || !A || !B || !C || !cu_seqlens || !y)
+    return fail(SSM_ERR_NULL, "x, dt, A, B, C, cu_seqlens and y are required");
+  PSsdArgs a = ssd_args(p);
+  if (!aligned(x, 16) || !aligned(B, 16) || !aligned(C, 16) || !aligned(y, 16) || a.xs % 8 || a.bs % 8 || a.cs % 8 ||
+      a.ys % 8 || !aligned(state, 16) || !aligned(state_out, 16) || !aligned(dt, 2) || !aligned(A, 4) ||
+      !aligned(dt_bias, 4) || !aligned(Dskip, 4) || !aligned(cu_seqlens, 4) || !aligned(state_idx, 4))
+    return fail(SSM_ERR_ALIGN, "rows of x, B, C and y, and the states, must be 16-byte aligned");
+  const size_t need = fwd_workspace(p);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
+    return fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes (16-byte aligned) needed, got %zu at %p", need,
+                workspace_bytes, workspace);
+  const PackedPlan pl = packed_plan(p);
+  a.x = static_cast<const uint16_t*>(x);
+  a.dt = static_cast<const uint16_t*>(dt);
+  a.B = static_cast<const uint16_t*>(B);
+  a.C = static_cast<const uint16_t*>(C);
+  a.dt_bias = dt_bias;
+  a.A = A;
+  a.Dskip = Dskip;
+  a.cu = cu_seqlens;
+  a.state = state;
+  a.idx = state_idx;
+  a.has = has_state;
+  a.state_out = state_out;
+  a.y = static_cast<uint16_t*>(y);
+  a.hblocks = pl.hblocks;
+  a.cps = pl.cps;
+  a.nseg = static_cast<int>(pl.nseg);
+  a.ws_state = static_cast<float*>(workspace);
+  a.ws_decay = need ? reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                               up256(size_t(pl.nseg) * p->nheads * kHead * p->dstate * 4))
+                    : nullptr;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  switch (p->dstate) {
+    case 64: return launch_fwd<64>(a, pl, st);
+    case 128: return launch_fwd<128>(a, pl, st);
+    default: return launch_fwd<256>(a, pl, st);
+  }
+}
+
+extern "C" ssm_status ssm_ssd_slot_update(const ssm_ssd_packed_params* p, float* state, const void* x, const void* dt,
+                                          const float* dt_bias, const float* A, const void* B, const void* C,
+                                          const float* Dskip, const int32_t* state_idx, void* y, void* stream) {
+  g_err[0] = 0;
+  if (ssm_status s = check_packed_ssd(p, true); s != SSM_OK) return s;
+  if (!state || !x || !dt || !A || !B || !C || !y) return fail(SSM_ERR_NULL, "state, x, dt, A, B, C and y are required");
+  if (p->nslots < 1) return fail(SSM_ERR_SHAPE, "nslots must be >= 1");
+  PSsdArgs a = ssd_args(p);
+  if (!aligned(state, 16) || !aligned(B, 8) || !aligned(C, 8) || a.bs % 4 || a.cs % 4 || !aligned(x, 2) ||
+      !aligned(dt, 2) || !aligned(y, 2) || !aligned(A, 4) || !aligned(dt_bias, 4) || !aligned(Dskip, 4) ||
+      !aligned(state_idx, 4))
+    return fail(SSM_ERR_ALIGN, "state must be 16-byte and the rows of B and C 8-byte aligned");
+  a.x = static_cast<const uint16_t*>(x);
+  a.dt = static_cast<const uint16_t*>(dt);
+  a.B = static_cast<const uint16_t*>(B);
+  a.C = static_cast<const uint16_t*>(C);
+  a.dt_bias = dt_bias;
+  a.A = A;
+  a.Dskip = Dskip;
+  a.idx = state_idx;
+  a.state_out = state;
+  a.y = static_cast<uint16_t*>(y);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  switch (p->dstate) {
+    case 64: return launch_step<64>(a, st);
+    case 128: return launch_step<128>(a, st);
+    default: return launch_step<256>(a, st);
+  }
+}
