@@ -372,6 +372,26 @@ ssm_status ssm_ssd_packed_fwd(const ssm_ssd_packed_params* p, const void* x, con
                               const uint8_t* has_state, float* state_out, void* y, void* workspace,
                               size_t workspace_bytes, void* stream);
 
+/* Bytes of device workspace ssm_ssd_packed_bwd needs (0 for invalid parameters).  Most of it are the states and adjoint
+ * states every 128 steps (64 for dstate 256): 512 * nheads * dstate bytes for each of about ntokens / 128 + nseqs. */
+size_t ssm_ssd_packed_bwd_workspace_bytes(const ssm_ssd_packed_params* p);
+
+/*
+ * Backward of ssm_ssd_packed_fwd for dy = dL/dy [ntokens][nheads][headdim] bf16 and, optionally, dstate_out = dL/d(last
+ * state) [nseqs][nheads][headdim][dstate] fp32 (by sequence, not by slot); the states are recomputed.  state is the pool
+ * as it was before the forward.  Outputs, overwritten: dx, ddt, dB, dC bf16 in the shapes of x, dt, B, C (dB and dC
+ * summed over the heads of a group); dA [nheads] fp32; dDskip, ddt_bias [nheads] and dstate [nseqs][nheads][headdim]
+ * [dstate] fp32 (the gradient of the state each sequence starts from, at zero where it has none), each optional.  Rows
+ * of dy and dx must be 16-byte, of dB and dC 8-byte aligned; outputs must not overlap inputs or each other.
+ * Deterministic.
+ */
+ssm_status ssm_ssd_packed_bwd(const ssm_ssd_packed_params* p, const void* x, const void* dt, const float* dt_bias,
+                              const float* A, const void* B, const void* C, const float* Dskip,
+                              const int32_t* cu_seqlens, const float* state, const int32_t* state_idx,
+                              const uint8_t* has_state, const void* dy, const float* dstate_out, void* dx, void* ddt,
+                              float* dA, void* dB, void* dC, float* dDskip, float* ddt_bias, float* dstate,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
 /* One step per row: x, y [ntokens][nheads][headdim], dt [ntokens][nheads], B, C [ntokens][ngroups][dstate] (rows 8-byte
  * aligned); the state in slot state_idx[r] is updated in place (16-byte aligned). */
 ssm_status ssm_ssd_slot_update(const ssm_ssd_packed_params* p, float* state, const void* x, const void* dt,

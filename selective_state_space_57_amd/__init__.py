@@ -18,7 +18,8 @@ from ._abi import (EULER_B, ZOH, SSM_BF16, SSM_F32, SSMError, Params, make_param
 
 __all__ = ["scan_fwd", "scan_bwd", "state_update", "conv_scan_fwd", "conv_state_update", "complex_scan_fwd",
            "complex_state_update", "conv1d_fwd", "conv1d_bwd", "ssd_fwd", "ssd_state_update", "ssd_workspace_bytes",
-           "conv1d_packed_fwd", "conv1d_slot_update", "conv1d_packed_bwd", "ssd_packed_fwd", "ssd_slot_update",
+           "conv1d_packed_fwd", "conv1d_slot_update", "conv1d_packed_bwd", "ssd_packed_fwd", "ssd_packed_bwd",
+           "ssd_slot_update",
            "gated_norm_fwd", "gated_norm_bwd", "EULER_B", "ZOH", "SSMError",
            "Params", "make_params", "workspace_bytes", "bwd_workspace_bytes", "plan_segments", "io_code"]
 
@@ -433,5 +434,5 @@ def ssd_state_update(state, x, dt, A, B, C, dt_bias=None, Dskip=None, z=None, *,
     return y
 
 
-from .packed import (conv1d_packed_fwd, conv1d_slot_update, conv1d_packed_bwd, ssd_packed_fwd, ssd_slot_update,  # noqa: E402
-                     gated_norm_fwd, gated_norm_bwd)
+from .packed import (conv1d_packed_fwd, conv1d_slot_update, conv1d_packed_bwd, ssd_packed_fwd, ssd_packed_bwd,  # noqa: E402
+                     ssd_slot_update, gated_norm_fwd, gated_norm_bwd)

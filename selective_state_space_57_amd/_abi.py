@@ -21,7 +21,8 @@ EXPORTS = ["ssm_scan_fwd_workspace_bytes", "ssm_scan_fwd", "ssm_state_update", "
            "ssm_ssd_fwd", "ssm_ssd_state_update", "ssm_ssd_fwd_workspace_bytes", "ssm_ssd_fwd_plan_segments",
            "ssm_conv1d_fwd", "ssm_conv1d_bwd", "ssm_scan_fwd_noalloc", "ssm_conv1d_packed_fwd", "ssm_conv1d_slot_update",
            "ssm_conv1d_packed_bwd", "ssm_conv1d_packed_bwd_workspace_bytes", "ssm_ssd_packed_fwd",
-           "ssm_ssd_packed_fwd_workspace_bytes", "ssm_ssd_slot_update", "ssm_gated_norm_fwd", "ssm_gated_norm_bwd",
+           "ssm_ssd_packed_fwd_workspace_bytes", "ssm_ssd_packed_bwd", "ssm_ssd_packed_bwd_workspace_bytes",
+           "ssm_ssd_slot_update", "ssm_gated_norm_fwd", "ssm_gated_norm_bwd",
            "ssm_gated_norm_bwd_workspace_bytes"]
 
 
@@ -133,6 +134,10 @@ def lib():
         L.ssm_ssd_packed_fwd_workspace_bytes.restype = S
         L.ssm_ssd_packed_fwd.argtypes = [QP] + [P] * 13 + [P, S, P]
         L.ssm_ssd_packed_fwd.restype = ctypes.c_int
+        L.ssm_ssd_packed_bwd_workspace_bytes.argtypes = [QP]
+        L.ssm_ssd_packed_bwd_workspace_bytes.restype = S
+        L.ssm_ssd_packed_bwd.argtypes = [QP] + [P] * 21 + [P, S, P]
+        L.ssm_ssd_packed_bwd.restype = ctypes.c_int
         L.ssm_ssd_slot_update.argtypes = [QP] + [P] * 11
         L.ssm_ssd_slot_update.restype = ctypes.c_int
         L.ssm_gated_norm_fwd.argtypes = [NP] + [P] * 6

@@ -61,6 +61,24 @@ template <int U>
 __device__ __forceinline__ pu4 lds_tr_operand(const void* base, int kk, int tile, int l16, int g4) {
   return join(lds_tr<U>(base, 32 * kk + 4 * g4, tile, l16), lds_tr<U>(base, 32 * kk + 16 + 4 * g4, tile, l16));
 }
+// the same with the lane's k as in lds_row_operand: rows 32 kk + 8 g4 .. + 7
+template <int U>
+__device__ __forceinline__ pu4 lds_tr_operand8(const void* base, int kk, int tile, int l16, int g4) {
+  return join(lds_tr<U>(base, 32 * kk + 8 * g4, tile, l16), lds_tr<U>(base, 32 * kk + 8 * g4 + 4, tile, l16));
+}
+// a tile whose 16 columns are numbered plainly (16 tile + column)
+template <int U>
+__device__ __forceinline__ pu2 lds_tr_plain(const void* base, int k0, int tile, int l16) {
+  const int byte = unit_at<U>(k0 + (l16 >> 2), 2 * tile + ((l16 & 3) >> 1)) + 8 * (l16 & 1);
+  return __builtin_bit_cast(pu2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                     (lds_pv4s*)(static_cast<const char*>(base) + byte)));
+}
+// operand of a plainly numbered tile; EIGHT: the lane's k as in lds_row_operand, else as in lds_tr_operand
+template <int U, bool EIGHT>
+__device__ __forceinline__ pu4 lds_tr_plain_operand(const void* base, int kk, int tile, int l16, int g4) {
+  return join(lds_tr_plain<U>(base, 32 * kk + (EIGHT ? 8 : 4) * g4, tile, l16),
+              lds_tr_plain<U>(base, 32 * kk + (EIGHT ? 8 * g4 + 4 : 4 * g4 + 16), tile, l16));
+}
 // operand whose row (or column) index is a row of LDS and whose k are 32 consecutive columns from 32 kk
 template <int U>
 __device__ __forceinline__ pu4 lds_row_operand(const void* base, int row, int kk, int g4) {
@@ -147,47 +165,33 @@ __device__ __forceinline__ float wave_suffix(float v, int lane) {
   return v + (row <= 2 ? r3 : 0.0f) + (row <= 1 ? r2 : 0.0f) + (row <= 0 ? r1 : 0.0f);
 }
 
-// Segments: sequence s is cut into max(1, ceil(chunks / cps)) segments of cps chunks, numbered over all sequences.
-struct Segment {
+// Pieces: sequence s is cut every `steps` tokens (segments of a walk, or chunk groups of the backward).  Piece i of a
+// sequence that begins at token b has the number s + b / steps + i: that is unique, needs no sum over the sequences
+// before it, and stays below nseqs + ntokens / steps + 1 (some numbers belong to no piece).
+struct Piece {
   int seq, begin, end;   // sequence and its tokens
-  int index, count;      // segment within the sequence, and how many it has
-  int first;             // number of the sequence's first segment
+  int index, count;      // piece within the sequence, and how many it has (an empty sequence has one)
+  int first;             // number of the sequence's first piece
 };
-__device__ __forceinline__ int segments_of(int tokens, int cps) {
-  const int chunks = (tokens + kChunk - 1) / kChunk;
-  return chunks > cps ? (chunks + cps - 1) / cps : 1;
+__host__ __device__ constexpr int64_t piece_numbers(int64_t nseqs, int64_t ntokens, int64_t steps) {
+  return nseqs + ntokens / steps + 1;
 }
-// Segment `want` over all sequences; false past the last.  Every lane of the wave takes part and gets the answer.
-__device__ __forceinline__ bool find_segment(const int32_t* cu, int nseqs, int ntokens, int cps, int want, int lane,
-                                             Segment& out) {
-  int before = 0;
-  for (int s0 = 0; s0 < nseqs; s0 += 64) {
-    const int s = s0 + lane;
-    int begin = 0, end = 0, n = 0;
-    if (s < nseqs) {
-      seq_range(cu, s, ntokens, begin, end);
-      n = segments_of(end - begin, cps);
-    }
-    int sum = n;   // inclusive sum over the lanes
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      const int v = __shfl_up(sum, m);
-      if (lane >= m) sum += v;
-    }
-    const uint64_t hit = __ballot(n > 0 && want >= before + sum - n && want < before + sum);
-    if (hit) {
-      const int l = __builtin_ctzll(hit);
-      out.seq = s0 + l;
-      out.begin = __builtin_amdgcn_readlane(begin, l);
-      out.end = __builtin_amdgcn_readlane(end, l);
-      out.count = __builtin_amdgcn_readlane(n, l);
-      out.first = before + __builtin_amdgcn_readlane(sum, l) - out.count;
-      out.index = want - out.first;
-      return true;
-    }
-    before += __builtin_amdgcn_readlane(sum, 63);
+__device__ __forceinline__ void pieces_of(const int32_t* cu, int s, int ntokens, int steps, Piece& p) {
+  seq_range(cu, s, ntokens, p.begin, p.end);
+  p.seq = s;
+  p.first = s + p.begin / steps;
+  p.count = max((p.end - p.begin + steps - 1) / steps, 1);
+}
+// The piece of that number; false where there is none.
+__device__ __forceinline__ bool find_piece(const int32_t* cu, int nseqs, int ntokens, int steps, int number, Piece& p) {
+  int lo = 0, hi = nseqs;   // the last sequence whose first piece has at most this number
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if (mid + min(max(cu[mid], 0), ntokens) / steps <= number) lo = mid; else hi = mid;
   }
-  return false;
+  pieces_of(cu, lo, ntokens, steps, p);
+  p.index = number - p.first;
+  return p.index >= 0 && p.index < p.count;
 }
 
 // Step size, its weight and the decay's logarithm (base 2) of one step; zeros behind the sequence.
@@ -221,10 +225,35 @@ inline int heads_per_group(const ssm_ssd_packed_params* p) { return p->dstate ==
 struct PackedPlan {
   int hblocks;    // workgroups per group of heads
   int cps;        // chunks per segment
-  int64_t nseg;   // segments at most, over all sequences
+  int64_t nseg;   // numbers of segments
   bool split;     // whether a sequence can have more than one
 };
-PackedPlan packed_plan(const ssm_ssd_packed_params* p);
+// `multiple`: segments are whole numbers of that many chunks.
+PackedPlan packed_plan(const ssm_ssd_packed_params* p, int multiple);
+
+// A walk over the states of packed sequences, chunk by chunk and from each sequence's first state (ssm_packed_states.hip):
+// forward, S <- exp(c_63) S + sum_s (phi_s exp(c_63 - c_s) v_s) k_s^T with v = x, k = B, or in reverse order,
+// G <- exp(c_63) G + sum_t exp(c_t) v_t k_t^T with v = dy, k = C.
+struct StatesArgs {
+  const uint16_t* v;
+  const uint16_t* k;
+  const uint16_t* dt;
+  const float* dt_bias;
+  const float* A;
+  const int32_t* cu;
+  const float* init;     // [slots][H][64][N], or by sequence where idx and has are null
+  const int32_t* idx;
+  const uint8_t* has;
+  float* last;           // [seqs][H][64][N] or null: the state behind the whole walk of a sequence
+  float* ws_state;       // [nseg][H][64][N]: state entering each segment (where a sequence has more than one)
+  float* ws_decay;       // [nseg][H]
+  float* save;           // [numbers][H][64][N] or null: state entering each group of `group` chunks
+  int64_t vs, ks, dts, nslots;
+  int T, S, H, G, hpg, hblocks, cps, nseg, nwork, group;
+  int softplus, zoh;
+};
+// Brings ws_state up to date where a sequence can have several segments (split), and then, with save or last, walks all.
+ssm_status launch_states(StatesArgs a, int dstate, bool reverse, bool split, hipStream_t st);
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 

@@ -12,12 +12,12 @@
 // meet, and the workgroup 4 heads).  What heads share is done once: B and C are copied to LDS for all of them, a chunk
 // ahead, and the 10 lower tiles of C B^T are shared out over the waves.  Everything else belongs to one wave, so a chunk
 // has two barriers only, and every operand is read from LDS once per wave for all of its columns.
-// Sequences longer than a segment: a first pass runs the state recurrence of each segment from zero, a second joins
-// the segments' states in order, and the full pass starts every segment from its state.
+// Sequences longer than a segment: a walk over the states alone (ssm_packed_states.hip) finds the state entering every
+// segment first, and all segments run at once.
 //
 // Precision: fp32 state and accumulation; x, B and C enter the matrix cores as they are.  The weighted x of the state
-// update is split into two bf16 parts (2^-18 relative), so the state keeps fp32 quality over long sequences.  M and the
-// state's copy that meets C are rounded once to bf16 (2^-9 relative, as the output is): they only reach y, which is
+// update is split into two bf16 parts (2^-18 relative), so the state keeps fp32 quality over long sequences.  M (but for s = t) and
+// the state's copy that meets C are rounded once to bf16 (2^-9 relative, as the output is): they only reach y, which is
 // rounded to bf16 itself.
 #include "packed_ssd.hpp"
 
@@ -38,11 +38,10 @@ struct PSsdArgs {
   const uint8_t* has;
   float* state_out;
   uint16_t* y;
-  float* ws_state;   // [segments][H][64][N]
-  float* ws_decay;   // [segments][H]
+  const float* ws_state;   // [segments][H][64][N]: the state entering each, where a sequence has several
   int64_t xs, dts, bs, cs, ys, nslots;
   int T, S, H, G, hpg, hblocks;   // hblocks: workgroups per group
-  int cps, nseg, nwork;
+  int cps, nwork;
   int softplus, zoh;
 };
 
@@ -53,10 +52,10 @@ struct alignas(16) HeadScalars {
   float c[kChunk];     // c_t, base 2
   float phi[kChunk];
   float w[kChunk];     // phi_s exp(c_63 - c_s)
+  float own[kChunk];   // M[t][t] + D
 };
 
-// STATES: the first pass (the state recurrence alone, from zero)
-template <int N, bool STATES>
+template <int N>
 __global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
 packed_ssd_fwd_kernel(PSsdArgs a) {
   constexpr int NW = kWaves;
@@ -68,9 +67,9 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
   constexpr int NK = N / 32;
   constexpr bool kOneC = N == 256;       // (two copies of C would not fit the LDS)
   __shared__ alignas(16) uint16_t sB0[kChunk * N], sB1[kChunk * N];
-  __shared__ alignas(16) uint16_t sC0[STATES ? 8 : kChunk * N], sC1[STATES || kOneC ? 8 : kChunk * N];
+  __shared__ alignas(16) uint16_t sC0[kChunk * N], sC1[kOneC ? 8 : kChunk * N];
   __shared__ alignas(16) uint16_t sX[NW][kChunk * 16 * PT];
-  __shared__ pf4 sCB[STATES ? 1 : 10][64];
+  __shared__ pf4 sCB[10][64];   // tiles of C B^T on and below the diagonal
   __shared__ HeadScalars sS[NW];
 
   const int item = xcd_item();
@@ -79,9 +78,8 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
   const int hb = item % (a.G * a.hblocks);
-  Segment seg;
-  if (!find_segment(a.cu, a.S, a.T, a.cps, item / (a.G * a.hblocks), lane, seg)) return;
-  if (STATES && seg.index == seg.count - 1) return;   // nothing starts from the last segment's end
+  Piece seg;
+  if (!find_piece(a.cu, a.S, a.T, a.cps * kChunk, item / (a.G * a.hblocks), seg)) return;
   const int g = hb / a.hblocks;
   const int hg = (hb % a.hblocks) * (NW / kParts) + wave / kParts;   // head within the group
   const int p0 = (wave % kParts) * 16 * PT;            // first column of this wave
@@ -89,7 +87,7 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
   const int h = g * a.hpg + (on ? hg : a.hpg - 1);
 
   const int t_begin = seg.begin + seg.index * a.cps * kChunk;
-  const int t_end = min(seg.end, seg.index == seg.count - 1 ? seg.end : t_begin + a.cps * kChunk);
+  const int t_end = min(seg.end, t_begin + a.cps * kChunk);
   const int nchunks = (t_end - t_begin + kChunk - 1) / kChunk;
 
   const float Ah = a.A[h];
@@ -127,13 +125,11 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
   };
   {
     const float* from = nullptr;
-    if constexpr (!STATES) {
-      if (seg.count > 1) {
-        from = a.ws_state + (int64_t(seg.first + seg.index) * a.H + h) * head_size;
-      } else if (a.state && (!a.has || a.has[seg.seq])) {
-        const int64_t slot = slot_of(a.idx, seg.seq, a.nslots);
-        if (slot >= 0) from = a.state + (slot * a.H + h) * head_size;
-      }
+    if (seg.count > 1) {
+      from = a.ws_state + (int64_t(seg.first + seg.index) * a.H + h) * head_size;
+    } else if (a.state && (!a.has || a.has[seg.seq])) {
+      const int64_t slot = slot_of(a.idx, seg.seq, a.nslots);
+      if (slot >= 0) from = a.state + (slot * a.H + h) * head_size;
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -141,7 +137,6 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
       for (int pt = 0; pt < PT; ++pt)
         S[nt][pt] = from ? *reinterpret_cast<const pf4*>(from + entry(nt, pt)) : pf4{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  float decay = 0.0f;   // sum of log2 decays over the segment (first pass)
 
   HeadScalars& sc = sS[wave];
   const uint16_t* X = sX[wave];
@@ -151,7 +146,7 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
     wait_memory();    // this wave's copies of the chunk
     barrier_lds();    // everyone's, and the previous chunk's readers are done
     copy_group(ck + 1, Bn, Bg, a.bs, brow);
-    if constexpr (!STATES && !kOneC) copy_group(ck + 1, Cn, Cg, a.cs, crow);
+    if constexpr (!kOneC) copy_group(ck + 1, Cn, Cg, a.cs, crow);
     const uint32_t dt_next = load_dt(ck + 1);
     const int rows = rows_of(ck);
     {
@@ -166,7 +161,7 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
     }
     wave_lds_sync();
     const float total = sc.c[kChunk - 1];
-    if constexpr (!STATES) {
+    {
       // C B^T, tile i = (tb, sb), sb <= tb: rows s, columns t
 #pragma unroll
       for (int i = 0; i < 10; ++i) {
@@ -203,13 +198,18 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
             for (int c = 0; c < 4; ++c) {
               // (above the diagonal the difference can be large and positive: masked after the fact)
               m[c] = cb[c] * (hw_exp2(ct[tb] - cs[c]) * ph[c]);
-              if (sb == tb) m[c] = 4 * g4 + c <= l16 ? m[c] : 0.0f;
+              if (sb == tb) {
+                // a step's own x goes into its y in fp32, together with D
+                if (4 * g4 + c == l16) sc.own[16 * tb + l16] = m[c] + Dh;
+                m[c] = 4 * g4 + c < l16 ? m[c] : 0.0f;
+              }
             }
             half[e] = bf16x4(m[0], m[1], m[2], m[3]);
           }
           M[tb][kk] = join(half[0], half[1]);
         }
       }
+      wave_lds_sync();
       const int64_t t0 = t_begin + int64_t(ck) * kChunk;
       const auto ry = chunk_rsrc(a.y + int64_t(h) * kHead + p0, t0, a.ys, on ? rows : 0, 16 * PT);
       // a pair of column tiles at a time: Y^T[p][t = 16 tb + l16]
@@ -253,12 +253,13 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
         // a lane's two tiles of the pair are eight consecutive columns of step 16 tb + l16
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
+          const float own = sc.own[16 * tb + l16];
           const pu4 xv = lds_u4(X, unit_at<UX>(16 * tb + l16, 4 * pp + g4));
           const pf4 y0 = acc[0][tb], y1 = acc[1][tb];
-          const pu4 o = {pack_bf16(fmaf(Dh, lo_f32(xv[0]), y0[0]), fmaf(Dh, hi_f32(xv[0]), y0[1])),
-                         pack_bf16(fmaf(Dh, lo_f32(xv[1]), y0[2]), fmaf(Dh, hi_f32(xv[1]), y0[3])),
-                         pack_bf16(fmaf(Dh, lo_f32(xv[2]), y1[0]), fmaf(Dh, hi_f32(xv[2]), y1[1])),
-                         pack_bf16(fmaf(Dh, lo_f32(xv[3]), y1[2]), fmaf(Dh, hi_f32(xv[3]), y1[3]))};
+          const pu4 o = {pack_bf16(fmaf(own, lo_f32(xv[0]), y0[0]), fmaf(own, hi_f32(xv[0]), y0[1])),
+                         pack_bf16(fmaf(own, lo_f32(xv[1]), y0[2]), fmaf(own, hi_f32(xv[1]), y0[3])),
+                         pack_bf16(fmaf(own, lo_f32(xv[2]), y1[0]), fmaf(own, hi_f32(xv[2]), y1[1])),
+                         pack_bf16(fmaf(own, lo_f32(xv[3]), y1[2]), fmaf(own, hi_f32(xv[3]), y1[3]))};
           __builtin_amdgcn_raw_buffer_store_b128(
               o, ry, static_cast<int>(static_cast<uint32_t>(16 * tb + l16) * yrow + (32u * pp + 8u * g4) * 2u), 0, 0);
         }
@@ -300,13 +301,12 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
         S[nt][pt] = mma(b1, wl[pt][1], v);
       }
     }
-    if constexpr (STATES) decay += total;
     return dt_next;
   };
 
   uint32_t dtv = load_dt(0);
   copy_group(0, sB0, Bg, a.bs, brow);
-  if constexpr (!STATES) copy_group(0, sC0, Cg, a.cs, crow);
+  copy_group(0, sC0, Cg, a.cs, crow);
   copy_x(0);
   for (int ck = 0; ck < nchunks; ck += 2) {
     dtv = chunk(ck, sB0, sC0, sB1, kOneC ? sC0 : sC1, dtv);
@@ -314,60 +314,15 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
   }
   wait_memory();   // (the copies issued past the last chunk)
 
-  float* to = nullptr;
-  if constexpr (STATES) {
-    to = a.ws_state + (int64_t(seg.first + seg.index) * a.H + h) * head_size;
-    if (on && p0 == 0 && lane == 0) a.ws_decay[int64_t(seg.first + seg.index) * a.H + h] = decay;
-  } else if (a.state_out && seg.index == seg.count - 1) {
+  if (a.state_out && seg.index == seg.count - 1 && on) {
     const int64_t slot = slot_of(a.idx, seg.seq, a.nslots);
-    if (slot >= 0) to = a.state_out + (slot * a.H + h) * head_size;
-  }
-  if (to && on) {
+    if (slot >= 0) {
+      float* to = a.state_out + (slot * a.H + h) * head_size;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int pt = 0; pt < PT; ++pt) *reinterpret_cast<pf4*>(to + entry(nt, pt)) = S[nt][pt];
-  }
-}
-
-// Joins the segments of a sequence in order: the end state that the first pass left for segment j (from zero) gives
-// way to the state entering segment j.  A thread owns four entries; nothing to do for one segment.
-__global__ void __launch_bounds__(256) packed_ssd_join_kernel(PSsdArgs a, int entries) {
-  const int lane = threadIdx.x & 63;
-  int begin, end;
-  seq_range(a.cu, blockIdx.x, a.T, begin, end);
-  int count = segments_of(end - begin, a.cps);
-  if (count <= 1) return;
-  int before = 0;   // segments of the sequences before this one
-  for (int s0 = 0; s0 < static_cast<int>(blockIdx.x); s0 += 64) {
-    const int s = s0 + lane;
-    int n = 0;
-    if (s < static_cast<int>(blockIdx.x)) {
-      int b, e;
-      seq_range(a.cu, s, a.T, b, e);
-      n = segments_of(e - b, a.cps);
+        for (int pt = 0; pt < PT; ++pt) *reinterpret_cast<pf4*>(to + entry(nt, pt)) = S[nt][pt];
     }
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) n += __shfl_xor(n, m);
-    before += n;
-  }
-  count = min(count, a.nseg - before);   // (only a cu_seqlens that is not ordered reaches this bound)
-  const int64_t e = (int64_t(blockIdx.y) * 256 + threadIdx.x) * 4;
-  const int64_t per = int64_t(a.H) * entries;   // entries of a head
-  if (e >= per) return;
-  const int h = static_cast<int>(e / entries);
-  pf4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (a.state && (!a.has || a.has[blockIdx.x])) {
-    const int64_t slot = slot_of(a.idx, blockIdx.x, a.nslots);
-    if (slot >= 0) s = *reinterpret_cast<const pf4*>(a.state + slot * per + e);
-  }
-  for (int j = 0; j < count; ++j) {
-    float* at = a.ws_state + int64_t(before + j) * per + e;
-    const bool more = j + 1 < count;
-    const pf4 own = more ? *reinterpret_cast<const pf4*>(at) : pf4{0.0f, 0.0f, 0.0f, 0.0f};
-    const float d = more ? hw_exp2(a.ws_decay[int64_t(before + j) * a.H + h]) : 0.0f;
-    *reinterpret_cast<pf4*>(at) = s;
-    s = s * d + own;
   }
 }
 
@@ -424,18 +379,8 @@ __global__ void __launch_bounds__(256) packed_ssd_step_kernel(PSsdArgs a) {
 }
 
 template <int N>
-ssm_status launch_fwd(const PSsdArgs& args, const PackedPlan& pl, hipStream_t st) {
-  PSsdArgs a = args;
-  a.nwork = static_cast<int>(pl.nseg * a.G * a.hblocks);
-  const dim3 grid((a.nwork + 7) / 8 * 8), block(kWaves * 64);
-  if (pl.split) {
-    hipLaunchKernelGGL((packed_ssd_fwd_kernel<N, true>), grid, block, 0, st, a);
-    const int64_t entries = int64_t(kHead) * N;
-    const int64_t blocks = (a.H * entries / 4 + 255) / 256;
-    hipLaunchKernelGGL(packed_ssd_join_kernel, dim3(a.S, static_cast<uint32_t>(blocks)), dim3(256), 0, st, a,
-                       static_cast<int>(entries));
-  }
-  hipLaunchKernelGGL((packed_ssd_fwd_kernel<N, false>), grid, block, 0, st, a);
+ssm_status launch_fwd(const PSsdArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((packed_ssd_fwd_kernel<N>), dim3((a.nwork + 7) / 8 * 8), dim3(kWaves * 64), 0, st, a);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SSM_OK : fail(SSM_ERR_HIP, "packed SSD launch: %s", hipGetErrorString(e));
 }
@@ -449,7 +394,7 @@ ssm_status launch_step(const PSsdArgs& a, hipStream_t st) {
 }
 
 size_t fwd_workspace(const ssm_ssd_packed_params* p) {
-  const PackedPlan pl = packed_plan(p);
+  const PackedPlan pl = packed_plan(p, 1);
   if (!pl.split) return 0;
   return up256(size_t(pl.nseg) * p->nheads * kHead * p->dstate * 4) + up256(size_t(pl.nseg) * p->nheads * 4);
 }
@@ -508,14 +453,14 @@ ssm_status check_packed_ssd(const ssm_ssd_packed_params* p, bool step) {
   }
   if (step && p->ntokens * p->nheads >= (int64_t(1) << 29)) return fail(SSM_ERR_SHAPE, "too many rows for one launch");
   if (!step) {
-    const PackedPlan pl = packed_plan(p);
+    const PackedPlan pl = packed_plan(p, 1);
     if (pl.nseg * p->ngroups * pl.hblocks >= (int64_t(1) << 31) - 8) return fail(SSM_ERR_SHAPE, "too many work items");
     if (p->nheads * kHead * p->dstate / 1024 >= 65535) return fail(SSM_ERR_SHAPE, "nheads is too large");
   }
   return SSM_OK;
 }
 
-PackedPlan packed_plan(const ssm_ssd_packed_params* p) {
+PackedPlan packed_plan(const ssm_ssd_packed_params* p, int multiple) {
   PackedPlan pl{};
   const int64_t hpg = p->nheads / p->ngroups, per = heads_per_group(p);
   pl.hblocks = static_cast<int>((hpg + per - 1) / per);
@@ -528,9 +473,10 @@ PackedPlan packed_plan(const ssm_ssd_packed_params* p) {
     if (cps < 8) cps = 8;
   }
   if (cps > longest) cps = longest;
+  cps = (cps + multiple - 1) / multiple * multiple;
   pl.cps = static_cast<int>(cps);
   pl.split = longest > cps;
-  pl.nseg = pl.split ? p->nseqs + chunks / cps : p->nseqs;
+  pl.nseg = piece_numbers(p->nseqs, p->ntokens, cps * kChunk);
   return pl;
 }
 
@@ -560,7 +506,7 @@ extern "C" ssm_status ssm_ssd_packed_fwd(const ssm_ssd_packed_params* p, const v
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
     return fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes (16-byte aligned) needed, got %zu at %p", need,
                 workspace_bytes, workspace);
-  const PackedPlan pl = packed_plan(p);
+  const PackedPlan pl = packed_plan(p, 1);
   a.x = static_cast<const uint16_t*>(x);
   a.dt = static_cast<const uint16_t*>(dt);
   a.B = static_cast<const uint16_t*>(B);
@@ -576,16 +522,43 @@ extern "C" ssm_status ssm_ssd_packed_fwd(const ssm_ssd_packed_params* p, const v
   a.y = static_cast<uint16_t*>(y);
   a.hblocks = pl.hblocks;
   a.cps = pl.cps;
-  a.nseg = static_cast<int>(pl.nseg);
   a.ws_state = static_cast<float*>(workspace);
-  a.ws_decay = need ? reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                               up256(size_t(pl.nseg) * p->nheads * kHead * p->dstate * 4))
-                    : nullptr;
   hipStream_t st = static_cast<hipStream_t>(stream);
+  a.nwork = static_cast<int>(pl.nseg) * a.G * a.hblocks;
+  if (pl.split) {
+    StatesArgs w{};
+    w.v = a.x;
+    w.k = a.B;
+    w.dt = a.dt;
+    w.dt_bias = dt_bias;
+    w.A = A;
+    w.cu = cu_seqlens;
+    w.init = state;
+    w.idx = state_idx;
+    w.has = has_state;
+    w.ws_state = static_cast<float*>(workspace);
+    w.ws_decay = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                          up256(size_t(pl.nseg) * p->nheads * kHead * p->dstate * 4));
+    w.vs = a.xs;
+    w.ks = a.bs;
+    w.dts = a.dts;
+    w.nslots = p->nslots;
+    w.T = a.T;
+    w.S = a.S;
+    w.H = a.H;
+    w.G = a.G;
+    w.hpg = a.hpg;
+    w.hblocks = a.hblocks;
+    w.cps = a.cps;
+    w.nseg = static_cast<int>(pl.nseg);
+    w.softplus = a.softplus;
+    w.zoh = a.zoh;
+    if (ssm_status s = launch_states(w, static_cast<int>(p->dstate), false, true, st); s != SSM_OK) return s;
+  }
   switch (p->dstate) {
-    case 64: return launch_fwd<64>(a, pl, st);
-    case 128: return launch_fwd<128>(a, pl, st);
-    default: return launch_fwd<256>(a, pl, st);
+    case 64: return launch_fwd<64>(a, st);
+    case 128: return launch_fwd<128>(a, st);
+    default: return launch_fwd<256>(a, st);
   }
 }
 

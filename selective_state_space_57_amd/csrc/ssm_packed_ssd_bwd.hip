@@ -1,0 +1,725 @@
+// Backward of the SSD layer over packed sequences.  With S_t the states and G_t = dL/dS_t:
+//   G_t = dy_t C_t^T + a_{t+1} G_{t+1};  dx_t = phi_t G_t B_t + D dy_t;  dB_t = phi_t G_t^T x_t;  dC_t = S_t^T dy_t
+//   dphi_t = x_t . G_t B_t;  dl_t = a_t <G_t, S_{t-1}> (l = Delta A, the decay's logarithm)
+//   dDelta = A dl + phi'(Delta) dphi,  dA = sum Delta dl (+ sum dphi d phi/dA),  dD = sum dy . x
+// (dB and dC summed over the heads of a group).  In chunks of 64 steps, with c the running sum of l in the chunk, S the
+// state entering it and G the adjoint behind its last step, and for s <= t
+//   L[t][s] = exp(c_t - c_s),  E_t = exp(c_t),  F_s = exp(c_63 - c_s),  X[t][s] = dy_t . x_s,  Z[t][s] = C_t . B_s:
+//   dx_s = sum_t L Z phi_s dy_t + phi_s F_s G B_s + D dy_s
+//   dC_t = sum_s K B_s + E_t S^T dy_t,  dB_s = sum_t K C_t + phi_s F_s G^T x_s,  K[t][s] = L X phi_s
+//   dphi_s = sum_t W0[t][s] + F_s x_s . G B_s,  W0 = L X Z;  with W = W0 phi_s, u_t = E_t C_t . S^T dy_t and
+//   v_s = phi_s F_s B_s . G^T x_s:
+//   dl_r = sum_{t>=r} (sum_{s<t} W[t][s] - sum_{t'>t} W[t'][t]) + sum_{t>=r} u_t + sum_{s<r} v_s + exp(c_63) <G, S>
+// Every sum in dl_r has the decays of what it stands for in it, so nothing large cancels: only the row and column sums
+// of W do, and those are sums of the same fp32 numbers.
+//
+// Two walks (ssm_packed_states.hip) leave S and G at the boundaries of groups of chunks (two chunks; one for N = 256);
+// then a workgroup takes a group of chunks and runs over heads one after the other.  A wave owns 16 of the N columns of
+// the states (32 for N = 256) for every head: the sums of dB and dC over heads add up in its registers, and the states
+// inside the group are recomputed from the boundary's.  K is summed over heads in registers as well, and multiplied with
+// B and C once at the end.  What a head needs across waves (dx, and the sums over n in u, v and <G, S>) goes through LDS.
+//
+// Precision: fp32 accumulation; the states and the weighted B and C of their recomputation are split into two bf16 parts
+// (2^-18 relative), so that u, v and <G, S>, and with them dDelta and dA, are good to fp32 quality.  G in dx, M = L Z phi (but for s = t)
+// and the head sum K are rounded once to bf16: they only reach dx, dB and dC, which are bf16.
+#include "packed_ssd.hpp"
+
+namespace ssm57 {
+namespace {
+
+struct BwdArgs {
+  const uint16_t* x;
+  const uint16_t* dt;
+  const uint16_t* B;
+  const uint16_t* C;
+  const uint16_t* dy;
+  const float* dt_bias;
+  const float* A;
+  const float* Dskip;
+  const int32_t* cu;
+  const float* S;      // [numbers][H][64][N]: state entering each chunk group
+  const float* Gs;     // [numbers][H][64][N]: adjoint behind it
+  uint16_t* dx;
+  uint16_t* ddt;
+  uint16_t* dB;
+  uint16_t* dC;
+  float* part_b;       // [splits][T][G N]
+  float* part_c;
+  float* part_h;       // [numbers][chunks of a group][H][4]: sums of Delta dl (+ phi's share), ddt, dy . x
+  float* dA;
+  float* ddt_bias;
+  float* dD;
+  int64_t xs, dts, bs, cs, dys, dxs, ddts, dbs, dcs;
+  int T, S_, H, G, hpg, splits, hps, numbers, nwork;
+  int softplus, zoh;
+};
+
+// sizes by state width: waves, n-tiles of a wave, chunks of a group
+template <int N>
+struct Shape {
+  static constexpr int NW = N == 64 ? 4 : 8;
+  static constexpr int NTW = N / 16 / NW;
+  static constexpr int KC = N == 256 ? 1 : 2;
+};
+int group_of(int64_t dstate) { return dstate == 256 ? 1 : 2; }
+
+struct alignas(16) ChunkScalars {
+  float c[kChunk], phi[kChunk], f[kChunk];   // c_t (base 2), phi_t, exp(c_63 - c_t)
+};
+
+__host__ __device__ constexpr int tile_row(int i) { return i >= 6 ? 3 : (i >= 3 ? 2 : (i >= 1 ? 1 : 0)); }
+// place of the operand over 32 rows t (kk) of column tile sb: (0,0) (0,1) (1,0) (1,1) (2,1) (3,1)
+__host__ __device__ constexpr int m_slot(int sb, int kk) { return sb < 2 ? 2 * sb + kk : sb + 2; }
+
+// d phi / dA of the zero-order hold, phi = (exp(e) - 1) / A with e = Delta A: Delta^2 (e exp(e) - exp(e) + 1) / e^2, by
+// its series where the numerator cancels (the first term left out is below 2^-21 of the value for |e| < 1/2)
+__device__ __forceinline__ float zoh_slope(float delta, float e, float a) {
+  float p = 1.0f / 5760.0f;
+  p = fmaf(p, e, 1.0f / 840.0f);
+  p = fmaf(p, e, 1.0f / 144.0f);
+  p = fmaf(p, e, 1.0f / 30.0f);
+  p = fmaf(p, e, 0.125f);
+  p = fmaf(p, e, 1.0f / 3.0f);
+  p = fmaf(p, e, 0.5f);
+  const float direct = fabsf(e) < 0.5f ? 0.0f : (fmaf(e, a, -a) + 1.0f) / (e * e);
+  return delta * delta * (fabsf(e) < 0.5f ? p : direct);
+}
+
+template <int N>
+__global__ void __launch_bounds__(Shape<N>::NW * 64) __attribute__((amdgpu_waves_per_eu(Shape<N>::NW / 4, 2)))
+packed_ssd_bwd_kernel(BwdArgs a) {
+  constexpr int NW = Shape<N>::NW, NTW = Shape<N>::NTW, KC = Shape<N>::KC;
+  constexpr int U = N / 8, NK = N / 32;
+  constexpr int kTiles = (10 + NW - 1) / NW;   // tiles on and below the diagonal that a wave owns
+  __shared__ alignas(16) uint16_t sB[KC][kChunk * N], sC[KC][kChunk * N];
+  __shared__ alignas(16) uint16_t sX[KC][kChunk * kHead], sY[KC][kChunk * kHead];   // x and dy of the head
+  __shared__ pf4 sZ[KC][10][64];       // C B^T: rows t, columns s
+  __shared__ pu4 sM[6][64];            // M of the chunk, operands over t
+  __shared__ alignas(16) uint16_t sG[N * kHead];   // G of the chunk, transposed
+  __shared__ ChunkScalars sS[KC];
+  __shared__ float sU[NW][kChunk], sV[NW][kChunk], sE[NW], sRow[10][16], sCol[10][16], sOwn[4][16], sDirect[4][16], sDiag[4];
+
+  const int item = xcd_item();
+  if (item >= a.nwork) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, g4 = lane >> 4;
+  const int split = item % a.splits;
+  const int g = item / a.splits % a.G;
+  const int number = item / (a.splits * a.G);
+  const int h_begin = g * a.hpg + split * a.hps, h_end = min(h_begin + a.hps, (g + 1) * a.hpg);
+  Piece grp;
+  const bool found = find_piece(a.cu, a.S_, a.T, KC * kChunk, number, grp) && grp.end > grp.begin;
+  if (!found) {   // a number without chunks adds nothing to the sums over all of them
+    for (int h = h_begin + tid; h < h_end; h += NW * 64)
+#pragma unroll
+      for (int k = 0; k < KC; ++k)
+        *reinterpret_cast<pf4*>(a.part_h + ((int64_t(number) * KC + k) * a.H + h) * 4) = pf4{0.0f, 0.0f, 0.0f, 0.0f};
+    return;
+  }
+  const int t_begin = grp.begin + grp.index * KC * kChunk;
+  const int t_end = min(grp.end, t_begin + KC * kChunk);
+  auto rows_of = [&](int k) { return min(max(t_end - (t_begin + k * kChunk), 0), kChunk); };
+  auto first_of = [&](int k) -> int64_t { return rows_of(k) ? t_begin + int64_t(k) * kChunk : t_begin; };
+
+  // B and C of the group stay for all heads, and so does C B^T
+  {
+    const uint32_t brow = static_cast<uint32_t>(a.bs) * 2u, crow = static_cast<uint32_t>(a.cs) * 2u;
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      copy_rows<U, NW>(sB[k], chunk_rsrc(a.B + int64_t(g) * N, first_of(k), a.bs, rows_of(k), N), wave, lane, brow);
+      copy_rows<U, NW>(sC[k], chunk_rsrc(a.C + int64_t(g) * N, first_of(k), a.cs, rows_of(k), N), wave, lane, crow);
+    }
+    if (wave == 0) {   // the halves of operands that lie above the diagonal stay zero
+      reinterpret_cast<pu2*>(&sM[m_slot(1, 0)][lane])[0] = pu2{0u, 0u};
+      reinterpret_cast<pu2*>(&sM[m_slot(3, 1)][lane])[0] = pu2{0u, 0u};
+    }
+    wait_memory();
+    barrier_lds();
+#pragma unroll
+    for (int k = 0; k < KC; ++k)
+#pragma unroll
+      for (int i = 0; i < 10; ++i) {
+        if (i % NW != wave) continue;
+        const int tb = tile_row(i), sb = i - tb * (tb + 1) / 2;
+        pf4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk)
+          v = mma(lds_row_operand<U>(sC[k], 16 * tb + l16, kk, g4), lds_row_operand<U>(sB[k], 16 * sb + l16, kk, g4), v);
+        sZ[k][i][lane] = v;   // (read by the wave that wrote it)
+      }
+  }
+
+  const pf4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  pf4 aB[KC][NTW][4], aC[KC][NTW][4];   // dB^T, dC^T: n = 16 nt + 4 g4 + c, step 16 sb + l16
+  pf4 aK[KC][kTiles];                   // K: rows t, columns s
+#pragma unroll
+  for (int k = 0; k < KC; ++k) {
+#pragma unroll
+    for (int j = 0; j < NTW; ++j)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) aB[k][j][b] = aC[k][j][b] = zero;
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) aK[k][i] = zero;
+  }
+  const int64_t head_size = int64_t(kHead) * N;
+
+  for (int h = h_begin; h < h_end; ++h) {
+    const float Ah = a.A[h];
+    const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+    const float Dh = a.Dskip ? a.Dskip[h] : 0.0f;
+    barrier_lds();   // everyone is done with the head before
+    {
+      const uint32_t xrow = static_cast<uint32_t>(a.xs) * 2u, yrow = static_cast<uint32_t>(a.dys) * 2u;
+#pragma unroll
+      for (int k = 0; k < KC; ++k) {
+        copy_rows<8, NW>(sX[k], chunk_rsrc(a.x + int64_t(h) * kHead, first_of(k), a.xs, rows_of(k), kHead), wave, lane,
+                         xrow);
+        copy_rows<8, NW>(sY[k], chunk_rsrc(a.dy + int64_t(h) * kHead, first_of(k), a.dys, rows_of(k), kHead), wave, lane,
+                         yrow);
+      }
+    }
+    // states entering chunk k and adjoints behind it; p = 32 (pt/2) + 8 g4 + 4 (pt%2) + c, n = 16 nt + l16
+    pf4 S[KC][NTW][4], G[KC][NTW][4];
+    {
+      const float* s0 = a.S + (int64_t(number) * a.H + h) * head_size;
+      const float* g0 = a.Gs + (int64_t(number) * a.H + h) * head_size;
+#pragma unroll
+      for (int j = 0; j < NTW; ++j)
+#pragma unroll
+        for (int pt = 0; pt < 4; ++pt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int at = (32 * (pt >> 1) + 8 * g4 + 4 * (pt & 1) + c) * N + 16 * (NTW * wave + j) + l16;
+            S[0][j][pt][c] = s0[at];
+            G[KC - 1][j][pt][c] = g0[at];
+          }
+    }
+    float delta = 0.0f, la = 0.0f, u_in = 0.0f;   // of step `lane` of chunk `wave` (the waves below KC)
+    if (wave < KC) {
+      const int rows = rows_of(wave);
+      const int64_t t0 = first_of(wave);
+      const float dtv = lo_f32(a.dt[(lane < rows ? t0 + lane : t0) * a.dts + h]);
+      float phi;
+      step_scalars(dtv, bias, Ah, a.softplus, a.zoh, lane < rows, delta, phi, la);
+      u_in = dtv + bias;
+      sS[wave].c[lane] = wave_prefix(la, lane);
+      sS[wave].phi[lane] = phi;
+      sS[wave].f[lane] = hw_exp2(wave_suffix(la, lane) - la);
+    }
+    wait_memory();
+    barrier_lds();   // x, dy and the scalars are there
+    // inside the group: S behind its first chunk, G before its last
+    if constexpr (KC == 2) {
+      const float fade0 = hw_exp2(sS[0].c[kChunk - 1]), fade1 = hw_exp2(sS[1].c[kChunk - 1]);
+#pragma unroll
+      for (int j = 0; j < NTW; ++j) {
+#pragma unroll
+        for (int pt = 0; pt < 4; ++pt) {
+          S[1][j][pt] = S[0][j][pt] * fade0;
+          G[0][j][pt] = G[1][j][pt] * fade1;
+        }
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          pu2 bh[2], bl[2], ch[2], cl[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int k0 = 32 * kk + 16 * e + 4 * g4;
+            const pu2 b = lds_tr_plain<U>(sB[0], k0, NTW * wave + j, l16);
+            const pf4 ph = *reinterpret_cast<const pf4*>(&sS[0].phi[k0]), f = *reinterpret_cast<const pf4*>(&sS[0].f[k0]);
+            split_bf16x4(lo_f32(b[0]) * (ph[0] * f[0]), hi_f32(b[0]) * (ph[1] * f[1]), lo_f32(b[1]) * (ph[2] * f[2]),
+                         hi_f32(b[1]) * (ph[3] * f[3]), bh[e], bl[e]);
+            const pu2 c = lds_tr_plain<U>(sC[1], k0, NTW * wave + j, l16);
+            const pf4 cc = *reinterpret_cast<const pf4*>(&sS[1].c[k0]);
+            split_bf16x4(lo_f32(c[0]) * hw_exp2(cc[0]), hi_f32(c[0]) * hw_exp2(cc[1]), lo_f32(c[1]) * hw_exp2(cc[2]),
+                         hi_f32(c[1]) * hw_exp2(cc[3]), ch[e], cl[e]);
+          }
+#pragma unroll
+          for (int pt = 0; pt < 4; ++pt) {
+            const pu4 xt = lds_tr_operand<8>(sX[0], kk, pt, l16, g4), yt = lds_tr_operand<8>(sY[1], kk, pt, l16, g4);
+            S[1][j][pt] = mma(xt, join(bh[0], bh[1]), S[1][j][pt]);
+            S[1][j][pt] = mma(xt, join(bl[0], bl[1]), S[1][j][pt]);
+            G[0][j][pt] = mma(yt, join(ch[0], ch[1]), G[0][j][pt]);
+            G[0][j][pt] = mma(yt, join(cl[0], cl[1]), G[0][j][pt]);
+          }
+        }
+      }
+    }
+    float sum_a = 0.0f, sum_t = 0.0f, sum_d = 0.0f;   // this lane's share of part_h (the waves below KC)
+#pragma unroll
+    for (int k = 0; k < KC; ++k) {
+      part_ends();
+      const ChunkScalars& sc = sS[k];
+      // ---- products with the states: q^T = S^T dy^T, r^T = G^T x^T, <G, S>
+      float su[4] = {}, sv[4] = {};
+      pf4 ge = zero;
+#pragma unroll
+      for (int j = 0; j < NTW; ++j) {
+        const int nt = NTW * wave + j;
+        pu4 sh[2], sl[2], gh[2], gl[2];
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          pu2 h0, l0, h1, l1;
+          const pf4 s0 = S[k][j][2 * kk], s1 = S[k][j][2 * kk + 1];
+          split_bf16x4(s0[0], s0[1], s0[2], s0[3], h0, l0);
+          split_bf16x4(s1[0], s1[1], s1[2], s1[3], h1, l1);
+          sh[kk] = join(h0, h1);
+          sl[kk] = join(l0, l1);
+          const pf4 g0 = G[k][j][2 * kk], g1 = G[k][j][2 * kk + 1];
+          split_bf16x4(g0[0], g0[1], g0[2], g0[3], h0, l0);
+          split_bf16x4(g1[0], g1[1], g1[2], g1[3], h1, l1);
+          gh[kk] = join(h0, h1);
+          gl[kk] = join(l0, l1);
+          // the row of n = 16 nt + l16 holds G[.][n]
+          *reinterpret_cast<pu4*>(reinterpret_cast<char*>(sG) + unit_at<8>(16 * nt + l16, 4 * kk + g4)) = gh[kk];
+          ge = mma(sh[kk], gh[kk], ge);
+          ge = mma(sh[kk], gl[kk], ge);
+          ge = mma(sl[kk], gh[kk], ge);
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const pu4 y0 = lds_row_operand<8>(sY[k], 16 * b + l16, 0, g4), y1 = lds_row_operand<8>(sY[k], 16 * b + l16, 1, g4);
+          pf4 q = mma(sh[0], y0, zero);
+          q = mma(sl[0], y0, q);
+          q = mma(sh[1], y1, q);
+          q = mma(sl[1], y1, q);
+          const pu4 x0 = lds_row_operand<8>(sX[k], 16 * b + l16, 0, g4), x1 = lds_row_operand<8>(sX[k], 16 * b + l16, 1, g4);
+          pf4 r = mma(gh[0], x0, zero);
+          r = mma(gl[0], x0, r);
+          r = mma(gh[1], x1, r);
+          r = mma(gl[1], x1, r);
+          const int place = unit_at<U>(16 * b + l16, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1);
+          const pu2 cw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(sC[k]) + place);
+          const pu2 bw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(sB[k]) + place);
+          su[b] += (q[0] * lo_f32(cw[0]) + q[1] * hi_f32(cw[0])) + (q[2] * lo_f32(cw[1]) + q[3] * hi_f32(cw[1]));
+          sv[b] += (r[0] * lo_f32(bw[0]) + r[1] * hi_f32(bw[0])) + (r[2] * lo_f32(bw[1]) + r[3] * hi_f32(bw[1]));
+          const float e = hw_exp2(sc.c[16 * b + l16]), pf = sc.phi[16 * b + l16] * sc.f[16 * b + l16];
+          aC[k][j][b] += q * e;
+          aB[k][j][b] += r * pf;
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        su[b] += __shfl_xor(su[b], 16);
+        su[b] += __shfl_xor(su[b], 32);
+        sv[b] += __shfl_xor(sv[b], 16);
+        sv[b] += __shfl_xor(sv[b], 32);
+        if (g4 == 0) {
+          sU[wave][16 * b + l16] = su[b];
+          sV[wave][16 * b + l16] = sv[b];
+        }
+      }
+      {
+        // <G, S>: the diagonal of the products
+        float d = (l16 >> 2) == g4 ? ((l16 & 3) == 0 ? ge[0] : (l16 & 3) == 1 ? ge[1] : (l16 & 3) == 2 ? ge[2] : ge[3])
+                                   : 0.0f;
+#pragma unroll
+        for (int m = 32; m >= 1; m >>= 1) d += __shfl_xor(d, m);
+        if (lane == 0) sE[wave] = d;
+      }
+      // ---- tiles of L, X, Z
+#pragma unroll
+      for (int i = 0; i < 10; ++i) {
+        if (i % NW != wave) continue;
+        const int tb = tile_row(i), sb = i - tb * (tb + 1) / 2;
+        pf4 X = zero;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+          X = mma(lds_row_operand<8>(sY[k], 16 * tb + l16, kk, g4), lds_row_operand<8>(sX[k], 16 * sb + l16, kk, g4), X);
+        const pf4 Z = sZ[k][i][lane];
+        const pf4 ct = *reinterpret_cast<const pf4*>(&sc.c[16 * tb + 4 * g4]);
+        const float cs = sc.c[16 * sb + l16], ph = sc.phi[16 * sb + l16];
+        float m[4], row[4], col = 0.0f, own = 0.0f, direct = 0.0f, diag = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const bool below = sb < tb || l16 <= 4 * g4 + c;
+          const float L = below ? hw_exp2(ct[c] - cs) : 0.0f;
+          m[c] = L * Z[c] * ph;
+          const float lx = L * X[c];
+          aK[k][i / NW][c] = fmaf(lx, ph, aK[k][i / NW][c]);
+          const float w0 = lx * Z[c];
+          if (sb < tb) {
+            col += w0;
+            row[c] = w0 * ph;
+          } else {   // a step's own term is in its row and in its column, and would cancel but for rounding
+            const bool on = l16 == 4 * g4 + c;
+            col += on ? 0.0f : w0;
+            row[c] = on ? 0.0f : w0 * ph;
+            own += on ? w0 : 0.0f;
+            direct += on ? m[c] : 0.0f;   // a step's own dy goes into its dx in fp32, together with D
+            m[c] = on ? 0.0f : m[c];
+            diag += on ? X[c] : 0.0f;
+          }
+        }
+        reinterpret_cast<pu2*>(&sM[m_slot(sb, tb >> 1)][lane])[tb & 1] = bf16x4(m[0], m[1], m[2], m[3]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          row[c] += row_ror<8>(row[c]);
+          row[c] += row_ror<4>(row[c]);
+          row[c] += row_ror<2>(row[c]);
+          row[c] += row_ror<1>(row[c]);
+        }
+        if (l16 < 4) sRow[i][4 * g4 + l16] = l16 == 0 ? row[0] : l16 == 1 ? row[1] : l16 == 2 ? row[2] : row[3];
+        col += __shfl_xor(col, 16);
+        col += __shfl_xor(col, 32);
+        if (g4 == 0) sCol[i][l16] = col;
+        if (sb == tb) {
+          own += __shfl_xor(own, 16);
+          own += __shfl_xor(own, 32);
+          direct += __shfl_xor(direct, 16);
+          direct += __shfl_xor(direct, 32);
+          if (g4 == 0) {
+            sOwn[tb][l16] = own;
+            sDirect[tb][l16] = direct + Dh;
+          }
+#pragma unroll
+          for (int s = 32; s >= 1; s >>= 1) diag += __shfl_xor(diag, s);
+          if (lane == 0) sDiag[tb] = diag;
+        }
+      }
+      barrier_lds();   // M, G and the partial sums are there
+      // ---- dx: a pair of column tiles (32 p) of one tile of steps at a time
+      {
+        const int64_t t0 = first_of(k);
+        const auto rdx = chunk_rsrc(a.dx + int64_t(h) * kHead, t0, a.dxs, rows_of(k), kHead);
+#pragma unroll
+        for (int job = 0; job < 8 / NW; ++job) {
+          const int sb = (wave + NW * job) & 3, pp = (wave + NW * job) >> 2;
+          pf4 d[2] = {zero, zero};
+#pragma unroll
+          for (int kk = 0; kk < NK; ++kk) {
+            const pu4 b = lds_row_operand<U>(sB[k], 16 * sb + l16, kk, g4);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) d[e] = mma(lds_tr_operand8<8>(sG, kk, 2 * pp + e, l16, g4), b, d[e]);
+          }
+          const float pf = sc.phi[16 * sb + l16] * sc.f[16 * sb + l16];
+          d[0] *= pf;
+          d[1] *= pf;
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) {
+            if (sb >= 2 && kk == 0) continue;   // no step of the first half follows one of the second
+            const pu4 m = sM[m_slot(sb, kk)][lane];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) d[e] = mma(lds_tr_operand<8>(sY[k], kk, 2 * pp + e, l16, g4), m, d[e]);
+          }
+          const float dr = sDirect[sb][l16];
+          const pu4 yv = lds_u4(sY[k], unit_at<8>(16 * sb + l16, 4 * pp + g4));
+          const pu4 o = {pack_bf16(fmaf(dr, lo_f32(yv[0]), d[0][0]), fmaf(dr, hi_f32(yv[0]), d[0][1])),
+                         pack_bf16(fmaf(dr, lo_f32(yv[1]), d[0][2]), fmaf(dr, hi_f32(yv[1]), d[0][3])),
+                         pack_bf16(fmaf(dr, lo_f32(yv[2]), d[1][0]), fmaf(dr, hi_f32(yv[2]), d[1][1])),
+                         pack_bf16(fmaf(dr, lo_f32(yv[3]), d[1][2]), fmaf(dr, hi_f32(yv[3]), d[1][3]))};
+          __builtin_amdgcn_raw_buffer_store_b128(
+              o, rdx, static_cast<int>(static_cast<uint32_t>(16 * sb + l16) * (static_cast<uint32_t>(a.dxs) * 2u) +
+                                       (32u * pp + 8u * g4) * 2u), 0, 0);
+        }
+      }
+      // ---- the steps' own gradients, by wave k
+      if (wave == k) {
+        const int tl = lane >> 4;
+        float row = 0.0f, col = 0.0f, u = 0.0f, v = 0.0f, e = 0.0f;
+#pragma unroll
+        for (int o = 0; o < 4; ++o) {
+          row += o <= tl ? sRow[tl * (tl + 1) / 2 + min(o, tl)][l16] : 0.0f;
+          const int tt = max(o, tl);
+          col += o >= tl ? sCol[tt * (tt + 1) / 2 + tl][l16] : 0.0f;
+        }
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          u += sU[w][lane];
+          v += sV[w][lane];
+          e += sE[w];
+        }
+        const float phi = sc.phi[lane];
+        u *= hw_exp2(sc.c[lane]);
+        v *= sc.f[lane];
+        const float dphi = col + sOwn[tl][l16] + v;
+        const float before = phi * v;
+        const float dl = wave_suffix(row - phi * col + u, lane) + (wave_prefix(before, lane) - before) +
+                         hw_exp2(sc.c[kChunk - 1]) * e;
+        const float e1 = delta * Ah;
+        const float decay = hw_exp2(la);
+        float dd = Ah * dl + (a.zoh ? decay * dphi : dphi);
+        if (a.softplus) dd *= sigmoid(u_in);
+        const int rows = rows_of(k);
+        if (lane < rows) {
+          Elem<uint16_t>::st(a.ddt, (first_of(k) + lane) * a.ddts + h, dd);
+          sum_a = delta * dl + (a.zoh ? zoh_slope(delta, e1, decay) * dphi : 0.0f);
+          sum_t = dd;
+        }
+        sum_d = lane < 4 ? sDiag[lane] : 0.0f;
+      }
+      if (k + 1 < KC) barrier_lds();   // M, G and the partial sums are read
+    }
+    // ---- sums over a chunk's steps
+    if (wave < KC) {
+#pragma unroll
+      for (int m = 32; m >= 1; m >>= 1) {
+        sum_a += __shfl_xor(sum_a, m);
+        sum_t += __shfl_xor(sum_t, m);
+        sum_d += __shfl_xor(sum_d, m);
+      }
+      if (lane == 0)
+        *reinterpret_cast<pf4*>(a.part_h + ((int64_t(number) * KC + wave) * a.H + h) * 4) =
+            pf4{sum_a, sum_t, sum_d, 0.0f};
+    }
+  }
+
+  // ---- the heads' K with B and C, and the sums over this workgroup's heads
+#pragma unroll
+  for (int k = 0; k < KC; ++k) {
+    barrier_lds();   // (the last readers of what is written now are done)
+    uint16_t* sK = sX[k];   // K, row by row
+#pragma unroll
+    for (int i = 0; i < 10; ++i) {
+      if (i % NW != wave) continue;
+      const int tb = tile_row(i), sb = i - tb * (tb + 1) / 2;
+      const pf4 v = aK[k][i / NW];
+      reinterpret_cast<pu2*>(&sM[m_slot(sb, tb >> 1)][lane])[tb & 1] = bf16x4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int row = 16 * tb + 4 * g4 + c, byte = 2 * (l16 & 7);
+        char* at = reinterpret_cast<char*>(sK);
+        Elem<uint16_t>::st(reinterpret_cast<uint16_t*>(at + unit_at<8>(row, 2 * sb + (l16 >> 3)) + byte), 0, v[c]);
+        // (the tile right of an even diagonal tile belongs to the same operand)
+        if (sb == tb && (tb & 1) == 0)
+          *reinterpret_cast<uint16_t*>(at + unit_at<8>(row, 2 * (sb + 1) + (l16 >> 3)) + byte) = 0;
+      }
+    }
+    barrier_lds();
+#pragma unroll
+    for (int j = 0; j < NTW; ++j) {
+      const int nt = NTW * wave + j;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        const pu4 bt = lds_tr_plain_operand<U, true>(sB[k], kk, nt, l16, g4);
+        const pu4 ct = lds_tr_plain_operand<U, false>(sC[k], kk, nt, l16, g4);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          if (kk <= b / 2) aC[k][j][b] = mma(bt, lds_row_operand<8>(sK, 16 * b + l16, kk, g4), aC[k][j][b]);
+          if (kk == 1 || b < 2) aB[k][j][b] = mma(ct, sM[m_slot(b, kk)][lane], aB[k][j][b]);
+        }
+      }
+      const int rows = rows_of(k);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int t = 16 * b + l16;
+        const int64_t at = ((int64_t(split) * a.T + first_of(k) + t) * a.G + g) * N + 16 * nt + 4 * g4;
+        if (t < rows) {
+          *reinterpret_cast<pf4*>(a.part_b + at) = aB[k][j][b];
+          *reinterpret_cast<pf4*>(a.part_c + at) = aC[k][j][b];
+        }
+      }
+    }
+  }
+}
+
+// dB and dC: the splits' sums in order, rounded once.  A thread owns four columns of a row; rows outside every sequence
+// stay as they are.
+__global__ void __launch_bounds__(256) packed_ssd_bwd_bc_kernel(BwdArgs a, int cols) {
+  const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t t = at / (cols / 4);
+  const int col = static_cast<int>(at % (cols / 4)) * 4;
+  if (t >= a.T || t < a.cu[0] || t >= a.cu[a.S_]) return;
+  const float* part = (blockIdx.y ? a.part_c : a.part_b) + t * cols + col;
+  pf4 v = *reinterpret_cast<const pf4*>(part);
+  for (int s = 1; s < a.splits; ++s) v += *reinterpret_cast<const pf4*>(part + int64_t(s) * a.T * cols);
+  uint16_t* out = (blockIdx.y ? a.dC + t * a.dcs : a.dB + t * a.dbs) + col;
+  *reinterpret_cast<pu2*>(out) = bf16x4(v[0], v[1], v[2], v[3]);
+}
+
+// dA, ddt_bias and dD of a head: the chunks' sums, 256 interleaved runs joined in a fixed order
+__global__ void __launch_bounds__(256) packed_ssd_bwd_head_kernel(BwdArgs a, int chunks) {
+  __shared__ pf4 sum[256];
+  const int h = blockIdx.x;
+  pf4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = threadIdx.x; i < chunks; i += 256) v += *reinterpret_cast<const pf4*>(a.part_h + (int64_t(i) * a.H + h) * 4);
+  sum[threadIdx.x] = v;
+  __syncthreads();
+  for (int m = 128; m >= 1; m >>= 1) {
+    if (static_cast<int>(threadIdx.x) < m) sum[threadIdx.x] += sum[threadIdx.x + m];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    a.dA[h] = sum[0][0];
+    if (a.ddt_bias) a.ddt_bias[h] = sum[0][1];
+    if (a.dD) a.dD[h] = sum[0][2];
+  }
+}
+
+struct BwdPlan {
+  PackedPlan walk;
+  int group, splits, hps;
+  int64_t numbers;
+  size_t states, ws_state, ws_decay, part, part_h, total;   // bytes: one set of saved states, ..., one of part_b and part_c
+};
+BwdPlan bwd_plan(const ssm_ssd_packed_params* p) {
+  BwdPlan b{};
+  b.group = group_of(p->dstate);
+  b.walk = packed_plan(p, b.group);
+  b.numbers = piece_numbers(p->nseqs, p->ntokens, b.group * kChunk);
+  const int64_t hpg = p->nheads / p->ngroups;
+  // four workgroups for each CU: enough to even out their lengths; each split costs a partial dB and dC
+  int64_t splits = (1024 + b.numbers * p->ngroups - 1) / (b.numbers * p->ngroups);
+  if (splits > hpg) splits = hpg;
+  b.hps = static_cast<int>((hpg + splits - 1) / splits);
+  b.splits = static_cast<int>((hpg + b.hps - 1) / b.hps);
+  const size_t state = size_t(p->nheads) * kHead * p->dstate * 4;
+  b.states = up256(size_t(b.numbers) * state);
+  b.ws_state = b.walk.split ? up256(size_t(b.walk.nseg) * state) : 0;
+  b.ws_decay = b.walk.split ? up256(size_t(b.walk.nseg) * p->nheads * 4) : 0;
+  b.part = up256(size_t(b.splits) * p->ntokens * p->ngroups * p->dstate * 4);
+  b.part_h = up256(size_t(b.numbers) * b.group * p->nheads * 16);
+  b.total = 2 * b.states + b.ws_state + b.ws_decay + 2 * b.part + b.part_h;
+  return b;
+}
+
+ssm_status check_bwd(const ssm_ssd_packed_params* p) {
+  if (ssm_status s = check_packed_ssd(p, false); s != SSM_OK) return s;
+  const BwdPlan b = bwd_plan(p);
+  if (b.numbers * b.splits * p->ngroups >= (int64_t(1) << 31) - 8) return fail(SSM_ERR_SHAPE, "too many work items");
+  if (p->ntokens * p->ngroups * p->dstate / 1024 >= (int64_t(1) << 31)) return fail(SSM_ERR_SHAPE, "too many tokens");
+  return SSM_OK;
+}
+
+template <int N>
+void launch_bwd(const BwdArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((packed_ssd_bwd_kernel<N>), dim3((a.nwork + 7) / 8 * 8), dim3(Shape<N>::NW * 64), 0, st, a);
+}
+
+}  // namespace
+}  // namespace ssm57
+
+using namespace ssm57;
+
+extern "C" size_t ssm_ssd_packed_bwd_workspace_bytes(const ssm_ssd_packed_params* p) {
+  return check_bwd(p) == SSM_OK ? bwd_plan(p).total : 0;
+}
+
+extern "C" ssm_status ssm_ssd_packed_bwd(const ssm_ssd_packed_params* p, const void* x, const void* dt,
+                                         const float* dt_bias, const float* A, const void* B, const void* C,
+                                         const float* Dskip, const int32_t* cu_seqlens, const float* state,
+                                         const int32_t* state_idx, const uint8_t* has_state, const void* dy,
+                                         const float* dstate_out, void* dx, void* ddt, float* dA, void* dB, void* dC,
+                                         float* dDskip, float* ddt_bias, float* dstate, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+  g_err[0] = 0;
+  if (ssm_status s = check_bwd(p); s != SSM_OK) return s;
+  if (!x || !dt || !A || !B || !C || !cu_seqlens || !dy || !dx || !ddt || !dA || !dB || !dC)
+    return fail(SSM_ERR_NULL, "x, dt, A, B, C, cu_seqlens, dy, dx, ddt, dA, dB and dC are required");
+  auto row = [](int64_t s, int64_t dense) { return s ? s : dense; };
+  const int64_t heads = p->nheads * kHead, grp = p->ngroups * p->dstate;
+  BwdArgs a{};
+  a.xs = row(p->x_stride, heads);
+  a.dts = row(p->dt_stride, p->nheads);
+  a.bs = row(p->b_stride, grp);
+  a.cs = row(p->c_stride, grp);
+  a.dys = row(p->dy_stride, heads);
+  a.dxs = row(p->dx_stride, heads);
+  a.ddts = row(p->ddt_stride, p->nheads);
+  a.dbs = row(p->db_stride, grp);
+  a.dcs = row(p->dc_stride, grp);
+  if (!aligned(x, 16) || !aligned(B, 16) || !aligned(C, 16) || !aligned(dy, 16) || !aligned(dx, 16) || a.xs % 8 ||
+      a.bs % 8 || a.cs % 8 || a.dys % 8 || a.dxs % 8 || !aligned(state, 16) || !aligned(dstate_out, 16) ||
+      !aligned(dstate, 16) || !aligned(dB, 8) || !aligned(dC, 8) || a.dbs % 4 || a.dcs % 4 || !aligned(dt, 2) ||
+      !aligned(ddt, 2) || !aligned(A, 4) || !aligned(dt_bias, 4) || !aligned(Dskip, 4) || !aligned(cu_seqlens, 4) ||
+      !aligned(state_idx, 4) || !aligned(dA, 4) || !aligned(dDskip, 4) || !aligned(ddt_bias, 4))
+    return fail(SSM_ERR_ALIGN, "rows of x, B, C, dy and dx, and the states, must be 16-byte aligned, of dB and dC 8-byte");
+  const BwdPlan b = bwd_plan(p);
+  if (!workspace || workspace_bytes < b.total || !aligned(workspace, 16))
+    return fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes (16-byte aligned) needed, got %zu at %p", b.total,
+                workspace_bytes, workspace);
+  char* at = static_cast<char*>(workspace);
+  auto take = [&](size_t bytes) {
+    float* f = reinterpret_cast<float*>(at);
+    at += bytes;
+    return f;
+  };
+  float* save_s = take(b.states);
+  float* save_g = take(b.states);
+  StatesArgs w{};
+  w.ws_state = take(b.ws_state);
+  w.ws_decay = take(b.ws_decay);
+  a.part_b = take(b.part);
+  a.part_c = take(b.part);
+  a.part_h = take(b.part_h);
+  a.x = static_cast<const uint16_t*>(x);
+  a.dt = static_cast<const uint16_t*>(dt);
+  a.B = static_cast<const uint16_t*>(B);
+  a.C = static_cast<const uint16_t*>(C);
+  a.dy = static_cast<const uint16_t*>(dy);
+  a.dt_bias = dt_bias;
+  a.A = A;
+  a.Dskip = Dskip;
+  a.cu = cu_seqlens;
+  a.S = save_s;
+  a.Gs = save_g;
+  a.dx = static_cast<uint16_t*>(dx);
+  a.ddt = static_cast<uint16_t*>(ddt);
+  a.dB = static_cast<uint16_t*>(dB);
+  a.dC = static_cast<uint16_t*>(dC);
+  a.dA = dA;
+  a.ddt_bias = ddt_bias;
+  a.dD = dDskip;
+  a.T = static_cast<int>(p->ntokens);
+  a.S_ = static_cast<int>(p->nseqs);
+  a.H = static_cast<int>(p->nheads);
+  a.G = static_cast<int>(p->ngroups);
+  a.hpg = a.H / a.G;
+  a.splits = b.splits;
+  a.hps = b.hps;
+  a.numbers = static_cast<int>(b.numbers);
+  a.nwork = a.numbers * a.G * a.splits;
+  a.softplus = p->dt_softplus;
+  a.zoh = p->disc == SSM_DISC_ZOH;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+
+  w.dt = a.dt;
+  w.dt_bias = dt_bias;
+  w.A = A;
+  w.cu = cu_seqlens;
+  w.dts = a.dts;
+  w.T = a.T;
+  w.S = a.S_;
+  w.H = a.H;
+  w.G = a.G;
+  w.hpg = a.hpg;
+  w.hblocks = b.walk.hblocks;
+  w.cps = b.walk.cps;
+  w.nseg = static_cast<int>(b.walk.nseg);
+  w.group = b.group;
+  w.softplus = a.softplus;
+  w.zoh = a.zoh;
+  // the states, forward from the slots, then the adjoints, in reverse order from dstate_out
+  w.v = a.x;
+  w.vs = a.xs;
+  w.k = a.B;
+  w.ks = a.bs;
+  w.init = state;
+  w.idx = state_idx;
+  w.has = has_state;
+  w.nslots = p->nslots;
+  w.save = save_s;
+  if (ssm_status s = launch_states(w, static_cast<int>(p->dstate), false, b.walk.split, st); s != SSM_OK) return s;
+  w.v = a.dy;
+  w.vs = a.dys;
+  w.k = a.C;
+  w.ks = a.cs;
+  w.init = dstate_out;
+  w.idx = nullptr;
+  w.has = nullptr;
+  w.nslots = p->nseqs;
+  w.save = save_g;
+  w.last = dstate;
+  if (ssm_status s = launch_states(w, static_cast<int>(p->dstate), true, b.walk.split, st); s != SSM_OK) return s;
+  switch (p->dstate) {
+    case 64: launch_bwd<64>(a, st); break;
+    case 128: launch_bwd<128>(a, st); break;
+    default: launch_bwd<256>(a, st); break;
+  }
+  const int cols = static_cast<int>(grp);
+  hipLaunchKernelGGL(packed_ssd_bwd_bc_kernel, dim3(static_cast<uint32_t>((int64_t(a.T) * (cols / 4) + 255) / 256), 2),
+                     dim3(256), 0, st, a, cols);
+  hipLaunchKernelGGL(packed_ssd_bwd_head_kernel, dim3(a.H), dim3(256), 0, st, a, a.numbers * b.group);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? SSM_OK : fail(SSM_ERR_HIP, "packed SSD backward launch: %s", hipGetErrorString(e));
+}

@@ -1,0 +1,242 @@
+// The states of packed SSD sequences at the boundaries that other kernels start from: the segments of the forward, the
+// chunk groups of the backward, and the adjoint states walked in reverse order.
+//
+// As in the forward, a workgroup takes 8 heads of one group (4 for N = 256) over one segment, a wave holds the state of
+// a head (or of half of its columns) in registers, and the shared k rows (B or C) go to LDS once for all waves.  The
+// weighted v rows are split into two bf16 parts (2^-18 relative), so states keep fp32 quality.  A sequence of several
+// segments takes three launches: every segment from zero, a join in order, and the walk proper.
+#include "packed_ssd.hpp"
+
+namespace ssm57 {
+namespace {
+
+constexpr int kWaves = 8;
+
+// SAVE: the walk proper; otherwise the first pass, each segment from zero
+template <int N, bool REV, bool SAVE>
+__global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
+packed_states_kernel(StatesArgs a) {
+  constexpr int U = N / 8;
+  constexpr int NT = N / 16;             // 16-row tiles of the state
+  constexpr int PT = N == 256 ? 2 : 4;   // 16-column tiles of a wave
+  constexpr int kParts = 4 / PT;         // waves of a head
+  constexpr int UV = 2 * PT;             // 16-byte units of its columns
+  __shared__ alignas(16) uint16_t sK0[kChunk * N], sK1[kChunk * N];
+  __shared__ alignas(16) uint16_t sV[kWaves][kChunk * 16 * PT];
+  __shared__ alignas(16) float sW[kWaves][kChunk];
+
+  const int item = xcd_item();
+  if (item >= a.nwork) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l16 = lane & 15, g4 = lane >> 4;
+  const int hb = item % (a.G * a.hblocks);
+  Piece seg;
+  if (!find_piece(a.cu, a.S, a.T, a.cps * kChunk, item / (a.G * a.hblocks), seg)) return;
+  // (nothing starts from the end of the walk's last segment)
+  if (!SAVE && seg.index == (REV ? 0 : seg.count - 1)) return;
+  const int64_t number = seg.first + seg.index;
+  const int g = hb / a.hblocks;
+  const int hg = (hb % a.hblocks) * (kWaves / kParts) + wave / kParts;   // head within the group
+  const int p0 = (wave % kParts) * 16 * PT;                              // first column of this wave
+  const bool on = hg < a.hpg;                                            // (a wave without a head computes the last one's)
+  const int h = g * a.hpg + (on ? hg : a.hpg - 1);
+  const int t_begin = seg.begin + seg.index * a.cps * kChunk;
+  const int t_end = min(seg.end, t_begin + a.cps * kChunk);
+  const int nchunks = (t_end - t_begin + kChunk - 1) / kChunk;
+
+  const float Ah = a.A[h];
+  const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+  const uint16_t* vh = a.v + int64_t(h) * kHead + p0;
+  const uint16_t* kg = a.k + int64_t(g) * N;
+  const uint32_t vrow = static_cast<uint32_t>(a.vs) * 2u, krow = static_cast<uint32_t>(a.ks) * 2u;
+  // chunk of turn i: its first token and rows (a turn past the last has none)
+  auto place = [&](int i, int64_t& t0, int& rows) __attribute__((always_inline)) {
+    const int ck = REV ? nchunks - 1 - i : i;
+    t0 = t_begin + int64_t(ck) * kChunk;
+    rows = i < nchunks ? min(t_end - static_cast<int>(t0), kChunk) : 0;
+    if (rows <= 0) { t0 = 0; rows = 0; }
+  };
+  auto copy_k = [&](int i, uint16_t* dst) __attribute__((always_inline)) {
+    int64_t t0;
+    int rows;
+    place(i, t0, rows);
+    copy_rows<U, kWaves>(dst, chunk_rsrc(kg, t0, a.ks, rows, N), wave, lane, krow);
+  };
+  uint16_t* V = sV[wave];
+  auto copy_v = [&](int i) __attribute__((always_inline)) {
+    int64_t t0;
+    int rows;
+    place(i, t0, rows);
+    copy_rows<UV, 1>(V, chunk_rsrc(vh, t0, a.vs, rows, 16 * PT), 0, lane, vrow);
+  };
+  auto load_dt = [&](int i) __attribute__((always_inline)) -> uint32_t {
+    int64_t t0;
+    int rows;
+    place(i, t0, rows);
+    return a.dt[(lane < rows ? t0 + lane : t0) * a.dts + h];
+  };
+
+  // state tiles: S[nt][pt][c] = S[p][n], n = 32 (nt/2) + 8 g4 + 4 (nt%2) + c, p = p0 + 32 (pt/2) + 8 (l16/4) + 4 (pt%2) + l16%4
+  pf4 S[NT][PT];
+  const int64_t head_size = int64_t(kHead) * N;
+  const int lane_entry = (p0 + 8 * (l16 >> 2) + (l16 & 3)) * N + 8 * g4;
+  auto entry = [&](int nt, int pt) __attribute__((always_inline)) {
+    return lane_entry + (32 * (pt >> 1) + 4 * (pt & 1)) * N + 32 * (nt >> 1) + 4 * (nt & 1);
+  };
+  auto put = [&](float* to) __attribute__((always_inline)) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) *reinterpret_cast<pf4*>(to + entry(nt, pt)) = S[nt][pt];
+  };
+  {
+    const float* from = nullptr;
+    if constexpr (SAVE) {
+      if (seg.count > 1) {
+        from = a.ws_state + (number * a.H + h) * head_size;
+      } else if (a.init && (!a.has || a.has[seg.seq])) {
+        const int64_t slot = slot_of(a.idx, seg.seq, a.nslots);
+        if (slot >= 0) from = a.init + (slot * a.H + h) * head_size;
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+        S[nt][pt] = from ? *reinterpret_cast<const pf4*>(from + entry(nt, pt)) : pf4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  float decay = 0.0f;   // sum of log2 decays over the segment (first pass)
+  float* W = sW[wave];
+
+  auto chunk = [&](const int i, const uint16_t* K, uint16_t* Kn, const uint32_t dtv) __attribute__((always_inline))
+               -> uint32_t {
+    wait_memory();    // this wave's copies of the chunk
+    barrier_lds();    // everyone's, and the previous chunk's readers are done
+    copy_k(i + 1, Kn);
+    const uint32_t dt_next = load_dt(i + 1);
+    int64_t t0;
+    int rows;
+    place(i, t0, rows);
+    if constexpr (SAVE) {
+      // chunk number within the sequence: the group's first in walk order saves the state entering it
+      const int q = (static_cast<int>(t0) - seg.begin) / kChunk;
+      const bool starts = REV ? q % a.group == a.group - 1 || t0 + kChunk >= seg.end : q % a.group == 0;
+      if (a.save && starts && on) {
+        const int steps = a.group * kChunk;
+        put(a.save + ((int64_t(seg.seq) + seg.begin / steps + q / a.group) * a.H + h) * head_size);
+      }
+    }
+    float delta, phi, la;
+    step_scalars(lo_f32(dtv), bias, Ah, a.softplus, a.zoh, lane < rows, delta, phi, la);
+    const float c = wave_prefix(la, lane);
+    const float total = lane_value(c, 63);
+    // (exp(c_63 - c_s) from the sum behind step s: no difference of two large sums)
+    W[lane] = REV ? hw_exp2(c) : phi * hw_exp2(wave_suffix(la, lane) - la);
+    wave_lds_sync();
+    pu4 wh[PT][2], wl[PT][2];   // the weighted rows, in two parts
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const pf4 w0 = *reinterpret_cast<const pf4*>(&W[32 * kk + 4 * g4]);
+      const pf4 w1 = *reinterpret_cast<const pf4*>(&W[32 * kk + 16 + 4 * g4]);
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+        const pu4 v = lds_tr_operand<UV>(V, kk, pt, l16, g4);
+        pu2 h0, l0, h1, l1;
+        split_bf16x4(lo_f32(v[0]) * w0[0], hi_f32(v[0]) * w0[1], lo_f32(v[1]) * w0[2], hi_f32(v[1]) * w0[3], h0, l0);
+        split_bf16x4(lo_f32(v[2]) * w1[0], hi_f32(v[2]) * w1[1], lo_f32(v[3]) * w1[2], hi_f32(v[3]) * w1[3], h1, l1);
+        wh[pt][kk] = join(h0, h1);
+        wl[pt][kk] = join(l0, l1);
+      }
+    }
+    wait_lds();
+    copy_v(i + 1);   // every read of this chunk's rows has its value
+    const float fade = hw_exp2(total);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const pu4 b0 = lds_tr_operand<U>(K, 0, nt, l16, g4), b1 = lds_tr_operand<U>(K, 1, nt, l16, g4);
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+        pf4 v = S[nt][pt] * fade;
+        v = mma(b0, wh[pt][0], v);
+        v = mma(b0, wl[pt][0], v);
+        v = mma(b1, wh[pt][1], v);
+        S[nt][pt] = mma(b1, wl[pt][1], v);
+      }
+    }
+    decay += total;
+    return dt_next;
+  };
+
+  uint32_t dtv = load_dt(0);
+  copy_k(0, sK0);
+  copy_v(0);
+  for (int i = 0; i < nchunks; i += 2) {
+    dtv = chunk(i, sK0, sK1, dtv);
+    if (i + 1 < nchunks) dtv = chunk(i + 1, sK1, sK0, dtv);
+  }
+  wait_memory();   // (the copies issued past the last chunk)
+
+  if (!on) return;
+  if constexpr (!SAVE) {
+    put(a.ws_state + (number * a.H + h) * head_size);
+    if (p0 == 0 && lane == 0) a.ws_decay[number * a.H + h] = decay;
+  } else if (a.last && seg.index == (REV ? 0 : seg.count - 1)) {
+    put(a.last + (int64_t(seg.seq) * a.H + h) * head_size);
+  }
+}
+
+// Joins the segments of a sequence in walk order: the end state that the first pass left for a segment (from zero) gives
+// way to the state entering the segment.  A thread owns four entries; nothing to do for one segment.
+template <bool REV>
+__global__ void __launch_bounds__(256) packed_join_kernel(StatesArgs a, int entries) {
+  Piece seg;
+  pieces_of(a.cu, blockIdx.x, a.T, a.cps * kChunk, seg);
+  const int count = min(seg.count, a.nseg - seg.first);   // (only a cu_seqlens out of order reaches this bound)
+  if (count <= 1) return;
+  const int64_t e = (int64_t(blockIdx.y) * 256 + threadIdx.x) * 4;
+  const int64_t per = int64_t(a.H) * entries;
+  if (e >= per) return;
+  const int h = static_cast<int>(e / entries);
+  pf4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (a.init && (!a.has || a.has[seg.seq])) {
+    const int64_t slot = slot_of(a.idx, seg.seq, a.nslots);
+    if (slot >= 0) s = *reinterpret_cast<const pf4*>(a.init + slot * per + e);
+  }
+  for (int i = 0; i < count; ++i) {
+    const int64_t j = seg.first + (REV ? count - 1 - i : i);
+    float* at = a.ws_state + j * per + e;
+    const bool more = i + 1 < count;
+    const pf4 own = more ? *reinterpret_cast<const pf4*>(at) : pf4{0.0f, 0.0f, 0.0f, 0.0f};
+    const float d = more ? hw_exp2(a.ws_decay[j * a.H + h]) : 0.0f;
+    *reinterpret_cast<pf4*>(at) = s;
+    s = s * d + own;
+  }
+}
+
+template <int N, bool REV>
+ssm_status launch_states_of(const StatesArgs& a, bool split, hipStream_t st) {
+  const dim3 grid((a.nwork + 7) / 8 * 8), block(kWaves * 64);
+  if (split) {
+    hipLaunchKernelGGL((packed_states_kernel<N, REV, false>), grid, block, 0, st, a);
+    const int64_t entries = int64_t(kHead) * N;
+    hipLaunchKernelGGL(packed_join_kernel<REV>, dim3(a.S, static_cast<uint32_t>((a.H * entries / 4 + 255) / 256)),
+                       dim3(256), 0, st, a, static_cast<int>(entries));
+  }
+  if (a.save || a.last) hipLaunchKernelGGL((packed_states_kernel<N, REV, true>), grid, block, 0, st, a);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess ? SSM_OK : fail(SSM_ERR_HIP, "packed SSD states launch: %s", hipGetErrorString(e));
+}
+
+}  // namespace
+
+ssm_status launch_states(StatesArgs a, int dstate, bool reverse, bool split, hipStream_t st) {
+  a.nwork = a.nseg * a.G * a.hblocks;
+  switch (dstate) {
+    case 64: return reverse ? launch_states_of<64, true>(a, split, st) : launch_states_of<64, false>(a, split, st);
+    case 128: return reverse ? launch_states_of<128, true>(a, split, st) : launch_states_of<128, false>(a, split, st);
+    default: return reverse ? launch_states_of<256, true>(a, split, st) : launch_states_of<256, false>(a, split, st);
+  }
+}
+
+}  // namespace ssm57

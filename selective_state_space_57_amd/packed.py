@@ -339,6 +339,58 @@ def ssd_slot_update(state, x, dt, A, B, C, dt_bias=None, Dskip=None, *, state_id
     return y
 
 
+def ssd_packed_bwd(x, dt, A, B, C, dy, cu_seqlens, dt_bias=None, Dskip=None, *, state=None, state_idx=None,
+                   has_state=None, dstate_out=None, disc=EULER_B, softplus=True, segment_chunks=0, want_dstate=None,
+                   out=None, workspace=None, stream=None):
+    """Backward of ssd_packed_fwd for dy = dL/dy (T, H, 64) and optionally dstate_out = dL/d(last state) (S, H, 64, N)
+    float32, by sequence; the states are recomputed from ``state``, the pool as it was before the forward.  Returns dict
+    dx (T, H, 64), ddt (T, H), dB, dC (T, G, N) bfloat16, dA, dDskip, ddt_bias (H,) float32 and dstate (S, H, 64, N)
+    float32, the gradient of the state each sequence starts from (want_dstate; by default when ``state`` or
+    ``dstate_out`` is given).  ``out`` may hold dx, ddt, dB, dC to write into (rows of dx 16-byte, of dB and dC 8-byte
+    aligned).  Rows outside every sequence are left as they are."""
+    import torch
+    T = x.shape[0]
+    dev = _on_gpu(x, "x")
+    io = _dtype_code(x, "x")
+    f32 = torch.float32
+    H, P, G, N, xs, ds, bs, cs = _ssd_inputs(x, dt, A, B, C, dt_bias, Dskip, T, dev)
+    S = _sequences(cu_seqlens, dev)
+    slots = _pool(state, None, state_idx, has_state, (H, P, N), S, dev)
+    dys = _rows("dy", dy, (T, H, P), x.dtype, dev)
+    _whole("dstate_out", dstate_out, (S, H, P, N), f32, dev)
+    o = dict(out or {})
+    shapes = {"dx": (T, H, P), "ddt": (T, H), "dB": (T, G, N), "dC": (T, G, N)}
+    if set(o) - set(shapes):
+        raise ValueError("out: dx, ddt, dB and dC may be given, got %s" % sorted(o))
+    rows = {k: _rows(k, o.get(k), shp, x.dtype, dev, optional=True) for k, shp in shapes.items()}
+    ins = [("x", x), ("dt", dt), ("B", B), ("C", C), ("dy", dy)]
+    for k in shapes:
+        _apart(o.get(k), k, *ins)
+        ins.append((k, o.get(k)))
+    if want_dstate is None:
+        want_dstate = state is not None or dstate_out is not None
+    with _launch(dev, stream, x, dt, A, B, C, dy, cu_seqlens, dt_bias, Dskip, state, state_idx, has_state, dstate_out,
+                 workspace, *o.values()) as st:
+        for k, shp in shapes.items():
+            if o.get(k) is None:
+                o[k] = torch.empty(shp, dtype=x.dtype, device=dev)
+                rows[k] = 0
+        for k in ("dA", "dDskip", "ddt_bias"):
+            o[k] = torch.empty((H,), dtype=f32, device=dev)
+        o["dstate"] = torch.empty((S, H, P, N), dtype=f32, device=dev) if want_dstate else None
+        p = _abi.SsdPackedParams(T, S, H, P, G, N, slots, xs, ds, bs, cs, 0, dys, rows["dx"], rows["ddt"], rows["dB"],
+                                 rows["dC"], io, int(disc), int(bool(softplus)), int(segment_chunks), 0)
+        if workspace is None:
+            need = int(_abi.lib().ssm_ssd_packed_bwd_workspace_bytes(ctypes.byref(p)))
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+        _abi.check(_abi.lib().ssm_ssd_packed_bwd(
+            ctypes.byref(p), _ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(Dskip), _ptr(cu_seqlens),
+            _ptr(state), _ptr(state_idx), _ptr(has_state), _ptr(dy), _ptr(dstate_out), _ptr(o["dx"]), _ptr(o["ddt"]),
+            _ptr(o["dA"]), _ptr(o["dB"]), _ptr(o["dC"]), _ptr(o["dDskip"]), _ptr(o["ddt_bias"]), _ptr(o["dstate"]),
+            _ptr(workspace), workspace.numel() * workspace.element_size(), st))
+    return o
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # norm
 

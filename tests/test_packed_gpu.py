@@ -382,3 +382,40 @@ def test_ssd_step(H, G, N, rows, zoh):
     named = [int(i) for i in idx if 0 <= int(i) < rows + 2]
     rest = [n for n in range(rows + 2) if n not in named]
     assert torch.equal(pool[rest], before[rest])
+
+
+@pytest.mark.parametrize("k", range(len(SSD)))
+def test_ssd_packed_bwd(k):
+    torch, r, c, cul, rows, state, idx, has, first, how, kw = ssd_case(k)
+    H, G, N = c["x"].shape[1], c["B"].shape[1], c["B"].shape[2]
+    dy = r.wide(rows, H * 64, 16, torch.bfloat16, at=8).unflatten(1, (H, 64))
+    dl = r(len(cul) - 1, H, 64, N, scale=0.3)
+    ref = R.ssd_grads(f64(c["x"]), f64(c["dt"]), f64(c["A"]), f64(c["B"]), f64(c["C"]), f64(c["bias"]), f64(c["D"]), cul,
+                      first, f64(dy), f64(dl), **how)
+    inside = slice(cul[0], cul[-1])
+    # dx, dB, dC written side by side into wider rows, as the convolution's backward takes them
+    wide = torch.full((rows, H * 64 + 2 * G * N + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = {"dx": wide[:, :H * 64].unflatten(1, (H, 64)), "dB": wide[:, H * 64:H * 64 + G * N].unflatten(1, (G, N)),
+           "dC": wide[:, H * 64 + G * N:H * 64 + 2 * G * N].unflatten(1, (G, N)),
+           "ddt": torch.full((rows, H + 2), 7.0, dtype=torch.bfloat16, device="cuda")[:, 1:H + 1]}
+    args = (c["x"], c["dt"], c["A"], c["B"], c["C"], dy, c["cu"], c["bias"], c["D"])
+    got = ssm().ssd_packed_bwd(*args, state=state, state_idx=idx, has_state=has, dstate_out=dl, out=out, **kw)
+    torch.cuda.synchronize()
+    assert got["dx"] is out["dx"] and got["dB"] is out["dB"]
+    # dx: M, G and dx itself are rounded to bf16; dB and dC: the head sum K and the outputs; ddt: itself, on fp32 sums.
+    # The fp32 sums behind dA, ddt_bias, ddt: the two-part splits (2^-16) and the decays' logarithms (2^-17), a few of
+    # them in every term: 2^-14
+    near(got["dx"][inside], ref["dx"][inside], 3 * BF, "dx")
+    near(got["dB"][inside], ref["dB"][inside], 3 * BF, "dB")
+    near(got["dC"][inside], ref["dC"][inside], 3 * BF, "dC")
+    near(got["ddt"][inside], ref["ddt"][inside], BF + 2.0 ** -14, "ddt")
+    for n in ("dA", "ddt_bias", "dDskip"):
+        near(got[n], ref[n], 2.0 ** -14, n)
+    near(got["dstate"], ref["dstate"], TOL_STATE, "dstate")
+    for t in (wide, out["ddt"]):
+        assert bool((t[:cul[0]] == 7).all()) and bool((t[cul[-1]:] == 7).all())
+    assert bool((wide[:, H * 64 + 2 * G * N:] == 7).all())
+    again = ssm().ssd_packed_bwd(*args, state=state, state_idx=idx, has_state=has, dstate_out=dl, **kw)
+    for n in got:
+        a, b = (got[n], again[n]) if n in ("dA", "ddt_bias", "dDskip", "dstate") else (got[n][inside], again[n][inside])
+        assert torch.equal(a, b), n
