@@ -116,6 +116,12 @@ __device__ __forceinline__ void part_ends() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
+// The same value, unknown to the compiler: what is computed from it is computed here, and not kept in registers over
+// the loop around.
+__device__ __forceinline__ int afresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
 // Waits for this wave's LDS operations: what it read is in registers before anything that follows is issued.
 __device__ __forceinline__ void wait_lds() {
   asm volatile("" ::: "memory");
@@ -144,6 +150,25 @@ __device__ __forceinline__ float lanes_shl(float v) {   // lane i + K, 0 behind 
 __device__ __forceinline__ float lane_value(float v, int lane) {
   return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
 }
+// sums over the wave's four rows of 16 lanes (lanes that differ in their row), and over all 64 lanes, in every lane
+__device__ __forceinline__ float sum_rows(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);   // rows (0, 0, 2, 2) and (1, 1, 3, 3)
+  const uint32_t a0 = a[0], a1 = a[1];
+  const float w = __uint_as_float(a0) + __uint_as_float(a1);
+  const uint32_t x = __float_as_uint(w);
+  const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);   // halves (0, 0) and (1, 1)
+  const uint32_t b0 = b[0], b1 = b[1];
+  return __uint_as_float(b0) + __uint_as_float(b1);
+}
+__device__ __forceinline__ float sum_row(float v) {   // over the 16 lanes of a row
+  v += row_ror<8>(v);
+  v += row_ror<4>(v);
+  v += row_ror<2>(v);
+  return v + row_ror<1>(v);
+}
+__device__ __forceinline__ float sum_wave(float v) { return sum_rows(sum_row(v)); }
+
 // sum over lanes 0..lane
 __device__ __forceinline__ float wave_prefix(float v, int lane) {
   v += lanes_shr<1>(v);

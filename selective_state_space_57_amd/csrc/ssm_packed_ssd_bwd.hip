@@ -20,8 +20,9 @@
 // B and C once at the end.  What a head needs across waves (dx, and the sums over n in u, v and <G, S>) goes through LDS.
 //
 // Precision: fp32 accumulation; the states and the weighted B and C of their recomputation are split into two bf16 parts
-// (2^-18 relative), so that u, v and <G, S>, and with them dDelta and dA, are good to fp32 quality.  G in dx, M = L Z phi (but for s = t)
-// and the head sum K are rounded once to bf16: they only reach dx, dB and dC, which are bf16.
+// (2^-18 relative), so that u, v and <G, S>, and with them dDelta and dA, are good to fp32 quality.  G in dx, M = L Z phi
+// and the head sum K (both but for s = t, which is added in fp32) are rounded once to bf16: they only reach dx, dB and
+// dC, which are bf16 themselves.
 #include "packed_ssd.hpp"
 
 namespace ssm57 {
@@ -138,9 +139,7 @@ packed_ssd_bwd_kernel(BwdArgs a) {
     barrier_lds();
 #pragma unroll
     for (int k = 0; k < KC; ++k)
-#pragma unroll
-      for (int i = 0; i < 10; ++i) {
-        if (i % NW != wave) continue;
+      for (int i = wave; i < 10; i += NW) {
         const int tb = tile_row(i), sb = i - tb * (tb + 1) / 2;
         pf4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -179,21 +178,24 @@ packed_ssd_bwd_kernel(BwdArgs a) {
                          yrow);
       }
     }
-    // states entering chunk k and adjoints behind it; p = 32 (pt/2) + 8 g4 + 4 (pt%2) + c, n = 16 nt + l16
-    pf4 S[KC][NTW][4], G[KC][NTW][4];
+    // state entering the first chunk and adjoint behind the last; p = 32 (pt/2) + 8 g4 + 4 (pt%2) + c, n = 16 nt + l16
+    pf4 S[NTW][4], G[NTW][4];
     {
-      const float* s0 = a.S + (int64_t(number) * a.H + h) * head_size;
-      const float* g0 = a.Gs + (int64_t(number) * a.H + h) * head_size;
+      const auto rs = make_rsrc(a.S + (int64_t(number) * a.H + h) * head_size, head_size);
+      const auto rg = make_rsrc(a.Gs + (int64_t(number) * a.H + h) * head_size, head_size);
+      const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
 #pragma unroll
-      for (int j = 0; j < NTW; ++j)
+      for (int j = 0; j < NTW; ++j) {
+        const int at = (8 * g4 * N + 16 * (NTW * wave + j) + l16) * 4;
 #pragma unroll
         for (int pt = 0; pt < 4; ++pt)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int at = (32 * (pt >> 1) + 8 * g4 + 4 * (pt & 1) + c) * N + 16 * (NTW * wave + j) + l16;
-            S[0][j][pt][c] = s0[at];
-            G[KC - 1][j][pt][c] = g0[at];
+            const int row = (32 * (pt >> 1) + 4 * (pt & 1) + c) * N * 4;
+            S[j][pt][c] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, row, 0));
+            G[j][pt][c] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rg, at, row, 0));
           }
+      }
     }
     float delta = 0.0f, la = 0.0f, u_in = 0.0f;   // of step `lane` of chunk `wave` (the waves below KC)
     if (wave < KC) {
@@ -209,46 +211,42 @@ packed_ssd_bwd_kernel(BwdArgs a) {
     }
     wait_memory();
     barrier_lds();   // x, dy and the scalars are there
-    // inside the group: S behind its first chunk, G before its last
-    if constexpr (KC == 2) {
-      const float fade0 = hw_exp2(sS[0].c[kChunk - 1]), fade1 = hw_exp2(sS[1].c[kChunk - 1]);
+    // D += sum over the chunk's steps of (weight k) v^T: one step of the walk, for this wave's columns n.  The weights go
+    // to k, of which a wave has 16 columns, and not to v, of which it needs all 64.
+    auto advance = [&](pf4 (&D)[NTW][4], const uint16_t* K, const uint16_t* V, auto weight) __attribute__((always_inline)) {
+      const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
 #pragma unroll
-      for (int j = 0; j < NTW; ++j) {
+      for (int kk = 0; kk < 2; ++kk) {
+        pu4 kh[NTW], kl[NTW];
 #pragma unroll
-        for (int pt = 0; pt < 4; ++pt) {
-          S[1][j][pt] = S[0][j][pt] * fade0;
-          G[0][j][pt] = G[1][j][pt] * fade1;
-        }
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          pu2 bh[2], bl[2], ch[2], cl[2];
+        for (int j = 0; j < NTW; ++j) {
+          pu2 hi[2], lo[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int k0 = 32 * kk + 16 * e + 4 * g4;
-            const pu2 b = lds_tr_plain<U>(sB[0], k0, NTW * wave + j, l16);
-            const pf4 ph = *reinterpret_cast<const pf4*>(&sS[0].phi[k0]), f = *reinterpret_cast<const pf4*>(&sS[0].f[k0]);
-            split_bf16x4(lo_f32(b[0]) * (ph[0] * f[0]), hi_f32(b[0]) * (ph[1] * f[1]), lo_f32(b[1]) * (ph[2] * f[2]),
-                         hi_f32(b[1]) * (ph[3] * f[3]), bh[e], bl[e]);
-            const pu2 c = lds_tr_plain<U>(sC[1], k0, NTW * wave + j, l16);
-            const pf4 cc = *reinterpret_cast<const pf4*>(&sS[1].c[k0]);
-            split_bf16x4(lo_f32(c[0]) * hw_exp2(cc[0]), hi_f32(c[0]) * hw_exp2(cc[1]), lo_f32(c[1]) * hw_exp2(cc[2]),
-                         hi_f32(c[1]) * hw_exp2(cc[3]), ch[e], cl[e]);
+            const pu2 v = lds_tr_plain<U>(K, k0, NTW * wave + j, l16);
+            const pf4 w = weight(k0);
+            split_bf16x4(lo_f32(v[0]) * w[0], hi_f32(v[0]) * w[1], lo_f32(v[1]) * w[2], hi_f32(v[1]) * w[3], hi[e], lo[e]);
           }
+          kh[j] = join(hi[0], hi[1]);
+          kl[j] = join(lo[0], lo[1]);
+        }
 #pragma unroll
-          for (int pt = 0; pt < 4; ++pt) {
-            const pu4 xt = lds_tr_operand<8>(sX[0], kk, pt, l16, g4), yt = lds_tr_operand<8>(sY[1], kk, pt, l16, g4);
-            S[1][j][pt] = mma(xt, join(bh[0], bh[1]), S[1][j][pt]);
-            S[1][j][pt] = mma(xt, join(bl[0], bl[1]), S[1][j][pt]);
-            G[0][j][pt] = mma(yt, join(ch[0], ch[1]), G[0][j][pt]);
-            G[0][j][pt] = mma(yt, join(cl[0], cl[1]), G[0][j][pt]);
+        for (int pt = 0; pt < 4; ++pt) {
+          const pu4 v = lds_tr_operand<8>(V, kk, pt, l16, g4);
+#pragma unroll
+          for (int j = 0; j < NTW; ++j) {
+            D[j][pt] = mma(v, kh[j], D[j][pt]);
+            D[j][pt] = mma(v, kl[j], D[j][pt]);
           }
         }
       }
-    }
+    };
     float sum_a = 0.0f, sum_t = 0.0f, sum_d = 0.0f;   // this lane's share of part_h (the waves below KC)
-#pragma unroll
-    for (int k = 0; k < KC; ++k) {
-      part_ends();
+    // one chunk, from the state entering it and the adjoint behind it
+    auto chunk = [&](auto kc, const pf4 (&S)[NTW][4], const pf4 (&G)[NTW][4]) __attribute__((always_inline)) {
+      constexpr int k = decltype(kc)::value;
+      const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
       const ChunkScalars& sc = sS[k];
       // ---- products with the states: q^T = S^T dy^T, r^T = G^T x^T, <G, S>
       float su[4] = {}, sv[4] = {};
@@ -260,12 +258,12 @@ packed_ssd_bwd_kernel(BwdArgs a) {
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk) {
           pu2 h0, l0, h1, l1;
-          const pf4 s0 = S[k][j][2 * kk], s1 = S[k][j][2 * kk + 1];
+          const pf4 s0 = S[j][2 * kk], s1 = S[j][2 * kk + 1];
           split_bf16x4(s0[0], s0[1], s0[2], s0[3], h0, l0);
           split_bf16x4(s1[0], s1[1], s1[2], s1[3], h1, l1);
           sh[kk] = join(h0, h1);
           sl[kk] = join(l0, l1);
-          const pf4 g0 = G[k][j][2 * kk], g1 = G[k][j][2 * kk + 1];
+          const pf4 g0 = G[j][2 * kk], g1 = G[j][2 * kk + 1];
           split_bf16x4(g0[0], g0[1], g0[2], g0[3], h0, l0);
           split_bf16x4(g1[0], g1[1], g1[2], g1[3], h1, l1);
           gh[kk] = join(h0, h1);
@@ -278,15 +276,15 @@ packed_ssd_bwd_kernel(BwdArgs a) {
         }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
+          if ((b & 1) == 0) part_ends();
           const pu4 y0 = lds_row_operand<8>(sY[k], 16 * b + l16, 0, g4), y1 = lds_row_operand<8>(sY[k], 16 * b + l16, 1, g4);
-          pf4 q = mma(sh[0], y0, zero);
-          q = mma(sl[0], y0, q);
-          q = mma(sh[1], y1, q);
-          q = mma(sl[1], y1, q);
           const pu4 x0 = lds_row_operand<8>(sX[k], 16 * b + l16, 0, g4), x1 = lds_row_operand<8>(sX[k], 16 * b + l16, 1, g4);
-          pf4 r = mma(gh[0], x0, zero);
+          pf4 q = mma(sh[0], y0, zero), r = mma(gh[0], x0, zero);
+          q = mma(sl[0], y0, q);
           r = mma(gl[0], x0, r);
+          q = mma(sh[1], y1, q);
           r = mma(gh[1], x1, r);
+          q = mma(sl[1], y1, q);
           r = mma(gl[1], x1, r);
           const int place = unit_at<U>(16 * b + l16, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1);
           const pu2 cw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(sC[k]) + place);
@@ -298,12 +296,11 @@ packed_ssd_bwd_kernel(BwdArgs a) {
           aB[k][j][b] += r * pf;
         }
       }
+      part_ends();
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        su[b] += __shfl_xor(su[b], 16);
-        su[b] += __shfl_xor(su[b], 32);
-        sv[b] += __shfl_xor(sv[b], 16);
-        sv[b] += __shfl_xor(sv[b], 32);
+        su[b] = sum_rows(su[b]);
+        sv[b] = sum_rows(sv[b]);
         if (g4 == 0) {
           sU[wave][16 * b + l16] = su[b];
           sV[wave][16 * b + l16] = sv[b];
@@ -313,14 +310,15 @@ packed_ssd_bwd_kernel(BwdArgs a) {
         // <G, S>: the diagonal of the products
         float d = (l16 >> 2) == g4 ? ((l16 & 3) == 0 ? ge[0] : (l16 & 3) == 1 ? ge[1] : (l16 & 3) == 2 ? ge[2] : ge[3])
                                    : 0.0f;
-#pragma unroll
-        for (int m = 32; m >= 1; m >>= 1) d += __shfl_xor(d, m);
+        d = sum_wave(d);
         if (lane == 0) sE[wave] = d;
       }
+      part_ends();
       // ---- tiles of L, X, Z
 #pragma unroll
-      for (int i = 0; i < 10; ++i) {
-        if (i % NW != wave) continue;
+      for (int ti = 0; ti < kTiles; ++ti) {
+        const int i = wave + NW * ti;
+        if (i >= 10) break;
         const int tb = tile_row(i), sb = i - tb * (tb + 1) / 2;
         pf4 X = zero;
 #pragma unroll
@@ -330,50 +328,37 @@ packed_ssd_bwd_kernel(BwdArgs a) {
         const pf4 ct = *reinterpret_cast<const pf4*>(&sc.c[16 * tb + 4 * g4]);
         const float cs = sc.c[16 * sb + l16], ph = sc.phi[16 * sb + l16];
         float m[4], row[4], col = 0.0f, own = 0.0f, direct = 0.0f, diag = 0.0f;
+        const bool on_diagonal = sb == tb;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const bool below = sb < tb || l16 <= 4 * g4 + c;
-          const float L = below ? hw_exp2(ct[c] - cs) : 0.0f;
-          m[c] = L * Z[c] * ph;
+          const int above = on_diagonal ? l16 - (4 * g4 + c) : -1;   // column minus row
+          const float L = above <= 0 ? hw_exp2(ct[c] - cs) : 0.0f;
           const float lx = L * X[c];
-          aK[k][i / NW][c] = fmaf(lx, ph, aK[k][i / NW][c]);
-          const float w0 = lx * Z[c];
-          if (sb < tb) {
-            col += w0;
-            row[c] = w0 * ph;
-          } else {   // a step's own term is in its row and in its column, and would cancel but for rounding
-            const bool on = l16 == 4 * g4 + c;
-            col += on ? 0.0f : w0;
-            row[c] = on ? 0.0f : w0 * ph;
-            own += on ? w0 : 0.0f;
-            direct += on ? m[c] : 0.0f;   // a step's own dy goes into its dx in fp32, together with D
-            m[c] = on ? 0.0f : m[c];
-            diag += on ? X[c] : 0.0f;
-          }
+          aK[k][ti][c] = fmaf(lx, ph, aK[k][ti][c]);
+          const float mm = L * Z[c] * ph, w0 = lx * Z[c];
+          // a step's own terms: its dy goes into its dx in fp32, together with D, and W[t][t] is in its row and in its
+          // column and would cancel but for rounding
+          m[c] = above == 0 ? 0.0f : mm;
+          row[c] = above == 0 ? 0.0f : w0 * ph;
+          col += above == 0 ? 0.0f : w0;
+          own += above == 0 ? w0 : 0.0f;
+          direct += above == 0 ? mm : 0.0f;
+          diag += above == 0 ? X[c] : 0.0f;
         }
         reinterpret_cast<pu2*>(&sM[m_slot(sb, tb >> 1)][lane])[tb & 1] = bf16x4(m[0], m[1], m[2], m[3]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          row[c] += row_ror<8>(row[c]);
-          row[c] += row_ror<4>(row[c]);
-          row[c] += row_ror<2>(row[c]);
-          row[c] += row_ror<1>(row[c]);
-        }
+        for (int c = 0; c < 4; ++c) row[c] = sum_row(row[c]);
         if (l16 < 4) sRow[i][4 * g4 + l16] = l16 == 0 ? row[0] : l16 == 1 ? row[1] : l16 == 2 ? row[2] : row[3];
-        col += __shfl_xor(col, 16);
-        col += __shfl_xor(col, 32);
+        col = sum_rows(col);
         if (g4 == 0) sCol[i][l16] = col;
-        if (sb == tb) {
-          own += __shfl_xor(own, 16);
-          own += __shfl_xor(own, 32);
-          direct += __shfl_xor(direct, 16);
-          direct += __shfl_xor(direct, 32);
+        if (on_diagonal) {
+          own = sum_rows(own);
+          direct = sum_rows(direct);
+          diag = sum_wave(diag);
           if (g4 == 0) {
             sOwn[tb][l16] = own;
             sDirect[tb][l16] = direct + Dh;
           }
-#pragma unroll
-          for (int s = 32; s >= 1; s >>= 1) diag += __shfl_xor(diag, s);
           if (lane == 0) sDiag[tb] = diag;
         }
       }
@@ -413,6 +398,7 @@ packed_ssd_bwd_kernel(BwdArgs a) {
                                        (32u * pp + 8u * g4) * 2u), 0, 0);
         }
       }
+      part_ends();
       // ---- the steps' own gradients, by wave k
       if (wave == k) {
         const int tl = lane >> 4;
@@ -448,16 +434,37 @@ packed_ssd_bwd_kernel(BwdArgs a) {
         }
         sum_d = lane < 4 ? sDiag[lane] : 0.0f;
       }
-      if (k + 1 < KC) barrier_lds();   // M, G and the partial sums are read
+    };
+    if constexpr (KC == 2) {
+      const float fade0 = hw_exp2(sS[0].c[kChunk - 1]), fade1 = hw_exp2(sS[1].c[kChunk - 1]);
+      pf4 S1[NTW][4];
+#pragma unroll
+      for (int j = 0; j < NTW; ++j)
+#pragma unroll
+        for (int pt = 0; pt < 4; ++pt) S1[j][pt] = S[j][pt] * fade0;
+      advance(S1, sB[0], sX[0], [&](int k0) {
+        return *reinterpret_cast<const pf4*>(&sS[0].phi[k0]) * *reinterpret_cast<const pf4*>(&sS[0].f[k0]);
+      });
+      part_ends();
+      chunk(std::integral_constant<int, 1>{}, S1, G);
+      part_ends();
+#pragma unroll
+      for (int j = 0; j < NTW; ++j)
+#pragma unroll
+        for (int pt = 0; pt < 4; ++pt) G[j][pt] *= fade1;
+      advance(G, sC[1], sY[1], [&](int k0) {
+        const pf4 c = *reinterpret_cast<const pf4*>(&sS[1].c[k0]);
+        return pf4{hw_exp2(c[0]), hw_exp2(c[1]), hw_exp2(c[2]), hw_exp2(c[3])};
+      });
+      barrier_lds();   // M, G and the partial sums of the chunk behind are read
     }
+    part_ends();
+    chunk(std::integral_constant<int, 0>{}, S, G);
     // ---- sums over a chunk's steps
     if (wave < KC) {
-#pragma unroll
-      for (int m = 32; m >= 1; m >>= 1) {
-        sum_a += __shfl_xor(sum_a, m);
-        sum_t += __shfl_xor(sum_t, m);
-        sum_d += __shfl_xor(sum_d, m);
-      }
+      sum_a = sum_wave(sum_a);
+      sum_t = sum_wave(sum_t);
+      sum_d = sum_wave(sum_d);
       if (lane == 0)
         *reinterpret_cast<pf4*>(a.part_h + ((int64_t(number) * KC + wave) * a.H + h) * 4) =
             pf4{sum_a, sum_t, sum_d, 0.0f};
@@ -470,10 +477,21 @@ packed_ssd_bwd_kernel(BwdArgs a) {
     barrier_lds();   // (the last readers of what is written now are done)
     uint16_t* sK = sX[k];   // K, row by row
 #pragma unroll
-    for (int i = 0; i < 10; ++i) {
-      if (i % NW != wave) continue;
+    for (int ti = 0; ti < kTiles; ++ti) {
+      const int i = wave + NW * ti;
+      if (i >= 10) break;
       const int tb = tile_row(i), sb = i - tb * (tb + 1) / 2;
-      const pf4 v = aK[k][i / NW];
+      pf4 v = aK[k][ti];
+      if (sb == tb) {   // a step's own term is added in fp32
+        float own = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          own += l16 == 4 * g4 + c ? v[c] : 0.0f;
+          v[c] = l16 == 4 * g4 + c ? 0.0f : v[c];
+        }
+        own = sum_rows(own);
+        if (g4 == 0) sOwn[tb][l16] = own;
+      }
       reinterpret_cast<pu2*>(&sM[m_slot(sb, tb >> 1)][lane])[tb & 1] = bf16x4(v[0], v[1], v[2], v[3]);
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -504,9 +522,15 @@ packed_ssd_bwd_kernel(BwdArgs a) {
       for (int b = 0; b < 4; ++b) {
         const int t = 16 * b + l16;
         const int64_t at = ((int64_t(split) * a.T + first_of(k) + t) * a.G + g) * N + 16 * nt + 4 * g4;
+        const float own = sOwn[b][l16];
+        const int place = unit_at<U>(t, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1);
+        const pu2 cw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(sC[k]) + place);
+        const pu2 bw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(sB[k]) + place);
         if (t < rows) {
-          *reinterpret_cast<pf4*>(a.part_b + at) = aB[k][j][b];
-          *reinterpret_cast<pf4*>(a.part_c + at) = aC[k][j][b];
+          *reinterpret_cast<pf4*>(a.part_b + at) =
+              aB[k][j][b] + own * pf4{lo_f32(cw[0]), hi_f32(cw[0]), lo_f32(cw[1]), hi_f32(cw[1])};
+          *reinterpret_cast<pf4*>(a.part_c + at) =
+              aC[k][j][b] + own * pf4{lo_f32(bw[0]), hi_f32(bw[0]), lo_f32(bw[1]), hi_f32(bw[1])};
         }
       }
     }
