@@ -96,9 +96,10 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t chunk_rsrc(const uint16_t* bas
 template <int U, int NW>
 __device__ __forceinline__ void copy_rows(void* dst, __amdgpu_buffer_rsrc_t rsrc, int wave, int lane,
                                           uint32_t row_bytes) {
-  constexpr int kInstr = kChunk * U / (64 * NW);
+  constexpr int kInstr = (kChunk * U + 64 * NW - 1) / (64 * NW);
   constexpr int kStep = 64 * NW / U;   // rows between a lane's copies
-  static_assert(kInstr >= 1 && kStep % 8 == 0, "a lane's copies share their place in the row");
+  static_assert(kStep % 8 == 0, "a lane's copies share their place in the row");
+  if (kChunk * U < 64 * NW && wave >= kChunk * U / 64) return;   // (more waves than pieces)
   const int place = 64 * wave + lane;
   const int r = place / U;
   const uint32_t base = static_cast<uint32_t>(r) * row_bytes + 16u * static_cast<uint32_t>(swz_unit<U>(r, place % U));
@@ -244,7 +245,10 @@ __device__ __forceinline__ int xcd_item() {
 
 ssm_status check_packed_ssd(const ssm_ssd_packed_params* p, bool step);
 
-// Heads a workgroup of 8 waves takes: a wave holds the state of one for N <= 128, of half of one for N = 256.
+// Waves of a workgroup that walks a segment.  A wave holds the state of half of a head (32 columns: N / 2 registers a
+// lane), so four waves fit a SIMD for N <= 128 and two for N = 256.
+template <int N>
+constexpr int walk_waves = N == 256 ? 8 : 16;
 inline int heads_per_group(const ssm_ssd_packed_params* p) { return p->dstate == 256 ? 4 : 8; }
 
 struct PackedPlan {

@@ -7,11 +7,11 @@
 //   y_t = exp(c_t) S C_t + sum_{s<=t} M[t][s] x_s + D x_t,   M[t][s] = (C_t . B_s) exp(c_t - c_s) phi_s
 //   S  <- exp(c_63) S + sum_s (phi_s exp(c_63 - c_s) x_s) B_s^T
 //
-// A workgroup takes 8 heads of one group over one segment of a sequence and walks its chunks, one wave to a head, with
-// the state in registers (N x 64 fp32 = N VGPRs a lane; for N = 256 a wave takes half of a head's columns, which do not
-// meet, and the workgroup 4 heads).  What heads share is done once: B and C are copied to LDS for all of them, a chunk
-// ahead, and the 10 lower tiles of C B^T are shared out over the waves.  Everything else belongs to one wave, so a chunk
-// has two barriers only, and every operand is read from LDS once per wave for all of its columns.
+// A workgroup takes 8 heads of one group (4 for N = 256) over one segment of a sequence and walks its chunks.  A wave
+// holds the state of half of a head in registers (32 columns, which do not meet the other half's): four waves then share
+// a SIMD and cover each other's waits (with whole heads, two waves a SIMD, the 2.7B layer took 1.x times as long).
+// What heads share is done once: B and C are copied to LDS for all of them, a chunk ahead, and the 10 lower tiles of
+// C B^T are shared out over the waves.  Everything else belongs to one wave, so a chunk has two barriers only.
 // Sequences longer than a segment: a walk over the states alone (ssm_packed_states.hip) finds the state entering every
 // segment first, and all segments run at once.
 //
@@ -45,8 +45,6 @@ struct PSsdArgs {
   int softplus, zoh;
 };
 
-constexpr int kWaves = 8;
-
 // scalars of one chunk, per wave
 struct alignas(16) HeadScalars {
   float c[kChunk];     // c_t, base 2
@@ -56,11 +54,11 @@ struct alignas(16) HeadScalars {
 };
 
 template <int N>
-__global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
+__global__ void __launch_bounds__(walk_waves<N> * 64) __attribute__((amdgpu_waves_per_eu(walk_waves<N> / 4, walk_waves<N> / 4)))
 packed_ssd_fwd_kernel(PSsdArgs a) {
-  constexpr int NW = kWaves;
-  constexpr int PT = N == 256 ? 2 : 4;   // 16-column tiles of a wave
-  constexpr int kParts = 4 / PT;         // waves of a head
+  constexpr int NW = walk_waves<N>;
+  constexpr int PT = 2;        // 16-column tiles of a wave
+  constexpr int kParts = 2;    // waves of a head
   constexpr int UX = 2 * PT;             // 16-byte units of its columns
   constexpr int U = N / 8;
   constexpr int NT = N / 16;   // 16-row tiles of the state
@@ -104,15 +102,15 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
                         __attribute__((always_inline)) {
     const int64_t t0 = t_begin + int64_t(ck) * kChunk;
     const int rows = rows_of(ck);
-    copy_rows<U, NW>(dst, chunk_rsrc(src, rows ? t0 : 0, stride, rows, N), wave, lane, row_bytes);
+    copy_rows<U, NW>(dst, chunk_rsrc(src, rows ? t0 : 0, stride, rows, N), wave, afresh(lane), row_bytes);
   };
   auto copy_x = [&](int ck) __attribute__((always_inline)) {
     const int64_t t0 = t_begin + int64_t(ck) * kChunk;
     const int rows = rows_of(ck);
-    copy_rows<UX, 1>(sX[wave], chunk_rsrc(xh, rows ? t0 : 0, a.xs, rows, 16 * PT), 0, lane, xrow);
+    copy_rows<UX, 1>(sX[wave], chunk_rsrc(xh, rows ? t0 : 0, a.xs, rows, 16 * PT), 0, afresh(lane), xrow);
   };
   auto load_dt = [&](int ck) __attribute__((always_inline)) -> uint32_t {
-    const int64_t t = t_begin + int64_t(ck) * kChunk + lane;
+    const int64_t t = t_begin + int64_t(ck) * kChunk + afresh(lane);
     return a.dt[(t < t_end ? t : (t_begin < a.T ? t_begin : 0)) * a.dts + h];
   };
 
@@ -150,6 +148,7 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
     const uint32_t dt_next = load_dt(ck + 1);
     const int rows = rows_of(ck);
     {
+      const int lane = afresh(threadIdx.x) & 63;
       float delta, phi, la;
       step_scalars(lo_f32(dtv), bias, Ah, a.softplus, a.zoh, lane < rows, delta, phi, la);
       const float c = wave_prefix(la, lane);
@@ -163,9 +162,8 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
     const float total = sc.c[kChunk - 1];
     {
       // C B^T, tile i = (tb, sb), sb <= tb: rows s, columns t
-#pragma unroll
-      for (int i = 0; i < 10; ++i) {
-        if (i % NW != wave) continue;
+      for (int i = wave; i < 10; i += NW) {
+        const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
         const int tb = i >= 6 ? 3 : (i >= 3 ? 2 : (i >= 1 ? 1 : 0)), sb = i - tb * (tb + 1) / 2;
         pf4 v = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -174,94 +172,98 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
         sCB[i][lane] = v;
       }
       barrier_lds();
-      // M[t][s] of this head, operand over s: (tb, kk) = (0,0) (1,0) (2,0) (2,1) (3,0) (3,1)
-      pu4 M[4][2];
-      float ct[4];
-#pragma unroll
-      for (int tb = 0; tb < 4; ++tb) {
-        ct[tb] = sc.c[16 * tb + l16];
-#pragma unroll
-        for (int kk = 0; kk <= tb / 2; ++kk) {
-          pu2 half[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int sb = 2 * kk + e;
-            if (sb > tb) {
-              half[e] = pu2{0u, 0u};
-              continue;
-            }
-            const pf4 cb = sCB[tb * (tb + 1) / 2 + sb][lane];
-            const pf4 cs = *reinterpret_cast<const pf4*>(&sc.c[16 * sb + 4 * g4]);
-            const pf4 ph = *reinterpret_cast<const pf4*>(&sc.phi[16 * sb + 4 * g4]);
-            float m[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              // (above the diagonal the difference can be large and positive: masked after the fact)
-              m[c] = cb[c] * (hw_exp2(ct[tb] - cs[c]) * ph[c]);
-              if (sb == tb) {
-                // a step's own x goes into its y in fp32, together with D
-                if (4 * g4 + c == l16) sc.own[16 * tb + l16] = m[c] + Dh;
-                m[c] = 4 * g4 + c < l16 ? m[c] : 0.0f;
-              }
-            }
-            half[e] = bf16x4(m[0], m[1], m[2], m[3]);
-          }
-          M[tb][kk] = join(half[0], half[1]);
-        }
-      }
-      wave_lds_sync();
       const int64_t t0 = t_begin + int64_t(ck) * kChunk;
       const auto ry = chunk_rsrc(a.y + int64_t(h) * kHead + p0, t0, a.ys, on ? rows : 0, 16 * PT);
-      // a pair of column tiles at a time: Y^T[p][t = 16 tb + l16]
+      // two tiles of steps (32) at a time: Y^T[p][t = 16 tb + l16], tb = 2 th + i
 #pragma unroll
-      for (int pp = 0; pp < PT / 2; ++pp) {
+      for (int th = 0; th < 2; ++th) {
         part_ends();
-        pf4 acc[2][4];
+        const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
+        // (the state's bf16 copy is made again for the second half: kept, it would take N / 4 registers)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int tb = 0; tb < 4; ++tb) acc[e][tb] = pf4{0.0f, 0.0f, 0.0f, 0.0f};
+          for (int pt = 0; pt < PT; ++pt) asm volatile("" : "+v"(S[nt][pt]));
+        pf4 acc[2][PT];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) acc[i][pt] = pf4{0.0f, 0.0f, 0.0f, 0.0f};
         // what the entering state gives: S C_t, scaled by exp(c_t)
 #pragma unroll
         for (int kn = 0; kn < NK; ++kn) {
-          pu4 c[4];
+          pu4 c[2];
 #pragma unroll
-          for (int tb = 0; tb < 4; ++tb) c[tb] = lds_row_operand<U>(C, 16 * tb + l16, kn, g4);
+          for (int i = 0; i < 2; ++i) c[i] = lds_row_operand<U>(C, 32 * th + 16 * i + l16, kn, g4);
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const pf4 s0 = S[2 * kn][2 * pp + e], s1 = S[2 * kn + 1][2 * pp + e];
+          for (int pt = 0; pt < PT; ++pt) {
+            const pf4 s0 = S[2 * kn][pt], s1 = S[2 * kn + 1][pt];
             const pu4 s = join(bf16x4(s0[0], s0[1], s0[2], s0[3]), bf16x4(s1[0], s1[1], s1[2], s1[3]));
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb) acc[e][tb] = mma(s, c[tb], acc[e][tb]);
+            for (int i = 0; i < 2; ++i) acc[i][pt] = mma(s, c[i], acc[i][pt]);
           }
         }
+        float ct[2];
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-          const float f = hw_exp2(ct[tb]);
-          acc[0][tb] *= f;
-          acc[1][tb] *= f;
+        for (int i = 0; i < 2; ++i) {
+          ct[i] = sc.c[32 * th + 16 * i + l16];
+          const float f = hw_exp2(ct[i]);
+#pragma unroll
+          for (int pt = 0; pt < PT; ++pt) acc[i][pt] *= f;
         }
-        // inside the chunk: sum_{s<=t} x_s M[t][s]
+        // inside the chunk: sum_{s<t} x_s M[t][s], 32 steps s at a time
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+        for (int kk = 0; kk <= th; ++kk) {
+          pu4 xt[PT];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const pu4 xt = lds_tr_operand<UX>(X, kk, 2 * pp + e, l16, g4);
+          for (int pt = 0; pt < PT; ++pt) xt[pt] = lds_tr_operand<UX>(X, kk, pt, l16, g4);
 #pragma unroll
-            for (int tb = 2 * kk; tb < 4; ++tb) acc[e][tb] = mma(xt, M[tb][kk], acc[e][tb]);
+          for (int i = 0; i < 2; ++i) {
+            const int tb = 2 * th + i;
+            part_ends();
+            pu2 half[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int sb = 2 * kk + e;
+              if (sb > tb) {
+                half[e] = pu2{0u, 0u};
+                continue;
+              }
+              const pf4 cb = sCB[tb * (tb + 1) / 2 + sb][lane];
+              const pf4 cs = *reinterpret_cast<const pf4*>(&sc.c[16 * sb + 4 * g4]);
+              const pf4 ph = *reinterpret_cast<const pf4*>(&sc.phi[16 * sb + 4 * g4]);
+              float m[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                // (above the diagonal the difference can be large and positive: masked after the fact)
+                m[c] = cb[c] * (hw_exp2(ct[i] - cs[c]) * ph[c]);
+                if (sb == tb) {
+                  // a step's own x goes into its y in fp32, together with D
+                  if (4 * g4 + c == l16) sc.own[16 * tb + l16] = m[c] + Dh;
+                  m[c] = 4 * g4 + c < l16 ? m[c] : 0.0f;
+                }
+              }
+              half[e] = bf16x4(m[0], m[1], m[2], m[3]);
+            }
+            const pu4 M = join(half[0], half[1]);
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) acc[i][pt] = mma(xt[pt], M, acc[i][pt]);
           }
-        // a lane's two tiles of the pair are eight consecutive columns of step 16 tb + l16
+        }
+        wave_lds_sync();
+        // a lane's two tiles of columns are eight consecutive ones of its step
 #pragma unroll
-        for (int tb = 0; tb < 4; ++tb) {
-          const float own = sc.own[16 * tb + l16];
-          const pu4 xv = lds_u4(X, unit_at<UX>(16 * tb + l16, 4 * pp + g4));
-          const pf4 y0 = acc[0][tb], y1 = acc[1][tb];
+        for (int i = 0; i < 2; ++i) {
+          const int t = 32 * th + 16 * i + l16;
+          const float own = sc.own[t];
+          const pu4 xv = lds_u4(X, unit_at<UX>(t, g4));
+          const pf4 y0 = acc[i][0], y1 = acc[i][1];
           const pu4 o = {pack_bf16(fmaf(own, lo_f32(xv[0]), y0[0]), fmaf(own, hi_f32(xv[0]), y0[1])),
                          pack_bf16(fmaf(own, lo_f32(xv[1]), y0[2]), fmaf(own, hi_f32(xv[1]), y0[3])),
                          pack_bf16(fmaf(own, lo_f32(xv[2]), y1[0]), fmaf(own, hi_f32(xv[2]), y1[1])),
                          pack_bf16(fmaf(own, lo_f32(xv[3]), y1[2]), fmaf(own, hi_f32(xv[3]), y1[3]))};
           __builtin_amdgcn_raw_buffer_store_b128(
-              o, ry, static_cast<int>(static_cast<uint32_t>(16 * tb + l16) * yrow + (32u * pp + 8u * g4) * 2u), 0, 0);
+              o, ry, static_cast<int>(static_cast<uint32_t>(t) * yrow + 16u * g4), 0, 0);
         }
       }
       if constexpr (kOneC) {
@@ -271,34 +273,34 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
     }
     part_ends();
     // state update
-    pu4 wh[PT][2], wl[PT][2];   // phi_s exp(c_63 - c_s) x_s, in two parts
+    const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
+    const float fade = hw_exp2(total);
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       const pf4 w0 = *reinterpret_cast<const pf4*>(&sc.w[32 * kk + 4 * g4]);
       const pf4 w1 = *reinterpret_cast<const pf4*>(&sc.w[32 * kk + 16 + 4 * g4]);
+      pu4 wh[PT], wl[PT];   // the weighted rows, in two parts
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt) {
         const pu4 v = lds_tr_operand<UX>(X, kk, pt, l16, g4);
         pu2 h0, l0, h1, l1;
         split_bf16x4(lo_f32(v[0]) * w0[0], hi_f32(v[0]) * w0[1], lo_f32(v[1]) * w0[2], hi_f32(v[1]) * w0[3], h0, l0);
         split_bf16x4(lo_f32(v[2]) * w1[0], hi_f32(v[2]) * w1[1], lo_f32(v[3]) * w1[2], hi_f32(v[3]) * w1[3], h1, l1);
-        wh[pt][kk] = join(h0, h1);
-        wl[pt][kk] = join(l0, l1);
+        wh[pt] = join(h0, h1);
+        wl[pt] = join(l0, l1);
       }
-    }
-    wait_lds();
-    copy_x(ck + 1);   // every read of this chunk's x has its value
-    const float fade = hw_exp2(total);
+      if (kk == 1) {
+        wait_lds();
+        copy_x(ck + 1);   // every read of this chunk's rows has its value
+      }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const pu4 b0 = lds_tr_operand<U>(B, 0, nt, l16, g4), b1 = lds_tr_operand<U>(B, 1, nt, l16, g4);
+      for (int nt = 0; nt < NT; ++nt) {
+        const pu4 b = lds_tr_operand<U>(B, kk, nt, l16, g4);
 #pragma unroll
-      for (int pt = 0; pt < PT; ++pt) {
-        pf4 v = S[nt][pt] * fade;
-        v = mma(b0, wh[pt][0], v);
-        v = mma(b0, wl[pt][0], v);
-        v = mma(b1, wh[pt][1], v);
-        S[nt][pt] = mma(b1, wl[pt][1], v);
+        for (int pt = 0; pt < PT; ++pt) {
+          const pf4 v = mma(b, wh[pt], kk == 0 ? S[nt][pt] * fade : S[nt][pt]);
+          S[nt][pt] = mma(b, wl[pt], v);
+        }
       }
     }
     return dt_next;
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(256) packed_ssd_step_kernel(PSsdArgs a) {
 
 template <int N>
 ssm_status launch_fwd(const PSsdArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((packed_ssd_fwd_kernel<N>), dim3((a.nwork + 7) / 8 * 8), dim3(kWaves * 64), 0, st, a);
+  hipLaunchKernelGGL((packed_ssd_fwd_kernel<N>), dim3((a.nwork + 7) / 8 * 8), dim3(walk_waves<N> * 64), 0, st, a);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SSM_OK : fail(SSM_ERR_HIP, "packed SSD launch: %s", hipGetErrorString(e));
 }

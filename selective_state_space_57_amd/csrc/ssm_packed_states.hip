@@ -2,7 +2,7 @@
 // chunk groups of the backward, and the adjoint states walked in reverse order.
 //
 // As in the forward, a workgroup takes 8 heads of one group (4 for N = 256) over one segment, a wave holds the state of
-// a head (or of half of its columns) in registers, and the shared k rows (B or C) go to LDS once for all waves.  The
+// half of a head's columns in registers, and the shared k rows (B or C) go to LDS once for all waves.  The
 // weighted v rows are split into two bf16 parts (2^-18 relative), so states keep fp32 quality.  A sequence of several
 // segments takes three launches: every segment from zero, a join in order, and the walk proper.
 #include "packed_ssd.hpp"
@@ -10,16 +10,16 @@
 namespace ssm57 {
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int PT = 2;       // 16-column tiles of a wave
+constexpr int kParts = 2;   // waves of a head
 
 // SAVE: the walk proper; otherwise the first pass, each segment from zero
 template <int N, bool REV, bool SAVE>
-__global__ void __launch_bounds__(kWaves * 64) __attribute__((amdgpu_waves_per_eu(2, 2)))
+__global__ void __launch_bounds__(walk_waves<N> * 64) __attribute__((amdgpu_waves_per_eu(walk_waves<N> / 4, walk_waves<N> / 4)))
 packed_states_kernel(StatesArgs a) {
   constexpr int U = N / 8;
   constexpr int NT = N / 16;             // 16-row tiles of the state
-  constexpr int PT = N == 256 ? 2 : 4;   // 16-column tiles of a wave
-  constexpr int kParts = 4 / PT;         // waves of a head
+  constexpr int kWaves = walk_waves<N>;
   constexpr int UV = 2 * PT;             // 16-byte units of its columns
   __shared__ alignas(16) uint16_t sK0[kChunk * N], sK1[kChunk * N];
   __shared__ alignas(16) uint16_t sV[kWaves][kChunk * 16 * PT];
@@ -134,34 +134,33 @@ packed_states_kernel(StatesArgs a) {
     // (exp(c_63 - c_s) from the sum behind step s: no difference of two large sums)
     W[lane] = REV ? hw_exp2(c) : phi * hw_exp2(wave_suffix(la, lane) - la);
     wave_lds_sync();
-    pu4 wh[PT][2], wl[PT][2];   // the weighted rows, in two parts
+    const float fade = hw_exp2(total);
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       const pf4 w0 = *reinterpret_cast<const pf4*>(&W[32 * kk + 4 * g4]);
       const pf4 w1 = *reinterpret_cast<const pf4*>(&W[32 * kk + 16 + 4 * g4]);
+      pu4 wh[PT], wl[PT];   // the weighted rows, in two parts
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt) {
         const pu4 v = lds_tr_operand<UV>(V, kk, pt, l16, g4);
         pu2 h0, l0, h1, l1;
         split_bf16x4(lo_f32(v[0]) * w0[0], hi_f32(v[0]) * w0[1], lo_f32(v[1]) * w0[2], hi_f32(v[1]) * w0[3], h0, l0);
         split_bf16x4(lo_f32(v[2]) * w1[0], hi_f32(v[2]) * w1[1], lo_f32(v[3]) * w1[2], hi_f32(v[3]) * w1[3], h1, l1);
-        wh[pt][kk] = join(h0, h1);
-        wl[pt][kk] = join(l0, l1);
+        wh[pt] = join(h0, h1);
+        wl[pt] = join(l0, l1);
       }
-    }
-    wait_lds();
-    copy_v(i + 1);   // every read of this chunk's rows has its value
-    const float fade = hw_exp2(total);
+      if (kk == 1) {
+        wait_lds();
+        copy_v(i + 1);   // every read of this chunk's rows has its value
+      }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const pu4 b0 = lds_tr_operand<U>(K, 0, nt, l16, g4), b1 = lds_tr_operand<U>(K, 1, nt, l16, g4);
+      for (int nt = 0; nt < NT; ++nt) {
+        const pu4 b = lds_tr_operand<U>(K, kk, nt, l16, g4);
 #pragma unroll
-      for (int pt = 0; pt < PT; ++pt) {
-        pf4 v = S[nt][pt] * fade;
-        v = mma(b0, wh[pt][0], v);
-        v = mma(b0, wl[pt][0], v);
-        v = mma(b1, wh[pt][1], v);
-        S[nt][pt] = mma(b1, wl[pt][1], v);
+        for (int pt = 0; pt < PT; ++pt) {
+          const pf4 v = mma(b, wh[pt], kk == 0 ? S[nt][pt] * fade : S[nt][pt]);
+          S[nt][pt] = mma(b, wl[pt], v);
+        }
       }
     }
     decay += total;
@@ -216,7 +215,7 @@ __global__ void __launch_bounds__(256) packed_join_kernel(StatesArgs a, int entr
 
 template <int N, bool REV>
 ssm_status launch_states_of(const StatesArgs& a, bool split, hipStream_t st) {
-  const dim3 grid((a.nwork + 7) / 8 * 8), block(kWaves * 64);
+  const dim3 grid((a.nwork + 7) / 8 * 8), block(walk_waves<N> * 64);
   if (split) {
     hipLaunchKernelGGL((packed_states_kernel<N, REV, false>), grid, block, 0, st, a);
     const int64_t entries = int64_t(kHead) * N;
