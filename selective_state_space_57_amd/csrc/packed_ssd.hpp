@@ -245,11 +245,9 @@ __device__ __forceinline__ int xcd_item() {
 
 ssm_status check_packed_ssd(const ssm_ssd_packed_params* p, bool step);
 
-// Waves of a workgroup that walks a segment.  A wave holds the state of half of a head (32 columns: N / 2 registers a
-// lane), so four waves fit a SIMD for N <= 128 and two for N = 256.
-template <int N>
-constexpr int walk_waves = N == 256 ? 8 : 16;
-inline int heads_per_group(const ssm_ssd_packed_params* p) { return p->dstate == 256 ? 4 : 8; }
+// A workgroup that walks a segment: 8 waves, each with the state of half of a head (32 columns: N / 2 registers a lane).
+// For N <= 128 two workgroups share a CU and cover each other's waits.
+constexpr int kWalkWaves = 8, kWalkHeads = 4;
 
 struct PackedPlan {
   int hblocks;    // workgroups per group of heads

@@ -7,11 +7,10 @@
 //   y_t = exp(c_t) S C_t + sum_{s<=t} M[t][s] x_s + D x_t,   M[t][s] = (C_t . B_s) exp(c_t - c_s) phi_s
 //   S  <- exp(c_63) S + sum_s (phi_s exp(c_63 - c_s) x_s) B_s^T
 //
-// A workgroup takes 8 heads of one group (4 for N = 256) over one segment of a sequence and walks its chunks.  A wave
-// holds the state of half of a head in registers (32 columns, which do not meet the other half's): four waves then share
-// a SIMD and cover each other's waits (with whole heads, two waves a SIMD, the 2.7B layer took 1.x times as long).
-// What heads share is done once: B and C are copied to LDS for all of them, a chunk ahead, and the 10 lower tiles of
-// C B^T are shared out over the waves.  Everything else belongs to one wave, so a chunk has two barriers only.
+// A workgroup takes 4 heads of one group over one segment of a sequence and walks its chunks.  A wave holds the state of
+// half of a head in registers (32 columns, which do not meet the other half's): so four waves share a SIMD, of two
+// workgroups, and cover each other's waits.  What heads share is done once: B and C are copied to LDS for all of them,
+// and the 10 lower tiles of C B^T are shared out over the waves.  Everything else belongs to one wave.
 // Sequences longer than a segment: a walk over the states alone (ssm_packed_states.hip) finds the state entering every
 // segment first, and all segments run at once.
 //
@@ -54,24 +53,24 @@ struct alignas(16) HeadScalars {
 };
 
 template <int N>
-__global__ void __launch_bounds__(walk_waves<N> * 64) __attribute__((amdgpu_waves_per_eu(walk_waves<N> / 4, walk_waves<N> / 4)))
+__global__ void __launch_bounds__(kWalkWaves * 64) __attribute__((amdgpu_waves_per_eu(N == 256 ? 2 : 4, N == 256 ? 2 : 4)))
 packed_ssd_fwd_kernel(PSsdArgs a) {
-  constexpr int NW = walk_waves<N>;
+  constexpr int NW = kWalkWaves;
   constexpr int PT = 2;        // 16-column tiles of a wave
   constexpr int kParts = 2;    // waves of a head
   constexpr int UX = 2 * PT;             // 16-byte units of its columns
   constexpr int U = N / 8;
   constexpr int NT = N / 16;   // 16-row tiles of the state
   constexpr int NK = N / 32;
-  constexpr bool kOneC = N == 256;       // (two copies of C would not fit the LDS)
-  __shared__ alignas(16) uint16_t sB0[kChunk * N], sB1[kChunk * N];
-  __shared__ alignas(16) uint16_t sC0[kChunk * N], sC1[kOneC ? 8 : kChunk * N];
+  // (B and C once: two workgroups of 80 KB fit a CU, and the copy of the one runs beside the products of the other)
+  __shared__ alignas(16) uint16_t B[kChunk * N], C[kChunk * N];
   __shared__ alignas(16) uint16_t sX[NW][kChunk * 16 * PT];
   __shared__ pf4 sCB[10][64];   // tiles of C B^T on and below the diagonal
-  __shared__ HeadScalars sS[NW];
+  __shared__ HeadScalars sS[NW / kParts];   // (the waves of a head write the same values)
 
-  const int item = xcd_item();
-  if (item >= a.nwork) return;
+  // (in launch order, heads fastest: the heads of a segment go round the XCDs, so that segments of any length, and numbers
+  // without one, spread evenly; runs of items per XCD, which share B and C in its L2, left some with two rounds)
+  const int item = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
@@ -136,16 +135,15 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
         S[nt][pt] = from ? *reinterpret_cast<const pf4*>(from + entry(nt, pt)) : pf4{0.0f, 0.0f, 0.0f, 0.0f};
   }
 
-  HeadScalars& sc = sS[wave];
+  HeadScalars& sc = sS[wave / kParts];
   const uint16_t* X = sX[wave];
 
-  auto chunk = [&](const int ck, const uint16_t* B, const uint16_t* C, uint16_t* Bn, uint16_t* Cn, const uint32_t dtv)
-                   __attribute__((always_inline)) -> uint32_t {
-    wait_memory();    // this wave's copies of the chunk
-    barrier_lds();    // everyone's, and the previous chunk's readers are done
-    copy_group(ck + 1, Bn, Bg, a.bs, brow);
-    if constexpr (!kOneC) copy_group(ck + 1, Cn, Cg, a.cs, crow);
-    const uint32_t dt_next = load_dt(ck + 1);
+  uint32_t dtv = load_dt(0);
+  copy_x(0);
+  for (int ck = 0; ck < nchunks; ++ck) {
+    barrier_lds();    // everyone is done with the chunk before
+    copy_group(ck, B, Bg, a.bs, brow);
+    copy_group(ck, C, Cg, a.cs, crow);
     const int rows = rows_of(ck);
     {
       const int lane = afresh(threadIdx.x) & 63;
@@ -158,7 +156,9 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
       sc.phi[lane] = phi;
       sc.w[lane] = phi * hw_exp2(behind);
     }
-    wave_lds_sync();
+    wait_memory();    // this wave's copies
+    barrier_lds();    // and everyone's
+    dtv = load_dt(ck + 1);
     const float total = sc.c[kChunk - 1];
     {
       // C B^T, tile i = (tb, sb), sb <= tb: rows s, columns t
@@ -266,10 +266,6 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
               o, ry, static_cast<int>(static_cast<uint32_t>(t) * yrow + 16u * g4), 0, 0);
         }
       }
-      if constexpr (kOneC) {
-        barrier_lds();   // everyone is done with C
-        copy_group(ck + 1, Cn, Cg, a.cs, crow);
-      }
     }
     part_ends();
     // state update
@@ -303,16 +299,6 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
         }
       }
     }
-    return dt_next;
-  };
-
-  uint32_t dtv = load_dt(0);
-  copy_group(0, sB0, Bg, a.bs, brow);
-  copy_group(0, sC0, Cg, a.cs, crow);
-  copy_x(0);
-  for (int ck = 0; ck < nchunks; ck += 2) {
-    dtv = chunk(ck, sB0, sC0, sB1, kOneC ? sC0 : sC1, dtv);
-    if (ck + 1 < nchunks) dtv = chunk(ck + 1, sB1, kOneC ? sC0 : sC1, sB0, sC0, dtv);
   }
   wait_memory();   // (the copies issued past the last chunk)
 
@@ -382,7 +368,7 @@ __global__ void __launch_bounds__(256) packed_ssd_step_kernel(PSsdArgs a) {
 
 template <int N>
 ssm_status launch_fwd(const PSsdArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((packed_ssd_fwd_kernel<N>), dim3((a.nwork + 7) / 8 * 8), dim3(walk_waves<N> * 64), 0, st, a);
+  hipLaunchKernelGGL((packed_ssd_fwd_kernel<N>), dim3(a.nwork), dim3(kWalkWaves * 64), 0, st, a);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SSM_OK : fail(SSM_ERR_HIP, "packed SSD launch: %s", hipGetErrorString(e));
 }
@@ -464,14 +450,17 @@ ssm_status check_packed_ssd(const ssm_ssd_packed_params* p, bool step) {
 
 PackedPlan packed_plan(const ssm_ssd_packed_params* p, int multiple) {
   PackedPlan pl{};
-  const int64_t hpg = p->nheads / p->ngroups, per = heads_per_group(p);
-  pl.hblocks = static_cast<int>((hpg + per - 1) / per);
+  const int64_t hpg = p->nheads / p->ngroups;
+  pl.hblocks = static_cast<int>((hpg + kWalkHeads - 1) / kWalkHeads);
   const int64_t longest = (p->ntokens + kChunk - 1) / kChunk;      // chunks of one sequence, at most
-  const int64_t chunks = p->ntokens / kChunk + p->nseqs;           // and of all
   int64_t cps = p->segment_chunks;
   if (cps == 0) {
-    // one workgroup for each of the 256 CUs; a segment's state costs as much memory traffic as four chunks
-    cps = (chunks * p->ngroups * pl.hblocks + 255) / 256;
+    // Every workgroup resident at once, two to a CU: the chunks over the places that are left after about half a segment
+    // for the end of each sequence.  Where the sequences alone take more than half of the places, they follow one another
+    // and only long ones are cut.  A segment's state costs as much memory traffic as four chunks: eight at least.
+    const int64_t places = p->dstate == 256 ? 256 : 512, blocks = p->ngroups * pl.hblocks;
+    const int64_t work = (p->ntokens / kChunk + p->nseqs / 2 + 1) * blocks, ends = p->nseqs * blocks / 2;
+    cps = 2 * ends <= places ? (work + places - ends - 1) / (places - ends) : (2 * work + places - 1) / places;
     if (cps < 8) cps = 8;
   }
   if (cps > longest) cps = longest;

@@ -1,7 +1,7 @@
 // The states of packed SSD sequences at the boundaries that other kernels start from: the segments of the forward, the
 // chunk groups of the backward, and the adjoint states walked in reverse order.
 //
-// As in the forward, a workgroup takes 8 heads of one group (4 for N = 256) over one segment, a wave holds the state of
+// As in the forward, a workgroup takes 4 heads of one group over one segment, a wave holds the state of
 // half of a head's columns in registers, and the shared k rows (B or C) go to LDS once for all waves.  The
 // weighted v rows are split into two bf16 parts (2^-18 relative), so states keep fp32 quality.  A sequence of several
 // segments takes three launches: every segment from zero, a join in order, and the walk proper.
@@ -15,18 +15,19 @@ constexpr int kParts = 2;   // waves of a head
 
 // SAVE: the walk proper; otherwise the first pass, each segment from zero
 template <int N, bool REV, bool SAVE>
-__global__ void __launch_bounds__(walk_waves<N> * 64) __attribute__((amdgpu_waves_per_eu(walk_waves<N> / 4, walk_waves<N> / 4)))
+__global__ void __launch_bounds__(kWalkWaves * 64) __attribute__((amdgpu_waves_per_eu(N == 256 ? 2 : 4, N == 256 ? 2 : 4)))
 packed_states_kernel(StatesArgs a) {
   constexpr int U = N / 8;
   constexpr int NT = N / 16;             // 16-row tiles of the state
-  constexpr int kWaves = walk_waves<N>;
+  constexpr int kWaves = kWalkWaves;
   constexpr int UV = 2 * PT;             // 16-byte units of its columns
   __shared__ alignas(16) uint16_t sK0[kChunk * N], sK1[kChunk * N];
   __shared__ alignas(16) uint16_t sV[kWaves][kChunk * 16 * PT];
   __shared__ alignas(16) float sW[kWaves][kChunk];
 
-  const int item = xcd_item();
-  if (item >= a.nwork) return;
+  // (in launch order, heads fastest: the heads of a segment go round the XCDs, so that segments of any length, and numbers
+  // without one, spread evenly; runs of items per XCD, which share B and C in its L2, left some with two rounds)
+  const int item = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g4 = lane >> 4;
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(256) packed_join_kernel(StatesArgs a, int entr
 
 template <int N, bool REV>
 ssm_status launch_states_of(const StatesArgs& a, bool split, hipStream_t st) {
-  const dim3 grid((a.nwork + 7) / 8 * 8), block(walk_waves<N> * 64);
+  const dim3 grid(a.nwork), block(kWalkWaves * 64);
   if (split) {
     hipLaunchKernelGGL((packed_states_kernel<N, REV, false>), grid, block, 0, st, a);
     const int64_t entries = int64_t(kHead) * N;
