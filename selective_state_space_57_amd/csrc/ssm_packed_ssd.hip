@@ -457,11 +457,11 @@ PackedPlan packed_plan(const ssm_ssd_packed_params* p, int multiple) {
   if (cps == 0) {
     // Every workgroup resident at once, two to a CU: the chunks over the places that are left after about half a segment
     // for the end of each sequence.  Where the sequences alone take more than half of the places, they follow one another
-    // and only long ones are cut.  A segment's state costs as much memory traffic as four chunks: eight at least.
+    // and only long ones are cut.  Segments below four chunks cost more than they spread (their states weigh as much as four chunks).
     const int64_t places = p->dstate == 256 ? 256 : 512, blocks = p->ngroups * pl.hblocks;
     const int64_t work = (p->ntokens / kChunk + p->nseqs / 2 + 1) * blocks, ends = p->nseqs * blocks / 2;
     cps = 2 * ends <= places ? (work + places - ends - 1) / (places - ends) : (2 * work + places - 1) / places;
-    if (cps < 8) cps = 8;
+    if (cps < 4) cps = 4;
   }
   if (cps > longest) cps = longest;
   cps = (cps + multiple - 1) / multiple * multiple;

@@ -14,10 +14,11 @@
 // of W do, and those are sums of the same fp32 numbers.
 //
 // Two walks (ssm_packed_states.hip) leave S and G at the boundaries of groups of chunks (two chunks; one for N = 256);
-// then a workgroup takes a group of chunks and runs over heads one after the other.  A wave owns 16 of the N columns of
-// the states (32 for N = 256) for every head: the sums of dB and dC over heads add up in its registers, and the states
-// inside the group are recomputed from the boundary's.  K is summed over heads in registers as well, and multiplied with
-// B and C once at the end.  What a head needs across waves (dx, and the sums over n in u, v and <G, S>) goes through LDS.
+// then a workgroup takes a group of chunks and runs over heads one after the other.  A wave has one chunk and 16 of the N
+// columns of the states, for every head: the sums of dB and dC over heads add up in its registers, and the state or
+// adjoint inside the group is recomputed from the boundary's.  K is summed over heads in registers as well, and
+// multiplied with B and C once at the end.  What a head needs across waves (dx, and the sums over n in u, v and <G, S>)
+// goes through LDS.  The next head's states and x are on their way while this head's dx is computed.
 //
 // Precision: fp32 accumulation; the states and the weighted B and C of their recomputation are split into two bf16 parts
 // (2^-18 relative), so that u, v and <G, S>, and with them dDelta and dA, are good to fp32 quality.  G in dx, M = L Z phi
@@ -55,17 +56,21 @@ struct BwdArgs {
   int softplus, zoh;
 };
 
-// sizes by state width: waves, n-tiles of a wave, chunks of a group
+// sizes by state width: chunks of a group, waves of a chunk, waves
 template <int N>
 struct Shape {
-  static constexpr int NW = N == 64 ? 4 : 8;
-  static constexpr int NTW = N / 16 / NW;
   static constexpr int KC = N == 256 ? 1 : 2;
+  static constexpr int CW = N / 16;
+  static constexpr int NW = KC * CW;
 };
 int group_of(int64_t dstate) { return dstate == 256 ? 1 : 2; }
 
 struct alignas(16) ChunkScalars {
-  float c[kChunk], phi[kChunk], f[kChunk];   // c_t (base 2), phi_t, exp(c_63 - c_t)
+  float c[kChunk], phi[kChunk];   // c_t (base 2), phi_t
+  float e[kChunk];                // exp(c_t)
+  float pf[kChunk];               // phi_t exp(c_63 - c_t)
+  float f[kChunk];                // exp(c_63 - c_t)
+  float delta[kChunk], decay[kChunk], slope[kChunk];   // Delta_t, exp(Delta_t A), d Delta / d dt
 };
 
 __host__ __device__ constexpr int tile_row(int i) { return i >= 6 ? 3 : (i >= 3 ? 2 : (i >= 1 ? 1 : 0)); }
@@ -87,24 +92,25 @@ __device__ __forceinline__ float zoh_slope(float delta, float e, float a) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(Shape<N>::NW * 64) __attribute__((amdgpu_waves_per_eu(Shape<N>::NW / 4, 2)))
+__global__ void __launch_bounds__(Shape<N>::NW * 64) __attribute__((amdgpu_waves_per_eu(Shape<N>::NW / 4, 4)))
 packed_ssd_bwd_kernel(BwdArgs a) {
-  constexpr int NW = Shape<N>::NW, NTW = Shape<N>::NTW, KC = Shape<N>::KC;
+  constexpr int NW = Shape<N>::NW, CW = Shape<N>::CW, KC = Shape<N>::KC;
   constexpr int U = N / 8, NK = N / 32;
-  constexpr int kTiles = (10 + NW - 1) / NW;   // tiles on and below the diagonal that a wave owns
+  constexpr int kTiles = (10 + CW - 1) / CW;   // tiles on and below the diagonal that a wave owns
+  constexpr int kJobs = CW < 8 ? 8 / CW : 1;   // pieces of dx a wave computes
   __shared__ alignas(16) uint16_t sB[KC][kChunk * N], sC[KC][kChunk * N];
   __shared__ alignas(16) uint16_t sX[KC][kChunk * kHead], sY[KC][kChunk * kHead];   // x and dy of the head
-  __shared__ pf4 sZ[KC][10][64];       // C B^T: rows t, columns s
-  __shared__ pu4 sM[6][64];            // M of the chunk, operands over t
-  __shared__ alignas(16) uint16_t sG[N * kHead];   // G of the chunk, transposed
+  __shared__ pu4 sM[KC][6][64];                        // M, operands over t
+  __shared__ alignas(16) uint16_t sG[KC][N * kHead];   // G, transposed
   __shared__ ChunkScalars sS[KC];
-  __shared__ float sU[NW][kChunk], sV[NW][kChunk], sE[NW], sRow[10][16], sCol[10][16], sOwn[4][16], sDirect[4][16], sDiag[4];
+  __shared__ float sU[NW][kChunk], sV[NW][kChunk], sE[NW];
+  __shared__ float sRow[KC][10][16], sCol[KC][10][16], sOwn[KC][4][16], sDirect[KC][4][16], sDiag[KC][4];
 
   const int item = xcd_item();
   if (item >= a.nwork) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int l16 = lane & 15, g4 = lane >> 4;
+  const int k = wave / CW, nt = wave % CW;   // chunk and n-tile of the wave
   const int split = item % a.splits;
   const int g = item / a.splits % a.G;
   const int number = item / (a.splits * a.G);
@@ -114,227 +120,228 @@ packed_ssd_bwd_kernel(BwdArgs a) {
   if (!found) {   // a number without chunks adds nothing to the sums over all of them
     for (int h = h_begin + tid; h < h_end; h += NW * 64)
 #pragma unroll
-      for (int k = 0; k < KC; ++k)
-        *reinterpret_cast<pf4*>(a.part_h + ((int64_t(number) * KC + k) * a.H + h) * 4) = pf4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int i = 0; i < KC; ++i)
+        *reinterpret_cast<pf4*>(a.part_h + ((int64_t(number) * KC + i) * a.H + h) * 4) = pf4{0.0f, 0.0f, 0.0f, 0.0f};
     return;
   }
   const int t_begin = grp.begin + grp.index * KC * kChunk;
   const int t_end = min(grp.end, t_begin + KC * kChunk);
-  auto rows_of = [&](int k) { return min(max(t_end - (t_begin + k * kChunk), 0), kChunk); };
-  auto first_of = [&](int k) -> int64_t { return rows_of(k) ? t_begin + int64_t(k) * kChunk : t_begin; };
+  auto rows_of = [&](int i) { return min(max(t_end - (t_begin + i * kChunk), 0), kChunk); };
+  auto first_of = [&](int i) -> int64_t { return rows_of(i) ? t_begin + int64_t(i) * kChunk : t_begin; };
+  const int rows = rows_of(k);
+  const int64_t t_first = first_of(k);
+  // the tiles of this wave: tile_of(0) .. ; those of two chunks fall to different SIMDs
+  auto tile_of = [&](int ti) { return ((nt + CW - 2 * k) % CW) + CW * ti; };
+  const pf4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  const uint16_t* Bk = sB[k];
+  const uint16_t* Ck = sC[k];
+  const uint16_t* Xk = sX[k];
+  const uint16_t* Yk = sY[k];
 
-  // B and C of the group stay for all heads, and so does C B^T
+  // B and C of the group stay for all heads, and so does C B^T: rows t, columns s
   {
     const uint32_t brow = static_cast<uint32_t>(a.bs) * 2u, crow = static_cast<uint32_t>(a.cs) * 2u;
-#pragma unroll
-    for (int k = 0; k < KC; ++k) {
-      copy_rows<U, NW>(sB[k], chunk_rsrc(a.B + int64_t(g) * N, first_of(k), a.bs, rows_of(k), N), wave, lane, brow);
-      copy_rows<U, NW>(sC[k], chunk_rsrc(a.C + int64_t(g) * N, first_of(k), a.cs, rows_of(k), N), wave, lane, crow);
-    }
-    if (wave == 0) {   // the halves of operands that lie above the diagonal stay zero
-      reinterpret_cast<pu2*>(&sM[m_slot(1, 0)][lane])[0] = pu2{0u, 0u};
-      reinterpret_cast<pu2*>(&sM[m_slot(3, 1)][lane])[0] = pu2{0u, 0u};
+    copy_rows<U, CW>(sB[k], chunk_rsrc(a.B + int64_t(g) * N, t_first, a.bs, rows, N), nt, lane, brow);
+    copy_rows<U, CW>(sC[k], chunk_rsrc(a.C + int64_t(g) * N, t_first, a.cs, rows, N), nt, lane, crow);
+    if (nt == 0) {   // the halves of operands that lie above the diagonal stay zero
+      reinterpret_cast<pu2*>(&sM[k][m_slot(1, 0)][lane])[0] = pu2{0u, 0u};
+      reinterpret_cast<pu2*>(&sM[k][m_slot(3, 1)][lane])[0] = pu2{0u, 0u};
     }
     wait_memory();
     barrier_lds();
-#pragma unroll
-    for (int k = 0; k < KC; ++k)
-      for (int i = wave; i < 10; i += NW) {
-        const int tb = tile_row(i), sb = i - tb * (tb + 1) / 2;
-        pf4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int kk = 0; kk < NK; ++kk)
-          v = mma(lds_row_operand<U>(sC[k], 16 * tb + l16, kk, g4), lds_row_operand<U>(sB[k], 16 * sb + l16, kk, g4), v);
-        sZ[k][i][lane] = v;   // (read by the wave that wrote it)
-      }
   }
-
-  const pf4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  pf4 aB[KC][NTW][4], aC[KC][NTW][4];   // dB^T, dC^T: n = 16 nt + 4 g4 + c, step 16 sb + l16
-  pf4 aK[KC][kTiles];                   // K: rows t, columns s
+  pf4 aB[4], aC[4];   // dB^T, dC^T: n = 16 nt + 4 g4 + c, step 16 b + l16
+  pf4 aK[kTiles];     // K: rows t, columns s
 #pragma unroll
-  for (int k = 0; k < KC; ++k) {
+  for (int b = 0; b < 4; ++b) aB[b] = aC[b] = zero;
 #pragma unroll
-    for (int j = 0; j < NTW; ++j)
-#pragma unroll
-      for (int b = 0; b < 4; ++b) aB[k][j][b] = aC[k][j][b] = zero;
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) aK[k][i] = zero;
-  }
+  for (int i = 0; i < kTiles; ++i) aK[i] = zero;
   const int64_t head_size = int64_t(kHead) * N;
 
+  const uint32_t xrow = static_cast<uint32_t>(a.xs) * 2u, yrow = static_cast<uint32_t>(a.dys) * 2u;
+  auto copy_head = [&](uint16_t* dst, const uint16_t* src, int h, int64_t stride, uint32_t row_bytes)
+                       __attribute__((always_inline)) {
+    copy_rows<8, CW>(dst, chunk_rsrc(src + int64_t(h) * kHead, t_first, stride, rows, kHead), nt, afresh(lane), row_bytes);
+  };
+  // state entering the group and adjoint behind it; p = 32 (pt/2) + 8 g4 + 4 (pt%2) + c, n = 16 nt + l16
+  pf4 S[4], G[4];
+  auto load_states = [&](int h) __attribute__((always_inline)) {
+    const auto rs = make_rsrc(a.S + (int64_t(number) * a.H + h) * head_size, head_size);
+    const auto rg = make_rsrc(a.Gs + (int64_t(number) * a.H + h) * head_size, head_size);
+    const int l = afresh(lane);
+    const int at = (8 * (l >> 4) * N + 16 * nt + (l & 15)) * 4;
+#pragma unroll
+    for (int pt = 0; pt < 4; ++pt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int row = (32 * (pt >> 1) + 4 * (pt & 1) + c) * N * 4;
+        S[pt][c] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, row, 0));
+        G[pt][c] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rg, at, row, 0));
+      }
+  };
+  // D += sum over a chunk's steps of v (weight k)^T: one step of the walk, for this wave's columns n.  The weights go to k,
+  // of which a wave has 16 columns, and not to v, of which it needs all 64.
+  auto advance = [&](pf4 (&D)[4], const uint16_t* K, const uint16_t* V, const float* weight) __attribute__((always_inline)) {
+    const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      pu2 hi[2], lo[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int k0 = 32 * kk + 16 * e + 4 * g4;
+        const pu2 v = lds_tr_plain<U>(K, k0, nt, l16);
+        const pf4 w = *reinterpret_cast<const pf4*>(&weight[k0]);
+        split_bf16x4(lo_f32(v[0]) * w[0], hi_f32(v[0]) * w[1], lo_f32(v[1]) * w[2], hi_f32(v[1]) * w[3], hi[e], lo[e]);
+      }
+      const pu4 kh = join(hi[0], hi[1]), kl = join(lo[0], lo[1]);
+#pragma unroll
+      for (int pt = 0; pt < 4; ++pt) {
+        const pu4 v = lds_tr_operand<8>(V, kk, pt, l16, g4);
+        D[pt] = mma(v, kh, D[pt]);
+        D[pt] = mma(v, kl, D[pt]);
+      }
+    }
+  };
+
+  copy_head(sX[k], a.x, h_begin, a.xs, xrow);
+  load_states(h_begin);
   for (int h = h_begin; h < h_end; ++h) {
     const float Ah = a.A[h];
-    const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
     const float Dh = a.Dskip ? a.Dskip[h] : 0.0f;
     barrier_lds();   // everyone is done with the head before
-    {
-      const uint32_t xrow = static_cast<uint32_t>(a.xs) * 2u, yrow = static_cast<uint32_t>(a.dys) * 2u;
-#pragma unroll
-      for (int k = 0; k < KC; ++k) {
-        copy_rows<8, NW>(sX[k], chunk_rsrc(a.x + int64_t(h) * kHead, first_of(k), a.xs, rows_of(k), kHead), wave, lane,
-                         xrow);
-        copy_rows<8, NW>(sY[k], chunk_rsrc(a.dy + int64_t(h) * kHead, first_of(k), a.dys, rows_of(k), kHead), wave, lane,
-                         yrow);
-      }
-    }
-    // state entering the first chunk and adjoint behind the last; p = 32 (pt/2) + 8 g4 + 4 (pt%2) + c, n = 16 nt + l16
-    pf4 S[NTW][4], G[NTW][4];
-    {
-      const auto rs = make_rsrc(a.S + (int64_t(number) * a.H + h) * head_size, head_size);
-      const auto rg = make_rsrc(a.Gs + (int64_t(number) * a.H + h) * head_size, head_size);
-      const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
-#pragma unroll
-      for (int j = 0; j < NTW; ++j) {
-        const int at = (8 * g4 * N + 16 * (NTW * wave + j) + l16) * 4;
-#pragma unroll
-        for (int pt = 0; pt < 4; ++pt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int row = (32 * (pt >> 1) + 4 * (pt & 1) + c) * N * 4;
-            S[j][pt][c] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, row, 0));
-            G[j][pt][c] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rg, at, row, 0));
-          }
-      }
-    }
-    float delta = 0.0f, la = 0.0f, u_in = 0.0f;   // of step `lane` of chunk `wave` (the waves below KC)
-    if (wave < KC) {
-      const int rows = rows_of(wave);
-      const int64_t t0 = first_of(wave);
-      const float dtv = lo_f32(a.dt[(lane < rows ? t0 + lane : t0) * a.dts + h]);
-      float phi;
+    copy_head(sY[k], a.dy, h, a.dys, yrow);
+    constexpr int kScalarTile = CW - 1;   // the wave of a chunk that works on its steps
+    if (nt == kScalarTile) {
+      const int lane = afresh(threadIdx.x) & 63;
+      const float dtv = lo_f32(a.dt[(lane < rows ? t_first + lane : t_first) * a.dts + h]);
+      const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
+      float delta, phi, la;
       step_scalars(dtv, bias, Ah, a.softplus, a.zoh, lane < rows, delta, phi, la);
-      u_in = dtv + bias;
-      sS[wave].c[lane] = wave_prefix(la, lane);
-      sS[wave].phi[lane] = phi;
-      sS[wave].f[lane] = hw_exp2(wave_suffix(la, lane) - la);
+      const float c = wave_prefix(la, lane), f = hw_exp2(wave_suffix(la, lane) - la);
+      sS[k].c[lane] = c;
+      sS[k].phi[lane] = phi;
+      sS[k].e[lane] = hw_exp2(c);
+      sS[k].f[lane] = f;
+      sS[k].pf[lane] = phi * f;
+      sS[k].delta[lane] = delta;
+      sS[k].decay[lane] = hw_exp2(la);
+      sS[k].slope[lane] = a.softplus ? sigmoid(dtv + bias) : 1.0f;
     }
     wait_memory();
     barrier_lds();   // x, dy and the scalars are there
-    // D += sum over the chunk's steps of (weight k) v^T: one step of the walk, for this wave's columns n.  The weights go
-    // to k, of which a wave has 16 columns, and not to v, of which it needs all 64.
-    auto advance = [&](pf4 (&D)[NTW][4], const uint16_t* K, const uint16_t* V, auto weight) __attribute__((always_inline)) {
-      const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
+    const ChunkScalars& sc = sS[k];
+    if constexpr (KC == 2) {   // the state behind the first chunk, the adjoint before the last
+      if (k == 1) {
+        const float fade = sS[0].e[kChunk - 1];
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        pu4 kh[NTW], kl[NTW];
+        for (int pt = 0; pt < 4; ++pt) S[pt] *= fade;
+        advance(S, sB[0], sX[0], sS[0].pf);
+      } else {
+        const float fade = sS[KC - 1].e[kChunk - 1];
 #pragma unroll
-        for (int j = 0; j < NTW; ++j) {
-          pu2 hi[2], lo[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int k0 = 32 * kk + 16 * e + 4 * g4;
-            const pu2 v = lds_tr_plain<U>(K, k0, NTW * wave + j, l16);
-            const pf4 w = weight(k0);
-            split_bf16x4(lo_f32(v[0]) * w[0], hi_f32(v[0]) * w[1], lo_f32(v[1]) * w[2], hi_f32(v[1]) * w[3], hi[e], lo[e]);
-          }
-          kh[j] = join(hi[0], hi[1]);
-          kl[j] = join(lo[0], lo[1]);
-        }
-#pragma unroll
-        for (int pt = 0; pt < 4; ++pt) {
-          const pu4 v = lds_tr_operand<8>(V, kk, pt, l16, g4);
-#pragma unroll
-          for (int j = 0; j < NTW; ++j) {
-            D[j][pt] = mma(v, kh[j], D[j][pt]);
-            D[j][pt] = mma(v, kl[j], D[j][pt]);
-          }
-        }
+        for (int pt = 0; pt < 4; ++pt) G[pt] *= fade;
+        advance(G, sC[KC - 1], sY[KC - 1], sS[KC - 1].e);
       }
-    };
-    float sum_a = 0.0f, sum_t = 0.0f, sum_d = 0.0f;   // this lane's share of part_h (the waves below KC)
-    // one chunk, from the state entering it and the adjoint behind it
-    auto chunk = [&](auto kc, const pf4 (&S)[NTW][4], const pf4 (&G)[NTW][4]) __attribute__((always_inline)) {
-      constexpr int k = decltype(kc)::value;
-      const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
-      const ChunkScalars& sc = sS[k];
+    }
+    part_ends();
+    {
       // ---- products with the states: q^T = S^T dy^T, r^T = G^T x^T, <G, S>
-      float su[4] = {}, sv[4] = {};
+      const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
+      pu4 sh[2], sl[2], gh[2], gl[2];
       pf4 ge = zero;
 #pragma unroll
-      for (int j = 0; j < NTW; ++j) {
-        const int nt = NTW * wave + j;
-        pu4 sh[2], sl[2], gh[2], gl[2];
+      for (int kk = 0; kk < 2; ++kk) {
+        pu2 h0, l0, h1, l1;
+        split_bf16x4(S[2 * kk][0], S[2 * kk][1], S[2 * kk][2], S[2 * kk][3], h0, l0);
+        split_bf16x4(S[2 * kk + 1][0], S[2 * kk + 1][1], S[2 * kk + 1][2], S[2 * kk + 1][3], h1, l1);
+        sh[kk] = join(h0, h1);
+        sl[kk] = join(l0, l1);
+      }
+      part_ends();
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          pu2 h0, l0, h1, l1;
-          const pf4 s0 = S[j][2 * kk], s1 = S[j][2 * kk + 1];
-          split_bf16x4(s0[0], s0[1], s0[2], s0[3], h0, l0);
-          split_bf16x4(s1[0], s1[1], s1[2], s1[3], h1, l1);
-          sh[kk] = join(h0, h1);
-          sl[kk] = join(l0, l1);
-          const pf4 g0 = G[j][2 * kk], g1 = G[j][2 * kk + 1];
-          split_bf16x4(g0[0], g0[1], g0[2], g0[3], h0, l0);
-          split_bf16x4(g1[0], g1[1], g1[2], g1[3], h1, l1);
-          gh[kk] = join(h0, h1);
-          gl[kk] = join(l0, l1);
-          // the row of n = 16 nt + l16 holds G[.][n]
-          *reinterpret_cast<pu4*>(reinterpret_cast<char*>(sG) + unit_at<8>(16 * nt + l16, 4 * kk + g4)) = gh[kk];
-          ge = mma(sh[kk], gh[kk], ge);
-          ge = mma(sh[kk], gl[kk], ge);
-          ge = mma(sl[kk], gh[kk], ge);
-        }
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          if ((b & 1) == 0) part_ends();
-          const pu4 y0 = lds_row_operand<8>(sY[k], 16 * b + l16, 0, g4), y1 = lds_row_operand<8>(sY[k], 16 * b + l16, 1, g4);
-          const pu4 x0 = lds_row_operand<8>(sX[k], 16 * b + l16, 0, g4), x1 = lds_row_operand<8>(sX[k], 16 * b + l16, 1, g4);
-          pf4 q = mma(sh[0], y0, zero), r = mma(gh[0], x0, zero);
-          q = mma(sl[0], y0, q);
-          r = mma(gl[0], x0, r);
-          q = mma(sh[1], y1, q);
-          r = mma(gh[1], x1, r);
-          q = mma(sl[1], y1, q);
-          r = mma(gl[1], x1, r);
-          const int place = unit_at<U>(16 * b + l16, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1);
-          const pu2 cw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(sC[k]) + place);
-          const pu2 bw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(sB[k]) + place);
-          su[b] += (q[0] * lo_f32(cw[0]) + q[1] * hi_f32(cw[0])) + (q[2] * lo_f32(cw[1]) + q[3] * hi_f32(cw[1]));
-          sv[b] += (r[0] * lo_f32(bw[0]) + r[1] * hi_f32(bw[0])) + (r[2] * lo_f32(bw[1]) + r[3] * hi_f32(bw[1]));
-          const float e = hw_exp2(sc.c[16 * b + l16]), pf = sc.phi[16 * b + l16] * sc.f[16 * b + l16];
-          aC[k][j][b] += q * e;
-          aB[k][j][b] += r * pf;
-        }
+      for (int kk = 0; kk < 2; ++kk) {
+        pu2 h0, l0, h1, l1;
+        split_bf16x4(G[2 * kk][0], G[2 * kk][1], G[2 * kk][2], G[2 * kk][3], h0, l0);
+        split_bf16x4(G[2 * kk + 1][0], G[2 * kk + 1][1], G[2 * kk + 1][2], G[2 * kk + 1][3], h1, l1);
+        gh[kk] = join(h0, h1);
+        gl[kk] = join(l0, l1);
+        // the row of n = 16 nt + l16 holds G[.][n]
+        *reinterpret_cast<pu4*>(reinterpret_cast<char*>(sG[k]) + unit_at<8>(16 * nt + l16, 4 * kk + g4)) = gh[kk];
+        ge = mma(sh[kk], gh[kk], ge);
+        ge = mma(sh[kk], gl[kk], ge);
+        ge = mma(sl[kk], gh[kk], ge);
       }
       part_ends();
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        su[b] = sum_rows(su[b]);
-        sv[b] = sum_rows(sv[b]);
-        if (g4 == 0) {
-          sU[wave][16 * b + l16] = su[b];
-          sV[wave][16 * b + l16] = sv[b];
+        const int row = 16 * b + l16;
+        pf4 q = zero, r = zero;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          const pu4 y = lds_row_operand<8>(Yk, row, kk, g4), x = lds_row_operand<8>(Xk, row, kk, g4);
+          q = mma(sh[kk], y, q);
+          r = mma(gh[kk], x, r);
+          q = mma(sl[kk], y, q);
+          r = mma(gl[kk], x, r);
         }
+        const int place = unit_at<U>(row, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1);
+        const pu2 cw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(Ck) + place);
+        const pu2 bw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(Bk) + place);
+        const float su = sum_rows((q[0] * lo_f32(cw[0]) + q[1] * hi_f32(cw[0])) + (q[2] * lo_f32(cw[1]) + q[3] * hi_f32(cw[1])));
+        const float sv = sum_rows((r[0] * lo_f32(bw[0]) + r[1] * hi_f32(bw[0])) + (r[2] * lo_f32(bw[1]) + r[3] * hi_f32(bw[1])));
+        if (g4 == 0) {
+          sU[wave][row] = su;
+          sV[wave][row] = sv;
+        }
+        aC[b] += q * sc.e[row];
+        aB[b] += r * sc.pf[row];
+        asm volatile("" : "+v"(aB[b]), "+v"(aC[b]));   // (here, and not behind the loop with q and r kept for it)
+        part_ends();
       }
-      {
-        // <G, S>: the diagonal of the products
-        float d = (l16 >> 2) == g4 ? ((l16 & 3) == 0 ? ge[0] : (l16 & 3) == 1 ? ge[1] : (l16 & 3) == 2 ? ge[2] : ge[3])
-                                   : 0.0f;
-        d = sum_wave(d);
-        if (lane == 0) sE[wave] = d;
+      // <G, S>: the diagonal of the products
+      const float d = (l16 >> 2) == g4 ? ((l16 & 2) ? ((l16 & 1) ? ge[3] : ge[2]) : ((l16 & 1) ? ge[1] : ge[0])) : 0.0f;
+      const float total = sum_wave(d);
+      if (l == 0) sE[wave] = total;
+    }
+    part_ends();
+    // ---- tiles of L, X, Z
+#pragma unroll
+    for (int ti = 0; ti < kTiles; ++ti) {
+      const int i = tile_of(ti);
+      if (i >= 10) break;
+      const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
+      const int tb = tile_row(i), sb = i - tb * (tb + 1) / 2;
+      pf4 X = zero;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+        X = mma(lds_row_operand<8>(Yk, 16 * tb + l16, kk, g4), lds_row_operand<8>(Xk, 16 * sb + l16, kk, g4), X);
+      const pf4 ct = *reinterpret_cast<const pf4*>(&sc.c[16 * tb + 4 * g4]);
+      const float cs = sc.c[16 * sb + l16], ph = sc.phi[16 * sb + l16];
+      pf4 Z = zero;
+#pragma unroll
+      for (int kk = 0; kk < NK; ++kk) {
+        if (kk % 2 == 0) part_ends();
+        Z = mma(lds_row_operand<U>(Ck, 16 * tb + l16, kk, g4), lds_row_operand<U>(Bk, 16 * sb + l16, kk, g4), Z);
       }
       part_ends();
-      // ---- tiles of L, X, Z
-#pragma unroll
-      for (int ti = 0; ti < kTiles; ++ti) {
-        const int i = wave + NW * ti;
-        if (i >= 10) break;
-        const int tb = tile_row(i), sb = i - tb * (tb + 1) / 2;
-        pf4 X = zero;
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-          X = mma(lds_row_operand<8>(sY[k], 16 * tb + l16, kk, g4), lds_row_operand<8>(sX[k], 16 * sb + l16, kk, g4), X);
-        const pf4 Z = sZ[k][i][lane];
-        const pf4 ct = *reinterpret_cast<const pf4*>(&sc.c[16 * tb + 4 * g4]);
-        const float cs = sc.c[16 * sb + l16], ph = sc.phi[16 * sb + l16];
-        float m[4], row[4], col = 0.0f, own = 0.0f, direct = 0.0f, diag = 0.0f;
-        const bool on_diagonal = sb == tb;
+      float m[4], row[4], col = 0.0f;
+      if (sb < tb) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int above = on_diagonal ? l16 - (4 * g4 + c) : -1;   // column minus row
-          const float L = above <= 0 ? hw_exp2(ct[c] - cs) : 0.0f;
-          const float lx = L * X[c];
-          aK[k][ti][c] = fmaf(lx, ph, aK[k][ti][c]);
+          const float L = hw_exp2(ct[c] - cs), lx = L * X[c];
+          aK[ti][c] = fmaf(lx, ph, aK[ti][c]);
+          m[c] = L * Z[c] * ph;
+          const float w0 = lx * Z[c];
+          row[c] = w0 * ph;
+          col += w0;
+        }
+      } else {
+        float own = 0.0f, direct = 0.0f, diag = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int above = l16 - (4 * g4 + c);   // column minus row
+          const float L = above <= 0 ? hw_exp2(ct[c] - cs) : 0.0f, lx = L * X[c];
+          aK[ti][c] = fmaf(lx, ph, aK[ti][c]);
           const float mm = L * Z[c] * ph, w0 = lx * Z[c];
           // a step's own terms: its dy goes into its dx in fp32, together with D, and W[t][t] is in its row and in its
           // column and would cancel but for rounding
@@ -345,194 +352,157 @@ packed_ssd_bwd_kernel(BwdArgs a) {
           direct += above == 0 ? mm : 0.0f;
           diag += above == 0 ? X[c] : 0.0f;
         }
-        reinterpret_cast<pu2*>(&sM[m_slot(sb, tb >> 1)][lane])[tb & 1] = bf16x4(m[0], m[1], m[2], m[3]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) row[c] = sum_row(row[c]);
-        if (l16 < 4) sRow[i][4 * g4 + l16] = l16 == 0 ? row[0] : l16 == 1 ? row[1] : l16 == 2 ? row[2] : row[3];
-        col = sum_rows(col);
-        if (g4 == 0) sCol[i][l16] = col;
-        if (on_diagonal) {
-          own = sum_rows(own);
-          direct = sum_rows(direct);
-          diag = sum_wave(diag);
-          if (g4 == 0) {
-            sOwn[tb][l16] = own;
-            sDirect[tb][l16] = direct + Dh;
-          }
-          if (lane == 0) sDiag[tb] = diag;
+        own = sum_rows(own);
+        direct = sum_rows(direct);
+        diag = sum_wave(diag);
+        if (g4 == 0) {
+          sOwn[k][tb][l16] = own;
+          sDirect[k][tb][l16] = direct + Dh;
         }
+        if (l == 0) sDiag[k][tb] = diag;
       }
-      barrier_lds();   // M, G and the partial sums are there
-      // ---- dx: a pair of column tiles (32 p) of one tile of steps at a time
-      {
-        const int64_t t0 = first_of(k);
-        const auto rdx = chunk_rsrc(a.dx + int64_t(h) * kHead, t0, a.dxs, rows_of(k), kHead);
+      reinterpret_cast<pu2*>(&sM[k][m_slot(sb, tb >> 1)][l])[tb & 1] = bf16x4(m[0], m[1], m[2], m[3]);
 #pragma unroll
-        for (int job = 0; job < 8 / NW; ++job) {
-          const int sb = (wave + NW * job) & 3, pp = (wave + NW * job) >> 2;
-          pf4 d[2] = {zero, zero};
-#pragma unroll
-          for (int kk = 0; kk < NK; ++kk) {
-            const pu4 b = lds_row_operand<U>(sB[k], 16 * sb + l16, kk, g4);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) d[e] = mma(lds_tr_operand8<8>(sG, kk, 2 * pp + e, l16, g4), b, d[e]);
-          }
-          const float pf = sc.phi[16 * sb + l16] * sc.f[16 * sb + l16];
-          d[0] *= pf;
-          d[1] *= pf;
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk) {
-            if (sb >= 2 && kk == 0) continue;   // no step of the first half follows one of the second
-            const pu4 m = sM[m_slot(sb, kk)][lane];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) d[e] = mma(lds_tr_operand<8>(sY[k], kk, 2 * pp + e, l16, g4), m, d[e]);
-          }
-          const float dr = sDirect[sb][l16];
-          const pu4 yv = lds_u4(sY[k], unit_at<8>(16 * sb + l16, 4 * pp + g4));
-          const pu4 o = {pack_bf16(fmaf(dr, lo_f32(yv[0]), d[0][0]), fmaf(dr, hi_f32(yv[0]), d[0][1])),
-                         pack_bf16(fmaf(dr, lo_f32(yv[1]), d[0][2]), fmaf(dr, hi_f32(yv[1]), d[0][3])),
-                         pack_bf16(fmaf(dr, lo_f32(yv[2]), d[1][0]), fmaf(dr, hi_f32(yv[2]), d[1][1])),
-                         pack_bf16(fmaf(dr, lo_f32(yv[3]), d[1][2]), fmaf(dr, hi_f32(yv[3]), d[1][3]))};
-          __builtin_amdgcn_raw_buffer_store_b128(
-              o, rdx, static_cast<int>(static_cast<uint32_t>(16 * sb + l16) * (static_cast<uint32_t>(a.dxs) * 2u) +
-                                       (32u * pp + 8u * g4) * 2u), 0, 0);
-        }
-      }
-      part_ends();
-      // ---- the steps' own gradients, by wave k
-      if (wave == k) {
-        const int tl = lane >> 4;
-        float row = 0.0f, col = 0.0f, u = 0.0f, v = 0.0f, e = 0.0f;
-#pragma unroll
-        for (int o = 0; o < 4; ++o) {
-          row += o <= tl ? sRow[tl * (tl + 1) / 2 + min(o, tl)][l16] : 0.0f;
-          const int tt = max(o, tl);
-          col += o >= tl ? sCol[tt * (tt + 1) / 2 + tl][l16] : 0.0f;
-        }
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          u += sU[w][lane];
-          v += sV[w][lane];
-          e += sE[w];
-        }
-        const float phi = sc.phi[lane];
-        u *= hw_exp2(sc.c[lane]);
-        v *= sc.f[lane];
-        const float dphi = col + sOwn[tl][l16] + v;
-        const float before = phi * v;
-        const float dl = wave_suffix(row - phi * col + u, lane) + (wave_prefix(before, lane) - before) +
-                         hw_exp2(sc.c[kChunk - 1]) * e;
-        const float e1 = delta * Ah;
-        const float decay = hw_exp2(la);
-        float dd = Ah * dl + (a.zoh ? decay * dphi : dphi);
-        if (a.softplus) dd *= sigmoid(u_in);
-        const int rows = rows_of(k);
-        if (lane < rows) {
-          Elem<uint16_t>::st(a.ddt, (first_of(k) + lane) * a.ddts + h, dd);
-          sum_a = delta * dl + (a.zoh ? zoh_slope(delta, e1, decay) * dphi : 0.0f);
-          sum_t = dd;
-        }
-        sum_d = lane < 4 ? sDiag[lane] : 0.0f;
-      }
-    };
-    if constexpr (KC == 2) {
-      const float fade0 = hw_exp2(sS[0].c[kChunk - 1]), fade1 = hw_exp2(sS[1].c[kChunk - 1]);
-      pf4 S1[NTW][4];
-#pragma unroll
-      for (int j = 0; j < NTW; ++j)
-#pragma unroll
-        for (int pt = 0; pt < 4; ++pt) S1[j][pt] = S[j][pt] * fade0;
-      advance(S1, sB[0], sX[0], [&](int k0) {
-        return *reinterpret_cast<const pf4*>(&sS[0].phi[k0]) * *reinterpret_cast<const pf4*>(&sS[0].f[k0]);
-      });
-      part_ends();
-      chunk(std::integral_constant<int, 1>{}, S1, G);
-      part_ends();
-#pragma unroll
-      for (int j = 0; j < NTW; ++j)
-#pragma unroll
-        for (int pt = 0; pt < 4; ++pt) G[j][pt] *= fade1;
-      advance(G, sC[1], sY[1], [&](int k0) {
-        const pf4 c = *reinterpret_cast<const pf4*>(&sS[1].c[k0]);
-        return pf4{hw_exp2(c[0]), hw_exp2(c[1]), hw_exp2(c[2]), hw_exp2(c[3])};
-      });
-      barrier_lds();   // M, G and the partial sums of the chunk behind are read
+      for (int c = 0; c < 4; ++c) row[c] = sum_row(row[c]);
+      if (l16 < 4) sRow[k][i][4 * g4 + l16] = (l16 & 2) ? ((l16 & 1) ? row[3] : row[2]) : ((l16 & 1) ? row[1] : row[0]);
+      col = sum_rows(col);
+      if (g4 == 0) sCol[k][i][l16] = col;
+    }
+    barrier_lds();   // M, G and the partial sums are there, and x is read
+    if (h + 1 < h_end) {
+      copy_head(sX[k], a.x, h + 1, a.xs, xrow);
+      load_states(h + 1);
     }
     part_ends();
-    chunk(std::integral_constant<int, 0>{}, S, G);
-    // ---- sums over a chunk's steps
-    if (wave < KC) {
+    // ---- dx: a pair of column tiles (32 p) of one tile of steps at a time
+#pragma unroll
+    for (int j = 0; j < kJobs; ++j) {
+      const int job = nt + CW * j;
+      if (job >= 8) break;
+      const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
+      const int sb = job & 3, pp = job >> 2;
+      pf4 d[2] = {zero, zero};
+#pragma unroll
+      for (int kk = 0; kk < NK; ++kk) {
+        const pu4 b = lds_row_operand<U>(Bk, 16 * sb + l16, kk, g4);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) d[e] = mma(lds_tr_operand8<8>(sG[k], kk, 2 * pp + e, l16, g4), b, d[e]);
+      }
+      const float pf = sc.pf[16 * sb + l16];
+      d[0] *= pf;
+      d[1] *= pf;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        if (sb >= 2 && kk == 0) continue;   // no step of the first half follows one of the second
+        const pu4 m = sM[k][m_slot(sb, kk)][l];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) d[e] = mma(lds_tr_operand<8>(Yk, kk, 2 * pp + e, l16, g4), m, d[e]);
+      }
+      const float dr = sDirect[k][sb][l16];
+      const pu4 yv = lds_u4(Yk, unit_at<8>(16 * sb + l16, 4 * pp + g4));
+      const pu4 o = {pack_bf16(fmaf(dr, lo_f32(yv[0]), d[0][0]), fmaf(dr, hi_f32(yv[0]), d[0][1])),
+                     pack_bf16(fmaf(dr, lo_f32(yv[1]), d[0][2]), fmaf(dr, hi_f32(yv[1]), d[0][3])),
+                     pack_bf16(fmaf(dr, lo_f32(yv[2]), d[1][0]), fmaf(dr, hi_f32(yv[2]), d[1][1])),
+                     pack_bf16(fmaf(dr, lo_f32(yv[3]), d[1][2]), fmaf(dr, hi_f32(yv[3]), d[1][3]))};
+      __builtin_amdgcn_raw_buffer_store_b128(
+          o, chunk_rsrc(a.dx + int64_t(h) * kHead, t_first, a.dxs, rows, kHead),
+          static_cast<int>(static_cast<uint32_t>(16 * sb + l16) * (static_cast<uint32_t>(a.dxs) * 2u) +
+                           (32u * pp + 8u * g4) * 2u), 0, 0);
+    }
+    part_ends();
+    // ---- the steps' own gradients
+    if (nt == kScalarTile) {
+      const int lane = afresh(threadIdx.x) & 63, l16 = lane & 15, tl = lane >> 4;
+      float row = 0.0f, col = 0.0f, u = 0.0f, v = 0.0f, e = 0.0f;
+#pragma unroll
+      for (int o = 0; o < 4; ++o) {
+        row += o <= tl ? sRow[k][tl * (tl + 1) / 2 + min(o, tl)][l16] : 0.0f;
+        const int tt = max(o, tl);
+        col += o >= tl ? sCol[k][tt * (tt + 1) / 2 + tl][l16] : 0.0f;
+      }
+#pragma unroll
+      for (int w = 0; w < CW; ++w) {
+        u += sU[k * CW + w][lane];
+        v += sV[k * CW + w][lane];
+        e += sE[k * CW + w];
+      }
+      const float phi = sc.phi[lane];
+      u *= sc.e[lane];
+      v *= sc.f[lane];
+      const float dphi = col + sOwn[k][tl][l16] + v;
+      const float before = phi * v;
+      const float dl = wave_suffix(row - phi * col + u, lane) + (wave_prefix(before, lane) - before) + sc.e[kChunk - 1] * e;
+      const float delta = sc.delta[lane], decay = sc.decay[lane];
+      const float dd = (Ah * dl + (a.zoh ? decay * dphi : dphi)) * sc.slope[lane];
+      float sum_a = 0.0f, sum_t = 0.0f, sum_d = lane < 4 ? sDiag[k][lane] : 0.0f;
+      if (lane < rows) {
+        Elem<uint16_t>::st(a.ddt, (t_first + lane) * a.ddts + h, dd);
+        sum_a = delta * dl + (a.zoh ? zoh_slope(delta, delta * Ah, decay) * dphi : 0.0f);
+        sum_t = dd;
+      }
       sum_a = sum_wave(sum_a);
       sum_t = sum_wave(sum_t);
       sum_d = sum_wave(sum_d);
       if (lane == 0)
-        *reinterpret_cast<pf4*>(a.part_h + ((int64_t(number) * KC + wave) * a.H + h) * 4) =
-            pf4{sum_a, sum_t, sum_d, 0.0f};
+        *reinterpret_cast<pf4*>(a.part_h + ((int64_t(number) * KC + k) * a.H + h) * 4) = pf4{sum_a, sum_t, sum_d, 0.0f};
     }
   }
 
   // ---- the heads' K with B and C, and the sums over this workgroup's heads
+  barrier_lds();
+  const int l16 = lane & 15, g4 = lane >> 4;
+  uint16_t* sK = sX[k];   // K, row by row
 #pragma unroll
-  for (int k = 0; k < KC; ++k) {
-    barrier_lds();   // (the last readers of what is written now are done)
-    uint16_t* sK = sX[k];   // K, row by row
-#pragma unroll
-    for (int ti = 0; ti < kTiles; ++ti) {
-      const int i = wave + NW * ti;
-      if (i >= 10) break;
-      const int tb = tile_row(i), sb = i - tb * (tb + 1) / 2;
-      pf4 v = aK[k][ti];
-      if (sb == tb) {   // a step's own term is added in fp32
-        float own = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          own += l16 == 4 * g4 + c ? v[c] : 0.0f;
-          v[c] = l16 == 4 * g4 + c ? 0.0f : v[c];
-        }
-        own = sum_rows(own);
-        if (g4 == 0) sOwn[tb][l16] = own;
-      }
-      reinterpret_cast<pu2*>(&sM[m_slot(sb, tb >> 1)][lane])[tb & 1] = bf16x4(v[0], v[1], v[2], v[3]);
+  for (int ti = 0; ti < kTiles; ++ti) {
+    const int i = tile_of(ti);
+    if (i >= 10) break;
+    const int tb = tile_row(i), sb = i - tb * (tb + 1) / 2;
+    pf4 v = aK[ti];
+    if (sb == tb) {   // a step's own term is added in fp32
+      float own = 0.0f;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const int row = 16 * tb + 4 * g4 + c, byte = 2 * (l16 & 7);
-        char* at = reinterpret_cast<char*>(sK);
-        Elem<uint16_t>::st(reinterpret_cast<uint16_t*>(at + unit_at<8>(row, 2 * sb + (l16 >> 3)) + byte), 0, v[c]);
-        // (the tile right of an even diagonal tile belongs to the same operand)
-        if (sb == tb && (tb & 1) == 0)
-          *reinterpret_cast<uint16_t*>(at + unit_at<8>(row, 2 * (sb + 1) + (l16 >> 3)) + byte) = 0;
+        own += l16 == 4 * g4 + c ? v[c] : 0.0f;
+        v[c] = l16 == 4 * g4 + c ? 0.0f : v[c];
       }
+      own = sum_rows(own);
+      if (g4 == 0) sOwn[k][tb][l16] = own;
     }
-    barrier_lds();
+    reinterpret_cast<pu2*>(&sM[k][m_slot(sb, tb >> 1)][lane])[tb & 1] = bf16x4(v[0], v[1], v[2], v[3]);
 #pragma unroll
-    for (int j = 0; j < NTW; ++j) {
-      const int nt = NTW * wave + j;
+    for (int c = 0; c < 4; ++c) {
+      const int row = 16 * tb + 4 * g4 + c, byte = 2 * (l16 & 7);
+      char* at = reinterpret_cast<char*>(sK);
+      Elem<uint16_t>::st(reinterpret_cast<uint16_t*>(at + unit_at<8>(row, 2 * sb + (l16 >> 3)) + byte), 0, v[c]);
+      // (the tile right of an even diagonal tile belongs to the same operand)
+      if (sb == tb && (tb & 1) == 0)
+        *reinterpret_cast<uint16_t*>(at + unit_at<8>(row, 2 * (sb + 1) + (l16 >> 3)) + byte) = 0;
+    }
+  }
+  barrier_lds();
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        const pu4 bt = lds_tr_plain_operand<U, true>(sB[k], kk, nt, l16, g4);
-        const pu4 ct = lds_tr_plain_operand<U, false>(sC[k], kk, nt, l16, g4);
+  for (int kk = 0; kk < 2; ++kk) {
+    const pu4 bt = lds_tr_plain_operand<U, true>(Bk, kk, nt, l16, g4);
+    const pu4 ct = lds_tr_plain_operand<U, false>(Ck, kk, nt, l16, g4);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          if (kk <= b / 2) aC[k][j][b] = mma(bt, lds_row_operand<8>(sK, 16 * b + l16, kk, g4), aC[k][j][b]);
-          if (kk == 1 || b < 2) aB[k][j][b] = mma(ct, sM[m_slot(b, kk)][lane], aB[k][j][b]);
-        }
-      }
-      const int rows = rows_of(k);
+    for (int b = 0; b < 4; ++b) {
+      if (kk <= b / 2) aC[b] = mma(bt, lds_row_operand<8>(sK, 16 * b + l16, kk, g4), aC[b]);
+      if (kk == 1 || b < 2) aB[b] = mma(ct, sM[k][m_slot(b, kk)][lane], aB[b]);
+    }
+  }
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int t = 16 * b + l16;
-        const int64_t at = ((int64_t(split) * a.T + first_of(k) + t) * a.G + g) * N + 16 * nt + 4 * g4;
-        const float own = sOwn[b][l16];
-        const int place = unit_at<U>(t, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1);
-        const pu2 cw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(sC[k]) + place);
-        const pu2 bw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(sB[k]) + place);
-        if (t < rows) {
-          *reinterpret_cast<pf4*>(a.part_b + at) =
-              aB[k][j][b] + own * pf4{lo_f32(cw[0]), hi_f32(cw[0]), lo_f32(cw[1]), hi_f32(cw[1])};
-          *reinterpret_cast<pf4*>(a.part_c + at) =
-              aC[k][j][b] + own * pf4{lo_f32(bw[0]), hi_f32(bw[0]), lo_f32(bw[1]), hi_f32(bw[1])};
-        }
-      }
+  for (int b = 0; b < 4; ++b) {
+    const int t = 16 * b + l16;
+    const int64_t at = ((int64_t(split) * a.T + t_first + t) * a.G + g) * N + 16 * nt + 4 * g4;
+    const float own = sOwn[k][b][l16];
+    const int place = unit_at<U>(t, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1);
+    const pu2 cw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(Ck) + place);
+    const pu2 bw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(Bk) + place);
+    if (t < rows) {
+      *reinterpret_cast<pf4*>(a.part_b + at) =
+          aB[b] + own * pf4{lo_f32(cw[0]), hi_f32(cw[0]), lo_f32(cw[1]), hi_f32(cw[1])};
+      *reinterpret_cast<pf4*>(a.part_c + at) =
+          aC[b] + own * pf4{lo_f32(bw[0]), hi_f32(bw[0]), lo_f32(bw[1]), hi_f32(bw[1])};
     }
   }
 }
