@@ -373,7 +373,7 @@ ssm_status ssm_ssd_packed_fwd(const ssm_ssd_packed_params* p, const void* x, con
                               size_t workspace_bytes, void* stream);
 
 /* Bytes of device workspace ssm_ssd_packed_bwd needs (0 for invalid parameters).  Most of it are the states and adjoint
- * states every 128 steps (64 for dstate 256): 512 * nheads * dstate bytes for each of about ntokens / 128 + nseqs. */
+ * states of every chunk of 64 steps: 512 * nheads * dstate bytes for each of about ntokens / 64 + nseqs chunks. */
 size_t ssm_ssd_packed_bwd_workspace_bytes(const ssm_ssd_packed_params* p);
 
 /*

@@ -255,8 +255,7 @@ struct PackedPlan {
   int64_t nseg;   // numbers of segments
   bool split;     // whether a sequence can have more than one
 };
-// `multiple`: segments are whole numbers of that many chunks.
-PackedPlan packed_plan(const ssm_ssd_packed_params* p, int multiple);
+PackedPlan packed_plan(const ssm_ssd_packed_params* p);
 
 // A walk over the states of packed sequences, chunk by chunk and from each sequence's first state (ssm_packed_states.hip):
 // forward, S <- exp(c_63) S + sum_s (phi_s exp(c_63 - c_s) v_s) k_s^T with v = x, k = B, or in reverse order,
@@ -274,9 +273,9 @@ struct StatesArgs {
   float* last;           // [seqs][H][64][N] or null: the state behind the whole walk of a sequence
   float* ws_state;       // [nseg][H][64][N]: state entering each segment (where a sequence has more than one)
   float* ws_decay;       // [nseg][H]
-  float* save;           // [numbers][H][64][N] or null: state entering each group of `group` chunks
+  uint16_t* save;        // [chunk numbers][H][2][N][64] bf16 or null: state entering each chunk, in two parts, transposed
   int64_t vs, ks, dts, nslots;
-  int T, S, H, G, hpg, hblocks, cps, nseg, nwork, group;
+  int T, S, H, G, hpg, hblocks, cps, nseg, nwork;
   int softplus, zoh;
 };
 // Brings ws_state up to date where a sequence can have several segments (split), and then, with save or last, walks all.

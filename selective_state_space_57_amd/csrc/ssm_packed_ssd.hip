@@ -382,7 +382,7 @@ ssm_status launch_step(const PSsdArgs& a, hipStream_t st) {
 }
 
 size_t fwd_workspace(const ssm_ssd_packed_params* p) {
-  const PackedPlan pl = packed_plan(p, 1);
+  const PackedPlan pl = packed_plan(p);
   if (!pl.split) return 0;
   return up256(size_t(pl.nseg) * p->nheads * kHead * p->dstate * 4) + up256(size_t(pl.nseg) * p->nheads * 4);
 }
@@ -441,14 +441,14 @@ ssm_status check_packed_ssd(const ssm_ssd_packed_params* p, bool step) {
   }
   if (step && p->ntokens * p->nheads >= (int64_t(1) << 29)) return fail(SSM_ERR_SHAPE, "too many rows for one launch");
   if (!step) {
-    const PackedPlan pl = packed_plan(p, 1);
+    const PackedPlan pl = packed_plan(p);
     if (pl.nseg * p->ngroups * pl.hblocks >= (int64_t(1) << 31) - 8) return fail(SSM_ERR_SHAPE, "too many work items");
     if (p->nheads * kHead * p->dstate / 1024 >= 65535) return fail(SSM_ERR_SHAPE, "nheads is too large");
   }
   return SSM_OK;
 }
 
-PackedPlan packed_plan(const ssm_ssd_packed_params* p, int multiple) {
+PackedPlan packed_plan(const ssm_ssd_packed_params* p) {
   PackedPlan pl{};
   const int64_t hpg = p->nheads / p->ngroups;
   pl.hblocks = static_cast<int>((hpg + kWalkHeads - 1) / kWalkHeads);
@@ -464,7 +464,6 @@ PackedPlan packed_plan(const ssm_ssd_packed_params* p, int multiple) {
     if (cps < 4) cps = 4;
   }
   if (cps > longest) cps = longest;
-  cps = (cps + multiple - 1) / multiple * multiple;
   pl.cps = static_cast<int>(cps);
   pl.split = longest > cps;
   pl.nseg = piece_numbers(p->nseqs, p->ntokens, cps * kChunk);
@@ -497,7 +496,7 @@ extern "C" ssm_status ssm_ssd_packed_fwd(const ssm_ssd_packed_params* p, const v
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
     return fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes (16-byte aligned) needed, got %zu at %p", need,
                 workspace_bytes, workspace);
-  const PackedPlan pl = packed_plan(p, 1);
+  const PackedPlan pl = packed_plan(p);
   a.x = static_cast<const uint16_t*>(x);
   a.dt = static_cast<const uint16_t*>(dt);
   a.B = static_cast<const uint16_t*>(B);

@@ -13,15 +13,16 @@
 // Every sum in dl_r has the decays of what it stands for in it, so nothing large cancels: only the row and column sums
 // of W do, and those are sums of the same fp32 numbers.
 //
-// Two walks (ssm_packed_states.hip) leave S and G at the boundaries of groups of chunks (two chunks; one for N = 256);
-// then a workgroup takes a group of chunks and runs over heads one after the other.  A wave has one chunk and 16 of the N
-// columns of the states, for every head: the sums of dB and dC over heads add up in its registers, and the state or
-// adjoint inside the group is recomputed from the boundary's.  K is summed over heads in registers as well, and
-// multiplied with B and C once at the end.  What a head needs across waves (dx, and the sums over n in u, v and <G, S>)
-// goes through LDS.  The next head's states and x are on their way while this head's dx is computed.
+// Two walks (ssm_packed_states.hip) leave S and G of every chunk, split into two bf16 parts as the products want them;
+// then a workgroup takes a chunk and runs over heads one after the other.  A wave has 16 of the N columns of the states,
+// for every head: the sums of dB and dC over heads add up in its registers.  K is summed over heads in registers as well,
+// and multiplied with B and C once at the end.  What a head needs across waves (dx, and the sums over n in u, v and
+// <G, S>) goes through LDS.  The next head's states and x are on their way while this head's dx is computed.
+// Two workgroups share a CU (N <= 128), so that one's barriers and loads run beside the other's products: with chunks of
+// 128 steps to a workgroup, which halve the saved states but recompute them in between, one filled the LDS and took
+// 790 us instead of xxx for the 2.7B layer at 16384 tokens.
 //
-// Precision: fp32 accumulation; the states and the weighted B and C of their recomputation are split into two bf16 parts
-// (2^-18 relative), so that u, v and <G, S>, and with them dDelta and dA, are good to fp32 quality.  G in dx, M = L Z phi
+// Precision: fp32 accumulation; the states are split into two bf16 parts (2^-18 relative), so that u, v and <G, S>, and with them dDelta and dA, are good to fp32 quality.  G in dx, M = L Z phi
 // and the head sum K (both but for s = t, which is added in fp32) are rounded once to bf16: they only reach dx, dB and
 // dC, which are bf16 themselves.
 #include "packed_ssd.hpp"
@@ -39,15 +40,15 @@ struct BwdArgs {
   const float* A;
   const float* Dskip;
   const int32_t* cu;
-  const float* S;      // [numbers][H][64][N]: state entering each chunk group
-  const float* Gs;     // [numbers][H][64][N]: adjoint behind it
+  const uint16_t* S;   // [numbers][H][2][N][64]: state entering each chunk, high and low parts
+  const uint16_t* Gs;  // the adjoint behind it
   uint16_t* dx;
   uint16_t* ddt;
   uint16_t* dB;
   uint16_t* dC;
   float* part_b;       // [splits][T][G N]
   float* part_c;
-  float* part_h;       // [numbers][chunks of a group][H][4]: sums of Delta dl (+ phi's share), ddt, dy . x
+  float* part_h;       // [numbers][H][4]: sums of Delta dl (+ phi's share), ddt, dy . x
   float* dA;
   float* ddt_bias;
   float* dD;
@@ -55,15 +56,6 @@ struct BwdArgs {
   int T, S_, H, G, hpg, splits, hps, numbers, nwork;
   int softplus, zoh;
 };
-
-// sizes by state width: chunks of a group, waves of a chunk, waves
-template <int N>
-struct Shape {
-  static constexpr int KC = N == 256 ? 1 : 2;
-  static constexpr int CW = N / 16;
-  static constexpr int NW = KC * CW;
-};
-int group_of(int64_t dstate) { return dstate == 256 ? 1 : 2; }
 
 struct alignas(16) ChunkScalars {
   float c[kChunk], phi[kChunk];   // c_t (base 2), phi_t
@@ -92,60 +84,48 @@ __device__ __forceinline__ float zoh_slope(float delta, float e, float a) {
 }
 
 template <int N>
-__global__ void __launch_bounds__(Shape<N>::NW * 64) __attribute__((amdgpu_waves_per_eu(Shape<N>::NW / 4, 4)))
+__global__ void __launch_bounds__(N * 4) __attribute__((amdgpu_waves_per_eu(N == 64 ? 3 : 4)))
 packed_ssd_bwd_kernel(BwdArgs a) {
-  constexpr int NW = Shape<N>::NW, CW = Shape<N>::CW, KC = Shape<N>::KC;
+  constexpr int NW = N / 16;
   constexpr int U = N / 8, NK = N / 32;
-  constexpr int kTiles = (10 + CW - 1) / CW;   // tiles on and below the diagonal that a wave owns
-  constexpr int kJobs = CW < 8 ? 8 / CW : 1;   // pieces of dx a wave computes
-  __shared__ alignas(16) uint16_t sB[KC][kChunk * N], sC[KC][kChunk * N];
-  __shared__ alignas(16) uint16_t sX[KC][kChunk * kHead], sY[KC][kChunk * kHead];   // x and dy of the head
-  __shared__ pu4 sM[KC][6][64];                        // M, operands over t
-  __shared__ alignas(16) uint16_t sG[KC][N * kHead];   // G, transposed
-  __shared__ ChunkScalars sS[KC];
+  constexpr int kTiles = (10 + NW - 1) / NW;   // tiles on and below the diagonal that a wave owns
+  constexpr int kJobs = NW < 8 ? 8 / NW : 1;   // pieces of dx a wave computes
+  __shared__ alignas(16) uint16_t Bk[kChunk * N], Ck[kChunk * N];
+  __shared__ alignas(16) uint16_t Xk[kChunk * kHead], Yk[kChunk * kHead];   // x and dy of the head
+  __shared__ pu4 sM[6][64];                           // M, operands over t
+  __shared__ alignas(16) uint16_t sG[N * kHead];       // G, transposed
+  __shared__ ChunkScalars sc;
   __shared__ float sU[NW][kChunk], sV[NW][kChunk], sE[NW];
-  __shared__ float sRow[KC][10][16], sCol[KC][10][16], sOwn[KC][4][16], sDirect[KC][4][16], sDiag[KC][4];
+  __shared__ float sRow[10][16], sCol[10][16], sOwn[4][16], sDirect[4][16], sDiag[4];
 
   const int item = xcd_item();
   if (item >= a.nwork) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int k = wave / CW, nt = wave % CW;   // chunk and n-tile of the wave
+  const int nt = wave;   // n-tile of the wave
   const int split = item % a.splits;
   const int g = item / a.splits % a.G;
   const int number = item / (a.splits * a.G);
   const int h_begin = g * a.hpg + split * a.hps, h_end = min(h_begin + a.hps, (g + 1) * a.hpg);
-  Piece grp;
-  const bool found = find_piece(a.cu, a.S_, a.T, KC * kChunk, number, grp) && grp.end > grp.begin;
-  if (!found) {   // a number without chunks adds nothing to the sums over all of them
+  Piece ck;
+  if (!find_piece(a.cu, a.S_, a.T, kChunk, number, ck) || ck.end <= ck.begin) {
+    // a number without a chunk adds nothing to the sums over all of them
     for (int h = h_begin + tid; h < h_end; h += NW * 64)
-#pragma unroll
-      for (int i = 0; i < KC; ++i)
-        *reinterpret_cast<pf4*>(a.part_h + ((int64_t(number) * KC + i) * a.H + h) * 4) = pf4{0.0f, 0.0f, 0.0f, 0.0f};
+      *reinterpret_cast<pf4*>(a.part_h + (int64_t(number) * a.H + h) * 4) = pf4{0.0f, 0.0f, 0.0f, 0.0f};
     return;
   }
-  const int t_begin = grp.begin + grp.index * KC * kChunk;
-  const int t_end = min(grp.end, t_begin + KC * kChunk);
-  auto rows_of = [&](int i) { return min(max(t_end - (t_begin + i * kChunk), 0), kChunk); };
-  auto first_of = [&](int i) -> int64_t { return rows_of(i) ? t_begin + int64_t(i) * kChunk : t_begin; };
-  const int rows = rows_of(k);
-  const int64_t t_first = first_of(k);
-  // the tiles of this wave: tile_of(0) .. ; those of two chunks fall to different SIMDs
-  auto tile_of = [&](int ti) { return ((nt + CW - 2 * k) % CW) + CW * ti; };
+  const int64_t t_first = ck.begin + ck.index * kChunk;
+  const int rows = min(ck.end - static_cast<int>(t_first), kChunk);
   const pf4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  const uint16_t* Bk = sB[k];
-  const uint16_t* Ck = sC[k];
-  const uint16_t* Xk = sX[k];
-  const uint16_t* Yk = sY[k];
 
   // B and C of the group stay for all heads, and so does C B^T: rows t, columns s
   {
     const uint32_t brow = static_cast<uint32_t>(a.bs) * 2u, crow = static_cast<uint32_t>(a.cs) * 2u;
-    copy_rows<U, CW>(sB[k], chunk_rsrc(a.B + int64_t(g) * N, t_first, a.bs, rows, N), nt, lane, brow);
-    copy_rows<U, CW>(sC[k], chunk_rsrc(a.C + int64_t(g) * N, t_first, a.cs, rows, N), nt, lane, crow);
+    copy_rows<U, NW>(Bk, chunk_rsrc(a.B + int64_t(g) * N, t_first, a.bs, rows, N), nt, lane, brow);
+    copy_rows<U, NW>(Ck, chunk_rsrc(a.C + int64_t(g) * N, t_first, a.cs, rows, N), nt, lane, crow);
     if (nt == 0) {   // the halves of operands that lie above the diagonal stay zero
-      reinterpret_cast<pu2*>(&sM[k][m_slot(1, 0)][lane])[0] = pu2{0u, 0u};
-      reinterpret_cast<pu2*>(&sM[k][m_slot(3, 1)][lane])[0] = pu2{0u, 0u};
+      reinterpret_cast<pu2*>(&sM[m_slot(1, 0)][lane])[0] = pu2{0u, 0u};
+      reinterpret_cast<pu2*>(&sM[m_slot(3, 1)][lane])[0] = pu2{0u, 0u};
     }
     wait_memory();
     barrier_lds();
@@ -161,56 +141,32 @@ packed_ssd_bwd_kernel(BwdArgs a) {
   const uint32_t xrow = static_cast<uint32_t>(a.xs) * 2u, yrow = static_cast<uint32_t>(a.dys) * 2u;
   auto copy_head = [&](uint16_t* dst, const uint16_t* src, int h, int64_t stride, uint32_t row_bytes)
                        __attribute__((always_inline)) {
-    copy_rows<8, CW>(dst, chunk_rsrc(src + int64_t(h) * kHead, t_first, stride, rows, kHead), nt, afresh(lane), row_bytes);
+    copy_rows<8, NW>(dst, chunk_rsrc(src + int64_t(h) * kHead, t_first, stride, rows, kHead), nt, afresh(lane), row_bytes);
   };
-  // state entering the group and adjoint behind it; p = 32 (pt/2) + 8 g4 + 4 (pt%2) + c, n = 16 nt + l16
-  pf4 S[4], G[4];
+  // operands over p: n = 16 nt + l16, p = 32 kk + 8 g4 ..
+  pu4 sh[2], sl[2], gh[2], gl[2];
   auto load_states = [&](int h) __attribute__((always_inline)) {
-    const auto rs = make_rsrc(a.S + (int64_t(number) * a.H + h) * head_size, head_size);
-    const auto rg = make_rsrc(a.Gs + (int64_t(number) * a.H + h) * head_size, head_size);
+    const auto rs = make_rsrc(a.S + (int64_t(number) * a.H + h) * 2 * head_size, 2 * head_size);
+    const auto rg = make_rsrc(a.Gs + (int64_t(number) * a.H + h) * 2 * head_size, 2 * head_size);
     const int l = afresh(lane);
-    const int at = (8 * (l >> 4) * N + 16 * nt + (l & 15)) * 4;
-#pragma unroll
-    for (int pt = 0; pt < 4; ++pt)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int row = (32 * (pt >> 1) + 4 * (pt & 1) + c) * N * 4;
-        S[pt][c] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, row, 0));
-        G[pt][c] = __int_as_float(__builtin_amdgcn_raw_buffer_load_b32(rg, at, row, 0));
-      }
-  };
-  // D += sum over a chunk's steps of v (weight k)^T: one step of the walk, for this wave's columns n.  The weights go to k,
-  // of which a wave has 16 columns, and not to v, of which it needs all 64.
-  auto advance = [&](pf4 (&D)[4], const uint16_t* K, const uint16_t* V, const float* weight) __attribute__((always_inline)) {
-    const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
+    const int at = ((16 * nt + (l & 15)) * kHead + 8 * (l >> 4)) * 2;
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
-      pu2 hi[2], lo[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int k0 = 32 * kk + 16 * e + 4 * g4;
-        const pu2 v = lds_tr_plain<U>(K, k0, nt, l16);
-        const pf4 w = *reinterpret_cast<const pf4*>(&weight[k0]);
-        split_bf16x4(lo_f32(v[0]) * w[0], hi_f32(v[0]) * w[1], lo_f32(v[1]) * w[2], hi_f32(v[1]) * w[3], hi[e], lo[e]);
-      }
-      const pu4 kh = join(hi[0], hi[1]), kl = join(lo[0], lo[1]);
-#pragma unroll
-      for (int pt = 0; pt < 4; ++pt) {
-        const pu4 v = lds_tr_operand<8>(V, kk, pt, l16, g4);
-        D[pt] = mma(v, kh, D[pt]);
-        D[pt] = mma(v, kl, D[pt]);
-      }
+      sh[kk] = __builtin_bit_cast(pu4, __builtin_amdgcn_raw_buffer_load_b128(rs, at, 64 * kk, 0));
+      sl[kk] = __builtin_bit_cast(pu4, __builtin_amdgcn_raw_buffer_load_b128(rs, at, 64 * kk + N * kHead * 2, 0));
+      gh[kk] = __builtin_bit_cast(pu4, __builtin_amdgcn_raw_buffer_load_b128(rg, at, 64 * kk, 0));
+      gl[kk] = __builtin_bit_cast(pu4, __builtin_amdgcn_raw_buffer_load_b128(rg, at, 64 * kk + N * kHead * 2, 0));
     }
   };
 
-  copy_head(sX[k], a.x, h_begin, a.xs, xrow);
+  copy_head(Xk, a.x, h_begin, a.xs, xrow);
   load_states(h_begin);
   for (int h = h_begin; h < h_end; ++h) {
     const float Ah = a.A[h];
     const float Dh = a.Dskip ? a.Dskip[h] : 0.0f;
     barrier_lds();   // everyone is done with the head before
-    copy_head(sY[k], a.dy, h, a.dys, yrow);
-    constexpr int kScalarTile = CW - 1;   // the wave of a chunk that works on its steps
+    copy_head(Yk, a.dy, h, a.dys, yrow);
+    constexpr int kScalarTile = NW - 1;   // the wave of a chunk that works on its steps
     if (nt == kScalarTile) {
       const int lane = afresh(threadIdx.x) & 63;
       const float dtv = lo_f32(a.dt[(lane < rows ? t_first + lane : t_first) * a.dts + h]);
@@ -218,55 +174,26 @@ packed_ssd_bwd_kernel(BwdArgs a) {
       float delta, phi, la;
       step_scalars(dtv, bias, Ah, a.softplus, a.zoh, lane < rows, delta, phi, la);
       const float c = wave_prefix(la, lane), f = hw_exp2(wave_suffix(la, lane) - la);
-      sS[k].c[lane] = c;
-      sS[k].phi[lane] = phi;
-      sS[k].e[lane] = hw_exp2(c);
-      sS[k].f[lane] = f;
-      sS[k].pf[lane] = phi * f;
-      sS[k].delta[lane] = delta;
-      sS[k].decay[lane] = hw_exp2(la);
-      sS[k].slope[lane] = a.softplus ? sigmoid(dtv + bias) : 1.0f;
+      sc.c[lane] = c;
+      sc.phi[lane] = phi;
+      sc.e[lane] = hw_exp2(c);
+      sc.f[lane] = f;
+      sc.pf[lane] = phi * f;
+      sc.delta[lane] = delta;
+      sc.decay[lane] = hw_exp2(la);
+      sc.slope[lane] = a.softplus ? sigmoid(dtv + bias) : 1.0f;
     }
     wait_memory();
     barrier_lds();   // x, dy and the scalars are there
-    const ChunkScalars& sc = sS[k];
-    if constexpr (KC == 2) {   // the state behind the first chunk, the adjoint before the last
-      if (k == 1) {
-        const float fade = sS[0].e[kChunk - 1];
-#pragma unroll
-        for (int pt = 0; pt < 4; ++pt) S[pt] *= fade;
-        advance(S, sB[0], sX[0], sS[0].pf);
-      } else {
-        const float fade = sS[KC - 1].e[kChunk - 1];
-#pragma unroll
-        for (int pt = 0; pt < 4; ++pt) G[pt] *= fade;
-        advance(G, sC[KC - 1], sY[KC - 1], sS[KC - 1].e);
-      }
-    }
     part_ends();
     {
       // ---- products with the states: q^T = S^T dy^T, r^T = G^T x^T, <G, S>
       const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
-      pu4 sh[2], sl[2], gh[2], gl[2];
       pf4 ge = zero;
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
-        pu2 h0, l0, h1, l1;
-        split_bf16x4(S[2 * kk][0], S[2 * kk][1], S[2 * kk][2], S[2 * kk][3], h0, l0);
-        split_bf16x4(S[2 * kk + 1][0], S[2 * kk + 1][1], S[2 * kk + 1][2], S[2 * kk + 1][3], h1, l1);
-        sh[kk] = join(h0, h1);
-        sl[kk] = join(l0, l1);
-      }
-      part_ends();
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        pu2 h0, l0, h1, l1;
-        split_bf16x4(G[2 * kk][0], G[2 * kk][1], G[2 * kk][2], G[2 * kk][3], h0, l0);
-        split_bf16x4(G[2 * kk + 1][0], G[2 * kk + 1][1], G[2 * kk + 1][2], G[2 * kk + 1][3], h1, l1);
-        gh[kk] = join(h0, h1);
-        gl[kk] = join(l0, l1);
         // the row of n = 16 nt + l16 holds G[.][n]
-        *reinterpret_cast<pu4*>(reinterpret_cast<char*>(sG[k]) + unit_at<8>(16 * nt + l16, 4 * kk + g4)) = gh[kk];
+        *reinterpret_cast<pu4*>(reinterpret_cast<char*>(sG) + unit_at<8>(16 * nt + l16, 4 * kk + g4)) = gh[kk];
         ge = mma(sh[kk], gh[kk], ge);
         ge = mma(sh[kk], gl[kk], ge);
         ge = mma(sl[kk], gh[kk], ge);
@@ -307,7 +234,7 @@ packed_ssd_bwd_kernel(BwdArgs a) {
     // ---- tiles of L, X, Z
 #pragma unroll
     for (int ti = 0; ti < kTiles; ++ti) {
-      const int i = tile_of(ti);
+      const int i = nt + NW * ti;
       if (i >= 10) break;
       const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
       const int tb = tile_row(i), sb = i - tb * (tb + 1) / 2;
@@ -356,28 +283,28 @@ packed_ssd_bwd_kernel(BwdArgs a) {
         direct = sum_rows(direct);
         diag = sum_wave(diag);
         if (g4 == 0) {
-          sOwn[k][tb][l16] = own;
-          sDirect[k][tb][l16] = direct + Dh;
+          sOwn[tb][l16] = own;
+          sDirect[tb][l16] = direct + Dh;
         }
-        if (l == 0) sDiag[k][tb] = diag;
+        if (l == 0) sDiag[tb] = diag;
       }
-      reinterpret_cast<pu2*>(&sM[k][m_slot(sb, tb >> 1)][l])[tb & 1] = bf16x4(m[0], m[1], m[2], m[3]);
+      reinterpret_cast<pu2*>(&sM[m_slot(sb, tb >> 1)][l])[tb & 1] = bf16x4(m[0], m[1], m[2], m[3]);
 #pragma unroll
       for (int c = 0; c < 4; ++c) row[c] = sum_row(row[c]);
-      if (l16 < 4) sRow[k][i][4 * g4 + l16] = (l16 & 2) ? ((l16 & 1) ? row[3] : row[2]) : ((l16 & 1) ? row[1] : row[0]);
+      if (l16 < 4) sRow[i][4 * g4 + l16] = (l16 & 2) ? ((l16 & 1) ? row[3] : row[2]) : ((l16 & 1) ? row[1] : row[0]);
       col = sum_rows(col);
-      if (g4 == 0) sCol[k][i][l16] = col;
+      if (g4 == 0) sCol[i][l16] = col;
     }
     barrier_lds();   // M, G and the partial sums are there, and x is read
     if (h + 1 < h_end) {
-      copy_head(sX[k], a.x, h + 1, a.xs, xrow);
+      copy_head(Xk, a.x, h + 1, a.xs, xrow);
       load_states(h + 1);
     }
     part_ends();
     // ---- dx: a pair of column tiles (32 p) of one tile of steps at a time
 #pragma unroll
     for (int j = 0; j < kJobs; ++j) {
-      const int job = nt + CW * j;
+      const int job = nt + NW * j;
       if (job >= 8) break;
       const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
       const int sb = job & 3, pp = job >> 2;
@@ -386,7 +313,7 @@ packed_ssd_bwd_kernel(BwdArgs a) {
       for (int kk = 0; kk < NK; ++kk) {
         const pu4 b = lds_row_operand<U>(Bk, 16 * sb + l16, kk, g4);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) d[e] = mma(lds_tr_operand8<8>(sG[k], kk, 2 * pp + e, l16, g4), b, d[e]);
+        for (int e = 0; e < 2; ++e) d[e] = mma(lds_tr_operand8<8>(sG, kk, 2 * pp + e, l16, g4), b, d[e]);
       }
       const float pf = sc.pf[16 * sb + l16];
       d[0] *= pf;
@@ -394,11 +321,11 @@ packed_ssd_bwd_kernel(BwdArgs a) {
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) {
         if (sb >= 2 && kk == 0) continue;   // no step of the first half follows one of the second
-        const pu4 m = sM[k][m_slot(sb, kk)][l];
+        const pu4 m = sM[m_slot(sb, kk)][l];
 #pragma unroll
         for (int e = 0; e < 2; ++e) d[e] = mma(lds_tr_operand<8>(Yk, kk, 2 * pp + e, l16, g4), m, d[e]);
       }
-      const float dr = sDirect[k][sb][l16];
+      const float dr = sDirect[sb][l16];
       const pu4 yv = lds_u4(Yk, unit_at<8>(16 * sb + l16, 4 * pp + g4));
       const pu4 o = {pack_bf16(fmaf(dr, lo_f32(yv[0]), d[0][0]), fmaf(dr, hi_f32(yv[0]), d[0][1])),
                      pack_bf16(fmaf(dr, lo_f32(yv[1]), d[0][2]), fmaf(dr, hi_f32(yv[1]), d[0][3])),
@@ -416,25 +343,25 @@ packed_ssd_bwd_kernel(BwdArgs a) {
       float row = 0.0f, col = 0.0f, u = 0.0f, v = 0.0f, e = 0.0f;
 #pragma unroll
       for (int o = 0; o < 4; ++o) {
-        row += o <= tl ? sRow[k][tl * (tl + 1) / 2 + min(o, tl)][l16] : 0.0f;
+        row += o <= tl ? sRow[tl * (tl + 1) / 2 + min(o, tl)][l16] : 0.0f;
         const int tt = max(o, tl);
-        col += o >= tl ? sCol[k][tt * (tt + 1) / 2 + tl][l16] : 0.0f;
+        col += o >= tl ? sCol[tt * (tt + 1) / 2 + tl][l16] : 0.0f;
       }
 #pragma unroll
-      for (int w = 0; w < CW; ++w) {
-        u += sU[k * CW + w][lane];
-        v += sV[k * CW + w][lane];
-        e += sE[k * CW + w];
+      for (int w = 0; w < NW; ++w) {
+        u += sU[w][lane];
+        v += sV[w][lane];
+        e += sE[w];
       }
       const float phi = sc.phi[lane];
       u *= sc.e[lane];
       v *= sc.f[lane];
-      const float dphi = col + sOwn[k][tl][l16] + v;
+      const float dphi = col + sOwn[tl][l16] + v;
       const float before = phi * v;
       const float dl = wave_suffix(row - phi * col + u, lane) + (wave_prefix(before, lane) - before) + sc.e[kChunk - 1] * e;
       const float delta = sc.delta[lane], decay = sc.decay[lane];
       const float dd = (Ah * dl + (a.zoh ? decay * dphi : dphi)) * sc.slope[lane];
-      float sum_a = 0.0f, sum_t = 0.0f, sum_d = lane < 4 ? sDiag[k][lane] : 0.0f;
+      float sum_a = 0.0f, sum_t = 0.0f, sum_d = lane < 4 ? sDiag[lane] : 0.0f;
       if (lane < rows) {
         Elem<uint16_t>::st(a.ddt, (t_first + lane) * a.ddts + h, dd);
         sum_a = delta * dl + (a.zoh ? zoh_slope(delta, delta * Ah, decay) * dphi : 0.0f);
@@ -444,17 +371,17 @@ packed_ssd_bwd_kernel(BwdArgs a) {
       sum_t = sum_wave(sum_t);
       sum_d = sum_wave(sum_d);
       if (lane == 0)
-        *reinterpret_cast<pf4*>(a.part_h + ((int64_t(number) * KC + k) * a.H + h) * 4) = pf4{sum_a, sum_t, sum_d, 0.0f};
+        *reinterpret_cast<pf4*>(a.part_h + (int64_t(number) * a.H + h) * 4) = pf4{sum_a, sum_t, sum_d, 0.0f};
     }
   }
 
   // ---- the heads' K with B and C, and the sums over this workgroup's heads
   barrier_lds();
   const int l16 = lane & 15, g4 = lane >> 4;
-  uint16_t* sK = sX[k];   // K, row by row
+  uint16_t* sK = Xk;   // K, row by row
 #pragma unroll
   for (int ti = 0; ti < kTiles; ++ti) {
-    const int i = tile_of(ti);
+    const int i = nt + NW * ti;
     if (i >= 10) break;
     const int tb = tile_row(i), sb = i - tb * (tb + 1) / 2;
     pf4 v = aK[ti];
@@ -466,9 +393,9 @@ packed_ssd_bwd_kernel(BwdArgs a) {
         v[c] = l16 == 4 * g4 + c ? 0.0f : v[c];
       }
       own = sum_rows(own);
-      if (g4 == 0) sOwn[k][tb][l16] = own;
+      if (g4 == 0) sOwn[tb][l16] = own;
     }
-    reinterpret_cast<pu2*>(&sM[k][m_slot(sb, tb >> 1)][lane])[tb & 1] = bf16x4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<pu2*>(&sM[m_slot(sb, tb >> 1)][lane])[tb & 1] = bf16x4(v[0], v[1], v[2], v[3]);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const int row = 16 * tb + 4 * g4 + c, byte = 2 * (l16 & 7);
@@ -487,14 +414,14 @@ packed_ssd_bwd_kernel(BwdArgs a) {
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       if (kk <= b / 2) aC[b] = mma(bt, lds_row_operand<8>(sK, 16 * b + l16, kk, g4), aC[b]);
-      if (kk == 1 || b < 2) aB[b] = mma(ct, sM[k][m_slot(b, kk)][lane], aB[b]);
+      if (kk == 1 || b < 2) aB[b] = mma(ct, sM[m_slot(b, kk)][lane], aB[b]);
     }
   }
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     const int t = 16 * b + l16;
     const int64_t at = ((int64_t(split) * a.T + t_first + t) * a.G + g) * N + 16 * nt + 4 * g4;
-    const float own = sOwn[k][b][l16];
+    const float own = sOwn[b][l16];
     const int place = unit_at<U>(t, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1);
     const pu2 cw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(Ck) + place);
     const pu2 bw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(Bk) + place);
@@ -542,18 +469,17 @@ __global__ void __launch_bounds__(256) packed_ssd_bwd_head_kernel(BwdArgs a, int
 
 struct BwdPlan {
   PackedPlan walk;
-  int group, splits, hps;
+  int splits, hps;
   int64_t numbers;
   size_t states, ws_state, ws_decay, part, part_h, total;   // bytes: one set of saved states, ..., one of part_b and part_c
 };
 BwdPlan bwd_plan(const ssm_ssd_packed_params* p) {
   BwdPlan b{};
-  b.group = group_of(p->dstate);
-  b.walk = packed_plan(p, b.group);
-  b.numbers = piece_numbers(p->nseqs, p->ntokens, b.group * kChunk);
+  b.walk = packed_plan(p);
+  b.numbers = piece_numbers(p->nseqs, p->ntokens, kChunk);
   const int64_t hpg = p->nheads / p->ngroups;
-  // four workgroups for each CU: enough to even out their lengths; each split costs a partial dB and dC
-  int64_t splits = (1024 + b.numbers * p->ngroups - 1) / (b.numbers * p->ngroups);
+  // four workgroups for each place on the 256 CUs, to even out their lengths; each split costs a partial dB and dC
+  int64_t splits = (2048 + b.numbers * p->ngroups - 1) / (b.numbers * p->ngroups);
   if (splits > hpg) splits = hpg;
   b.hps = static_cast<int>((hpg + splits - 1) / splits);
   b.splits = static_cast<int>((hpg + b.hps - 1) / b.hps);
@@ -562,7 +488,7 @@ BwdPlan bwd_plan(const ssm_ssd_packed_params* p) {
   b.ws_state = b.walk.split ? up256(size_t(b.walk.nseg) * state) : 0;
   b.ws_decay = b.walk.split ? up256(size_t(b.walk.nseg) * p->nheads * 4) : 0;
   b.part = up256(size_t(b.splits) * p->ntokens * p->ngroups * p->dstate * 4);
-  b.part_h = up256(size_t(b.numbers) * b.group * p->nheads * 16);
+  b.part_h = up256(size_t(b.numbers) * p->nheads * 16);
   b.total = 2 * b.states + b.ws_state + b.ws_decay + 2 * b.part + b.part_h;
   return b;
 }
@@ -577,7 +503,7 @@ ssm_status check_bwd(const ssm_ssd_packed_params* p) {
 
 template <int N>
 void launch_bwd(const BwdArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL((packed_ssd_bwd_kernel<N>), dim3((a.nwork + 7) / 8 * 8), dim3(Shape<N>::NW * 64), 0, st, a);
+  hipLaunchKernelGGL((packed_ssd_bwd_kernel<N>), dim3((a.nwork + 7) / 8 * 8), dim3(N * 4), 0, st, a);
 }
 
 }  // namespace
@@ -645,8 +571,8 @@ extern "C" ssm_status ssm_ssd_packed_bwd(const ssm_ssd_packed_params* p, const v
   a.A = A;
   a.Dskip = Dskip;
   a.cu = cu_seqlens;
-  a.S = save_s;
-  a.Gs = save_g;
+  a.S = reinterpret_cast<uint16_t*>(save_s);
+  a.Gs = reinterpret_cast<uint16_t*>(save_g);
   a.dx = static_cast<uint16_t*>(dx);
   a.ddt = static_cast<uint16_t*>(ddt);
   a.dB = static_cast<uint16_t*>(dB);
@@ -680,7 +606,6 @@ extern "C" ssm_status ssm_ssd_packed_bwd(const ssm_ssd_packed_params* p, const v
   w.hblocks = b.walk.hblocks;
   w.cps = b.walk.cps;
   w.nseg = static_cast<int>(b.walk.nseg);
-  w.group = b.group;
   w.softplus = a.softplus;
   w.zoh = a.zoh;
   // the states, forward from the slots, then the adjoints, in reverse order from dstate_out
@@ -692,7 +617,7 @@ extern "C" ssm_status ssm_ssd_packed_bwd(const ssm_ssd_packed_params* p, const v
   w.idx = state_idx;
   w.has = has_state;
   w.nslots = p->nslots;
-  w.save = save_s;
+  w.save = reinterpret_cast<uint16_t*>(save_s);
   if (ssm_status s = launch_states(w, static_cast<int>(p->dstate), false, b.walk.split, st); s != SSM_OK) return s;
   w.v = a.dy;
   w.vs = a.dys;
@@ -702,7 +627,7 @@ extern "C" ssm_status ssm_ssd_packed_bwd(const ssm_ssd_packed_params* p, const v
   w.idx = nullptr;
   w.has = nullptr;
   w.nslots = p->nseqs;
-  w.save = save_g;
+  w.save = reinterpret_cast<uint16_t*>(save_g);
   w.last = dstate;
   if (ssm_status s = launch_states(w, static_cast<int>(p->dstate), true, b.walk.split, st); s != SSM_OK) return s;
   switch (p->dstate) {
@@ -713,7 +638,7 @@ extern "C" ssm_status ssm_ssd_packed_bwd(const ssm_ssd_packed_params* p, const v
   const int cols = static_cast<int>(grp);
   hipLaunchKernelGGL(packed_ssd_bwd_bc_kernel, dim3(static_cast<uint32_t>((int64_t(a.T) * (cols / 4) + 255) / 256), 2),
                      dim3(256), 0, st, a, cols);
-  hipLaunchKernelGGL(packed_ssd_bwd_head_kernel, dim3(a.H), dim3(256), 0, st, a, a.numbers * b.group);
+  hipLaunchKernelGGL(packed_ssd_bwd_head_kernel, dim3(a.H), dim3(256), 0, st, a, a.numbers);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SSM_OK : fail(SSM_ERR_HIP, "packed SSD backward launch: %s", hipGetErrorString(e));
 }

@@ -1,5 +1,5 @@
-// The states of packed SSD sequences at the boundaries that other kernels start from: the segments of the forward, the
-// chunk groups of the backward, and the adjoint states walked in reverse order.
+// The states of packed SSD sequences where other kernels start from them: at the segments of the forward, and at every
+// chunk for the backward, together with the adjoint states, which are walked in reverse order.
 //
 // As in the forward, a workgroup takes 4 heads of one group over one segment, a wave holds the state of
 // half of a head's columns in registers, and the shared k rows (B or C) go to LDS once for all waves.  The
@@ -78,18 +78,35 @@ packed_states_kernel(StatesArgs a) {
     return a.dt[(lane < rows ? t0 + lane : t0) * a.dts + h];
   };
 
-  // state tiles: S[nt][pt][c] = S[p][n], n = 32 (nt/2) + 8 g4 + 4 (nt%2) + c, p = p0 + 32 (pt/2) + 8 (l16/4) + 4 (pt%2) + l16%4
+  // state tiles: S[nt][pt][c] = S[p][n], n = 16 nt + l16, p = p0 + 8 g4 + 4 pt + c: a lane's two tiles are eight
+  // consecutive p of a row n, an operand over p as the backward wants it
   pf4 S[NT][PT];
   const int64_t head_size = int64_t(kHead) * N;
-  const int lane_entry = (p0 + 8 * (l16 >> 2) + (l16 & 3)) * N + 8 * g4;
-  auto entry = [&](int nt, int pt) __attribute__((always_inline)) {
-    return lane_entry + (32 * (pt >> 1) + 4 * (pt & 1)) * N + 32 * (nt >> 1) + 4 * (nt & 1);
-  };
+  const int lane_entry = ((p0 + 8 * g4) * N + l16) * 4;   // bytes
   auto put = [&](float* to) __attribute__((always_inline)) {
+    const auto r = make_rsrc(to, head_size);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int pt = 0; pt < PT; ++pt) *reinterpret_cast<pf4*>(to + entry(nt, pt)) = S[nt][pt];
+      for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float v = S[nt][pt][c];
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(v), r, lane_entry, ((4 * pt + c) * N + 16 * nt) * 4, 0);
+        }
+  };
+  // both parts of the state, rows n, in bf16
+  auto save = [&](uint16_t* to) __attribute__((always_inline)) {
+    const auto r = make_rsrc(to, 2 * head_size);
+    const int at = (l16 * kHead + p0 + 8 * g4) * 2;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      pu2 h0, l0, h1, l1;
+      split_bf16x4(S[nt][0][0], S[nt][0][1], S[nt][0][2], S[nt][0][3], h0, l0);
+      split_bf16x4(S[nt][1][0], S[nt][1][1], S[nt][1][2], S[nt][1][3], h1, l1);
+      __builtin_amdgcn_raw_buffer_store_b128(join(h0, h1), r, at, 16 * nt * kHead * 2, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(join(l0, l1), r, at, (N + 16 * nt) * kHead * 2, 0);
+    }
   };
   {
     const float* from = nullptr;
@@ -101,11 +118,15 @@ packed_states_kernel(StatesArgs a) {
         if (slot >= 0) from = a.init + (slot * a.H + h) * head_size;
       }
     }
+    const auto r = make_rsrc(from ? from : a.A, from ? head_size : 0);   // (an empty range reads as zeros)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt)
-        S[nt][pt] = from ? *reinterpret_cast<const pf4*>(from + entry(nt, pt)) : pf4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          S[nt][pt][c] = __int_as_float(
+              __builtin_amdgcn_raw_buffer_load_b32(r, lane_entry, ((4 * pt + c) * N + 16 * nt) * 4, 0));
   }
   float decay = 0.0f;   // sum of log2 decays over the segment (first pass)
   float* W = sW[wave];
@@ -120,13 +141,9 @@ packed_states_kernel(StatesArgs a) {
     int rows;
     place(i, t0, rows);
     if constexpr (SAVE) {
-      // chunk number within the sequence: the group's first in walk order saves the state entering it
-      const int q = (static_cast<int>(t0) - seg.begin) / kChunk;
-      const bool starts = REV ? q % a.group == a.group - 1 || t0 + kChunk >= seg.end : q % a.group == 0;
-      if (a.save && starts && on) {
-        const int steps = a.group * kChunk;
-        put(a.save + ((int64_t(seg.seq) + seg.begin / steps + q / a.group) * a.H + h) * head_size);
-      }
+      if (a.save && on)   // the chunk's number: its place in the sequence behind that of the sequence's first
+        save(a.save + ((int64_t(seg.seq) + seg.begin / kChunk + (static_cast<int>(t0) - seg.begin) / kChunk) * a.H + h) *
+                          2 * head_size);
     }
     float delta, phi, la;
     step_scalars(lo_f32(dtv), bias, Ah, a.softplus, a.zoh, lane < rows, delta, phi, la);
@@ -156,11 +173,11 @@ packed_states_kernel(StatesArgs a) {
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const pu4 b = lds_tr_operand<U>(K, kk, nt, l16, g4);
+        const pu4 b = lds_tr_plain_operand<U, false>(K, kk, nt, l16, g4);
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt) {
-          const pf4 v = mma(b, wh[pt], kk == 0 ? S[nt][pt] * fade : S[nt][pt]);
-          S[nt][pt] = mma(b, wl[pt], v);
+          const pf4 v = mma(wh[pt], b, kk == 0 ? S[nt][pt] * fade : S[nt][pt]);
+          S[nt][pt] = mma(wl[pt], b, v);
         }
       }
     }
