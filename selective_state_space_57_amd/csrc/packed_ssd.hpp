@@ -25,11 +25,26 @@ __device__ __forceinline__ pf4 mma(pu4 a, pu4 b, pf4 c) {
 }
 __device__ __forceinline__ pu2 bf16x4(float a, float b, float c, float d) { return pu2{pack_bf16(a, b), pack_bf16(c, d)}; }
 __device__ __forceinline__ pu4 join(pu2 a, pu2 b) { return pu4{a[0], a[1], b[0], b[1]}; }
-// v = hi + lo, each in bf16 (hi rounded to nearest, lo the rounded rest): 16 significant bits, off by at most 2^-18 v
-__device__ __forceinline__ void split_bf16x4(float a, float b, float c, float d, pu2& hi, pu2& lo) {
-  hi = bf16x4(a, b, c, d);
-  lo = bf16x4(a - lo_f32(hi[0]), b - hi_f32(hi[0]), c - lo_f32(hi[1]), d - hi_f32(hi[1]));
+// Eight values in three bf16 parts, each the rounded rest behind the ones before it: 24 significant bits, all of an fp32
+// value (a third part costs half as much again in products, and keeps states and what hangs on them at fp32 quality: with
+// two, dA and the step sizes' gradients were 1.4e-6 to 3e-6 off, ten times an fp32 computation).
+struct Parts {
+  pu4 p[3];
+};
+__device__ __forceinline__ Parts split3(pf4 a, pf4 b) {
+  Parts o;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const pu2 u = bf16x4(a[0], a[1], a[2], a[3]), v = bf16x4(b[0], b[1], b[2], b[3]);
+    o.p[i] = join(u, v);
+    if (i < 2) {
+      a = pf4{a[0] - lo_f32(u[0]), a[1] - hi_f32(u[0]), a[2] - lo_f32(u[1]), a[3] - hi_f32(u[1])};
+      b = pf4{b[0] - lo_f32(v[0]), b[1] - hi_f32(v[0]), b[2] - lo_f32(v[1]), b[3] - hi_f32(v[1])};
+    }
+  }
+  return o;
 }
+__device__ __forceinline__ pf4 unpack4(uint32_t a, uint32_t b) { return pf4{lo_f32(a), hi_f32(a), lo_f32(b), hi_f32(b)}; }
 
 // Rows of a chunk in LDS: U 16-byte units each, unit u of row r at u ^ swz(r).  16-byte reads go 8 lanes at a time over
 // 128 bytes of banks: 8 consecutive rows of one unit need 8 different places (the low three bits).  Transposing reads
@@ -170,22 +185,35 @@ __device__ __forceinline__ float sum_row(float v) {   // over the 16 lanes of a 
 }
 __device__ __forceinline__ float sum_wave(float v) { return sum_rows(sum_row(v)); }
 
-// sum over lanes 0..lane
-__device__ __forceinline__ float wave_prefix(float v, int lane) {
+// sums over the lanes of the 16-lane row up to this one, or from it on
+__device__ __forceinline__ float row_prefix(float v) {
   v += lanes_shr<1>(v);
   v += lanes_shr<2>(v);
   v += lanes_shr<4>(v);
-  v += lanes_shr<8>(v);
-  const float r0 = lane_value(v, 15), r1 = lane_value(v, 31), r2 = lane_value(v, 47);
-  const int row = lane >> 4;
-  return v + (row >= 1 ? r0 : 0.0f) + (row >= 2 ? r1 : 0.0f) + (row >= 3 ? r2 : 0.0f);
+  return v + lanes_shr<8>(v);
 }
-// sum over lanes lane..63
-__device__ __forceinline__ float wave_suffix(float v, int lane) {
+__device__ __forceinline__ float row_suffix(float v) {
   v += lanes_shl<1>(v);
   v += lanes_shl<2>(v);
   v += lanes_shl<4>(v);
-  v += lanes_shl<8>(v);
+  return v + lanes_shl<8>(v);
+}
+// the same for the row, and the sum over the rows before it
+__device__ __forceinline__ void row_prefix(float v, int lane, float& in_row, float& before) {
+  in_row = row_prefix(v);
+  const float r0 = lane_value(in_row, 15), r1 = lane_value(in_row, 31), r2 = lane_value(in_row, 47);
+  const int row = lane >> 4;
+  before = (row >= 1 ? r0 : 0.0f) + (row >= 2 ? r1 : 0.0f) + (row >= 3 ? r2 : 0.0f);
+}
+// sum over lanes 0..lane
+__device__ __forceinline__ float wave_prefix(float v, int lane) {
+  float in_row, before;
+  row_prefix(v, lane, in_row, before);
+  return in_row + before;
+}
+// sum over lanes lane..63
+__device__ __forceinline__ float wave_suffix(float v, int lane) {
+  v = row_suffix(v);
   const float r1 = lane_value(v, 16), r2 = lane_value(v, 32), r3 = lane_value(v, 48);
   const int row = lane >> 4;
   return v + (row <= 2 ? r3 : 0.0f) + (row <= 1 ? r2 : 0.0f) + (row <= 0 ? r1 : 0.0f);
@@ -220,11 +248,41 @@ __device__ __forceinline__ bool find_piece(const int32_t* cu, int nseqs, int nto
   return p.index >= 0 && p.index < p.count;
 }
 
+// exp(-|u|), good to about 2^-23: the rounding of the exponent's product with log2(e), which the exponential would
+// magnify by |u|, is put back (a step's errors are the same for every column of a head, so they do not average out in
+// dA and the step sizes' gradients).
+__device__ __forceinline__ float exp_neg_abs(float u) {
+  constexpr float kLog2eLo = 1.925963033500e-8f;   // log2(e) - float(log2(e))
+  const float x = -fabsf(u);
+  const float p = x * kLog2e;
+  const float rest = fmaf(x, kLog2e, -p) + x * kLog2eLo;
+  const float v = hw_exp2(p);
+  return fmaf(v * kLn2, rest, v);
+}
+// log(1 + v), 0 <= v <= 1: 2 atanh(s), s = v / (2 + v) <= 1/3, by its series (the first term left out is 3e-9 of it)
+__device__ __forceinline__ float log1p_series(float v) {
+  const float s = v / (2.0f + v), q = s * s;
+  float p = 1.0f / 15.0f;
+  p = fmaf(p, q, 1.0f / 13.0f);
+  p = fmaf(p, q, 1.0f / 11.0f);
+  p = fmaf(p, q, 1.0f / 9.0f);
+  p = fmaf(p, q, 1.0f / 7.0f);
+  p = fmaf(p, q, 0.2f);
+  p = fmaf(p, q, 1.0f / 3.0f);
+  return 2.0f * fmaf(s * q, p, s);
+}
+__device__ __forceinline__ float softplus_fine(float u) { return fmaxf(u, 0.0f) + log1p_series(exp_neg_abs(u)); }
+// its derivative 1 / (1 + exp(-u))
+__device__ __forceinline__ float softplus_slope(float u) {
+  const float v = exp_neg_abs(u);
+  return (u >= 0.0f ? 1.0f : v) / (1.0f + v);
+}
+
 // Step size, its weight and the decay's logarithm (base 2) of one step; zeros behind the sequence.
 __device__ __forceinline__ void step_scalars(float dt, float bias, float A, bool use_softplus, bool zoh, bool live,
                                              float& delta, float& phi, float& la) {
   const float u = dt + bias;
-  delta = use_softplus ? softplus(u) : u;
+  delta = use_softplus ? softplus_fine(u) : u;
   delta = live ? delta : 0.0f;
   la = delta * A * kLog2e;
   phi = delta;
@@ -273,7 +331,7 @@ struct StatesArgs {
   float* last;           // [seqs][H][64][N] or null: the state behind the whole walk of a sequence
   float* ws_state;       // [nseg][H][64][N]: state entering each segment (where a sequence has more than one)
   float* ws_decay;       // [nseg][H]
-  uint16_t* save;        // [chunk numbers][H][2][N][64] bf16 or null: state entering each chunk, in two parts, transposed
+  float* save;           // [chunk numbers][H][N][64] or null: state entering each chunk, transposed
   int64_t vs, ks, dts, nslots;
   int T, S, H, G, hpg, hblocks, cps, nseg, nwork;
   int softplus, zoh;

@@ -15,7 +15,7 @@
 // segment first, and all segments run at once.
 //
 // Precision: fp32 state and accumulation; x, B and C enter the matrix cores as they are.  The weighted x of the state
-// update is split into two bf16 parts (2^-18 relative), so the state keeps fp32 quality over long sequences.  M (but for s = t) and
+// update is split into three bf16 parts, so the state keeps fp32 quality over long sequences.  M (but for s = t) and
 // the state's copy that meets C are rounded once to bf16 (2^-9 relative, as the output is): they only reach y, which is
 // rounded to bf16 itself.
 #include "packed_ssd.hpp"
@@ -275,15 +275,11 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
     for (int kk = 0; kk < 2; ++kk) {
       const pf4 w0 = *reinterpret_cast<const pf4*>(&sc.w[32 * kk + 4 * g4]);
       const pf4 w1 = *reinterpret_cast<const pf4*>(&sc.w[32 * kk + 16 + 4 * g4]);
-      pu4 wh[PT], wl[PT];   // the weighted rows, in two parts
+      Parts w[PT];   // the weighted rows
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt) {
         const pu4 v = lds_tr_operand<UX>(X, kk, pt, l16, g4);
-        pu2 h0, l0, h1, l1;
-        split_bf16x4(lo_f32(v[0]) * w0[0], hi_f32(v[0]) * w0[1], lo_f32(v[1]) * w0[2], hi_f32(v[1]) * w0[3], h0, l0);
-        split_bf16x4(lo_f32(v[2]) * w1[0], hi_f32(v[2]) * w1[1], lo_f32(v[3]) * w1[2], hi_f32(v[3]) * w1[3], h1, l1);
-        wh[pt] = join(h0, h1);
-        wl[pt] = join(l0, l1);
+        w[pt] = split3(unpack4(v[0], v[1]) * w0, unpack4(v[2], v[3]) * w1);
       }
       if (kk == 1) {
         wait_lds();
@@ -294,8 +290,10 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
         const pu4 b = lds_tr_operand<U>(B, kk, nt, l16, g4);
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt) {
-          const pf4 v = mma(b, wh[pt], kk == 0 ? S[nt][pt] * fade : S[nt][pt]);
-          S[nt][pt] = mma(b, wl[pt], v);
+          pf4 v = kk == 0 ? S[nt][pt] * fade : S[nt][pt];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) v = mma(b, w[pt].p[i], v);
+          S[nt][pt] = v;
         }
       }
     }

@@ -13,8 +13,8 @@
 // Every sum in dl_r has the decays of what it stands for in it, so nothing large cancels: only the row and column sums
 // of W do, and those are sums of the same fp32 numbers.
 //
-// Two walks (ssm_packed_states.hip) leave S and G of every chunk, split into two bf16 parts as the products want them;
-// then a workgroup takes a chunk and runs over heads one after the other.  A wave has 16 of the N columns of the states,
+// Two walks (ssm_packed_states.hip) leave S and G of every chunk, transposed, so that a lane's eight consecutive p are an
+// operand; then a workgroup takes a chunk and runs over heads one after the other.  A wave has 16 of the N columns of the states,
 // for every head: the sums of dB and dC over heads add up in its registers.  K is summed over heads in registers as well,
 // and multiplied with B and C once at the end.  What a head needs across waves (dx, and the sums over n in u, v and
 // <G, S>) goes through LDS.  The next head's states and x are on their way while this head's dx is computed.
@@ -22,7 +22,7 @@
 // 128 steps to a workgroup, which halve the saved states but recompute them in between, one filled the LDS and took
 // 790 us instead of xxx for the 2.7B layer at 16384 tokens.
 //
-// Precision: fp32 accumulation; the states are split into two bf16 parts (2^-18 relative), so that u, v and <G, S>, and with them dDelta and dA, are good to fp32 quality.  G in dx, M = L Z phi
+// Precision: fp32 accumulation; the states are split into three bf16 parts, so that u, v and <G, S>, and with them dDelta and dA, are good to fp32 quality.  G in dx, M = L Z phi
 // and the head sum K (both but for s = t, which is added in fp32) are rounded once to bf16: they only reach dx, dB and
 // dC, which are bf16 themselves.
 #include "packed_ssd.hpp"
@@ -40,8 +40,8 @@ struct BwdArgs {
   const float* A;
   const float* Dskip;
   const int32_t* cu;
-  const uint16_t* S;   // [numbers][H][2][N][64]: state entering each chunk, high and low parts
-  const uint16_t* Gs;  // the adjoint behind it
+  const float* S;      // [numbers][H][N][64]: state entering each chunk
+  const float* Gs;     // [numbers][H][N][64]: adjoint behind it
   uint16_t* dx;
   uint16_t* ddt;
   uint16_t* dB;
@@ -58,7 +58,10 @@ struct BwdArgs {
 };
 
 struct alignas(16) ChunkScalars {
-  float c[kChunk], phi[kChunk];   // c_t (base 2), phi_t
+  // c_t (base 2) as the sum over the 16 steps up to t of its tile and the sum before the tile: differences of steps near
+  // each other then carry the rounding of a short sum only
+  float c[kChunk], before[4];
+  float phi[kChunk];
   float e[kChunk];                // exp(c_t)
   float pf[kChunk];               // phi_t exp(c_63 - c_t)
   float f[kChunk];                // exp(c_63 - c_t)
@@ -96,7 +99,7 @@ packed_ssd_bwd_kernel(BwdArgs a) {
   __shared__ alignas(16) uint16_t sG[N * kHead];       // G, transposed
   __shared__ ChunkScalars sc;
   __shared__ float sU[NW][kChunk], sV[NW][kChunk], sE[NW];
-  __shared__ float sRow[10][16], sCol[10][16], sOwn[4][16], sDirect[4][16], sDiag[4];
+  __shared__ float sRow[10][16], sCol[10][16], sOwn[4][16], sDirect[4][16], sDiag[4], sTotal[10];
 
   const int item = xcd_item();
   if (item >= a.nwork) return;
@@ -143,19 +146,18 @@ packed_ssd_bwd_kernel(BwdArgs a) {
                        __attribute__((always_inline)) {
     copy_rows<8, NW>(dst, chunk_rsrc(src + int64_t(h) * kHead, t_first, stride, rows, kHead), nt, afresh(lane), row_bytes);
   };
-  // operands over p: n = 16 nt + l16, p = 32 kk + 8 g4 ..
-  pu4 sh[2], sl[2], gh[2], gl[2];
+  // S and G of this wave's columns: n = 16 nt + l16, p = 32 (i/2) + 8 g4 + 4 (i%2) + c
+  pf4 S[4], G[4];
   auto load_states = [&](int h) __attribute__((always_inline)) {
-    const auto rs = make_rsrc(a.S + (int64_t(number) * a.H + h) * 2 * head_size, 2 * head_size);
-    const auto rg = make_rsrc(a.Gs + (int64_t(number) * a.H + h) * 2 * head_size, 2 * head_size);
+    const auto rs = make_rsrc(a.S + (int64_t(number) * a.H + h) * head_size, head_size);
+    const auto rg = make_rsrc(a.Gs + (int64_t(number) * a.H + h) * head_size, head_size);
     const int l = afresh(lane);
-    const int at = ((16 * nt + (l & 15)) * kHead + 8 * (l >> 4)) * 2;
+    const int at = ((16 * nt + (l & 15)) * kHead + 8 * (l >> 4)) * 4;
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      sh[kk] = __builtin_bit_cast(pu4, __builtin_amdgcn_raw_buffer_load_b128(rs, at, 64 * kk, 0));
-      sl[kk] = __builtin_bit_cast(pu4, __builtin_amdgcn_raw_buffer_load_b128(rs, at, 64 * kk + N * kHead * 2, 0));
-      gh[kk] = __builtin_bit_cast(pu4, __builtin_amdgcn_raw_buffer_load_b128(rg, at, 64 * kk, 0));
-      gl[kk] = __builtin_bit_cast(pu4, __builtin_amdgcn_raw_buffer_load_b128(rg, at, 64 * kk + N * kHead * 2, 0));
+    for (int i = 0; i < 4; ++i) {
+      const int p = (32 * (i >> 1) + 4 * (i & 1)) * 4;
+      S[i] = __builtin_bit_cast(pf4, __builtin_amdgcn_raw_buffer_load_b128(rs, at, p, 0));
+      G[i] = __builtin_bit_cast(pf4, __builtin_amdgcn_raw_buffer_load_b128(rg, at, p, 0));
     }
   };
 
@@ -173,62 +175,66 @@ packed_ssd_bwd_kernel(BwdArgs a) {
       const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
       float delta, phi, la;
       step_scalars(dtv, bias, Ah, a.softplus, a.zoh, lane < rows, delta, phi, la);
-      const float c = wave_prefix(la, lane), f = hw_exp2(wave_suffix(la, lane) - la);
-      sc.c[lane] = c;
+      float in_row, before;
+      row_prefix(la, lane, in_row, before);
+      const float f = hw_exp2(wave_suffix(la, lane) - la);
+      sc.c[lane] = in_row;
+      if ((lane & 15) == 0) sc.before[lane >> 4] = before;
       sc.phi[lane] = phi;
-      sc.e[lane] = hw_exp2(c);
+      sc.e[lane] = hw_exp2(in_row + before);
       sc.f[lane] = f;
       sc.pf[lane] = phi * f;
       sc.delta[lane] = delta;
       sc.decay[lane] = hw_exp2(la);
-      sc.slope[lane] = a.softplus ? sigmoid(dtv + bias) : 1.0f;
+      sc.slope[lane] = a.softplus ? softplus_slope(dtv + bias) : 1.0f;
     }
     wait_memory();
     barrier_lds();   // x, dy and the scalars are there
     part_ends();
     {
-      // ---- products with the states: q^T = S^T dy^T, r^T = G^T x^T, <G, S>
+      // ---- products with the states: <G, S>, q^T = S^T dy^T, r^T = G^T x^T
       const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
-      pf4 ge = zero;
+      float e = 0.0f;
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        // the row of n = 16 nt + l16 holds G[.][n]
-        *reinterpret_cast<pu4*>(reinterpret_cast<char*>(sG) + unit_at<8>(16 * nt + l16, 4 * kk + g4)) = gh[kk];
-        ge = mma(sh[kk], gh[kk], ge);
-        ge = mma(sh[kk], gl[kk], ge);
-        ge = mma(sl[kk], gh[kk], ge);
-      }
-      part_ends();
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int row = 16 * b + l16;
-        pf4 q = zero, r = zero;
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) {
-          const pu4 y = lds_row_operand<8>(Yk, row, kk, g4), x = lds_row_operand<8>(Xk, row, kk, g4);
-          q = mma(sh[kk], y, q);
-          r = mma(gh[kk], x, r);
-          q = mma(sl[kk], y, q);
-          r = mma(gl[kk], x, r);
-        }
-        const int place = unit_at<U>(row, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1);
-        const pu2 cw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(Ck) + place);
-        const pu2 bw = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(Bk) + place);
-        const float su = sum_rows((q[0] * lo_f32(cw[0]) + q[1] * hi_f32(cw[0])) + (q[2] * lo_f32(cw[1]) + q[3] * hi_f32(cw[1])));
-        const float sv = sum_rows((r[0] * lo_f32(bw[0]) + r[1] * hi_f32(bw[0])) + (r[2] * lo_f32(bw[1]) + r[3] * hi_f32(bw[1])));
-        if (g4 == 0) {
-          sU[wave][row] = su;
-          sV[wave][row] = sv;
-        }
-        aC[b] += q * sc.e[row];
-        aB[b] += r * sc.pf[row];
-        asm volatile("" : "+v"(aB[b]), "+v"(aC[b]));   // (here, and not behind the loop with q and r kept for it)
+        for (int c = 0; c < 4; ++c) e = fmaf(S[i][c], G[i][c], e);
+      e = sum_wave(e);
+      if (l == 0) sE[wave] = e;
+      // sum over p of D rows against V's rows, the sum's share in u or v, and its part of dC or dB
+      auto product = [&](pf4 (&D)[4], const uint16_t* V, const uint16_t* K, float* out, const float* weight,
+                         pf4 (&acc)[4], bool keep) __attribute__((always_inline)) {
         part_ends();
-      }
-      // <G, S>: the diagonal of the products
-      const float d = (l16 >> 2) == g4 ? ((l16 & 2) ? ((l16 & 1) ? ge[3] : ge[2]) : ((l16 & 1) ? ge[1] : ge[0])) : 0.0f;
-      const float total = sum_wave(d);
-      if (l == 0) sE[wave] = total;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(D[i]));   // (split now, not before)
+        const Parts d[2] = {split3(D[0], D[1]), split3(D[2], D[3])};
+        if (keep) {   // the row of n = 16 nt + l16 holds G[.][n]
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk)
+            *reinterpret_cast<pu4*>(reinterpret_cast<char*>(sG) + unit_at<8>(16 * nt + l16, 4 * kk + g4)) = d[kk].p[0];
+        }
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          part_ends();
+          const int row = 16 * b + l16;
+          pf4 q[2] = {zero, zero};
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) {
+            const pu4 v = lds_row_operand<8>(V, row, kk, g4);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) q[kk] = mma(d[kk].p[i], v, q[kk]);
+          }
+          const pf4 t = q[0] + q[1];
+          const pu2 w = *reinterpret_cast<const pu2*>(reinterpret_cast<const char*>(K) +
+                                                      unit_at<U>(row, 2 * nt + (g4 >> 1)) + 8 * (g4 & 1));
+          const float s = sum_rows((t[0] * lo_f32(w[0]) + t[1] * hi_f32(w[0])) + (t[2] * lo_f32(w[1]) + t[3] * hi_f32(w[1])));
+          if (g4 == 0) out[row] = s;
+          acc[b] += t * weight[row];
+          asm volatile("" : "+v"(acc[b]));   // (here, and not behind the loop with t kept for it)
+        }
+      };
+      product(S, Yk, Ck, sU[wave], sc.e, aC, false);
+      product(G, Xk, Bk, sV[wave], sc.pf, aB, true);
     }
     part_ends();
     // ---- tiles of L, X, Z
@@ -242,7 +248,7 @@ packed_ssd_bwd_kernel(BwdArgs a) {
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)
         X = mma(lds_row_operand<8>(Yk, 16 * tb + l16, kk, g4), lds_row_operand<8>(Xk, 16 * sb + l16, kk, g4), X);
-      const pf4 ct = *reinterpret_cast<const pf4*>(&sc.c[16 * tb + 4 * g4]);
+      const pf4 ct = *reinterpret_cast<const pf4*>(&sc.c[16 * tb + 4 * g4]) + (sc.before[tb] - sc.before[sb]);
       const float cs = sc.c[16 * sb + l16], ph = sc.phi[16 * sb + l16];
       pf4 Z = zero;
 #pragma unroll
@@ -250,6 +256,7 @@ packed_ssd_bwd_kernel(BwdArgs a) {
         if (kk % 2 == 0) part_ends();
         Z = mma(lds_row_operand<U>(Ck, 16 * tb + l16, kk, g4), lds_row_operand<U>(Bk, 16 * sb + l16, kk, g4), Z);
       }
+      part_ends();
       part_ends();
       float m[4], row[4], col = 0.0f;
       if (sb < tb) {
@@ -289,11 +296,15 @@ packed_ssd_bwd_kernel(BwdArgs a) {
         if (l == 0) sDiag[tb] = diag;
       }
       reinterpret_cast<pu2*>(&sM[m_slot(sb, tb >> 1)][l])[tb & 1] = bf16x4(m[0], m[1], m[2], m[3]);
+      asm volatile("" : "+v"(aK[ti]));
+      part_ends();
 #pragma unroll
       for (int c = 0; c < 4; ++c) row[c] = sum_row(row[c]);
       if (l16 < 4) sRow[i][4 * g4 + l16] = (l16 & 2) ? ((l16 & 1) ? row[3] : row[2]) : ((l16 & 1) ? row[1] : row[0]);
       col = sum_rows(col);
       if (g4 == 0) sCol[i][l16] = col;
+      const float tile = sum_rows((row[0] + row[1]) + (row[2] + row[3]));
+      if (l == 0) sTotal[i] = tile;
     }
     barrier_lds();   // M, G and the partial sums are there, and x is read
     if (h + 1 < h_end) {
@@ -340,25 +351,35 @@ packed_ssd_bwd_kernel(BwdArgs a) {
     // ---- the steps' own gradients
     if (nt == kScalarTile) {
       const int lane = afresh(threadIdx.x) & 63, l16 = lane & 15, tl = lane >> 4;
-      float row = 0.0f, col = 0.0f, u = 0.0f, v = 0.0f, e = 0.0f;
+      part_ends();
+      // sums of W over the row, and of W0 over the column, of step `lane`: in its own tile, and in those beside and below
+      const float row = sRow[tl * (tl + 1) / 2 + tl][l16], col = sCol[tl * (tl + 1) / 2 + tl][l16];
+      float row_off = 0.0f, col_off = 0.0f, u = 0.0f, v = 0.0f, e = 0.0f;
 #pragma unroll
       for (int o = 0; o < 4; ++o) {
-        row += o <= tl ? sRow[tl * (tl + 1) / 2 + min(o, tl)][l16] : 0.0f;
+        row_off += o < tl ? sRow[tl * (tl + 1) / 2 + min(o, tl)][l16] : 0.0f;
         const int tt = max(o, tl);
-        col += o >= tl ? sCol[tt * (tt + 1) / 2 + tl][l16] : 0.0f;
+        col_off += o > tl ? sCol[tt * (tt + 1) / 2 + tl][l16] : 0.0f;
       }
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
+        if (w % 4 == 0) part_ends();
         u += sU[w][lane];
         v += sV[w][lane];
         e += sE[w];
+        asm volatile("" : "+v"(u), "+v"(v), "+v"(e));
       }
       const float phi = sc.phi[lane];
       u *= sc.e[lane];
       v *= sc.f[lane];
-      const float dphi = col + sOwn[tl][l16] + v;
-      const float before = phi * v;
-      const float dl = wave_suffix(row - phi * col + u, lane) + (wave_prefix(before, lane) - before) + sc.e[kChunk - 1] * e;
+      const float dphi = col + col_off + sOwn[tl][l16] + v;
+      const float before = phi * v, off = phi * col_off;
+      // sum_{t>=r, s<r} W: the tiles below and beside the step's own, in full (their numbers are tb (tb + 1) / 2 + sb), the
+      // rows from r on of those beside, the columns before r of those below, and the own tile's corner, where alone rows
+      // less columns are taken, over 16 steps (over the whole chunk, sums much larger than dl would cancel)
+      const float far = tl == 1 ? sTotal[3] + sTotal[6] : tl == 2 ? sTotal[6] + sTotal[7] : 0.0f;
+      const float dl = row_suffix(row_off + (row - phi * col)) + (row_prefix(off) - off) + far + wave_suffix(u, lane) +
+                       (wave_prefix(before, lane) - before) + sc.e[kChunk - 1] * e;
       const float delta = sc.delta[lane], decay = sc.decay[lane];
       const float dd = (Ah * dl + (a.zoh ? decay * dphi : dphi)) * sc.slope[lane];
       float sum_a = 0.0f, sum_t = 0.0f, sum_d = lane < 4 ? sDiag[lane] : 0.0f;
@@ -571,8 +592,8 @@ extern "C" ssm_status ssm_ssd_packed_bwd(const ssm_ssd_packed_params* p, const v
   a.A = A;
   a.Dskip = Dskip;
   a.cu = cu_seqlens;
-  a.S = reinterpret_cast<uint16_t*>(save_s);
-  a.Gs = reinterpret_cast<uint16_t*>(save_g);
+  a.S = save_s;
+  a.Gs = save_g;
   a.dx = static_cast<uint16_t*>(dx);
   a.ddt = static_cast<uint16_t*>(ddt);
   a.dB = static_cast<uint16_t*>(dB);
@@ -617,7 +638,7 @@ extern "C" ssm_status ssm_ssd_packed_bwd(const ssm_ssd_packed_params* p, const v
   w.idx = state_idx;
   w.has = has_state;
   w.nslots = p->nslots;
-  w.save = reinterpret_cast<uint16_t*>(save_s);
+  w.save = save_s;
   if (ssm_status s = launch_states(w, static_cast<int>(p->dstate), false, b.walk.split, st); s != SSM_OK) return s;
   w.v = a.dy;
   w.vs = a.dys;
@@ -627,7 +648,7 @@ extern "C" ssm_status ssm_ssd_packed_bwd(const ssm_ssd_packed_params* p, const v
   w.idx = nullptr;
   w.has = nullptr;
   w.nslots = p->nseqs;
-  w.save = reinterpret_cast<uint16_t*>(save_g);
+  w.save = save_g;
   w.last = dstate;
   if (ssm_status s = launch_states(w, static_cast<int>(p->dstate), true, b.walk.split, st); s != SSM_OK) return s;
   switch (p->dstate) {

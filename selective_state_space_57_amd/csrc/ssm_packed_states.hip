@@ -3,7 +3,7 @@
 //
 // As in the forward, a workgroup takes 4 heads of one group over one segment, a wave holds the state of
 // half of a head's columns in registers, and the shared k rows (B or C) go to LDS once for all waves.  The
-// weighted v rows are split into two bf16 parts (2^-18 relative), so states keep fp32 quality.  A sequence of several
+// weighted v rows are split into three bf16 parts, so states keep fp32 quality.  A sequence of several
 // segments takes three launches: every segment from zero, a join in order, and the walk proper.
 #include "packed_ssd.hpp"
 
@@ -95,18 +95,15 @@ packed_states_kernel(StatesArgs a) {
           __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(v), r, lane_entry, ((4 * pt + c) * N + 16 * nt) * 4, 0);
         }
   };
-  // both parts of the state, rows n, in bf16
-  auto save = [&](uint16_t* to) __attribute__((always_inline)) {
-    const auto r = make_rsrc(to, 2 * head_size);
-    const int at = (l16 * kHead + p0 + 8 * g4) * 2;
+  // the state with n as rows
+  auto save = [&](float* to) __attribute__((always_inline)) {
+    const auto r = make_rsrc(to, head_size);
+    const int at = (l16 * kHead + p0 + 8 * g4) * 4;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      pu2 h0, l0, h1, l1;
-      split_bf16x4(S[nt][0][0], S[nt][0][1], S[nt][0][2], S[nt][0][3], h0, l0);
-      split_bf16x4(S[nt][1][0], S[nt][1][1], S[nt][1][2], S[nt][1][3], h1, l1);
-      __builtin_amdgcn_raw_buffer_store_b128(join(h0, h1), r, at, 16 * nt * kHead * 2, 0);
-      __builtin_amdgcn_raw_buffer_store_b128(join(l0, l1), r, at, (N + 16 * nt) * kHead * 2, 0);
-    }
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(pu4, S[nt][pt]), r, at, (16 * nt * kHead + 4 * pt) * 4, 0);
   };
   {
     const float* from = nullptr;
@@ -143,7 +140,7 @@ packed_states_kernel(StatesArgs a) {
     if constexpr (SAVE) {
       if (a.save && on)   // the chunk's number: its place in the sequence behind that of the sequence's first
         save(a.save + ((int64_t(seg.seq) + seg.begin / kChunk + (static_cast<int>(t0) - seg.begin) / kChunk) * a.H + h) *
-                          2 * head_size);
+                          head_size);
     }
     float delta, phi, la;
     step_scalars(lo_f32(dtv), bias, Ah, a.softplus, a.zoh, lane < rows, delta, phi, la);
@@ -157,15 +154,11 @@ packed_states_kernel(StatesArgs a) {
     for (int kk = 0; kk < 2; ++kk) {
       const pf4 w0 = *reinterpret_cast<const pf4*>(&W[32 * kk + 4 * g4]);
       const pf4 w1 = *reinterpret_cast<const pf4*>(&W[32 * kk + 16 + 4 * g4]);
-      pu4 wh[PT], wl[PT];   // the weighted rows, in two parts
+      Parts w[PT];   // the weighted rows
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt) {
         const pu4 v = lds_tr_operand<UV>(V, kk, pt, l16, g4);
-        pu2 h0, l0, h1, l1;
-        split_bf16x4(lo_f32(v[0]) * w0[0], hi_f32(v[0]) * w0[1], lo_f32(v[1]) * w0[2], hi_f32(v[1]) * w0[3], h0, l0);
-        split_bf16x4(lo_f32(v[2]) * w1[0], hi_f32(v[2]) * w1[1], lo_f32(v[3]) * w1[2], hi_f32(v[3]) * w1[3], h1, l1);
-        wh[pt] = join(h0, h1);
-        wl[pt] = join(l0, l1);
+        w[pt] = split3(unpack4(v[0], v[1]) * w0, unpack4(v[2], v[3]) * w1);
       }
       if (kk == 1) {
         wait_lds();
@@ -176,8 +169,10 @@ packed_states_kernel(StatesArgs a) {
         const pu4 b = lds_tr_plain_operand<U, false>(K, kk, nt, l16, g4);
 #pragma unroll
         for (int pt = 0; pt < PT; ++pt) {
-          const pf4 v = mma(wh[pt], b, kk == 0 ? S[nt][pt] * fade : S[nt][pt]);
-          S[nt][pt] = mma(wl[pt], b, v);
+          pf4 v = kk == 0 ? S[nt][pt] * fade : S[nt][pt];
+#pragma unroll
+          for (int i = 0; i < 3; ++i) v = mma(w[pt].p[i], b, v);
+          S[nt][pt] = v;
         }
       }
     }
