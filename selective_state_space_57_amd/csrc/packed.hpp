@@ -60,6 +60,27 @@ struct Pack<uint16_t, 8> {
   }
 };
 
+// M consecutive floats in as few loads (stores) as they make up; 4-byte alignment is all a 16-byte access needs here.
+typedef float pf4u __attribute__((ext_vector_type(4), aligned(4)));
+template <int M>
+__device__ __forceinline__ void load_floats(const float* p, float* o) {
+#pragma unroll
+  for (int i = 0; i + 4 <= M; i += 4) {
+    const pf4u v = *reinterpret_cast<const pf4u*>(p + i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[i + k] = v[k];
+  }
+#pragma unroll
+  for (int i = M / 4 * 4; i < M; ++i) o[i] = p[i];
+}
+template <int M>
+__device__ __forceinline__ void store_floats(float* p, const float* o) {
+#pragma unroll
+  for (int i = 0; i + 4 <= M; i += 4) *reinterpret_cast<pf4u*>(p + i) = pf4u{o[i], o[i + 1], o[i + 2], o[i + 3]};
+#pragma unroll
+  for (int i = M / 4 * 4; i < M; ++i) p[i] = o[i];
+}
+
 __device__ __forceinline__ float sigmoid(float v) { return hw_rcp(1.0f + hw_exp2(-v * kLog2e)); }
 
 // The last s in [0, nseqs] with cu[s] <= t (empty sequences at t are passed over), or -1: token t belongs to sequence

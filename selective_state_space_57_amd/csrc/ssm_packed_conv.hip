@@ -6,7 +6,8 @@
 //   dbias = sum_t dpre_t
 // All of it is a stream of x (and du) in and u (dx) out, bound by memory: a thread owns V channels (16 bytes of a row)
 // and walks down a tile of tokens with the K - 1 inputs before it in registers, so each value is read once and a halo
-// of K - 1 rows per tile (out of the L2) on top.
+// of K - 1 rows per tile (out of the L2) on top.  At 4.3 TB/s forward (16384 tokens of 5376 bf16 channels: 81 us); the
+// backward pass, three rows of two inputs and the partial sums of dw on top, 2.6 TB/s (8191 tokens: 100 us).
 #include "packed.hpp"
 
 namespace ssm57 {
@@ -40,24 +41,51 @@ template <int K, int V>
 struct Taps {
   float w[K][V], b[V];
   __device__ __forceinline__ void load(const PConvArgs& a, int c) {
+    float t[V * K];
+    load_floats<V * K>(a.w + int64_t(c) * K, t);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
-      for (int k = 0; k < K; ++k) w[k][v] = a.w[int64_t(c + v) * K + k];
-      b[v] = a.bias ? a.bias[c + v] : 0.0f;
+      for (int k = 0; k < K; ++k) w[k][v] = t[v * K + k];
+      b[v] = 0.0f;
     }
+    if (a.bias) load_floats<V>(a.bias + c, b);
   }
 };
 
-// window of sequence s before its first token (oldest first): the slot's, or zeros
+// a slot's window of V channels from channel c on, oldest input first
+template <int K, int V>
+__device__ __forceinline__ void get_window(const float* p, float (&win)[K][V]) {
+  if constexpr (K > 1) {
+    float t[V * (K - 1)];
+    load_floats<V * (K - 1)>(p, t);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int k = 0; k < K - 1; ++k) win[k][v] = t[v * (K - 1) + k];
+  }
+}
+// win[first] .. win[first + K - 2]
+template <int K, int V>
+__device__ __forceinline__ void put_window(float* p, const float (&win)[K][V], int first) {
+  if constexpr (K > 1) {
+    float t[V * (K - 1)];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int k = 0; k < K - 1; ++k) t[v * (K - 1) + k] = first ? win[k + 1][v] : win[k][v];
+    store_floats<V * (K - 1)>(p, t);
+  }
+}
+// window of sequence s before its first token: the slot's, or zeros
 template <int K, int V>
 __device__ __forceinline__ void load_window(const PConvArgs& a, int s, int c, float (&win)[K][V]) {
   const int64_t slot = a.state && (!a.has || a.has[s]) ? slot_of(a.idx, s, a.nslots) : -1;
 #pragma unroll
   for (int k = 0; k < K - 1; ++k)
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      win[k][v] = slot >= 0 ? a.state[(slot * a.C + c + v) * (K - 1) + k] : 0.0f;
+    for (int v = 0; v < V; ++v) win[k][v] = 0.0f;
+  if (slot >= 0) get_window<K, V>(a.state + (slot * a.C + c) * (K - 1), win);
 }
 
 template <int K, int V>
@@ -127,10 +155,7 @@ __global__ void __launch_bounds__(kThreads) packed_conv_fwd_kernel(PConvArgs a) 
             p.get(win[k]);
           }
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-          for (int k = 0; k < K - 1; ++k) a.state_out[(slot * a.C + c + v) * (K - 1) + k] = win[k][v];
+        put_window<K, V>(a.state_out + (slot * a.C + c) * (K - 1), win, 0);
       }
     }
     return;
@@ -144,7 +169,7 @@ __global__ void __launch_bounds__(kThreads) packed_conv_fwd_kernel(PConvArgs a) 
     p.load(x + int64_t(max(t0 - (K - 1) + k, 0)) * a.xs);   // (a row before the sequence is read, and not used)
     p.get(win[k]);
   }
-  constexpr int kAhead = 8;   // rows in flight
+  constexpr int kAhead = 8;   // rows in flight (4: 88 instead of 81 us, 16: 153, too many registers)
   for (int tb = t0; tb < t1; tb += kAhead) {
     Pack<T, V> row[kAhead];
 #pragma unroll
@@ -176,12 +201,13 @@ __global__ void __launch_bounds__(kThreads) packed_conv_step_kernel(PConvArgs a)
   float win[K][V], pre[V];
   Pack<T, V> p;
   p.load(static_cast<const T*>(a.x) + int64_t(row) * a.xs + c);
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-#pragma unroll
-    for (int k = 0; k < K - 1; ++k) win[k][v] = slot >= 0 ? st[v * (K - 1) + k] : 0.0f;
+  if constexpr (K > 1) get_window<K, V>(st, win);   // (without a slot, the first one's, and not used)
   Taps<K, V> tp;
   tp.load(a, c);
+#pragma unroll
+  for (int k = 0; k < K - 1; ++k)
+#pragma unroll
+    for (int v = 0; v < V; ++v) win[k][v] = slot >= 0 ? win[k][v] : 0.0f;
   p.get(win[K - 1]);
   conv_pre<K, V>(tp, win, pre);
   if (a.silu) {
@@ -189,12 +215,7 @@ __global__ void __launch_bounds__(kThreads) packed_conv_step_kernel(PConvArgs a)
     for (int v = 0; v < V; ++v) pre[v] *= sigmoid(pre[v]);
   }
   Pack<T, V>::store(static_cast<T*>(a.u) + int64_t(row) * a.us + c, pre);
-  if (slot >= 0) {
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int k = 0; k < K - 1; ++k) st[v * (K - 1) + k] = win[k + 1][v];
-  }
+  if (slot >= 0) put_window<K, V>(st, win, 1);
 }
 
 // Backward.  A tile's threads walk its tokens and K - 1 more (whose dpre reaches back into the tile); acc[j] is dx of
@@ -273,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) packed_conv_bwd_kernel(PConvArgs a) 
     }
   }
   float acc[K][V] = {}, gw[K][V] = {}, gb[V] = {};
-  constexpr int kAhead = 4;
+  constexpr int kAhead = 4;   // rows in flight (2: 112 instead of 100 us, 8: 100)
   const int tend = min(t1 + K - 1, a.T);
   for (int tb = t0; tb < t1 + K - 1; tb += kAhead) {
     Pack<T, V> rx[kAhead], rg[kAhead];
@@ -402,15 +423,17 @@ bool rows_aligned(const void* ptr, int64_t stride, int64_t dim, int elem) {
   return aligned(ptr, 16) && stride % v == 0 && dim % v == 0;
 }
 
-// tokens per tile: as long as the launch still has about 8 waves for each of the 1024 SIMDs (a longer tile re-reads
+// tokens per tile: as long as the launch still has about `waves` for each of the 1024 SIMDs (a longer tile re-reads
 // fewer halo rows and writes fewer partial sums), and at most `most`
-int tile_of(const PConvArgs& a, int v, int most) {
+int tile_of(const PConvArgs& a, int v, int waves, int most) {
   const int64_t lanes = (a.C + v - 1) / v;
-  int64_t tile = int64_t(a.T) * lanes / (int64_t(8) * 1024 * 64);
+  int64_t tile = int64_t(a.T) * lanes / (int64_t(waves) * 1024 * 64);
   tile = tile < 8 ? 8 : (tile > most ? most : tile);
   return static_cast<int>(tile / 8 * 8);
 }
-constexpr int kFwdTile = 64, kBwdTile = 64;
+// Measured on bf16 rows of 5376 channels, width 4: forward, 16384 tokens (352 MB moved), tiles of 16, 32, 40, 64 and 128
+// tokens (8, 4, 4, 2 and 1 waves) 85, 94, 89, 81 and 91 us; backward, 8191 tokens (264 MB), 32 and 64 tokens 103 and 100.
+constexpr int kFwdWaves = 2, kBwdWaves = 1, kMostTokens = 64;
 
 template <typename F>
 ssm_status by_width(int width, F&& f) {
@@ -429,7 +452,7 @@ int elem_size(const ssm_conv_packed_params* p) { return p->io_dtype == SSM_BF16 
 size_t bwd_workspace(const ssm_conv_packed_params* p) {
   const PConvArgs a = args_of(p);
   // whichever of the vector and the scalar form runs: the scalar form's tiles are never shorter
-  const int tile = tile_of(a, 16 / elem_size(p), kBwdTile);
+  const int tile = tile_of(a, 16 / elem_size(p), kBwdWaves, kMostTokens);
   return size_t((a.T + tile - 1) / tile) * (p->width + 1) * a.C * 4;
 }
 
@@ -461,7 +484,7 @@ extern "C" ssm_status ssm_conv1d_packed_fwd(const ssm_conv_packed_params* p, con
   a.u = u;
   const bool vec = rows_aligned(x, a.xs, a.C, es) && rows_aligned(u, a.us, a.C, es);
   const int V = vec ? 16 / es : 1;
-  a.tile = tile_of(a, V, kFwdTile);
+  a.tile = tile_of(a, V, kFwdWaves, kMostTokens);
   a.ntiles = (a.T + a.tile - 1) / a.tile;
   const dim3 grid(a.ntiles + a.S, (a.C + V * kThreads - 1) / (V * kThreads));
   if (grid.y > 65535) return fail(SSM_ERR_SHAPE, "dim is too large");
@@ -545,7 +568,7 @@ extern "C" ssm_status ssm_conv1d_packed_bwd(const ssm_conv_packed_params* p, con
   const bool vec = rows_aligned(x, a.xs, a.C, es) && rows_aligned(du, a.dus, a.C, es) &&
                    rows_aligned(dx, a.dxs, a.C, es);
   const int V = vec ? 16 / es : 1;
-  a.tile = tile_of(a, V, kBwdTile);
+  a.tile = tile_of(a, V, kBwdWaves, kMostTokens);
   a.ntiles = (a.T + a.tile - 1) / a.tile;
   const dim3 grid(a.ntiles + (dstate && p->width > 1 ? a.S : 0), (a.C + V * kThreads - 1) / (V * kThreads));
   if (grid.y > 65535) return fail(SSM_ERR_SHAPE, "dim is too large");

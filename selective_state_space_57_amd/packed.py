@@ -16,7 +16,6 @@ Rows outside every sequence are left as they are in outputs too: unset where the
 from __future__ import annotations
 
 import ctypes
-from contextlib import contextmanager
 
 from . import _abi
 from ._abi import EULER_B
@@ -37,6 +36,8 @@ def _dtype_code(t, name):
 
 def _rows(name, t, shape, dtype, device, optional=False):
     """Checks a tensor of rows and returns the stride between them (0 for an absent tensor)."""
+    if t is not None and t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
+        return t.numel() // max(shape[0], 1)
     if t is None:
         if not optional:
             raise ValueError("%s is required" % name)
@@ -61,6 +62,8 @@ def _rows(name, t, shape, dtype, device, optional=False):
 
 def _whole(name, t, shape, dtype, device, optional=True):
     """Checks a contiguous tensor."""
+    if t is not None and t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
+        return
     if t is None:
         if not optional:
             raise ValueError("%s is required" % name)
@@ -81,25 +84,37 @@ def _on_gpu(t, name):
     return t.device
 
 
-@contextmanager
-def _launch(device, stream, *tensors):
+class _launch:
     """The device made current and the stream's handle; tensors made inside belong to that stream, and the memory of
     ``tensors`` is not given away before a given stream has used it."""
-    import torch
-    if stream is None:
-        if device.index == torch.cuda.current_device():
-            yield torch.cuda.current_stream(device).cuda_stream
-            return
-        with torch.cuda.device(device):
-            yield torch.cuda.current_stream(device).cuda_stream
-        return
-    if stream.device != device:
-        raise ValueError("stream: expected one of %s, got %s" % (device, stream.device))
-    with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield stream.cuda_stream
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    __slots__ = ("device", "stream", "tensors", "inside")
+
+    def __init__(self, device, stream, *tensors):
+        self.device, self.stream, self.tensors, self.inside = device, stream, tensors, ()
+
+    def __enter__(self):
+        import torch
+        if self.stream is None:
+            if self.device.index != torch.cuda.current_device():
+                self._enter(torch.cuda.device(self.device))
+            return torch.cuda.current_stream(self.device).cuda_stream
+        if self.stream.device != self.device:
+            raise ValueError("stream: expected one of %s, got %s" % (self.device, self.stream.device))
+        self._enter(torch.cuda.device(self.device))
+        self._enter(torch.cuda.stream(self.stream))
+        return self.stream.cuda_stream
+
+    def _enter(self, context):
+        context.__enter__()
+        self.inside = (context,) + self.inside
+
+    def __exit__(self, *error):
+        for context in self.inside:
+            context.__exit__(*error)
+        if self.stream is not None and error[0] is None:
+            for t in self.tensors:
+                if t is not None:
+                    t.record_stream(self.stream)
 
 
 def _apart(out, name, *ins, may_be=()):
