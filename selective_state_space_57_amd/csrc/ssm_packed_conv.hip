@@ -7,13 +7,16 @@
 // All of it is a stream of x (and du) in and u (dx) out, bound by memory: a thread owns V channels (16 bytes of a row)
 // and walks down a tile of tokens with the K - 1 inputs before it in registers, so each value is read once and a halo
 // of K - 1 rows per tile (out of the L2) on top.  At 4.3 TB/s forward (16384 tokens of 5376 bf16 channels: 81 us); the
-// backward pass, three rows of two inputs and the partial sums of dw on top, 2.6 TB/s (8191 tokens: 100 us).
+// backward pass computes as long as it reads (280 instructions for a wave's row of 512 channels), 3.0 TB/s (8191 tokens:
+// 87 us).
+#include <algorithm>
+
 #include "packed.hpp"
 
 namespace ssm57 {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kBwdThreads = 64;
 
 struct PConvArgs {
   const void* x;
@@ -222,8 +225,8 @@ __global__ void __launch_bounds__(kThreads) packed_conv_step_kernel(PConvArgs a)
 // the token j steps back.  dw and dbias of the tile go to the workspace, summed over the tiles in order afterwards.
 // Block ntiles + s gives the gradient of sequence s's window.
 template <typename T, int V, int K>
-__global__ void __launch_bounds__(kThreads) packed_conv_bwd_kernel(PConvArgs a) {
-  const int c = (blockIdx.y * kThreads + threadIdx.x) * V;
+__global__ void __launch_bounds__(kBwdThreads) packed_conv_bwd_kernel(PConvArgs a) {
+  const int c = (blockIdx.y * kBwdThreads + threadIdx.x) * V;
   if (c >= a.C) return;
   const T* x = static_cast<const T*>(a.x) + c;
   const T* du = static_cast<const T*>(a.du) + c;
@@ -423,17 +426,32 @@ bool rows_aligned(const void* ptr, int64_t stride, int64_t dim, int elem) {
   return aligned(ptr, 16) && stride % v == 0 && dim % v == 0;
 }
 
-// tokens per tile: as long as the launch still has about `waves` for each of the 1024 SIMDs (a longer tile re-reads
-// fewer halo rows and writes fewer partial sums), and at most `most`
-int tile_of(const PConvArgs& a, int v, int waves, int most) {
+// Tokens per tile of the forward: as long as the launch still has about two waves for each of the 1024 SIMDs (a longer
+// tile re-reads fewer halo rows), and at most 64.  Measured on bf16 rows of 5376 channels, width 4, 16384 tokens (352 MB
+// moved): tiles of 16, 32, 40, 64 and 128 tokens 85, 94, 89, 81 and 91 us.
+int fwd_tile(const PConvArgs& a, int v) {
   const int64_t lanes = (a.C + v - 1) / v;
-  int64_t tile = int64_t(a.T) * lanes / (int64_t(waves) * 1024 * 64);
-  tile = tile < 8 ? 8 : (tile > most ? most : tile);
+  int64_t tile = int64_t(a.T) * lanes / (2 * 1024 * 64);
+  tile = tile < 8 ? 8 : (tile > 64 ? 64 : tile);
   return static_cast<int>(tile / 8 * 8);
 }
-// Measured on bf16 rows of 5376 channels, width 4: forward, 16384 tokens (352 MB moved), tiles of 16, 32, 40, 64 and 128
-// tokens (8, 4, 4, 2 and 1 waves) 85, 94, 89, 81 and 91 us; backward, 8191 tokens (264 MB), 32 and 64 tokens 103 and 100.
-constexpr int kFwdWaves = 2, kBwdWaves = 1, kMostTokens = 64;
+// Tokens per tile of the backward, which computes as long as it reads: its waves on the busiest SIMD, times the rows that
+// each of them walks (the halo, and about 8 rows' worth of taps and partial sums, on top), as few as possible.  Measured
+// on 8191 tokens of the same rows (264 MB): 32, 48, 64 and 96 tokens (3, 2, 2 and 1 waves) 105, 87, 100 and 104 us.
+int bwd_tile(const PConvArgs& a, int v, int K) {
+  const int64_t across = (a.C + v * kBwdThreads - 1) / (v * kBwdThreads);
+  int best = 8;
+  int64_t least = INT64_MAX;
+  for (int tile = 8; tile <= 64; tile += 8) {
+    const int64_t waves = (a.T + tile - 1) / tile * across;
+    const int64_t cost = (waves + 1023) / 1024 * (tile + K - 1 + 8);
+    if (cost < least) {
+      least = cost;
+      best = tile;
+    }
+  }
+  return best;
+}
 
 template <typename F>
 ssm_status by_width(int width, F&& f) {
@@ -451,8 +469,8 @@ int elem_size(const ssm_conv_packed_params* p) { return p->io_dtype == SSM_BF16 
 
 size_t bwd_workspace(const ssm_conv_packed_params* p) {
   const PConvArgs a = args_of(p);
-  // whichever of the vector and the scalar form runs: the scalar form's tiles are never shorter
-  const int tile = tile_of(a, 16 / elem_size(p), kBwdWaves, kMostTokens);
+  // for whichever of the vector and the scalar form runs
+  const int tile = std::min(bwd_tile(a, 16 / elem_size(p), p->width), bwd_tile(a, 1, p->width));
   return size_t((a.T + tile - 1) / tile) * (p->width + 1) * a.C * 4;
 }
 
@@ -484,7 +502,7 @@ extern "C" ssm_status ssm_conv1d_packed_fwd(const ssm_conv_packed_params* p, con
   a.u = u;
   const bool vec = rows_aligned(x, a.xs, a.C, es) && rows_aligned(u, a.us, a.C, es);
   const int V = vec ? 16 / es : 1;
-  a.tile = tile_of(a, V, kFwdWaves, kMostTokens);
+  a.tile = fwd_tile(a, V);
   a.ntiles = (a.T + a.tile - 1) / a.tile;
   const dim3 grid(a.ntiles + a.S, (a.C + V * kThreads - 1) / (V * kThreads));
   if (grid.y > 65535) return fail(SSM_ERR_SHAPE, "dim is too large");
@@ -568,17 +586,17 @@ extern "C" ssm_status ssm_conv1d_packed_bwd(const ssm_conv_packed_params* p, con
   const bool vec = rows_aligned(x, a.xs, a.C, es) && rows_aligned(du, a.dus, a.C, es) &&
                    rows_aligned(dx, a.dxs, a.C, es);
   const int V = vec ? 16 / es : 1;
-  a.tile = tile_of(a, V, kBwdWaves, kMostTokens);
+  a.tile = bwd_tile(a, V, p->width);
   a.ntiles = (a.T + a.tile - 1) / a.tile;
-  const dim3 grid(a.ntiles + (dstate && p->width > 1 ? a.S : 0), (a.C + V * kThreads - 1) / (V * kThreads));
+  const dim3 grid(a.ntiles + (dstate && p->width > 1 ? a.S : 0), (a.C + V * kBwdThreads - 1) / (V * kBwdThreads));
   if (grid.y > 65535) return fail(SSM_ERR_SHAPE, "dim is too large");
   hipStream_t st = static_cast<hipStream_t>(stream);
   return by_width(p->width, [&](auto k) {
     constexpr int K = decltype(k)::value;
-    if (es == 2 && vec) hipLaunchKernelGGL((packed_conv_bwd_kernel<uint16_t, 8, K>), grid, dim3(kThreads), 0, st, a);
-    else if (es == 2) hipLaunchKernelGGL((packed_conv_bwd_kernel<uint16_t, 1, K>), grid, dim3(kThreads), 0, st, a);
-    else if (vec) hipLaunchKernelGGL((packed_conv_bwd_kernel<float, 4, K>), grid, dim3(kThreads), 0, st, a);
-    else hipLaunchKernelGGL((packed_conv_bwd_kernel<float, 1, K>), grid, dim3(kThreads), 0, st, a);
+    if (es == 2 && vec) hipLaunchKernelGGL((packed_conv_bwd_kernel<uint16_t, 8, K>), grid, dim3(kBwdThreads), 0, st, a);
+    else if (es == 2) hipLaunchKernelGGL((packed_conv_bwd_kernel<uint16_t, 1, K>), grid, dim3(kBwdThreads), 0, st, a);
+    else if (vec) hipLaunchKernelGGL((packed_conv_bwd_kernel<float, 4, K>), grid, dim3(kBwdThreads), 0, st, a);
+    else hipLaunchKernelGGL((packed_conv_bwd_kernel<float, 1, K>), grid, dim3(kBwdThreads), 0, st, a);
     hipLaunchKernelGGL(packed_conv_reduce_kernel, dim3((a.C + 15) / 16, K + 1), dim3(kThreads), 0, st, a, K);
   });
 }
