@@ -78,6 +78,15 @@ def _whole(name, t, shape, dtype, device, optional=True):
         raise ValueError("%s must be contiguous" % name)
 
 
+def _space(t, device):
+    """Checks a given workspace and returns its bytes."""
+    if t is None:
+        return 0
+    if t.device != device or not t.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor on %s" % device)
+    return t.numel() * t.element_size()
+
+
 def _on_gpu(t, name):
     if not t.is_cuda:
         raise ValueError("%s: expected a tensor on the GPU, got %s" % (name, t.device))
@@ -272,7 +281,7 @@ def conv1d_packed_bwd(x, conv_w, du, cu_seqlens, conv_bias=None, *, state=None, 
         _abi.check(_abi.lib().ssm_conv1d_packed_bwd(
             ctypes.byref(p), _ptr(x), _ptr(conv_w), _ptr(conv_bias), _ptr(cu_seqlens), _ptr(state), _ptr(state_idx),
             _ptr(has_state), _ptr(du), _ptr(dstate_out), _ptr(dx), _ptr(out["dweight"]), _ptr(out["dbias"]),
-            _ptr(out["dstate"]) if K > 1 else 0, _ptr(workspace), workspace.numel() * workspace.element_size(), st))
+            _ptr(out["dstate"]) if K > 1 else 0, _ptr(workspace), _space(workspace, dev), st))
     return out
 
 
@@ -325,7 +334,7 @@ def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, dt_bias=None, Dskip=None, *, stat
         _abi.check(_abi.lib().ssm_ssd_packed_fwd(
             ctypes.byref(p), _ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(Dskip), _ptr(cu_seqlens),
             _ptr(state), _ptr(state_idx), _ptr(has_state), _ptr(state_out), _ptr(y), _ptr(workspace),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), st))
+            _space(workspace, dev), st))
     return y
 
 
@@ -402,7 +411,7 @@ def ssd_packed_bwd(x, dt, A, B, C, dy, cu_seqlens, dt_bias=None, Dskip=None, *, 
             ctypes.byref(p), _ptr(x), _ptr(dt), _ptr(dt_bias), _ptr(A), _ptr(B), _ptr(C), _ptr(Dskip), _ptr(cu_seqlens),
             _ptr(state), _ptr(state_idx), _ptr(has_state), _ptr(dy), _ptr(dstate_out), _ptr(o["dx"]), _ptr(o["ddt"]),
             _ptr(o["dA"]), _ptr(o["dB"]), _ptr(o["dC"]), _ptr(o["dDskip"]), _ptr(o["ddt_bias"]), _ptr(o["dstate"]),
-            _ptr(workspace), workspace.numel() * workspace.element_size(), st))
+            _ptr(workspace), _space(workspace, dev), st))
     return o
 
 
@@ -470,5 +479,5 @@ def gated_norm_bwd(x, weight, dy, bias=None, z=None, *, groups=1, eps=1e-5, gate
             workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
         _abi.check(_abi.lib().ssm_gated_norm_bwd(
             ctypes.byref(p), _ptr(x), _ptr(z), _ptr(weight), _ptr(bias), _ptr(dy), _ptr(dx), _ptr(dz), _ptr(out["dweight"]),
-            _ptr(out["dbias"]), _ptr(workspace), workspace.numel() * workspace.element_size(), st))
+            _ptr(out["dbias"]), _ptr(workspace), _space(workspace, dev), st))
     return out

@@ -299,8 +299,7 @@ def ssd_case(k):
     cu, cul, rows = packed(lens, lead, tail)
     bf = torch.bfloat16
     wide = r(rows, H * 64 + 2 * G * N + extra, dtype=bf)
-    c = dict(cu=cu, x=wide[:, :H * 64].view(rows, H, 64) if extra == 0 and False else
-             wide[:, :H * 64].unflatten(1, (H, 64)))
+    c = dict(cu=cu, x=wide[:, :H * 64].unflatten(1, (H, 64)))
     c["B"] = wide[:, H * 64:H * 64 + G * N].unflatten(1, (G, N))
     c["C"] = wide[:, H * 64 + G * N:H * 64 + 2 * G * N].unflatten(1, (G, N))
     c["dt"] = r.wide(rows, H, 3, bf)
@@ -322,8 +321,8 @@ def ssd_ref(c, cul, first, how):
                  **how)
 
 
-# y stands behind three roundings to bf16 (M, the state's copy, y itself); the state behind the two-part split (2^-16)
-# and decays whose logarithms, up to 2^7 in a chunk, are summed in fp32 (2^-17), a few of them along a sequence
+# y stands behind three roundings to bf16 (M, the state's copy, y itself); the state behind decays whose logarithms, up to
+# 2^7 in a chunk, are summed in fp32 (2^-17), a few of them along a sequence, and far smaller roundings of its products
 TOL_Y, TOL_STATE = 3 * BF, 2.0 ** -15
 
 
@@ -403,8 +402,8 @@ def test_ssd_packed_bwd(k):
     torch.cuda.synchronize()
     assert got["dx"] is out["dx"] and got["dB"] is out["dB"]
     # dx: M, G and dx itself are rounded to bf16; dB and dC: the head sum K and the outputs; ddt: itself, on fp32 sums.
-    # The fp32 sums behind dA, ddt_bias, ddt: the two-part splits (2^-16) and the decays' logarithms (2^-17), a few of
-    # them in every term: 2^-14
+    # The fp32 sums behind dA, ddt_bias, ddt: products (2^-16 at most) and the decays' logarithms (2^-17), a few of them
+    # in every term: 2^-14
     near(got["dx"][inside], ref["dx"][inside], 3 * BF, "dx")
     near(got["dB"][inside], ref["dB"][inside], 3 * BF, "dB")
     near(got["dC"][inside], ref["dC"][inside], 3 * BF, "dC")
