@@ -331,13 +331,14 @@ struct StatesArgs {
   float* last;           // [seqs][H][64][N] or null: the state behind the whole walk of a sequence
   float* ws_state;       // [nseg][H][64][N]: state entering each segment (where a sequence has more than one)
   float* ws_decay;       // [nseg][H]
-  float* save;           // [chunk numbers][H][N][64] or null: state entering each chunk, transposed
+  float* save;           // [chunk numbers][H][N][64] or null (no walk behind the join): state entering each chunk, transposed
   int64_t vs, ks, dts, nslots;
-  int T, S, H, G, hpg, hblocks, cps, nseg, nwork;
+  int T, S, H, G, hpg, hblocks, cps, nseg;
   int softplus, zoh;
 };
-// Brings ws_state up to date where a sequence can have several segments (split), and then, with save or last, walks all.
-ssm_status launch_states(StatesArgs a, int dstate, bool reverse, bool split, hipStream_t st);
+// Brings ws_state up to date where a sequence can have several segments (split), and then, with save, walks all: f in
+// order, and beside it r, over the same segments, in reverse order (or null).
+ssm_status launch_states(const StatesArgs& f, const StatesArgs* r, int dstate, bool split, hipStream_t st);
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 

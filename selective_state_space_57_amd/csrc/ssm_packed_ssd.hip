@@ -541,7 +541,7 @@ extern "C" ssm_status ssm_ssd_packed_fwd(const ssm_ssd_packed_params* p, const v
     w.nseg = static_cast<int>(pl.nseg);
     w.softplus = a.softplus;
     w.zoh = a.zoh;
-    if (ssm_status s = launch_states(w, static_cast<int>(p->dstate), false, true, st); s != SSM_OK) return s;
+    if (ssm_status s = launch_states(w, nullptr, static_cast<int>(p->dstate), true, st); s != SSM_OK) return s;
   }
   switch (p->dstate) {
     case 64: return launch_fwd<64>(a, st);

@@ -510,7 +510,7 @@ BwdPlan bwd_plan(const ssm_ssd_packed_params* p) {
   b.ws_decay = b.walk.split ? up256(size_t(b.walk.nseg) * p->nheads * 4) : 0;
   b.part = up256(size_t(b.splits) * p->ntokens * p->ngroups * p->dstate * 4);
   b.part_h = up256(size_t(b.numbers) * p->nheads * 16);
-  b.total = 2 * b.states + b.ws_state + b.ws_decay + 2 * b.part + b.part_h;
+  b.total = 2 * (b.states + b.ws_state + b.ws_decay + b.part) + b.part_h;
   return b;
 }
 
@@ -580,6 +580,8 @@ extern "C" ssm_status ssm_ssd_packed_bwd(const ssm_ssd_packed_params* p, const v
   StatesArgs w{};
   w.ws_state = take(b.ws_state);
   w.ws_decay = take(b.ws_decay);
+  float* walk_g = take(b.ws_state);
+  float* decay_g = take(b.ws_decay);
   a.part_b = take(b.part);
   a.part_c = take(b.part);
   a.part_h = take(b.part_h);
@@ -629,7 +631,7 @@ extern "C" ssm_status ssm_ssd_packed_bwd(const ssm_ssd_packed_params* p, const v
   w.nseg = static_cast<int>(b.walk.nseg);
   w.softplus = a.softplus;
   w.zoh = a.zoh;
-  // the states, forward from the slots, then the adjoints, in reverse order from dstate_out
+  // the states, forward from the slots, and the adjoints, in reverse order from dstate_out
   w.v = a.x;
   w.vs = a.xs;
   w.k = a.B;
@@ -639,18 +641,20 @@ extern "C" ssm_status ssm_ssd_packed_bwd(const ssm_ssd_packed_params* p, const v
   w.has = has_state;
   w.nslots = p->nslots;
   w.save = save_s;
-  if (ssm_status s = launch_states(w, static_cast<int>(p->dstate), false, b.walk.split, st); s != SSM_OK) return s;
-  w.v = a.dy;
-  w.vs = a.dys;
-  w.k = a.C;
-  w.ks = a.cs;
-  w.init = dstate_out;
-  w.idx = nullptr;
-  w.has = nullptr;
-  w.nslots = p->nseqs;
-  w.save = save_g;
-  w.last = dstate;
-  if (ssm_status s = launch_states(w, static_cast<int>(p->dstate), true, b.walk.split, st); s != SSM_OK) return s;
+  StatesArgs r = w;
+  r.ws_state = walk_g;
+  r.ws_decay = decay_g;
+  r.v = a.dy;
+  r.vs = a.dys;
+  r.k = a.C;
+  r.ks = a.cs;
+  r.init = dstate_out;
+  r.idx = nullptr;
+  r.has = nullptr;
+  r.nslots = p->nseqs;
+  r.save = save_g;
+  r.last = dstate;
+  if (ssm_status s = launch_states(w, &r, static_cast<int>(p->dstate), b.walk.split, st); s != SSM_OK) return s;
   switch (p->dstate) {
     case 64: launch_bwd<64>(a, st); break;
     case 128: launch_bwd<128>(a, st); break;

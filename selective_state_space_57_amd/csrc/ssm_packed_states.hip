@@ -15,15 +15,11 @@ constexpr int kParts = 2;   // waves of a head
 
 // SAVE: the walk proper; otherwise the first pass, each segment from zero
 template <int N, bool REV, bool SAVE>
-__global__ void __launch_bounds__(kWalkWaves * 64) __attribute__((amdgpu_waves_per_eu(N == 256 ? 2 : 4, N == 256 ? 2 : 4)))
-packed_states_kernel(StatesArgs a) {
+__device__ __forceinline__ void walk(const StatesArgs& a, uint16_t* sK0, uint16_t* sK1, uint16_t* V, float* W) {
   constexpr int U = N / 8;
   constexpr int NT = N / 16;             // 16-row tiles of the state
   constexpr int kWaves = kWalkWaves;
   constexpr int UV = 2 * PT;             // 16-byte units of its columns
-  __shared__ alignas(16) uint16_t sK0[kChunk * N], sK1[kChunk * N];
-  __shared__ alignas(16) uint16_t sV[kWaves][kChunk * 16 * PT];
-  __shared__ alignas(16) float sW[kWaves][kChunk];
 
   // (in launch order, heads fastest: the heads of a segment go round the XCDs, so that segments of any length, and numbers
   // without one, spread evenly; runs of items per XCD, which share B and C in its L2, left some with two rounds)
@@ -64,7 +60,6 @@ packed_states_kernel(StatesArgs a) {
     place(i, t0, rows);
     copy_rows<U, kWaves>(dst, chunk_rsrc(kg, t0, a.ks, rows, N), wave, lane, krow);
   };
-  uint16_t* V = sV[wave];
   auto copy_v = [&](int i) __attribute__((always_inline)) {
     int64_t t0;
     int rows;
@@ -126,7 +121,6 @@ packed_states_kernel(StatesArgs a) {
               __builtin_amdgcn_raw_buffer_load_b32(r, lane_entry, ((4 * pt + c) * N + 16 * nt) * 4, 0));
   }
   float decay = 0.0f;   // sum of log2 decays over the segment (first pass)
-  float* W = sW[wave];
 
   auto chunk = [&](const int i, const uint16_t* K, uint16_t* Kn, const uint32_t dtv) __attribute__((always_inline))
                -> uint32_t {
@@ -138,7 +132,7 @@ packed_states_kernel(StatesArgs a) {
     int rows;
     place(i, t0, rows);
     if constexpr (SAVE) {
-      if (a.save && on)   // the chunk's number: its place in the sequence behind that of the sequence's first
+      if (on)   // the chunk's number: its place in the sequence behind that of the sequence's first
         save(a.save + ((int64_t(seg.seq) + seg.begin / kChunk + (static_cast<int>(t0) - seg.begin) / kChunk) * a.H + h) *
                           head_size);
     }
@@ -198,10 +192,24 @@ packed_states_kernel(StatesArgs a) {
   }
 }
 
+// The walk over states (f) and, in blocks of y = 1, the one over adjoints in reverse order (r), which do not depend on each
+// other: side by side they fill the CUs that either one's last round leaves idle.
+template <int N, bool SAVE>
+__global__ void __launch_bounds__(kWalkWaves * 64) __attribute__((amdgpu_waves_per_eu(N == 256 ? 2 : 4, N == 256 ? 2 : 4)))
+packed_states_kernel(StatesArgs f, StatesArgs r) {
+  __shared__ alignas(16) uint16_t sK0[kChunk * N], sK1[kChunk * N];
+  __shared__ alignas(16) uint16_t sV[kWalkWaves][kChunk * 16 * PT];
+  __shared__ alignas(16) float sW[kWalkWaves][kChunk];
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  if (blockIdx.y == 0) walk<N, false, SAVE>(f, sK0, sK1, sV[wave], sW[wave]);
+  else walk<N, true, SAVE>(r, sK0, sK1, sV[wave], sW[wave]);
+}
+
 // Joins the segments of a sequence in walk order: the end state that the first pass left for a segment (from zero) gives
 // way to the state entering the segment.  A thread owns four entries; nothing to do for one segment.
-template <bool REV>
-__global__ void __launch_bounds__(256) packed_join_kernel(StatesArgs a, int entries) {
+__global__ void __launch_bounds__(256) packed_join_kernel(StatesArgs f, StatesArgs r, int entries) {
+  const bool rev = blockIdx.z != 0;
+  const StatesArgs& a = rev ? r : f;
   Piece seg;
   pieces_of(a.cu, blockIdx.x, a.T, a.cps * kChunk, seg);
   const int count = min(seg.count, a.nseg - seg.first);   // (only a cu_seqlens out of order reaches this bound)
@@ -216,7 +224,7 @@ __global__ void __launch_bounds__(256) packed_join_kernel(StatesArgs a, int entr
     if (slot >= 0) s = *reinterpret_cast<const pf4*>(a.init + slot * per + e);
   }
   for (int i = 0; i < count; ++i) {
-    const int64_t j = seg.first + (REV ? count - 1 - i : i);
+    const int64_t j = seg.first + (rev ? count - 1 - i : i);
     float* at = a.ws_state + j * per + e;
     const bool more = i + 1 < count;
     const pf4 own = more ? *reinterpret_cast<const pf4*>(at) : pf4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -226,28 +234,29 @@ __global__ void __launch_bounds__(256) packed_join_kernel(StatesArgs a, int entr
   }
 }
 
-template <int N, bool REV>
-ssm_status launch_states_of(const StatesArgs& a, bool split, hipStream_t st) {
-  const dim3 grid(a.nwork), block(kWalkWaves * 64);
+template <int N>
+ssm_status launch_states_of(const StatesArgs& f, const StatesArgs& r, int walks, bool split, hipStream_t st) {
+  const dim3 grid(f.nseg * f.G * f.hblocks, walks), block(kWalkWaves * 64);
   if (split) {
-    hipLaunchKernelGGL((packed_states_kernel<N, REV, false>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((packed_states_kernel<N, false>), grid, block, 0, st, f, r);
     const int64_t entries = int64_t(kHead) * N;
-    hipLaunchKernelGGL(packed_join_kernel<REV>, dim3(a.S, static_cast<uint32_t>((a.H * entries / 4 + 255) / 256)),
-                       dim3(256), 0, st, a, static_cast<int>(entries));
+    hipLaunchKernelGGL(packed_join_kernel, dim3(f.S, static_cast<uint32_t>((f.H * entries / 4 + 255) / 256), walks),
+                       dim3(256), 0, st, f, r, static_cast<int>(entries));
   }
-  if (a.save || a.last) hipLaunchKernelGGL((packed_states_kernel<N, REV, true>), grid, block, 0, st, a);
+  if (f.save) hipLaunchKernelGGL((packed_states_kernel<N, true>), grid, block, 0, st, f, r);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SSM_OK : fail(SSM_ERR_HIP, "packed SSD states launch: %s", hipGetErrorString(e));
 }
 
 }  // namespace
 
-ssm_status launch_states(StatesArgs a, int dstate, bool reverse, bool split, hipStream_t st) {
-  a.nwork = a.nseg * a.G * a.hblocks;
+ssm_status launch_states(const StatesArgs& f, const StatesArgs* r, int dstate, bool split, hipStream_t st) {
+  const int walks = r ? 2 : 1;
+  const StatesArgs& back = r ? *r : f;
   switch (dstate) {
-    case 64: return reverse ? launch_states_of<64, true>(a, split, st) : launch_states_of<64, false>(a, split, st);
-    case 128: return reverse ? launch_states_of<128, true>(a, split, st) : launch_states_of<128, false>(a, split, st);
-    default: return reverse ? launch_states_of<256, true>(a, split, st) : launch_states_of<256, false>(a, split, st);
+    case 64: return launch_states_of<64>(f, back, walks, split, st);
+    case 128: return launch_states_of<128>(f, back, walks, split, st);
+    default: return launch_states_of<256>(f, back, walks, split, st);
   }
 }
 
