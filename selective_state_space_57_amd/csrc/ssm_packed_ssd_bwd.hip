@@ -40,8 +40,8 @@ struct BwdArgs {
   const float* A;
   const float* Dskip;
   const int32_t* cu;
-  const float* S;      // [numbers][H][N][64]: state entering each chunk
-  const float* Gs;     // [numbers][H][N][64]: adjoint behind it
+  const float* S;      // [numbers][H][64 N] as state_operand lays them out: state entering each chunk
+  const float* Gs;     // likewise: adjoint behind it
   uint16_t* dx;
   uint16_t* ddt;
   uint16_t* dB;
@@ -152,12 +152,11 @@ packed_ssd_bwd_kernel(BwdArgs a) {
     const auto rs = make_rsrc(a.S + (int64_t(number) * a.H + h) * head_size, head_size);
     const auto rg = make_rsrc(a.Gs + (int64_t(number) * a.H + h) * head_size, head_size);
     const int l = afresh(lane);
-    const int at = ((16 * nt + (l & 15)) * kHead + 8 * (l >> 4)) * 4;
+    const int at = state_operand(nt, 0, l);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int p = (32 * (i >> 1) + 4 * (i & 1)) * 4;
-      S[i] = __builtin_bit_cast(pf4, __builtin_amdgcn_raw_buffer_load_b128(rs, at, p, 0));
-      G[i] = __builtin_bit_cast(pf4, __builtin_amdgcn_raw_buffer_load_b128(rg, at, p, 0));
+      S[i] = __builtin_bit_cast(pf4, __builtin_amdgcn_raw_buffer_load_b128(rs, at, state_operand(0, i, 0), 0));
+      G[i] = __builtin_bit_cast(pf4, __builtin_amdgcn_raw_buffer_load_b128(rg, at, state_operand(0, i, 0), 0));
     }
   };
 

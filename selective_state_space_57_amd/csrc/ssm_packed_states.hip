@@ -90,15 +90,15 @@ __device__ __forceinline__ void walk(const StatesArgs& a, uint16_t* sK0, uint16_
           __builtin_amdgcn_raw_buffer_store_b32(__float_as_int(v), r, lane_entry, ((4 * pt + c) * N + 16 * nt) * 4, 0);
         }
   };
-  // the state with n as rows
+  // the state as operands over p (state_operand): a tile and lane after the other
   auto save = [&](float* to) __attribute__((always_inline)) {
     const auto r = make_rsrc(to, head_size);
-    const int at = (l16 * kHead + p0 + 8 * g4) * 4;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int pt = 0; pt < PT; ++pt)
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(pu4, S[nt][pt]), r, at, (16 * nt * kHead + 4 * pt) * 4, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(pu4, S[nt][pt]), r, state_operand(0, p0 / 16, lane),
+                                               state_operand(nt, pt, 0), 0);
   };
   {
     const float* from = nullptr;
