@@ -315,14 +315,14 @@ struct PackedPlan {
 };
 PackedPlan packed_plan(const ssm_ssd_packed_params* p);
 
-// A walk over the states of packed sequences, chunk by chunk and from each sequence's first state (ssm_packed_states.hip):
-// forward, S <- exp(c_63) S + sum_s (phi_s exp(c_63 - c_s) v_s) k_s^T with v = x, k = B, or in reverse order,
-// G <- exp(c_63) G + sum_t exp(c_t) v_t k_t^T with v = dy, k = C.
 // Byte of a lane's four values of a saved state: S[p][n] for n = 16 nt + lane % 16, p = 32 (i / 2) + 8 (lane / 16) +
 // 4 (i % 2) + 0..3, so that tiles 2j and 2j + 1 are an operand over 32 p, and a wave's access one run of 1 KB (against rows
 // of 64 p, 16 bytes of every 32 at a time: walks of 16384 tokens, 2.7B layer, 379 instead of 483 us).
 __host__ __device__ constexpr int state_operand(int nt, int i, int lane) { return ((nt * 4 + i) * 64 + lane) * 16; }
 
+// A walk over the states of packed sequences, chunk by chunk and from each sequence's first state (ssm_packed_states.hip):
+// forward, S <- exp(c_63) S + sum_s (phi_s exp(c_63 - c_s) v_s) k_s^T with v = x, k = B, or in reverse order,
+// G <- exp(c_63) G + sum_t exp(c_t) v_t k_t^T with v = dy, k = C.
 struct StatesArgs {
   const uint16_t* v;
   const uint16_t* k;

@@ -15,9 +15,14 @@
 // segment first, and all segments run at once.
 //
 // Precision: fp32 state and accumulation; x, B and C enter the matrix cores as they are.  The weighted x of the state
-// update is split into three bf16 parts, so the state keeps fp32 quality over long sequences.  M (but for s = t) and
-// the state's copy that meets C are rounded once to bf16 (2^-9 relative, as the output is): they only reach y, which is
-// rounded to bf16 itself.
+// update is split into three bf16 parts, so the state keeps fp32 quality over long sequences (two parts, 2^-17, are 11 %
+// faster).  M (but for s = t) and the state's copy that meets C are rounded once to bf16 (2^-8 at most, as the output
+// is): they only reach y, which is rounded to bf16 itself.
+//
+// Measured on 16384 tokens of 80 heads, N = 128 (0.40 GB in and out, 43 GFLOP): 280 us, 200 of them this pass, 85 the walk
+// and its join.  VALU busy 45 % of the cycles, MFMA 18 %, the rest waits: leaving out a part saves 70 us (M x and C S^T),
+// 53 (the state's update), 19 (the stores) or 6 (C B^T).  The step kernel: 256 tokens of the same layer 250 us, 5.4 TB/s
+// of states.
 #include "packed_ssd.hpp"
 
 namespace ssm57 {

@@ -13,18 +13,21 @@
 // Every sum in dl_r has the decays of what it stands for in it, so nothing large cancels: only the row and column sums
 // of W do, and those are sums of the same fp32 numbers.
 //
-// Two walks (ssm_packed_states.hip) leave S and G of every chunk, transposed, so that a lane's eight consecutive p are an
-// operand; then a workgroup takes a chunk and runs over heads one after the other.  A wave has 16 of the N columns of the states,
-// for every head: the sums of dB and dC over heads add up in its registers.  K is summed over heads in registers as well,
-// and multiplied with B and C once at the end.  What a head needs across waves (dx, and the sums over n in u, v and
-// <G, S>) goes through LDS.  The next head's states and x are on their way while this head's dx is computed.
+// Two walks (ssm_packed_states.hip) leave S and G of every chunk, laid out as operands over p; then a workgroup takes a
+// chunk and runs over heads one after the other.  A wave has 16 of the N columns of the states, for every head: the sums
+// of dB and dC over heads add up in its registers.  K is summed over heads in registers as well, and multiplied with B and
+// C once at the end.  What a head needs across waves (dx, and the sums over n in u, v and <G, S>) goes through LDS.  The
+// next head's states and x are on their way while this head's dx is computed.
 // Two workgroups share a CU (N <= 128), so that one's barriers and loads run beside the other's products: with chunks of
 // 128 steps to a workgroup, which halve the saved states but recompute them in between, one filled the LDS and took
-// 790 us instead of xxx for the 2.7B layer at 16384 tokens.
+// 790 us instead of 566 (2.7B layer, 16384 tokens, states in two bf16 parts each).
+// Measured on that layer: 642 us with three parts, in a call of 1081 us whose walks, join and sums over heads are the rest.
+// It reads 1.3 GB of states and 0.35 GB of inputs (2.6 TB/s) and multiplies at about 12 % of the matrix cores' cycles,
+// VALU 35 %: no single one is full, the six stages of a head with their five barriers are its time.
 //
-// Precision: fp32 accumulation; the states are split into three bf16 parts, so that u, v and <G, S>, and with them dDelta and dA, are good to fp32 quality.  G in dx, M = L Z phi
-// and the head sum K (both but for s = t, which is added in fp32) are rounded once to bf16: they only reach dx, dB and
-// dC, which are bf16 themselves.
+// Precision: fp32 accumulation; the states are split into three bf16 parts, so that u, v and <G, S>, and with them dDelta
+// and dA, are good to fp32 quality.  G in dx, M = L Z phi and the head sum K (both but for s = t, which is added in fp32)
+// are rounded once to bf16: they only reach dx, dB and dC, which are bf16 themselves.
 #include "packed_ssd.hpp"
 
 namespace ssm57 {
@@ -99,6 +102,10 @@ packed_ssd_bwd_kernel(BwdArgs a) {
   __shared__ alignas(16) uint16_t sG[N * kHead];       // G, transposed
   __shared__ ChunkScalars sc;
   __shared__ float sU[NW][kChunk], sV[NW][kChunk], sE[NW];
+  // of 8 waves, two have a second tile of K: it waits in LDS and not in a register of every wave, one of which the compiler
+  // would keep in scratch memory (16384 tokens, 2.7B layer: 642 us, else 690)
+  constexpr int kHeld = NW == 8 ? 1 : kTiles;
+  __shared__ pf4 sK2[kHeld < kTiles ? 2 : 1][64];
   __shared__ float sRow[10][16], sCol[10][16], sOwn[4][16], sDirect[4][16], sDiag[4], sTotal[10];
 
   const int item = xcd_item();
@@ -134,11 +141,12 @@ packed_ssd_bwd_kernel(BwdArgs a) {
     barrier_lds();
   }
   pf4 aB[4], aC[4];   // dB^T, dC^T: n = 16 nt + 4 g4 + c, step 16 b + l16
-  pf4 aK[kTiles];     // K: rows t, columns s
+  pf4 aK[kHeld];      // K: rows t, columns s
 #pragma unroll
   for (int b = 0; b < 4; ++b) aB[b] = aC[b] = zero;
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i) aK[i] = zero;
+  for (int i = 0; i < kHeld; ++i) aK[i] = zero;
+  if (kHeld < kTiles && nt < 10 - NW) sK2[nt][lane] = zero;
   const int64_t head_size = int64_t(kHead) * N;
 
   const uint32_t xrow = static_cast<uint32_t>(a.xs) * 2u, yrow = static_cast<uint32_t>(a.dys) * 2u;
@@ -256,13 +264,13 @@ packed_ssd_bwd_kernel(BwdArgs a) {
         Z = mma(lds_row_operand<U>(Ck, 16 * tb + l16, kk, g4), lds_row_operand<U>(Bk, 16 * sb + l16, kk, g4), Z);
       }
       part_ends();
-      part_ends();
+      pf4 k = ti < kHeld ? aK[min(ti, kHeld - 1)] : sK2[nt][l];
       float m[4], row[4], col = 0.0f;
       if (sb < tb) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const float L = hw_exp2(ct[c] - cs), lx = L * X[c];
-          aK[ti][c] = fmaf(lx, ph, aK[ti][c]);
+          k[c] = fmaf(lx, ph, k[c]);
           m[c] = L * Z[c] * ph;
           const float w0 = lx * Z[c];
           row[c] = w0 * ph;
@@ -274,7 +282,7 @@ packed_ssd_bwd_kernel(BwdArgs a) {
         for (int c = 0; c < 4; ++c) {
           const int above = l16 - (4 * g4 + c);   // column minus row
           const float L = above <= 0 ? hw_exp2(ct[c] - cs) : 0.0f, lx = L * X[c];
-          aK[ti][c] = fmaf(lx, ph, aK[ti][c]);
+          k[c] = fmaf(lx, ph, k[c]);
           const float mm = L * Z[c] * ph, w0 = lx * Z[c];
           // a step's own terms: its dy goes into its dx in fp32, together with D, and W[t][t] is in its row and in its
           // column and would cancel but for rounding
@@ -295,7 +303,12 @@ packed_ssd_bwd_kernel(BwdArgs a) {
         if (l == 0) sDiag[tb] = diag;
       }
       reinterpret_cast<pu2*>(&sM[m_slot(sb, tb >> 1)][l])[tb & 1] = bf16x4(m[0], m[1], m[2], m[3]);
-      asm volatile("" : "+v"(aK[ti]));
+      if (ti < kHeld) {
+        aK[min(ti, kHeld - 1)] = k;
+        asm volatile("" : "+v"(aK[min(ti, kHeld - 1)]));
+      } else {
+        sK2[nt][l] = k;
+      }
       part_ends();
 #pragma unroll
       for (int c = 0; c < 4; ++c) row[c] = sum_row(row[c]);
@@ -404,7 +417,7 @@ packed_ssd_bwd_kernel(BwdArgs a) {
     const int i = nt + NW * ti;
     if (i >= 10) break;
     const int tb = tile_row(i), sb = i - tb * (tb + 1) / 2;
-    pf4 v = aK[ti];
+    pf4 v = ti < kHeld ? aK[min(ti, kHeld - 1)] : sK2[nt][lane];
     if (sb == tb) {   // a step's own term is added in fp32
       float own = 0.0f;
 #pragma unroll

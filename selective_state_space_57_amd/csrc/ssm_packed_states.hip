@@ -1,10 +1,13 @@
 // The states of packed SSD sequences where other kernels start from them: at the segments of the forward, and at every
 // chunk for the backward, together with the adjoint states, which are walked in reverse order.
 //
-// As in the forward, a workgroup takes 4 heads of one group over one segment, a wave holds the state of
-// half of a head's columns in registers, and the shared k rows (B or C) go to LDS once for all waves.  The
-// weighted v rows are split into three bf16 parts, so states keep fp32 quality.  A sequence of several
-// segments takes three launches: every segment from zero, a join in order, and the walk proper.
+// As in the forward, a workgroup takes 4 heads of one group over one segment, a wave holds the state of half of a head's
+// columns in registers, and the shared k rows (B or C) go to LDS once for all waves.  The weighted v rows are split into
+// three bf16 parts, so states keep fp32 quality.  A sequence of several segments takes three launches: every segment from
+// zero, a join in order, and the walk proper, which saves the state entering every chunk.
+//
+// Measured on 16384 tokens of 80 heads, N = 128: the forward's first pass 85 us and its join 20; for the backward both first
+// passes 140 us, the joins 38 and both walks 360, in which they write 1.3 GB (3.7 TB/s): the saving is their bound.
 #include "packed_ssd.hpp"
 
 namespace ssm57 {
