@@ -20,7 +20,7 @@
 // is): they only reach y, which is rounded to bf16 itself.
 //
 // Measured on 16384 tokens of 80 heads, N = 128 (0.40 GB in and out, 43 GFLOP): 280 us, 200 of them this pass, 85 the walk
-// and its join.  VALU busy 45 % of the cycles, MFMA 18 %, the rest waits: leaving out a part saves 70 us (M x and C S^T),
+// and its join.  VALU 42 % of the cycles, MFMA 19 %, the rest waits: leaving out a part saves 70 us (M x and C S^T),
 // 53 (the state's update), 19 (the stores) or 6 (C B^T).  The step kernel: 256 tokens of the same layer 250 us, 5.4 TB/s
 // of states.
 #include "packed_ssd.hpp"

@@ -22,8 +22,8 @@
 // 128 steps to a workgroup, which halve the saved states but recompute them in between, one filled the LDS and took
 // 790 us instead of 566 (2.7B layer, 16384 tokens, states in two bf16 parts each).
 // Measured on that layer: 642 us with three parts, in a call of 1081 us whose walks, join and sums over heads are the rest.
-// It reads 1.3 GB of states and 0.35 GB of inputs (2.6 TB/s) and multiplies at about 12 % of the matrix cores' cycles,
-// VALU 35 %: no single one is full, the six stages of a head with their five barriers are its time.
+// It reads 1.4 GB of states and 0.34 GB of inputs (2.7 TB/s), MFMA 11 % and VALU 41 % of the cycles: no single one is full,
+// the stages of a head and the barriers between them are its time.
 //
 // Precision: fp32 accumulation; the states are split into three bf16 parts, so that u, v and <G, S>, and with them dDelta
 // and dA, are good to fp32 quality.  G in dx, M = L Z phi and the head sum K (both but for s = t, which is added in fp32)
