@@ -226,14 +226,19 @@ struct Piece {
   int seq, begin, end;   // sequence and its tokens
   int index, count;      // piece within the sequence, and how many it has (an empty sequence has one)
   int first;             // number of the sequence's first piece
+  int place;             // of its first piece among those of sequences that have several
 };
 __host__ __device__ constexpr int64_t piece_numbers(int64_t nseqs, int64_t ntokens, int64_t steps) {
   return nseqs + ntokens / steps + 1;
 }
+// What only sequences of several pieces need is kept at place 2 (b / steps) + i: a sequence longer than `steps` has at most
+// twice as many pieces as it has whole ones, so these stay apart, and below 2 (ntokens / steps) however many sequences.
+__host__ __device__ constexpr int64_t piece_places(int64_t ntokens, int64_t steps) { return 2 * (ntokens / steps); }
 __device__ __forceinline__ void pieces_of(const int32_t* cu, int s, int ntokens, int steps, Piece& p) {
   seq_range(cu, s, ntokens, p.begin, p.end);
   p.seq = s;
   p.first = s + p.begin / steps;
+  p.place = 2 * (p.begin / steps);
   p.count = max((p.end - p.begin + steps - 1) / steps, 1);
 }
 // The piece of that number; false where there is none.
@@ -311,6 +316,7 @@ struct PackedPlan {
   int hblocks;    // workgroups per group of heads
   int cps;        // chunks per segment
   int64_t nseg;   // numbers of segments
+  int64_t places; // for the states that enter segments
   bool split;     // whether a sequence can have more than one
 };
 PackedPlan packed_plan(const ssm_ssd_packed_params* p);
@@ -334,8 +340,8 @@ struct StatesArgs {
   const int32_t* idx;
   const uint8_t* has;
   float* last;           // [seqs][H][64][N] or null: the state behind the whole walk of a sequence
-  float* ws_state;       // [nseg][H][64][N]: state entering each segment (where a sequence has more than one)
-  float* ws_decay;       // [nseg][H]
+  float* ws_state;       // [places][H][64][N]: state entering each segment (where a sequence has more than one)
+  float* ws_decay;       // [places][H]
   float* save;           // [chunk numbers][H][64 N] or null (no walk behind the join): state entering each chunk
   int64_t vs, ks, dts, nslots;
   int T, S, H, G, hpg, hblocks, cps, nseg;

@@ -42,7 +42,7 @@ struct PSsdArgs {
   const uint8_t* has;
   float* state_out;
   uint16_t* y;
-  const float* ws_state;   // [segments][H][64][N]: the state entering each, where a sequence has several
+  const float* ws_state;   // [places][H][64][N]: the state entering each, where a sequence has several
   int64_t xs, dts, bs, cs, ys, nslots;
   int T, S, H, G, hpg, hblocks;   // hblocks: workgroups per group
   int cps, nwork;
@@ -128,7 +128,7 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
   {
     const float* from = nullptr;
     if (seg.count > 1) {
-      from = a.ws_state + (int64_t(seg.first + seg.index) * a.H + h) * head_size;
+      from = a.ws_state + (int64_t(seg.place + seg.index) * a.H + h) * head_size;
     } else if (a.state && (!a.has || a.has[seg.seq])) {
       const int64_t slot = slot_of(a.idx, seg.seq, a.nslots);
       if (slot >= 0) from = a.state + (slot * a.H + h) * head_size;
@@ -387,7 +387,7 @@ ssm_status launch_step(const PSsdArgs& a, hipStream_t st) {
 size_t fwd_workspace(const ssm_ssd_packed_params* p) {
   const PackedPlan pl = packed_plan(p);
   if (!pl.split) return 0;
-  return up256(size_t(pl.nseg) * p->nheads * kHead * p->dstate * 4) + up256(size_t(pl.nseg) * p->nheads * 4);
+  return up256(size_t(pl.places) * p->nheads * kHead * p->dstate * 4) + up256(size_t(pl.places) * p->nheads * 4);
 }
 
 PSsdArgs ssd_args(const ssm_ssd_packed_params* p) {
@@ -470,6 +470,7 @@ PackedPlan packed_plan(const ssm_ssd_packed_params* p) {
   pl.cps = static_cast<int>(cps);
   pl.split = longest > cps;
   pl.nseg = piece_numbers(p->nseqs, p->ntokens, cps * kChunk);
+  pl.places = piece_places(p->ntokens, cps * kChunk);
   return pl;
 }
 
@@ -531,7 +532,7 @@ extern "C" ssm_status ssm_ssd_packed_fwd(const ssm_ssd_packed_params* p, const v
     w.has = has_state;
     w.ws_state = static_cast<float*>(workspace);
     w.ws_decay = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                          up256(size_t(pl.nseg) * p->nheads * kHead * p->dstate * 4));
+                                          up256(size_t(pl.places) * p->nheads * kHead * p->dstate * 4));
     w.vs = a.xs;
     w.ks = a.bs;
     w.dts = a.dts;

@@ -518,8 +518,8 @@ BwdPlan bwd_plan(const ssm_ssd_packed_params* p) {
   b.splits = static_cast<int>((hpg + b.hps - 1) / b.hps);
   const size_t state = size_t(p->nheads) * kHead * p->dstate * 4;
   b.states = up256(size_t(b.numbers) * state);
-  b.ws_state = b.walk.split ? up256(size_t(b.walk.nseg) * state) : 0;
-  b.ws_decay = b.walk.split ? up256(size_t(b.walk.nseg) * p->nheads * 4) : 0;
+  b.ws_state = b.walk.split ? up256(size_t(b.walk.places) * state) : 0;
+  b.ws_decay = b.walk.split ? up256(size_t(b.walk.places) * p->nheads * 4) : 0;
   b.part = up256(size_t(b.splits) * p->ntokens * p->ngroups * p->dstate * 4);
   b.part_h = up256(size_t(b.numbers) * p->nheads * 16);
   b.total = 2 * (b.states + b.ws_state + b.ws_decay + b.part) + b.part_h;

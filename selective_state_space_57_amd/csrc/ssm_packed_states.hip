@@ -35,7 +35,7 @@ __device__ __forceinline__ void walk(const StatesArgs& a, uint16_t* sK0, uint16_
   if (!find_piece(a.cu, a.S, a.T, a.cps * kChunk, item / (a.G * a.hblocks), seg)) return;
   // (nothing starts from the end of the walk's last segment)
   if (!SAVE && seg.index == (REV ? 0 : seg.count - 1)) return;
-  const int64_t number = seg.first + seg.index;
+  const int64_t kept = seg.place + seg.index;
   const int g = hb / a.hblocks;
   const int hg = (hb % a.hblocks) * (kWaves / kParts) + wave / kParts;   // head within the group
   const int p0 = (wave % kParts) * 16 * PT;                              // first column of this wave
@@ -107,7 +107,7 @@ __device__ __forceinline__ void walk(const StatesArgs& a, uint16_t* sK0, uint16_
     const float* from = nullptr;
     if constexpr (SAVE) {
       if (seg.count > 1) {
-        from = a.ws_state + (number * a.H + h) * head_size;
+        from = a.ws_state + (kept * a.H + h) * head_size;
       } else if (a.init && (!a.has || a.has[seg.seq])) {
         const int64_t slot = slot_of(a.idx, seg.seq, a.nslots);
         if (slot >= 0) from = a.init + (slot * a.H + h) * head_size;
@@ -188,8 +188,8 @@ __device__ __forceinline__ void walk(const StatesArgs& a, uint16_t* sK0, uint16_
 
   if (!on) return;
   if constexpr (!SAVE) {
-    put(a.ws_state + (number * a.H + h) * head_size);
-    if (p0 == 0 && lane == 0) a.ws_decay[number * a.H + h] = decay;
+    put(a.ws_state + (kept * a.H + h) * head_size);
+    if (p0 == 0 && lane == 0) a.ws_decay[kept * a.H + h] = decay;
   } else if (a.last && seg.index == (REV ? 0 : seg.count - 1)) {
     put(a.last + (int64_t(seg.seq) * a.H + h) * head_size);
   }
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(256) packed_join_kernel(StatesArgs f, StatesAr
   const StatesArgs& a = rev ? r : f;
   Piece seg;
   pieces_of(a.cu, blockIdx.x, a.T, a.cps * kChunk, seg);
-  const int count = min(seg.count, a.nseg - seg.first);   // (only a cu_seqlens out of order reaches this bound)
+  const int count = seg.count;
   if (count <= 1) return;
   const int64_t e = (int64_t(blockIdx.y) * 256 + threadIdx.x) * 4;
   const int64_t per = int64_t(a.H) * entries;
@@ -232,14 +232,14 @@ __global__ void __launch_bounds__(256) packed_join_kernel(StatesArgs f, StatesAr
     float d[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {   // (the last one's end is not needed: nothing was left there)
-      const int64_t j = seg.first + (rev ? count - 1 - min(i + k, count - 2) : min(i + k, count - 2));
+      const int64_t j = seg.place + (rev ? count - 1 - min(i + k, count - 2) : min(i + k, count - 2));
       own[k] = *reinterpret_cast<const pf4*>(a.ws_state + j * per + e);
       d[k] = a.ws_decay[j * a.H + h];
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
       if (i + k >= count) break;
-      const int64_t j = seg.first + (rev ? count - 1 - i - k : i + k);
+      const int64_t j = seg.place + (rev ? count - 1 - i - k : i + k);
       *reinterpret_cast<pf4*>(a.ws_state + j * per + e) = s;
       s = s * hw_exp2(d[k]) + own[k];
     }

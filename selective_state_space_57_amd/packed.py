@@ -11,6 +11,7 @@ device: which sequences start from their slot (None: all, when ``state`` is give
 states and may be ``state`` itself.  Nothing is read on the host, so a call can be captured into a graph.
 
 Work runs on the current stream of the tensors' device, or on ``stream``; what a call allocates belongs to that stream.
+A given workspace serves one call at a time: calls that overlap, and graphs replayed side by side, take one each.
 Rows outside every sequence are left as they are in outputs too: unset where the call allocates the output.
 """
 from __future__ import annotations
@@ -371,7 +372,8 @@ def ssd_packed_bwd(x, dt, A, B, C, dy, cu_seqlens, dt_bias=None, Dskip=None, *, 
     dx (T, H, 64), ddt (T, H), dB, dC (T, G, N) bfloat16, dA, dDskip, ddt_bias (H,) float32 and dstate (S, H, 64, N)
     float32, the gradient of the state each sequence starts from (want_dstate; by default when ``state`` or
     ``dstate_out`` is given).  ``out`` may hold dx, ddt, dB, dC to write into (rows of dx 16-byte, of dB and dC 8-byte
-    aligned).  Rows outside every sequence are left as they are."""
+    aligned).  Rows outside every sequence are left as they are.  The workspace holds the states and adjoint states of
+    every chunk of 64 steps: 512 H N bytes for each of about T / 64 + S chunks."""
     import torch
     T = x.shape[0]
     dev = _on_gpu(x, "x")

@@ -153,6 +153,16 @@ def test_one_chunk_runs_need_no_workspace(lib):
     assert size(ctypes.byref(ssd_params(ntokens=6400, nseqs=1, segment_chunks=100))) == 0
 
 
+def test_workspace_does_not_grow_with_short_sequences(lib):
+    """Only sequences of several segments need their states kept between passes: at most two places for every whole
+    segment of the tokens."""
+    size = lib.ssm_ssd_packed_fwd_workspace_bytes
+    state = 6 * 64 * 128 * 4
+    for nseqs in (1, 100, 16384):
+        p = ssd_params(ntokens=16384, nseqs=nseqs, segment_chunks=4)
+        assert size(ctypes.byref(p)) <= 2 * (16384 // 256) * (state + 6 * 4) + 512, nseqs
+
+
 def test_python_forms_want_the_gpu():
     """Tensors in host memory are refused before the library is called."""
     x, w, cu = torch.zeros(4, 8), torch.zeros(8, 4), torch.tensor([0, 4], dtype=torch.int32)

@@ -5,6 +5,8 @@ that the Python forms refuse.
 Tolerances: test_packed_gpu.py's, a rounding of a stage's output (2^-8 in bf16) counted once for every factor that
 carries it on.
 """
+import ctypes
+
 import pytest
 
 import packed_ref as R
@@ -326,6 +328,42 @@ def test_offsets_past_32_bits():
     sa = ssm().ssd_slot_update(big, *(t if t is A else t[:2] for t in cut(far)), state_idx=idx)
     sb = ssm().ssd_slot_update(small, *(t if t is A else t[:2] for t in cut(near_)))
     assert torch.equal(sa, sb) and torch.equal(big[idx.long()], small)
+
+
+@pytest.mark.parametrize("lens", [[200, 3, 0, 65, 1, 64, 128, 129] * 4, [63, 65] * 9 + [700], [66] * 40, [1, 640, 1]])
+def test_cut_sequences_among_short_ones(lens):
+    """Segments of one chunk, kept states side by side, against no segments at all; nothing behind the workspace is
+    written."""
+    torch, r, k, cu, cul, x, idx, conv, state = setup(9, lens, H=3, G=1, groups=1)
+    S = len(lens)
+    dy, dl = r(x.shape[0], 3, 64, dtype=torch.bfloat16), r(S, 3, 64, 64, scale=0.3)
+    z, xbc, dt = k.cut(x)
+    xs, B, C = k.heads(xbc)
+    args = (xs, dt, k.A, B, C)
+    m = ssm()
+
+    def run(chunks, fwd, bwd):
+        out = state.clone()
+        y = m.ssd_packed_fwd(*args, cu, k.bias, k.skip, state=state, state_out=out, state_idx=idx, segment_chunks=chunks,
+                             workspace=fwd)
+        return dict(m.ssd_packed_bwd(*args, dy, cu, k.bias, k.skip, state=state, state_idx=idx, dstate_out=dl,
+                                     segment_chunks=chunks, workspace=bwd), y=y, state=out)
+
+    def space(name, chunks):
+        p = m._abi.SsdPackedParams(ntokens=x.shape[0], nseqs=S, nheads=3, headdim=64, ngroups=1, dstate=64, nslots=S + 2,
+                                   io_dtype=m.SSM_BF16, dt_softplus=1, segment_chunks=chunks)
+        n = int(getattr(m._abi.lib(), name)(ctypes.byref(p)))
+        return torch.full((n + 4096,), 7, dtype=torch.uint8, device="cuda"), n
+
+    wf, nf = space("ssm_ssd_packed_fwd_workspace_bytes", 1)
+    wb, nb = space("ssm_ssd_packed_bwd_workspace_bytes", 1)
+    got, ref = run(1, wf, wb), run(1000, None, None)
+    torch.cuda.synchronize()
+    assert bool((wf[nf:] == 7).all()) and bool((wb[nb:] == 7).all())
+    # each side is within its own tolerance of the same 64-bit values
+    for n, tol in (("y", 3 * BF), ("dx", 3 * BF), ("dB", 3 * BF), ("dC", 3 * BF), ("ddt", BF + 2.0 ** -14),
+                   ("state", TOL_STATE), ("dstate", TOL_STATE), ("dA", 2.0 ** -14), ("ddt_bias", 2.0 ** -14)):
+        near(got[n], f64(ref[n]), 2 * tol, n)
 
 
 def test_refusals():
