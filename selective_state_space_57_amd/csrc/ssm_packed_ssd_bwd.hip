@@ -467,10 +467,31 @@ packed_ssd_bwd_kernel(BwdArgs a) {
   }
 }
 
-// dB and dC: the splits' sums in order, rounded once.  A thread owns four columns of a row; rows outside every sequence
-// stay as they are.
-__global__ void __launch_bounds__(256) packed_ssd_bwd_bc_kernel(BwdArgs a, int cols) {
-  const int64_t at = int64_t(blockIdx.x) * 256 + threadIdx.x;
+// What the workgroups left in parts.  The first H blocks: dA, ddt_bias and dD of a head, the chunks' sums, 256 interleaved
+// runs joined in a fixed order.  The others: dB (y = 0) and dC, the splits' sums in order, rounded once; a thread owns four
+// columns of a row, and rows outside every sequence stay as they are.
+__global__ void __launch_bounds__(256) packed_ssd_bwd_sums_kernel(BwdArgs a, int cols) {
+  if (static_cast<int>(blockIdx.x) < a.H) {
+    __shared__ pf4 sum[256];
+    if (blockIdx.y) return;
+    const int h = blockIdx.x;
+    pf4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = threadIdx.x; i < a.numbers; i += 256)
+      v += *reinterpret_cast<const pf4*>(a.part_h + (int64_t(i) * a.H + h) * 4);
+    sum[threadIdx.x] = v;
+    __syncthreads();
+    for (int m = 128; m >= 1; m >>= 1) {
+      if (static_cast<int>(threadIdx.x) < m) sum[threadIdx.x] += sum[threadIdx.x + m];
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+      a.dA[h] = sum[0][0];
+      if (a.ddt_bias) a.ddt_bias[h] = sum[0][1];
+      if (a.dD) a.dD[h] = sum[0][2];
+    }
+    return;
+  }
+  const int64_t at = int64_t(blockIdx.x - a.H) * 256 + threadIdx.x;
   const int64_t t = at / (cols / 4);
   const int col = static_cast<int>(at % (cols / 4)) * 4;
   if (t >= a.T || t < a.cu[0] || t >= a.cu[a.S_]) return;
@@ -479,25 +500,6 @@ __global__ void __launch_bounds__(256) packed_ssd_bwd_bc_kernel(BwdArgs a, int c
   for (int s = 1; s < a.splits; ++s) v += *reinterpret_cast<const pf4*>(part + int64_t(s) * a.T * cols);
   uint16_t* out = (blockIdx.y ? a.dC + t * a.dcs : a.dB + t * a.dbs) + col;
   *reinterpret_cast<pu2*>(out) = bf16x4(v[0], v[1], v[2], v[3]);
-}
-
-// dA, ddt_bias and dD of a head: the chunks' sums, 256 interleaved runs joined in a fixed order
-__global__ void __launch_bounds__(256) packed_ssd_bwd_head_kernel(BwdArgs a, int chunks) {
-  __shared__ pf4 sum[256];
-  const int h = blockIdx.x;
-  pf4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int i = threadIdx.x; i < chunks; i += 256) v += *reinterpret_cast<const pf4*>(a.part_h + (int64_t(i) * a.H + h) * 4);
-  sum[threadIdx.x] = v;
-  __syncthreads();
-  for (int m = 128; m >= 1; m >>= 1) {
-    if (static_cast<int>(threadIdx.x) < m) sum[threadIdx.x] += sum[threadIdx.x + m];
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) {
-    a.dA[h] = sum[0][0];
-    if (a.ddt_bias) a.ddt_bias[h] = sum[0][1];
-    if (a.dD) a.dD[h] = sum[0][2];
-  }
 }
 
 struct BwdPlan {
@@ -511,7 +513,8 @@ BwdPlan bwd_plan(const ssm_ssd_packed_params* p) {
   b.walk = packed_plan(p);
   b.numbers = piece_numbers(p->nseqs, p->ntokens, kChunk);
   const int64_t hpg = p->nheads / p->ngroups;
-  // four workgroups for each place on the 256 CUs, to even out their lengths; each split costs a partial dB and dC
+  // four workgroups for each place on the 256 CUs, to even out their lengths; each split costs a partial dB and dC (16384
+  // tokens, 2.7B layer: about 1024, 2048 and 4096 workgroups 1180, 1137 and 1166 us a call on one card)
   int64_t splits = (2048 + b.numbers * p->ngroups - 1) / (b.numbers * p->ngroups);
   if (splits > hpg) splits = hpg;
   b.hps = static_cast<int>((hpg + splits - 1) / splits);
@@ -673,9 +676,8 @@ extern "C" ssm_status ssm_ssd_packed_bwd(const ssm_ssd_packed_params* p, const v
     default: launch_bwd<256>(a, st); break;
   }
   const int cols = static_cast<int>(grp);
-  hipLaunchKernelGGL(packed_ssd_bwd_bc_kernel, dim3(static_cast<uint32_t>((int64_t(a.T) * (cols / 4) + 255) / 256), 2),
-                     dim3(256), 0, st, a, cols);
-  hipLaunchKernelGGL(packed_ssd_bwd_head_kernel, dim3(a.H), dim3(256), 0, st, a, a.numbers);
+  hipLaunchKernelGGL(packed_ssd_bwd_sums_kernel,
+                     dim3(static_cast<uint32_t>(a.H + (int64_t(a.T) * (cols / 4) + 255) / 256), 2), dim3(256), 0, st, a, cols);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SSM_OK : fail(SSM_ERR_HIP, "packed SSD backward launch: %s", hipGetErrorString(e));
 }
