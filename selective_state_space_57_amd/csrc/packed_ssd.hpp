@@ -31,6 +31,16 @@ __device__ __forceinline__ pu4 join(pu2 a, pu2 b) { return pu4{a[0], a[1], b[0],
 struct Parts {
   pu4 p[3];
 };
+// what four packed values leave of the ones they were rounded from
+__device__ __forceinline__ pf4 rest_of(pf4 a, pu2 u) {
+  return pf4{a[0] - lo_f32(u[0]), a[1] - hi_f32(u[0]), a[2] - lo_f32(u[1]), a[3] - hi_f32(u[1])};
+}
+// Four values in two bf16 parts (2^-16 of the value is left out at most).
+__device__ __forceinline__ void split2(pf4 a, pu2& hi, pu2& lo) {
+  hi = bf16x4(a[0], a[1], a[2], a[3]);
+  const pf4 r = rest_of(a, hi);
+  lo = bf16x4(r[0], r[1], r[2], r[3]);
+}
 __device__ __forceinline__ Parts split3(pf4 a, pf4 b) {
   Parts o;
 #pragma unroll
@@ -38,8 +48,8 @@ __device__ __forceinline__ Parts split3(pf4 a, pf4 b) {
     const pu2 u = bf16x4(a[0], a[1], a[2], a[3]), v = bf16x4(b[0], b[1], b[2], b[3]);
     o.p[i] = join(u, v);
     if (i < 2) {
-      a = pf4{a[0] - lo_f32(u[0]), a[1] - hi_f32(u[0]), a[2] - lo_f32(u[1]), a[3] - hi_f32(u[1])};
-      b = pf4{b[0] - lo_f32(v[0]), b[1] - hi_f32(v[0]), b[2] - lo_f32(v[1]), b[3] - hi_f32(v[1])};
+      a = rest_of(a, u);
+      b = rest_of(b, v);
     }
   }
   return o;

@@ -16,8 +16,10 @@
 //
 // Precision: fp32 state and accumulation; x, B and C enter the matrix cores as they are.  The weighted x of the state
 // update is split into three bf16 parts, so the state keeps fp32 quality over long sequences (two parts, 2^-17, are 11 %
-// faster).  M (but for s = t) and the state's copy that meets C are rounded once to bf16 (2^-8 at most, as the output
-// is): they only reach y, which is rounded to bf16 itself.
+// faster).  M (but for s = t, which is added in fp32) and the state that meets C only reach y: they are split into two,
+// which leave out 2^-16 of them at most, so that y is the 64-bit value rounded once but for 5e-5 of it in the 2-norm
+// (rounded to bf16 once each, they added 1.4e-3 to the rounding's own 1.66e-3; 16384 tokens of the 2.7B layer then take
+// 282 us instead of 337).
 //
 // Measured on 16384 tokens of 80 heads, N = 128 (0.40 GB in and out, 43 GFLOP): 280 us, 200 of them this pass, 85 the walk
 // and its join.  VALU 42 % of the cycles, MFMA 19 %, the rest waits: leaving out a part saves 70 us (M x and C S^T),
@@ -202,10 +204,13 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
           for (int i = 0; i < 2; ++i) c[i] = lds_row_operand<U>(C, 32 * th + 16 * i + l16, kn, g4);
 #pragma unroll
           for (int pt = 0; pt < PT; ++pt) {
-            const pf4 s0 = S[2 * kn][pt], s1 = S[2 * kn + 1][pt];
-            const pu4 s = join(bf16x4(s0[0], s0[1], s0[2], s0[3]), bf16x4(s1[0], s1[1], s1[2], s1[3]));
+            pu2 hi[2], lo[2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) acc[i][pt] = mma(s, c[i], acc[i][pt]);
+            for (int e = 0; e < 2; ++e) split2(S[2 * kn + e][pt], hi[e], lo[e]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) acc[i][pt] = mma(join(lo[0], lo[1]), c[i], acc[i][pt]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) acc[i][pt] = mma(join(hi[0], hi[1]), c[i], acc[i][pt]);
           }
         }
         float ct[2];
@@ -226,18 +231,18 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
           for (int i = 0; i < 2; ++i) {
             const int tb = 2 * th + i;
             part_ends();
-            pu2 half[2];
+            pu2 hi[2], lo[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int sb = 2 * kk + e;
               if (sb > tb) {
-                half[e] = pu2{0u, 0u};
+                hi[e] = lo[e] = pu2{0u, 0u};
                 continue;
               }
               const pf4 cb = sCB[tb * (tb + 1) / 2 + sb][lane];
               const pf4 cs = *reinterpret_cast<const pf4*>(&sc.c[16 * sb + 4 * g4]);
               const pf4 ph = *reinterpret_cast<const pf4*>(&sc.phi[16 * sb + 4 * g4]);
-              float m[4];
+              pf4 m;
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
                 // (above the diagonal the difference can be large and positive: masked after the fact)
@@ -248,11 +253,12 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
                   m[c] = 4 * g4 + c < l16 ? m[c] : 0.0f;
                 }
               }
-              half[e] = bf16x4(m[0], m[1], m[2], m[3]);
+              split2(m, hi[e], lo[e]);
             }
-            const pu4 M = join(half[0], half[1]);
 #pragma unroll
-            for (int pt = 0; pt < PT; ++pt) acc[i][pt] = mma(xt[pt], M, acc[i][pt]);
+            for (int pt = 0; pt < PT; ++pt) acc[i][pt] = mma(xt[pt], join(lo[0], lo[1]), acc[i][pt]);
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) acc[i][pt] = mma(xt[pt], join(hi[0], hi[1]), acc[i][pt]);
           }
         }
         wave_lds_sync();
