@@ -16,18 +16,21 @@
 // Two walks (ssm_packed_states.hip) leave S and G of every chunk, laid out as operands over p; then a workgroup takes a
 // chunk and runs over heads one after the other.  A wave has 16 of the N columns of the states, for every head: the sums
 // of dB and dC over heads add up in its registers.  K is summed over heads in registers as well, and multiplied with B and
-// C once at the end.  What a head needs across waves (dx, and the sums over n in u, v and <G, S>) goes through LDS.  The
-// next head's states and x are on their way while this head's dx is computed.
+// C once at the end.  What a head needs across waves (dx, and the sums over n in u, v and <G, S>) goes through LDS, where
+// the parts of G take turns and M's second part takes the place of x.  The next head's states are on their way while this
+// head's dx is computed.
 // Two workgroups share a CU (N <= 128), so that one's barriers and loads run beside the other's products: with chunks of
 // 128 steps to a workgroup, which halve the saved states but recompute them in between, one filled the LDS and took
 // 790 us instead of 566 (2.7B layer, 16384 tokens, states in two bf16 parts each).
-// Measured on that layer: 642 us with three parts, in a call of 1081 us whose walks, join and sums over heads are the rest.
-// It reads 1.4 GB of states and 0.34 GB of inputs (2.7 TB/s), MFMA 11 % and VALU 41 % of the cycles: no single one is full,
-// the stages of a head and the barriers between them are its time.
+// Measured on that layer: a call of 1249 us.
+// It reads 1.4 GB of states and 0.34 GB of inputs, MFMA and VALU are below half of the cycles: no single one is full, the
+// stages of a head and the barriers between them are its time.
 //
 // Precision: fp32 accumulation; the states are split into three bf16 parts, so that u, v and <G, S>, and with them dDelta
 // and dA, are good to fp32 quality.  G in dx, M = L Z phi and the head sum K (both but for s = t, which is added in fp32)
-// are rounded once to bf16: they only reach dx, dB and dC, which are bf16 themselves.
+// only reach dx, dB and dC: they are split into two parts, which leave out 2^-16 at most, so that these are the 64-bit
+// values rounded once but for 1e-4 of them in the 2-norm (rounded to bf16 once each: 1e-3 to 2.4e-3, beside the outputs'
+// own 1.66e-3, in a call of 1141 us).
 #include "packed_ssd.hpp"
 
 namespace ssm57 {
@@ -168,12 +171,25 @@ packed_ssd_bwd_kernel(BwdArgs a) {
     }
   };
 
-  copy_head(Xk, a.x, h_begin, a.xs, xrow);
+  // second parts of this wave's tiles as operands over t, laid out as sM (the halves above the diagonal are zeros)
+  auto put_parts = [&](pu4 (*to)[64], const pu2 (&lo)[kTiles]) __attribute__((always_inline)) {
+    const int l = afresh(lane);
+#pragma unroll
+    for (int ti = 0; ti < kTiles; ++ti) {
+      const int i = nt + NW * ti;
+      if (i >= 10) break;
+      const int tb = tile_row(i), sb = i - tb * (tb + 1) / 2;
+      pu2* at = reinterpret_cast<pu2*>(&to[m_slot(sb, tb >> 1)][l]);
+      at[tb & 1] = lo[ti];
+      if (sb == tb && (tb & 1)) at[0] = pu2{0u, 0u};
+    }
+  };
   load_states(h_begin);
   for (int h = h_begin; h < h_end; ++h) {
     const float Ah = a.A[h];
     const float Dh = a.Dskip ? a.Dskip[h] : 0.0f;
     barrier_lds();   // everyone is done with the head before
+    copy_head(Xk, a.x, h, a.xs, xrow);
     copy_head(Yk, a.dy, h, a.dys, yrow);
     constexpr int kScalarTile = NW - 1;   // the wave of a chunk that works on its steps
     if (nt == kScalarTile) {
@@ -198,6 +214,7 @@ packed_ssd_bwd_kernel(BwdArgs a) {
     wait_memory();
     barrier_lds();   // x, dy and the scalars are there
     part_ends();
+    pu4 g_lo[2];   // the second part of this wave's G, as its rows of sG
     {
       // ---- products with the states: <G, S>, q^T = S^T dy^T, r^T = G^T x^T
       const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
@@ -219,6 +236,8 @@ packed_ssd_bwd_kernel(BwdArgs a) {
 #pragma unroll
           for (int kk = 0; kk < 2; ++kk)
             *reinterpret_cast<pu4*>(reinterpret_cast<char*>(sG) + unit_at<8>(16 * nt + l16, 4 * kk + g4)) = d[kk].p[0];
+#pragma unroll
+          for (int kk = 0; kk < 2; ++kk) g_lo[kk] = d[kk].p[1];
         }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -245,6 +264,7 @@ packed_ssd_bwd_kernel(BwdArgs a) {
     }
     part_ends();
     // ---- tiles of L, X, Z
+    pu2 m_lo[kTiles];
 #pragma unroll
     for (int ti = 0; ti < kTiles; ++ti) {
       const int i = nt + NW * ti;
@@ -265,7 +285,8 @@ packed_ssd_bwd_kernel(BwdArgs a) {
       }
       part_ends();
       pf4 k = ti < kHeld ? aK[min(ti, kHeld - 1)] : sK2[nt][l];
-      float m[4], row[4], col = 0.0f;
+      pf4 m;
+      float row[4], col = 0.0f;
       if (sb < tb) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -302,7 +323,9 @@ packed_ssd_bwd_kernel(BwdArgs a) {
         }
         if (l == 0) sDiag[tb] = diag;
       }
-      reinterpret_cast<pu2*>(&sM[m_slot(sb, tb >> 1)][l])[tb & 1] = bf16x4(m[0], m[1], m[2], m[3]);
+      pu2 m_hi;
+      split2(m, m_hi, m_lo[ti]);
+      reinterpret_cast<pu2*>(&sM[m_slot(sb, tb >> 1)][l])[tb & 1] = m_hi;
       if (ti < kHeld) {
         aK[min(ti, kHeld - 1)] = k;
         asm volatile("" : "+v"(aK[min(ti, kHeld - 1)]));
@@ -319,41 +342,71 @@ packed_ssd_bwd_kernel(BwdArgs a) {
       if (l == 0) sTotal[i] = tile;
     }
     barrier_lds();   // M, G and the partial sums are there, and x is read
-    if (h + 1 < h_end) {
-      copy_head(Xk, a.x, h + 1, a.xs, xrow);
-      load_states(h + 1);
-    }
+    if (h + 1 < h_end) load_states(h + 1);
+    pu4 (*sMl)[64] = reinterpret_cast<pu4(*)[64]>(Xk);   // M's second part takes the place of x
+    put_parts(sMl, m_lo);
     part_ends();
-    // ---- dx: a pair of column tiles (32 p) of one tile of steps at a time
+    // ---- dx: a pair of column tiles (32 p) of one tile of steps at a time.  G's parts take turns in sG.
+    pf4 d[kJobs][2], dm[kJobs][2];
+    auto add_g = [&]() __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < kJobs; ++j) {
+        const int job = nt + NW * j;
+        if (job >= 8) break;
+        const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
+        const int sb = job & 3, pp = job >> 2;
+#pragma unroll
+        for (int kk = 0; kk < NK; ++kk) {
+          const pu4 b = lds_row_operand<U>(Bk, 16 * sb + l16, kk, g4);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) d[j][e] = mma(lds_tr_operand8<8>(sG, kk, 2 * pp + e, l16, g4), b, d[j][e]);
+        }
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < kJobs; ++j) d[j][0] = d[j][1] = dm[j][0] = dm[j][1] = zero;
+    add_g();
+    barrier_lds();   // the first part of G is read, the second of M is there
+    part_ends();
+    {
+      const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk)
+        *reinterpret_cast<pu4*>(reinterpret_cast<char*>(sG) + unit_at<8>(16 * nt + l16, 4 * kk + g4)) = g_lo[kk];
+#pragma unroll
+      for (int j = 0; j < kJobs; ++j) {
+        const int job = nt + NW * j;
+        if (job >= 8) break;
+        const int sb = job & 3, pp = job >> 2;
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) {
+          if (sb >= 2 && kk == 0) continue;   // no step of the first half follows one of the second
+          const pu4 m = sM[m_slot(sb, kk)][l], ml = sMl[m_slot(sb, kk)][l];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const pu4 y = lds_tr_operand<8>(Yk, kk, 2 * pp + e, l16, g4);
+            dm[j][e] = mma(y, ml, dm[j][e]);
+            dm[j][e] = mma(y, m, dm[j][e]);
+          }
+        }
+      }
+    }
+    barrier_lds();   // the second part of G is there
+    part_ends();
+    add_g();
 #pragma unroll
     for (int j = 0; j < kJobs; ++j) {
       const int job = nt + NW * j;
       if (job >= 8) break;
       const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
       const int sb = job & 3, pp = job >> 2;
-      pf4 d[2] = {zero, zero};
-#pragma unroll
-      for (int kk = 0; kk < NK; ++kk) {
-        const pu4 b = lds_row_operand<U>(Bk, 16 * sb + l16, kk, g4);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) d[e] = mma(lds_tr_operand8<8>(sG, kk, 2 * pp + e, l16, g4), b, d[e]);
-      }
-      const float pf = sc.pf[16 * sb + l16];
-      d[0] *= pf;
-      d[1] *= pf;
-#pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        if (sb >= 2 && kk == 0) continue;   // no step of the first half follows one of the second
-        const pu4 m = sM[m_slot(sb, kk)][l];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) d[e] = mma(lds_tr_operand<8>(Yk, kk, 2 * pp + e, l16, g4), m, d[e]);
-      }
-      const float dr = sDirect[sb][l16];
+      const float pf = sc.pf[16 * sb + l16], dr = sDirect[sb][l16];
       const pu4 yv = lds_u4(Yk, unit_at<8>(16 * sb + l16, 4 * pp + g4));
-      const pu4 o = {pack_bf16(fmaf(dr, lo_f32(yv[0]), d[0][0]), fmaf(dr, hi_f32(yv[0]), d[0][1])),
-                     pack_bf16(fmaf(dr, lo_f32(yv[1]), d[0][2]), fmaf(dr, hi_f32(yv[1]), d[0][3])),
-                     pack_bf16(fmaf(dr, lo_f32(yv[2]), d[1][0]), fmaf(dr, hi_f32(yv[2]), d[1][1])),
-                     pack_bf16(fmaf(dr, lo_f32(yv[3]), d[1][2]), fmaf(dr, hi_f32(yv[3]), d[1][3]))};
+      const pf4 d0 = dm[j][0] + d[j][0] * pf, d1 = dm[j][1] + d[j][1] * pf;
+      const pu4 o = {pack_bf16(fmaf(dr, lo_f32(yv[0]), d0[0]), fmaf(dr, hi_f32(yv[0]), d0[1])),
+                     pack_bf16(fmaf(dr, lo_f32(yv[1]), d0[2]), fmaf(dr, hi_f32(yv[1]), d0[3])),
+                     pack_bf16(fmaf(dr, lo_f32(yv[2]), d1[0]), fmaf(dr, hi_f32(yv[2]), d1[1])),
+                     pack_bf16(fmaf(dr, lo_f32(yv[3]), d1[2]), fmaf(dr, hi_f32(yv[3]), d1[3]))};
       __builtin_amdgcn_raw_buffer_store_b128(
           o, chunk_rsrc(a.dx + int64_t(h) * kHead, t_first, a.dxs, rows, kHead),
           static_cast<int>(static_cast<uint32_t>(16 * sb + l16) * (static_cast<uint32_t>(a.dxs) * 2u) +
@@ -411,7 +464,9 @@ packed_ssd_bwd_kernel(BwdArgs a) {
   // ---- the heads' K with B and C, and the sums over this workgroup's heads
   barrier_lds();
   const int l16 = lane & 15, g4 = lane >> 4;
-  uint16_t* sK = Xk;   // K, row by row
+  // K in two parts: row by row where x and dy were, and as operands over t in sM and where G was
+  pu4 (*sMl)[64] = reinterpret_cast<pu4(*)[64]>(sG);
+  pu2 k_lo[kTiles];
 #pragma unroll
   for (int ti = 0; ti < kTiles; ++ti) {
     const int i = nt + NW * ti;
@@ -428,17 +483,25 @@ packed_ssd_bwd_kernel(BwdArgs a) {
       own = sum_rows(own);
       if (g4 == 0) sOwn[tb][l16] = own;
     }
-    reinterpret_cast<pu2*>(&sM[m_slot(sb, tb >> 1)][lane])[tb & 1] = bf16x4(v[0], v[1], v[2], v[3]);
+    pu2 hi;
+    split2(v, hi, k_lo[ti]);
+    reinterpret_cast<pu2*>(&sM[m_slot(sb, tb >> 1)][lane])[tb & 1] = hi;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int row = 16 * tb + 4 * g4 + c, byte = 2 * (l16 & 7);
-      char* at = reinterpret_cast<char*>(sK);
-      Elem<uint16_t>::st(reinterpret_cast<uint16_t*>(at + unit_at<8>(row, 2 * sb + (l16 >> 3)) + byte), 0, v[c]);
-      // (the tile right of an even diagonal tile belongs to the same operand)
-      if (sb == tb && (tb & 1) == 0)
-        *reinterpret_cast<uint16_t*>(at + unit_at<8>(row, 2 * (sb + 1) + (l16 >> 3)) + byte) = 0;
+    for (int part = 0; part < 2; ++part) {
+      char* at = reinterpret_cast<char*>(part ? Yk : Xk);
+      const pu2 k = part ? k_lo[ti] : hi;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int row = 16 * tb + 4 * g4 + c, byte = 2 * (l16 & 7);
+        *reinterpret_cast<uint16_t*>(at + unit_at<8>(row, 2 * sb + (l16 >> 3)) + byte) =
+            static_cast<uint16_t>(k[c >> 1] >> (16 * (c & 1)));
+        // (the tile right of an even diagonal tile belongs to the same operand)
+        if (sb == tb && (tb & 1) == 0)
+          *reinterpret_cast<uint16_t*>(at + unit_at<8>(row, 2 * (sb + 1) + (l16 >> 3)) + byte) = 0;
+      }
     }
   }
+  put_parts(sMl, k_lo);
   barrier_lds();
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk) {
@@ -446,8 +509,14 @@ packed_ssd_bwd_kernel(BwdArgs a) {
     const pu4 ct = lds_tr_plain_operand<U, false>(Ck, kk, nt, l16, g4);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      if (kk <= b / 2) aC[b] = mma(bt, lds_row_operand<8>(sK, 16 * b + l16, kk, g4), aC[b]);
-      if (kk == 1 || b < 2) aB[b] = mma(ct, sM[m_slot(b, kk)][lane], aB[b]);
+      if (kk <= b / 2) {
+        aC[b] = mma(bt, lds_row_operand<8>(Yk, 16 * b + l16, kk, g4), aC[b]);
+        aC[b] = mma(bt, lds_row_operand<8>(Xk, 16 * b + l16, kk, g4), aC[b]);
+      }
+      if (kk == 1 || b < 2) {
+        aB[b] = mma(ct, sMl[m_slot(b, kk)][lane], aB[b]);
+        aB[b] = mma(ct, sM[m_slot(b, kk)][lane], aB[b]);
+      }
     }
   }
 #pragma unroll
