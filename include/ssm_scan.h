@@ -319,7 +319,8 @@ ssm_status ssm_conv1d_packed_fwd(const ssm_conv_packed_params* p, const void* x,
                                  const int32_t* cu_seqlens, const float* state, const int32_t* state_idx,
                                  const uint8_t* has_state, float* state_out, void* u, void* stream);
 
-/* One token per row: x, u [ntokens][dim]; row r shifts the window in slot state_idx[r] in place. */
+/* One token per row: x, u [ntokens][dim]; row r shifts the window in slot state_idx[r] in place (nslots >= 1 where there
+ * is a window: width > 1). */
 ssm_status ssm_conv1d_slot_update(const ssm_conv_packed_params* p, const void* x, const float* weight, const float* bias,
                                   float* state, const int32_t* state_idx, void* u, void* stream);
 

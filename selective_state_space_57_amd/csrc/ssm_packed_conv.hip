@@ -523,6 +523,8 @@ extern "C" ssm_status ssm_conv1d_slot_update(const ssm_conv_packed_params* p, co
   if (ssm_status s = check_pconv(p, true); s != SSM_OK) return s;
   if (!x || !weight || !u || (p->width > 1 && !state))
     return fail(SSM_ERR_NULL, "x, weight, u and (for width > 1) state are required");
+  // (a row without a slot reads the first one's window, and does not use it)
+  if (p->width > 1 && p->nslots < 1) return fail(SSM_ERR_SHAPE, "nslots must be >= 1");
   const int es = elem_size(p);
   if (!aligned(x, es) || !aligned(u, es) || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(state, 4) ||
       !aligned(state_idx, 4))
