@@ -340,8 +340,9 @@ ssm_status ssm_conv1d_packed_bwd(const ssm_conv_packed_params* p, const void* x,
                                  void* stream);
 
 typedef struct {
-  int64_t ntokens;   /* rows, >= 1 and below 2^30 */
-  int64_t nseqs;     /* sequences, >= 1 (ignored by ssm_ssd_slot_update) */
+  int64_t ntokens;   /* rows, >= 1 and below 2^30; ssm_ssd_slot_update: ntokens * nheads below 2^22 */
+  int64_t nseqs;     /* sequences, 1 to 2^20 (ignored by ssm_ssd_slot_update); about (nseqs + ntokens / segment) * ceil(nheads
+                        / ngroups / 4) * ngroups workgroups of 512 threads must be below 2^32 threads */
   int64_t nheads;    /* H, a multiple of ngroups */
   int64_t headdim;   /* P: must be 64 */
   int64_t ngroups;   /* G */

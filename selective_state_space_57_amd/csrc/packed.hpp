@@ -106,4 +106,7 @@ __device__ __forceinline__ int64_t slot_of(const int32_t* idx, int s, int64_t ns
   return k >= 0 && k < nslots ? k : -1;
 }
 
+// A launch takes fewer than 2^32 threads along a dimension of its grid.
+inline bool fits_launch(int64_t blocks, int threads) { return blocks * threads < (int64_t(1) << 32); }
+
 }  // namespace ssm57

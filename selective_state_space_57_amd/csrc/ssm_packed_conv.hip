@@ -504,6 +504,7 @@ extern "C" ssm_status ssm_conv1d_packed_fwd(const ssm_conv_packed_params* p, con
   const int V = vec ? 16 / es : 1;
   a.tile = fwd_tile(a, V);
   a.ntiles = (a.T + a.tile - 1) / a.tile;
+  if (!fits_launch(int64_t(a.ntiles) + a.S, kThreads)) return fail(SSM_ERR_SHAPE, "too many tokens and sequences for one launch");
   const dim3 grid(a.ntiles + a.S, (a.C + V * kThreads - 1) / (V * kThreads));
   if (grid.y > 65535) return fail(SSM_ERR_SHAPE, "dim is too large");
   hipStream_t st = static_cast<hipStream_t>(stream);

@@ -448,10 +448,13 @@ ssm_status check_packed_ssd(const ssm_ssd_packed_params* p, bool step) {
     if (r.s >= most || r.row >= most)
       return fail(SSM_ERR_SHAPE, "rows and row strides must stay below 2^24 elements");
   }
-  if (step && p->ntokens * p->nheads >= (int64_t(1) << 29)) return fail(SSM_ERR_SHAPE, "too many rows for one launch");
+  if (step && !fits_launch(p->ntokens * p->nheads * (kHead / 16), 256))
+    return fail(SSM_ERR_SHAPE, "ntokens * nheads must be below 2^22 for one launch (got %lld)",
+                (long long)(p->ntokens * p->nheads));
   if (!step) {
     const PackedPlan pl = packed_plan(p);
-    if (pl.nseg * p->ngroups * pl.hblocks >= (int64_t(1) << 31) - 8) return fail(SSM_ERR_SHAPE, "too many work items");
+    if (!fits_launch(pl.nseg * p->ngroups * pl.hblocks, kWalkWaves * 64))
+      return fail(SSM_ERR_SHAPE, "too many work items (segments times workgroups of 4 heads) for one launch");
     if (p->nheads * kHead * p->dstate / 1024 >= 65535) return fail(SSM_ERR_SHAPE, "nheads is too large");
   }
   return SSM_OK;

@@ -601,8 +601,11 @@ BwdPlan bwd_plan(const ssm_ssd_packed_params* p) {
 ssm_status check_bwd(const ssm_ssd_packed_params* p) {
   if (ssm_status s = check_packed_ssd(p, false); s != SSM_OK) return s;
   const BwdPlan b = bwd_plan(p);
-  if (b.numbers * b.splits * p->ngroups >= (int64_t(1) << 31) - 8) return fail(SSM_ERR_SHAPE, "too many work items");
-  if (p->ntokens * p->ngroups * p->dstate / 1024 >= (int64_t(1) << 31)) return fail(SSM_ERR_SHAPE, "too many tokens");
+  // (the main pass's grid is rounded up to the 8 XCDs; the sums' blocks take four columns of a row a thread)
+  if (!fits_launch(b.numbers * b.splits * p->ngroups + 7, static_cast<int>(p->dstate) * 4))
+    return fail(SSM_ERR_SHAPE, "too many work items (chunks times groups) for one launch");
+  if (!fits_launch(p->nheads + p->ntokens * p->ngroups * p->dstate / 1024 + 1, 256))
+    return fail(SSM_ERR_SHAPE, "ntokens * ngroups * dstate is too large for one launch");
   return SSM_OK;
 }
 
