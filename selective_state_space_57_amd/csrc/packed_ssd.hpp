@@ -229,6 +229,35 @@ __device__ __forceinline__ float wave_suffix(float v, int lane) {
   return v + (row <= 2 ? r3 : 0.0f) + (row <= 1 ? r2 : 0.0f) + (row <= 0 ? r1 : 0.0f);
 }
 
+// A double moved across lanes by two 32-bit DPP moves (0 where the source or the row mask gives none).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double lanes_move(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const int lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, ROWS, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, ROWS, 0xf, false);
+  return __builtin_bit_cast(double, static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32 | static_cast<uint32_t>(lo));
+}
+// Running sum over lanes 0..lane of the decays' logarithms, and the sum over all, in 64 bits: what is left between two steps
+// is a difference of two of these, which a few steps that decay (nearly) everything make large.  In fp32 one such step
+// of 2^12 would cost the decays between all steps behind it 2^-12.
+struct DecaySum {
+  double upto, all;
+  __device__ __forceinline__ float behind() const { return static_cast<float>(all - upto); }   // sum over the lanes behind
+};
+__device__ __forceinline__ DecaySum sum_decays(float la) {
+  double d = la;
+  d += lanes_move<0x111, 0xf>(d);   // row_shr: 1, 2, 4, 8
+  d += lanes_move<0x112, 0xf>(d);
+  d += lanes_move<0x114, 0xf>(d);
+  d += lanes_move<0x118, 0xf>(d);
+  d += lanes_move<0x142, 0xa>(d);   // row_bcast: lane 15 into the second and fourth row, then lane 31 into the last two
+  d += lanes_move<0x143, 0xc>(d);
+  const uint64_t u = __builtin_bit_cast(uint64_t, d);
+  const uint32_t lo = __builtin_amdgcn_readlane(static_cast<int>(u), 63);
+  const uint32_t hi = __builtin_amdgcn_readlane(static_cast<int>(u >> 32), 63);
+  return DecaySum{d, __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo)};
+}
+
 // Pieces: sequence s is cut every `steps` tokens (segments of a walk, or chunk groups of the backward).  Piece i of a
 // sequence that begins at token b has the number s + b / steps + i: that is unique, needs no sum over the sequences
 // before it, and stays below nseqs + ntokens / steps + 1 (some numbers belong to no piece).
@@ -293,13 +322,22 @@ __device__ __forceinline__ float softplus_slope(float u) {
   return (u >= 0.0f ? 1.0f : v) / (1.0f + v);
 }
 
+// Logarithm (base 2) of a step's decay.  Held within 2^14, far behind where its exponential is 0 (or infinite): sums of it
+// stay finite, and so do their differences.  (A NaN stays one.)
+__device__ __forceinline__ float decay_log(float delta, float A) {
+  constexpr float kMost = 16384.0f;
+  float la = delta * A * kLog2e;
+  la = la < -kMost ? -kMost : la;
+  return la > kMost ? kMost : la;
+}
+
 // Step size, its weight and the decay's logarithm (base 2) of one step; zeros behind the sequence.
 __device__ __forceinline__ void step_scalars(float dt, float bias, float A, bool use_softplus, bool zoh, bool live,
                                              float& delta, float& phi, float& la) {
   const float u = dt + bias;
   delta = use_softplus ? softplus_fine(u) : u;
   delta = live ? delta : 0.0f;
-  la = delta * A * kLog2e;
+  la = decay_log(delta, A);
   phi = delta;
   if (zoh && A != 0.0f) {
     const float e = delta * A;

@@ -18,7 +18,7 @@
 // update is split into three bf16 parts, so the state keeps fp32 quality over long sequences (two parts, 2^-17, are 11 %
 // faster).  M (but for s = t, which is added in fp32) and the state that meets C only reach y: they are split into two,
 // which leave out 2^-16 of them at most, so that y is the 64-bit value rounded once but for 5e-5 of it in the 2-norm
-// (rounded to bf16 once each, they added 1.4e-3 to the rounding's own 1.66e-3; 16384 tokens of the 2.7B layer then take
+// (rounded to bf16 once each, they added 1.4e-3 to the rounding's own 1.66e-3; 16384 tokens of the 2.7B layer then took
 // 282 us instead of 337).
 //
 // Measured on 16384 tokens of 80 heads, N = 128 (0.40 GB in and out, 43 GFLOP): 280 us, 200 of them this pass, 85 the walk
@@ -53,10 +53,13 @@ struct PSsdArgs {
 
 // scalars of one chunk, per wave
 struct alignas(16) HeadScalars {
-  float c[kChunk];     // c_t, base 2
-  float phi[kChunk];
+  // c_t (base 2), rounded to fp32: differences of these are good to their own rounding, and the rests r_t that the
+  // rounding left go into factors, exp(c_t - c_s) = exp2(c[t] - c[s]) exp2(r_t) exp2(-r_s)
+  float c[kChunk];
+  float rest[kChunk];  // exp2(r_t)
+  float phi[kChunk];   // phi_s exp2(-r_s)
   float w[kChunk];     // phi_s exp(c_63 - c_s)
-  float own[kChunk];   // M[t][t] + D
+  float own[kChunk];   // M[t][t] exp2(-r_t)
 };
 
 template <int N>
@@ -156,17 +159,16 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
       const int lane = afresh(threadIdx.x) & 63;
       float delta, phi, la;
       step_scalars(lo_f32(dtv), bias, Ah, a.softplus, a.zoh, lane < rows, delta, phi, la);
-      const float c = wave_prefix(la, lane);
-      // exp(c_63 - c_s) from the sum behind step s: no difference of two large sums
-      const float behind = wave_suffix(la, lane) - la;
+      const DecaySum sum = sum_decays(la);
+      const float c = static_cast<float>(sum.upto), r = static_cast<float>(sum.upto - c);
       sc.c[lane] = c;
-      sc.phi[lane] = phi;
-      sc.w[lane] = phi * hw_exp2(behind);
+      sc.rest[lane] = hw_exp2(r);
+      sc.phi[lane] = phi * hw_exp2(-r);
+      sc.w[lane] = phi * hw_exp2(sum.behind());
     }
     wait_memory();    // this wave's copies
     barrier_lds();    // and everyone's
     dtv = load_dt(ck + 1);
-    const float total = sc.c[kChunk - 1];
     {
       // C B^T, tile i = (tb, sb), sb <= tb: rows s, columns t
       for (int i = wave; i < 10; i += NW) {
@@ -249,7 +251,7 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
                 m[c] = cb[c] * (hw_exp2(ct[i] - cs[c]) * ph[c]);
                 if (sb == tb) {
                   // a step's own x goes into its y in fp32, together with D
-                  if (4 * g4 + c == l16) sc.own[16 * tb + l16] = m[c] + Dh;
+                  if (4 * g4 + c == l16) sc.own[16 * tb + l16] = m[c];
                   m[c] = 4 * g4 + c < l16 ? m[c] : 0.0f;
                 }
               }
@@ -266,9 +268,9 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int t = 32 * th + 16 * i + l16;
-          const float own = sc.own[t];
+          const float up = sc.rest[t], own = fmaf(sc.own[t], up, Dh);
           const pu4 xv = lds_u4(X, unit_at<UX>(t, g4));
-          const pf4 y0 = acc[i][0], y1 = acc[i][1];
+          const pf4 y0 = acc[i][0] * up, y1 = acc[i][1] * up;
           const pu4 o = {pack_bf16(fmaf(own, lo_f32(xv[0]), y0[0]), fmaf(own, hi_f32(xv[0]), y0[1])),
                          pack_bf16(fmaf(own, lo_f32(xv[1]), y0[2]), fmaf(own, hi_f32(xv[1]), y0[3])),
                          pack_bf16(fmaf(own, lo_f32(xv[2]), y1[0]), fmaf(own, hi_f32(xv[2]), y1[1])),
@@ -281,7 +283,7 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
     part_ends();
     // state update
     const int l = afresh(lane), l16 = l & 15, g4 = l >> 4;
-    const float fade = hw_exp2(total);
+    const float fade = hw_exp2(sc.c[kChunk - 1]) * sc.rest[kChunk - 1];
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
       const pf4 w0 = *reinterpret_cast<const pf4*>(&sc.w[32 * kk + 4 * g4]);

@@ -64,14 +64,13 @@ struct BwdArgs {
 };
 
 struct alignas(16) ChunkScalars {
-  // c_t (base 2) as the sum over the 16 steps up to t of its tile and the sum before the tile: differences of steps near
-  // each other then carry the rounding of a short sum only
-  float c[kChunk], before[4];
+  // c_t (base 2) in two parts: differences of the first are good to their own rounding, and the second is what it leaves
+  float c[kChunk], rest[kChunk];
   float phi[kChunk];
   float e[kChunk];                // exp(c_t)
   float pf[kChunk];               // phi_t exp(c_63 - c_t)
   float f[kChunk];                // exp(c_63 - c_t)
-  float delta[kChunk], decay[kChunk], slope[kChunk];   // Delta_t, exp(Delta_t A), d Delta / d dt
+  float delta[kChunk], slope[kChunk];   // Delta_t, d Delta / d dt
 };
 
 __host__ __device__ constexpr int tile_row(int i) { return i >= 6 ? 3 : (i >= 3 ? 2 : (i >= 1 ? 1 : 0)); }
@@ -198,17 +197,15 @@ packed_ssd_bwd_kernel(BwdArgs a) {
       const float bias = a.dt_bias ? a.dt_bias[h] : 0.0f;
       float delta, phi, la;
       step_scalars(dtv, bias, Ah, a.softplus, a.zoh, lane < rows, delta, phi, la);
-      float in_row, before;
-      row_prefix(la, lane, in_row, before);
-      const float f = hw_exp2(wave_suffix(la, lane) - la);
-      sc.c[lane] = in_row;
-      if ((lane & 15) == 0) sc.before[lane >> 4] = before;
+      const DecaySum sum = sum_decays(la);
+      const float c = static_cast<float>(sum.upto), f = hw_exp2(sum.behind());
+      sc.c[lane] = c;
+      sc.rest[lane] = static_cast<float>(sum.upto - c);
       sc.phi[lane] = phi;
-      sc.e[lane] = hw_exp2(in_row + before);
+      sc.e[lane] = hw_exp2(c);
       sc.f[lane] = f;
       sc.pf[lane] = phi * f;
       sc.delta[lane] = delta;
-      sc.decay[lane] = hw_exp2(la);
       sc.slope[lane] = a.softplus ? softplus_slope(dtv + bias) : 1.0f;
     }
     wait_memory();
@@ -275,8 +272,7 @@ packed_ssd_bwd_kernel(BwdArgs a) {
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk)
         X = mma(lds_row_operand<8>(Yk, 16 * tb + l16, kk, g4), lds_row_operand<8>(Xk, 16 * sb + l16, kk, g4), X);
-      const pf4 ct = *reinterpret_cast<const pf4*>(&sc.c[16 * tb + 4 * g4]) + (sc.before[tb] - sc.before[sb]);
-      const float cs = sc.c[16 * sb + l16], ph = sc.phi[16 * sb + l16];
+      const float ph = sc.phi[16 * sb + l16];
       pf4 Z = zero;
 #pragma unroll
       for (int kk = 0; kk < NK; ++kk) {
@@ -284,13 +280,16 @@ packed_ssd_bwd_kernel(BwdArgs a) {
         Z = mma(lds_row_operand<U>(Ck, 16 * tb + l16, kk, g4), lds_row_operand<U>(Bk, 16 * sb + l16, kk, g4), Z);
       }
       part_ends();
+      // c_t - c_s
+      const pf4 gap = (*reinterpret_cast<const pf4*>(&sc.c[16 * tb + 4 * g4]) - sc.c[16 * sb + l16]) +
+                      (*reinterpret_cast<const pf4*>(&sc.rest[16 * tb + 4 * g4]) - sc.rest[16 * sb + l16]);
       pf4 k = ti < kHeld ? aK[min(ti, kHeld - 1)] : sK2[nt][l];
       pf4 m;
       float row[4], col = 0.0f;
       if (sb < tb) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const float L = hw_exp2(ct[c] - cs), lx = L * X[c];
+          const float L = hw_exp2(gap[c]), lx = L * X[c];
           k[c] = fmaf(lx, ph, k[c]);
           m[c] = L * Z[c] * ph;
           const float w0 = lx * Z[c];
@@ -302,7 +301,7 @@ packed_ssd_bwd_kernel(BwdArgs a) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int above = l16 - (4 * g4 + c);   // column minus row
-          const float L = above <= 0 ? hw_exp2(ct[c] - cs) : 0.0f, lx = L * X[c];
+          const float L = above <= 0 ? hw_exp2(gap[c]) : 0.0f, lx = L * X[c];
           k[c] = fmaf(lx, ph, k[c]);
           const float mm = L * Z[c] * ph, w0 = lx * Z[c];
           // a step's own terms: its dy goes into its dx in fp32, together with D, and W[t][t] is in its row and in its
@@ -443,9 +442,11 @@ packed_ssd_bwd_kernel(BwdArgs a) {
       // rows from r on of those beside, the columns before r of those below, and the own tile's corner, where alone rows
       // less columns are taken, over 16 steps (over the whole chunk, sums much larger than dl would cancel)
       const float far = tl == 1 ? sTotal[3] + sTotal[6] : tl == 2 ? sTotal[6] + sTotal[7] : 0.0f;
-      const float dl = row_suffix(row_off + (row - phi * col)) + (row_prefix(off) - off) + far + wave_suffix(u, lane) +
+      float dl = row_suffix(row_off + (row - phi * col)) + (row_prefix(off) - off) + far + wave_suffix(u, lane) +
                        (wave_prefix(before, lane) - before) + sc.e[kChunk - 1] * e;
-      const float delta = sc.delta[lane], decay = sc.decay[lane];
+      const float delta = sc.delta[lane], decay = hw_exp2(decay_log(delta, Ah));
+      // (dl = a <G, S> is nothing where a is: what the sums leave by rounding would count Delta times in dA)
+      dl = decay == 0.0f ? 0.0f : dl;
       const float dd = (Ah * dl + (a.zoh ? decay * dphi : dphi)) * sc.slope[lane];
       float sum_a = 0.0f, sum_t = 0.0f, sum_d = lane < 4 ? sDiag[lane] : 0.0f;
       if (lane < rows) {

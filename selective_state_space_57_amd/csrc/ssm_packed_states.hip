@@ -141,10 +141,9 @@ __device__ __forceinline__ void walk(const StatesArgs& a, uint16_t* sK0, uint16_
     }
     float delta, phi, la;
     step_scalars(lo_f32(dtv), bias, Ah, a.softplus, a.zoh, lane < rows, delta, phi, la);
-    const float c = wave_prefix(la, lane);
-    const float total = lane_value(c, 63);
-    // (exp(c_63 - c_s) from the sum behind step s: no difference of two large sums)
-    W[lane] = REV ? hw_exp2(c) : phi * hw_exp2(wave_suffix(la, lane) - la);
+    const DecaySum sum = sum_decays(la);
+    const float total = static_cast<float>(sum.all);
+    W[lane] = REV ? hw_exp2(static_cast<float>(sum.upto)) : phi * hw_exp2(sum.behind());
     wave_lds_sync();
     const float fade = hw_exp2(total);
 #pragma unroll

@@ -7,12 +7,14 @@ value at most, three 2^-24.  The decays' logarithms are summed without loss that
 import pytest
 
 import packed_ref as R
-from test_packed_gpu import BF, SSD, f64, ssd_case, ssd_ref, ssm, T, within
+from test_packed_gpu import BF, SSD, Rand, T, f64, packed, ssd_case, ssd_ref, ssm, within
 
 pytestmark = pytest.mark.gpu
 
 # what stands before the last rounding, of the sum of the magnitudes: 2^-16 (parts) + 2^-15 (sums) + 2^-19 (step, decay)
 REST = 2.0 ** -14
+# a decay below fp32's smallest normal number, 2^-126, is zero: what it multiplies, below 2^25 here, is lost up to 2^-101
+TINY = 2.0 ** -100
 
 
 @pytest.mark.parametrize("k", range(len(SSD)))
@@ -23,7 +25,7 @@ def test_y_is_rounded_once(k):
                              state_idx=idx, has_state=has, **kw)
     torch.cuda.synchronize()
     inside = slice(cul[0], cul[-1])
-    within(y[inside], (BF * ref.abs() + REST * mag + 1e-30)[inside], ref[inside], "y")
+    within(y[inside], (BF * ref.abs() + REST * mag + TINY)[inside], ref[inside], "y")
 
 
 @pytest.mark.parametrize("k", range(len(SSD)))
@@ -42,4 +44,74 @@ def test_gradients_are_rounded_once(k):
     torch.cuda.synchronize()
     inside = slice(cul[0], cul[-1])
     for n in ("dx", "dB", "dC"):
-        within(got[n][inside], (BF * ref[n].abs() + REST * mag[n] + 1e-30)[inside], ref[n][inside], n)
+        within(got[n][inside], (BF * ref[n].abs() + REST * mag[n] + TINY)[inside], ref[n][inside], n)
+
+
+RESETS = [(64, False, (200, 500)), (128, False, (1000, 1e4)), (128, True, (200, 1e4)), (256, False, (20, 200, 1e4)),
+          (64, True, (3, 10, 1000))]
+
+
+def resetting(N, zoh, strong):
+    """A quarter of the steps large, the others 1e-3 to 0.1."""
+    torch = T()
+    r = Rand(40 + N + zoh)
+    H, lens = 4, [130, 64, 200, 3]
+    cu, cul, rows = packed(lens)
+    bf = torch.bfloat16
+    x, dy = r(rows, H, 64, dtype=bf), r(rows, H, 64, dtype=bf)
+    B, C = r(rows, 1, N, dtype=bf), r(rows, 1, N, dtype=bf)
+    A = -torch.tensor([1.0, 8.0, 16.0, 12.0]).cuda()
+    u = torch.rand(rows, H, generator=r.g) * 4.6 - 6.9                       # softplus: 1e-3 to 0.1
+    big = torch.tensor(strong)[torch.randint(0, len(strong), (rows, H), generator=r.g)]
+    dt = torch.where(torch.rand(rows, H, generator=r.g) < 0.25, big, u).to(bf).cuda()
+    D = r(H)
+    state, dl = r(len(lens), H, 64, N), r(len(lens), H, 64, N, scale=0.3)
+    wide = [f64(t) for t in (x, dt, A, B, C)]
+    mags = [wide[0].abs(), wide[1], wide[2], wide[3].abs(), wide[4].abs()]
+    return torch, x, dt, A, B, C, D, dy, cu, cul, state, dl, wide, mags
+
+
+# What decays between ordinary steps behind one that resets the state is as good as without it.
+
+@pytest.mark.parametrize("N,zoh,strong", RESETS)
+def test_y_behind_steps_that_reset_the_state(N, zoh, strong):
+    torch, x, dt, A, B, C, D, dy, cu, cul, state, dl, wide, mags = resetting(N, zoh, strong)
+    first = f64(state)
+    ref, last, mag = R.ssd(*wide, None, f64(D), cul, first, True, zoh)
+    out = torch.empty_like(state)
+    y = ssm().ssd_packed_fwd(x, dt, A, B, C, cu, None, D, state=state, state_out=out, disc=int(zoh))
+    torch.cuda.synchronize()
+    within(y, BF * ref.abs() + REST * mag + TINY, ref, "y")
+    # three parts; decays and sums as above, on the state's own magnitudes
+    big = R.ssd(*mags, None, None, cul, first.abs(), True, zoh)[1]
+    within(out, 2.0 ** -15 * big + TINY, last, "state")
+
+
+@pytest.mark.parametrize("N,zoh,strong", RESETS)
+def test_gradients_behind_steps_that_reset_the_state(N, zoh, strong):
+    torch, x, dt, A, B, C, D, dy, cu, cul, state, dl, wide, mags = resetting(N, zoh, strong)
+    first = f64(state)
+    got = ssm().ssd_packed_bwd(x, dt, A, B, C, dy, cu, None, D, state=state, dstate_out=dl, disc=int(zoh))
+    torch.cuda.synchronize()
+    g = R.ssd_grads(*wide, None, f64(D), cul, first, f64(dy), f64(dl), True, zoh)
+    gm = R.ssd_grads(*mags, None, f64(D).abs(), cul, first.abs(), f64(dy).abs(), f64(dl).abs(), True, zoh)
+    mag = R.ssd(*wide, None, f64(D), cul, first, True, zoh)[2]
+    for n in ("dx", "dB", "dC"):
+        within(got[n], BF * g[n].abs() + REST * gm[n] + TINY, g[n], n)
+    within(got["dstate"], 2.0 ** -15 * gm["dstate"] + TINY, g["dstate"], "dstate")
+    # dl of a step is what sums over the steps of its chunk leave: of rows and columns of W, whose magnitudes are those of
+    # |dy| |y| and |x| |dx|, about 16 roundings of 2^-24 each of twice the chunk's; nothing where the step's decay is 0
+    om = (f64(dy).abs() * mag).sum(-1) + (f64(x).abs() * gm["dx"]).sum(-1)
+    u, d, a, phi = R.steps(wide[1], None, wide[2], True, zoh)
+    tol = torch.zeros_like(om)
+    for b, e in zip(cul, cul[1:]):
+        for t in range(b, e, 64):
+            tol[t:min(t + 64, e)] = 2.0 ** -19 * om[t:min(t + 64, e)].sum(0)
+    tol = torch.where(a > 2.0 ** -126, tol, torch.zeros_like(tol))
+    dphi = (f64(x).abs() * (gm["dx"] - f64(D).abs()[:, None] * f64(dy).abs())).sum(-1) / phi
+    slope = 1 / (1 + torch.exp(-u))
+    ddt = (wide[2].abs() * tol + 2.0 ** -17 * dphi) * slope
+    within(got["ddt"], BF * g["ddt"].abs() + 2 * ddt + TINY, g["ddt"], "ddt")
+    by_a = (d * a - phi).abs() / wide[2].abs() * dphi if zoh else torch.zeros_like(d)
+    within(got["dA"], (d * tol + 2.0 ** -17 * by_a).sum(0) + 2.0 ** -17 * gm["dA"].abs() + TINY, g["dA"], "dA")
+    within(got["ddt_bias"], ddt.sum(0) + 2.0 ** -17 * g["ddt"].abs().sum(0) + TINY, g["ddt_bias"], "ddt_bias")
