@@ -294,10 +294,10 @@ __device__ __forceinline__ bool find_piece(const int32_t* cu, int nseqs, int nto
 
 // exp(-|u|), good to about 2^-23: the rounding of the exponent's product with log2(e), which the exponential would
 // magnify by |u|, is put back (a step's errors are the same for every column of a head, so they do not average out in
-// dA and the step sizes' gradients).
+// dA and the step sizes' gradients).  It is 0 from 128 on, infinite u among them (whose rest would be no number; NaN stays).
 __device__ __forceinline__ float exp_neg_abs(float u) {
   constexpr float kLog2eLo = 1.925963033500e-8f;   // log2(e) - float(log2(e))
-  const float x = -fabsf(u);
+  const float x = fabsf(u) > 128.0f ? -128.0f : -fabsf(u);
   const float p = x * kLog2e;
   const float rest = fmaf(x, kLog2e, -p) + x * kLog2eLo;
   const float v = hw_exp2(p);

@@ -77,9 +77,11 @@ __host__ __device__ constexpr int tile_row(int i) { return i >= 6 ? 3 : (i >= 3 
 // place of the operand over 32 rows t (kk) of column tile sb: (0,0) (0,1) (1,0) (1,1) (2,1) (3,1)
 __host__ __device__ constexpr int m_slot(int sb, int kk) { return sb < 2 ? 2 * sb + kk : sb + 2; }
 
-// d phi / dA of the zero-order hold, phi = (exp(e) - 1) / A with e = Delta A: Delta^2 (e exp(e) - exp(e) + 1) / e^2, by
-// its series where the numerator cancels (the first term left out is below 2^-21 of the value for |e| < 1/2)
-__device__ __forceinline__ float zoh_slope(float delta, float e, float a) {
+// d phi / dA of the zero-order hold, phi = (exp(e) - 1) / A with e = Delta A: (e exp(e) - exp(e) + 1) / A^2, by its series
+// times Delta^2 where the numerator cancels (the first term left out is below 2^-21 of the value for |e| < 1/2); 1 / A^2
+// where the decay a = exp(e) is 0
+__device__ __forceinline__ float zoh_slope(float delta, float A, float a) {
+  const float e = delta * A;
   float p = 1.0f / 5760.0f;
   p = fmaf(p, e, 1.0f / 840.0f);
   p = fmaf(p, e, 1.0f / 144.0f);
@@ -87,8 +89,7 @@ __device__ __forceinline__ float zoh_slope(float delta, float e, float a) {
   p = fmaf(p, e, 0.125f);
   p = fmaf(p, e, 1.0f / 3.0f);
   p = fmaf(p, e, 0.5f);
-  const float direct = fabsf(e) < 0.5f ? 0.0f : (fmaf(e, a, -a) + 1.0f) / (e * e);
-  return delta * delta * (fabsf(e) < 0.5f ? p : direct);
+  return fabsf(e) < 0.5f ? delta * delta * p : ((a == 0.0f ? 0.0f : fmaf(e, a, -a)) + 1.0f) / (A * A);
 }
 
 template <int N>
@@ -451,7 +452,7 @@ packed_ssd_bwd_kernel(BwdArgs a) {
       float sum_a = 0.0f, sum_t = 0.0f, sum_d = lane < 4 ? sDiag[lane] : 0.0f;
       if (lane < rows) {
         Elem<uint16_t>::st(a.ddt, (t_first + lane) * a.ddts + h, dd);
-        sum_a = delta * dl + (a.zoh ? zoh_slope(delta, delta * Ah, decay) * dphi : 0.0f);
+        sum_a = delta * dl + (a.zoh ? zoh_slope(delta, Ah, decay) * dphi : 0.0f);
         sum_t = dd;
       }
       sum_a = sum_wave(sum_a);

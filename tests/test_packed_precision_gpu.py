@@ -115,3 +115,63 @@ def test_gradients_behind_steps_that_reset_the_state(N, zoh, strong):
     by_a = (d * a - phi).abs() / wide[2].abs() * dphi if zoh else torch.zeros_like(d)
     within(got["dA"], (d * tol + 2.0 ** -17 * by_a).sum(0) + 2.0 ** -17 * gm["dA"].abs() + TINY, g["dA"], "dA")
     within(got["ddt_bias"], ddt.sum(0) + 2.0 ** -17 * g["ddt"].abs().sum(0) + TINY, g["ddt_bias"], "ddt_bias")
+
+
+LOWEST = [float("-inf"), -3.3895313892515355e38]     # (the lowest of bf16)
+
+
+def masked(N):
+    """A batch with steps that are masked by their step size, and where they are."""
+    torch = T()
+    r = Rand(50 + N)
+    H, lens = 3, [70, 1, 129]
+    cu, cul, rows = packed(lens)
+    bf = torch.bfloat16
+    x, dy = r(rows, H, 64, dtype=bf), r(rows, H, 64, dtype=bf)
+    B, C = r(rows, 1, N, dtype=bf), r(rows, 1, N, dtype=bf)
+    dt, A, D = r(rows, H, dtype=bf), -torch.rand(H, generator=r.g).cuda() * 7 - 1, r(H)
+    off = (torch.rand(rows, H, generator=r.g) < 0.3).cuda()
+    off[70] = True
+    state, dl = r(3, H, 64, N), r(3, H, 64, N, scale=0.3)
+    return torch, x, dt, A, B, C, D, dy, cu, cul, state, dl, off
+
+
+@pytest.mark.parametrize("low", LOWEST)
+@pytest.mark.parametrize("N,zoh", [(64, False), (128, True), (256, False)])
+def test_steps_masked_by_their_size(low, N, zoh):
+    """softplus of -infinity and of the type's lowest value is 0: such a step leaves the state as it is, and has no gradient.
+    -200 gives 0 as well, in ordinary arithmetic: all outputs are the same bits."""
+    torch, x, dt, A, B, C, D, dy, cu, cul, state, dl, off = masked(N)
+    res = []
+    for v in (low, -200.0):
+        d = torch.where(off, torch.full_like(dt, v), dt)
+        out, pool = torch.empty_like(state), state.clone()
+        y = ssm().ssd_packed_fwd(x, d, A, B, C, cu, None, D, state=state, state_out=out, disc=int(zoh))
+        g = ssm().ssd_packed_bwd(x, d, A, B, C, dy, cu, None, D, state=state, dstate_out=dl, disc=int(zoh))
+        s = ssm().ssd_slot_update(pool, x[:3], d[:3], A, B[:3], C[:3], None, D, disc=int(zoh))
+        torch.cuda.synchronize()
+        res.append(dict(g, y=y, out=out, s=s, pool=pool))
+    for n, t in res[0].items():
+        assert bool(t.isfinite().all()), n
+        assert torch.equal(t, res[1][n]), n
+    assert bool((res[0]["ddt"][off] == 0).all())
+    assert torch.equal(res[0]["out"][1], state[1])        # one step, masked
+
+
+@pytest.mark.parametrize("N", [64, 128])
+def test_largest_steps_under_zero_order_hold(N):
+    """A step of the type's largest value resets the state to -x B / A; nothing of it is infinite.  Steps of 1e4 do the same in
+    ordinary arithmetic: all outputs are the same bits."""
+    torch, x, dt, A, B, C, D, dy, cu, cul, state, dl, off = masked(N)
+    res = []
+    for v in (3.3895313892515355e38, 1e4):
+        d = torch.where(off, torch.full_like(dt, v), dt)
+        out, pool = torch.empty_like(state), state.clone()
+        y = ssm().ssd_packed_fwd(x, d, A, B, C, cu, None, D, state=state, state_out=out, disc=1)
+        g = ssm().ssd_packed_bwd(x, d, A, B, C, dy, cu, None, D, state=state, dstate_out=dl, disc=1)
+        s = ssm().ssd_slot_update(pool, x[:3], d[:3], A, B[:3], C[:3], None, D, disc=1)
+        torch.cuda.synchronize()
+        res.append(dict(g, y=y, out=out, s=s, pool=pool))
+    for n, t in res[0].items():
+        assert bool(t.isfinite().all()), n
+        assert torch.equal(t, res[1][n]), n
