@@ -366,7 +366,8 @@ size_t ssm_ssd_packed_fwd_workspace_bytes(const ssm_ssd_packed_params* p);
  *   S_t = exp(Delta_t A) S_{t-1} + phi_t x_t B_t^T,  y_t = S_t C_t + Dskip x_t
  * x, y [ntokens][nheads][headdim]; dt [ntokens][nheads]; B, C [ntokens][ngroups][dstate], bf16; A, dt_bias, Dskip [nheads]
  * fp32 (dt_bias, Dskip NULL = 0); state, state_out [nslots][nheads][headdim][dstate] fp32 or NULL.  Rows of x, B, C and
- * y, the states and the workspace must be 16-byte aligned.  y must not overlap an input.
+ * y, the states and the workspace must be 16-byte aligned.  y must not overlap an input.  What is not finite reaches no
+ * earlier step and no other sequence: an entry of x makes its own column of y and of the state NaN from its step on.
  */
 ssm_status ssm_ssd_packed_fwd(const ssm_ssd_packed_params* p, const void* x, const void* dt, const float* dt_bias,
                               const float* A, const void* B, const void* C, const float* Dskip,
@@ -385,7 +386,7 @@ size_t ssm_ssd_packed_bwd_workspace_bytes(const ssm_ssd_packed_params* p);
  * summed over the heads of a group); dA [nheads] fp32; dDskip, ddt_bias [nheads] and dstate [nseqs][nheads][headdim]
  * [dstate] fp32 (the gradient of the state each sequence starts from, at zero where it has none), each optional.  Rows
  * of dy and dx must be 16-byte, of dB and dC 8-byte aligned; outputs must not overlap inputs or each other.
- * Deterministic.
+ * Deterministic.  What is not finite in a sequence may reach any gradient of that sequence, but no other one's.
  */
 ssm_status ssm_ssd_packed_bwd(const ssm_ssd_packed_params* p, const void* x, const void* dt, const float* dt_bias,
                               const float* A, const void* B, const void* C, const float* Dskip,

@@ -56,6 +56,14 @@ __device__ __forceinline__ Parts split3(pf4 a, pf4 b) {
 }
 __device__ __forceinline__ pf4 unpack4(uint32_t a, uint32_t b) { return pf4{lo_f32(a), hi_f32(a), lo_f32(b), hi_f32(b)}; }
 
+// Packed bf16 pairs: the larger magnitude's bits of each half, and whether either half of the magnitudes is not finite.
+typedef unsigned short pus2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t larger_bits(uint32_t most, uint32_t pair) {
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(pus2, most),
+                                                                __builtin_bit_cast(pus2, pair & 0x7fff7fffu)));
+}
+__device__ __forceinline__ bool not_finite(uint32_t most) { return most >= 0x7f800000u || (most & 0xffffu) >= 0x7f80u; }
+
 // Rows of a chunk in LDS: U 16-byte units each, unit u of row r at u ^ swz(r).  16-byte reads go 8 lanes at a time over
 // 128 bytes of banks: 8 consecutive rows of one unit need 8 different places (the low three bits).  Transposing reads
 // go 32 lanes over 256 bytes: 8 consecutive rows x 4 consecutive units, one 8-byte half of each, spread over all 16

@@ -77,6 +77,7 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
   __shared__ alignas(16) uint16_t sX[NW][kChunk * 16 * PT];
   __shared__ pf4 sCB[10][64];   // tiles of C B^T on and below the diagonal
   __shared__ HeadScalars sS[NW / kParts];   // (the waves of a head write the same values)
+  __shared__ alignas(8) uint8_t sSpoilt[NW][16 * PT];   // per column, the chunk's first step whose x is not finite
 
   // (in launch order, heads fastest: the heads of a segment go round the XCDs, so that segments of any length, and numbers
   // without one, spread evenly; runs of items per XCD, which share B and C in its L2, left some with two rounds)
@@ -169,6 +170,33 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
     wait_memory();    // this wave's copies
     barrier_lds();    // and everyone's
     dtv = load_dt(ck + 1);
+    // M is 0 for s > t, but 0 times what is not finite is not 0.  Such an x is taken out, and its column of y and of the state
+    // is made NaN from its step on: nothing in front of it changes.  (Looking for one takes 10 of 342 us, 16384 tokens of the
+    // 2.7B layer.)
+    bool spoilt;
+    {
+      uint32_t most = 0u;
+#pragma unroll
+      for (int i = 0; i < kChunk * UX / 64; ++i) {
+        const pu4 v = lds_u4(X, (64 * i + afresh(lane)) * 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) most = larger_bits(most, v[j]);
+      }
+      spoilt = __builtin_amdgcn_ballot_w64(not_finite(most)) != 0;
+    }
+    if (spoilt) {
+      const int p = afresh(lane) % (16 * PT);
+      int first = kChunk;
+      for (int r = kChunk - 1; r >= 0; --r) {
+        uint16_t* at = sX[wave] + (unit_at<UX>(r, p >> 3) >> 1) + (p & 7);
+        if ((*at & 0x7f80u) == 0x7f80u) {
+          first = r;
+          *at = 0;
+        }
+      }
+      sSpoilt[wave][p] = static_cast<uint8_t>(first);
+      wave_lds_sync();
+    }
     {
       // C B^T, tile i = (tb, sb), sb <= tb: rows s, columns t
       for (int i = wave; i < 10; i += NW) {
@@ -271,10 +299,17 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
           const float up = sc.rest[t], own = fmaf(sc.own[t], up, Dh);
           const pu4 xv = lds_u4(X, unit_at<UX>(t, g4));
           const pf4 y0 = acc[i][0] * up, y1 = acc[i][1] * up;
-          const pu4 o = {pack_bf16(fmaf(own, lo_f32(xv[0]), y0[0]), fmaf(own, hi_f32(xv[0]), y0[1])),
+          pu4 o = {pack_bf16(fmaf(own, lo_f32(xv[0]), y0[0]), fmaf(own, hi_f32(xv[0]), y0[1])),
                          pack_bf16(fmaf(own, lo_f32(xv[1]), y0[2]), fmaf(own, hi_f32(xv[1]), y0[3])),
                          pack_bf16(fmaf(own, lo_f32(xv[2]), y1[0]), fmaf(own, hi_f32(xv[2]), y1[1])),
                          pack_bf16(fmaf(own, lo_f32(xv[3]), y1[2]), fmaf(own, hi_f32(xv[3]), y1[3]))};
+          if (spoilt) {
+            const pu2 first = *reinterpret_cast<const pu2*>(&sSpoilt[wave][8 * g4]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (static_cast<int>((first[j >> 2] >> (8 * (j & 3))) & 0xffu) <= t)
+                o[j >> 1] = (j & 1) ? (o[j >> 1] & 0xffffu) | 0x7fc00000u : (o[j >> 1] & 0xffff0000u) | 0x7fc0u;
+          }
           __builtin_amdgcn_raw_buffer_store_b128(
               o, ry, static_cast<int>(static_cast<uint32_t>(t) * yrow + 16u * g4), 0, 0);
         }
@@ -308,6 +343,15 @@ packed_ssd_fwd_kernel(PSsdArgs a) {
           for (int i = 0; i < 3; ++i) v = mma(b, w[pt].p[i], v);
           S[nt][pt] = v;
         }
+      }
+    }
+    if (spoilt) {
+#pragma unroll
+      for (int pt = 0; pt < PT; ++pt) {
+        const int p = 32 * (pt >> 1) + 8 * (l16 >> 2) + 4 * (pt & 1) + (l16 & 3);
+        const float add = sSpoilt[wave][p] < kChunk ? __builtin_nanf("") : 0.0f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) S[nt][pt] += add;
       }
     }
   }

@@ -312,7 +312,8 @@ def ssd_packed_fwd(x, dt, A, B, C, cu_seqlens, dt_bias=None, Dskip=None, *, stat
     """The Mamba-2 SSD layer over packed tokens, without the gate: x (T, H, 64), dt (T, H), B, C (T, G, N) bfloat16 (rows
     of x, B and C 16-byte aligned); A, dt_bias, Dskip (H,) float32; state / state_out (slots, H, 64, N) float32.  N is 64,
     128 or 256.  segment_chunks: 0 = the library's choice of the 64-step chunks of a sequence that run one after the
-    other.  Returns y (T, H, 64); its rows outside every sequence are left as they are."""
+    other.  Returns y (T, H, 64); its rows outside every sequence are left as they are.  What is not finite reaches no earlier
+    step and no other sequence: an entry of x makes its own column of y and of the state NaN from its step on."""
     import torch
     T = x.shape[0]
     dev = _on_gpu(x, "x")
@@ -372,7 +373,8 @@ def ssd_packed_bwd(x, dt, A, B, C, dy, cu_seqlens, dt_bias=None, Dskip=None, *, 
     dx (T, H, 64), ddt (T, H), dB, dC (T, G, N) bfloat16, dA, dDskip, ddt_bias (H,) float32 and dstate (S, H, 64, N)
     float32, the gradient of the state each sequence starts from (want_dstate; by default when ``state`` or
     ``dstate_out`` is given).  ``out`` may hold dx, ddt, dB, dC to write into (rows of dx 16-byte, of dB and dC 8-byte
-    aligned).  Rows outside every sequence are left as they are.  The workspace holds the states and adjoint states of
+    aligned).  Rows outside every sequence are left as they are.  What is not finite in a sequence reaches the parameters'
+    gradients and may reach any gradient of that sequence, but no other one's.  The workspace holds the states and adjoint states of
     every chunk of 64 steps: 512 H N bytes for each of about T / 64 + S chunks."""
     import torch
     T = x.shape[0]

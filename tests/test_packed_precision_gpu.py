@@ -175,3 +175,46 @@ def test_largest_steps_under_zero_order_hold(N):
     for n, t in res[0].items():
         assert bool(t.isfinite().all()), n
         assert torch.equal(t, res[1][n]), n
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("N,at", [(64, 5), (64, 17), (128, 31), (128, 32), (128, 47), (128, 63), (256, 40), (256, 90)])
+def test_what_is_not_finite_reaches_nothing_earlier(N, at, value):
+    """One entry of x reaches its own column from its step on; one of B, C or dt its own group or head, and no earlier step."""
+    torch = T()
+    r = Rand(60 + N + at)
+    H = 3
+    cu, cul, rows = packed([130, 64])
+    bf = torch.bfloat16
+    c = dict(x=r(rows, H, 64, dtype=bf), dt=r(rows, H, dtype=bf), B=r(rows, 1, N, dtype=bf), C=r(rows, 1, N, dtype=bf))
+    A, bias, D = -torch.rand(H, generator=r.g).cuda() - 0.5, r(H) - 3, r(H)
+    state = r(2, H, 64, N)
+
+    def run(**kw):
+        c2, out = dict(c, **kw), torch.empty_like(state)
+        y = ssm().ssd_packed_fwd(c2["x"], c2["dt"], A, c2["B"], c2["C"], cu, bias, D, state=state, state_out=out)
+        torch.cuda.synchronize()
+        return y, out
+
+    def spoil(name, *place):
+        t = c[name].clone()
+        t[(at,) + place] = value
+        return {name: t}
+
+    clean, end = run()
+    others = torch.ones(H, 64, dtype=torch.bool)
+    others[1, 37] = False
+    y, out = run(**spoil("x", 1, 37))
+    assert torch.equal(y[:at], clean[:at]) and torch.equal(y[130:], clean[130:])
+    assert torch.equal(y[:, others], clean[:, others]) and torch.equal(out[:, others], end[:, others])
+    assert not bool(y[at:130, 1, 37].isfinite().any()) and not bool(out[0, 1, 37].isfinite().any())
+    for name, place in (("B", (0, 9)), ("C", (0, 9)), ("dt", (1,))):
+        if name == "dt" and value == float("-inf"):
+            continue                                            # (a masked step)
+        y, out = run(**spoil(name, *place))
+        assert torch.equal(y[:at], clean[:at]) and torch.equal(y[130:], clean[130:]), name
+        assert not bool(y[at].isfinite().all()), name
+        if name == "C":
+            assert torch.equal(y[at + 1:], clean[at + 1:]) and torch.equal(out, end)
+        if name == "dt":
+            assert torch.equal(y[:, [0, 2]], clean[:, [0, 2]]) and torch.equal(out[:, [0, 2]], end[:, [0, 2]])
