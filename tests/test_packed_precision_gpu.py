@@ -7,7 +7,7 @@ value at most, three 2^-24.  The decays' logarithms are summed without loss that
 import pytest
 
 import packed_ref as R
-from test_packed_gpu import BF, SSD, Rand, T, f64, packed, ssd_case, ssd_ref, ssm, within
+from test_packed_gpu import BF, SSD, Rand, T, f64, near, packed, ssd_case, ssd_ref, ssm, within
 
 pytestmark = pytest.mark.gpu
 
@@ -218,3 +218,34 @@ def test_what_is_not_finite_reaches_nothing_earlier(N, at, value):
             assert torch.equal(y[at + 1:], clean[at + 1:]) and torch.equal(out, end)
         if name == "dt":
             assert torch.equal(y[:, [0, 2]], clean[:, [0, 2]]) and torch.equal(out[:, [0, 2]], end[:, [0, 2]])
+
+
+@pytest.mark.parametrize("H,G,N,zoh", [(24, 1, 128, False), (10, 2, 64, True), (6, 1, 256, False)])
+def test_states_and_step_gradients_keep_32_bits(H, G, N, zoh):
+    """A layer's step sizes (1e-3 to 0.1) and decays (A from -16 to -1).  States and their gradients are fp32 products in three
+    parts (2^-24 left out) and decays good to 2^-22; independent roundings, fewer than four of 2^-22 behind every term: 2^-20 of
+    the 2-norm.  dA, ddt_bias and dDskip are sums over tokens of terms behind about twice as many: 2^-19.  (Two parts would
+    leave 2.4e-6 in the states, 2^-18.7.)"""
+    torch = T()
+    r = Rand(110 + N)
+    lens = [300, 1, 170, 200]
+    cu, cul, rows = packed(lens)
+    bf = torch.bfloat16
+    x, B, C = (R.silu(r(rows, *s)).to(bf) for s in ((H, 64), (G, N), (G, N)))
+    dt, dy = r(rows, H, dtype=bf), r(rows, H, 64, dtype=bf)
+    A = -torch.exp(torch.rand(H, generator=r.g) * 2.77).cuda()
+    step = torch.exp(torch.rand(H, generator=r.g) * 4.6 - 6.9)
+    bias, D = (step + torch.log(-torch.expm1(-step))).cuda(), 1 + r(H, scale=0.1)
+    state, dl = r(4, H, 64, N, scale=0.3), r(4, H, 64, N, scale=0.3)
+    out = torch.empty_like(state)
+    ssm().ssd_packed_fwd(x, dt, A, B, C, cu, bias, D, state=state, state_out=out, disc=int(zoh))
+    got = ssm().ssd_packed_bwd(x, dt, A, B, C, dy, cu, bias, D, state=state, dstate_out=dl, disc=int(zoh))
+    torch.cuda.synchronize()
+    wide = [t.double() for t in (x, dt, A, B, C, bias, D)]
+    with torch.device("cuda"):
+        last = R.ssd(*wide, cul, state.double(), True, zoh)[1].cpu()
+        ref = {k: v.cpu() for k, v in R.ssd_grads(*wide, cul, state.double(), dy.double(), dl.double(), True, zoh).items()}
+    near(out, last, 2.0 ** -20, "state")
+    near(got["dstate"], ref["dstate"], 2.0 ** -20, "dstate")
+    for n in ("dA", "ddt_bias", "dDskip"):
+        near(got[n], ref[n], 2.0 ** -19, n)
