@@ -245,7 +245,7 @@ def test_states_and_step_gradients_keep_32_bits(H, G, N, zoh):
     with torch.device("cuda"):
         last = R.ssd(*wide, cul, state.double(), True, zoh)[1].cpu()
         ref = {k: v.cpu() for k, v in R.ssd_grads(*wide, cul, state.double(), dy.double(), dl.double(), True, zoh).items()}
-    near(out, last, 2.0 ** -20, "state")
+    near(out, last, 2.0 ** -21, "state")
     near(got["dstate"], ref["dstate"], 2.0 ** -20, "dstate")
     for n in ("dA", "ddt_bias", "dDskip"):
         near(got[n], ref[n], 2.0 ** -19, n)
