@@ -6,11 +6,15 @@
 //
 // Bound by memory: x, z (and dy) are read once and y (dx, dz) written once.  A team of lanes (one wave, a workgroup of
 // 4 waves, or one of 16) holds a whole group of a row in registers, so nothing is read twice and nothing but the sums
-// goes through LDS.  A workgroup keeps its group and walks down the rows, so weight and bias are read once per
+// goes through LDS.  That holds up to groups of 8192 channels (4096 where rows are not 16-byte aligned).  Above, the
+// workgroup of 16 waves has 128 registers a lane: enough for the forward (its form for unaligned rows spills up to 12), but
+// not for the backward, which spills 62 to 140 with a gate (212 to 372 bytes a lane; up to 175 for unaligned rows) and goes
+// through scratch memory for them.  A workgroup keeps its group and walks down the rows, so weight and bias are read once per
 // workgroup, and the backward's weight gradient adds up in registers; the workgroups' partial sums are joined in a fixed
 // order by a second kernel.  The team is the smallest that holds the group at the given number of chunks per lane.
 // Measured with gate, bf16, rows of 5120: 16384 rows in one group 90 us (5.6 TB/s), gradients of 8191 rows in 8 groups
-// 89 us (4.7 TB/s; 106 with a partial sum for each team instead of each workgroup).
+// 89 us (4.7 TB/s; 106 with a partial sum for each team instead of each workgroup).  Gradients of 420 MB of gated rows in
+// one group: 5120 channels of fp32 111 us, 10240 and 16384 of bf16 385 and 299 us (1.1 and 1.4 TB/s), 16384 of fp32 202 us.
 #include "packed.hpp"
 
 namespace ssm57 {

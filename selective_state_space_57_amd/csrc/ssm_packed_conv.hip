@@ -6,9 +6,10 @@
 //   dbias = sum_t dpre_t
 // All of it is a stream of x (and du) in and u (dx) out, bound by memory: a thread owns V channels (16 bytes of a row)
 // and walks down a tile of tokens with the K - 1 inputs before it in registers, so each value is read once and a halo
-// of K - 1 rows per tile (out of the L2) on top.  At 4.3 TB/s forward (16384 tokens of 5376 bf16 channels: 81 us); the
-// backward pass computes as long as it reads (280 instructions for a wave's row of 512 channels), 3.0 TB/s (8191 tokens:
-// 87 us).
+// of K - 1 rows per tile (out of the L2) on top.  At 4.3 TB/s forward (16384 tokens of 5376 bf16 channels: 81 us).  The
+// backward takes 87 us for 8191 tokens (3.0 TB/s): neither memory nor its arithmetic (280 instructions for a wave's row of
+// 512 channels, VALU 56 % of the cycles) is full; at 194 registers a lane two waves share a SIMD, and latency shows.  In
+// fp32 (114 registers) it reaches 3.9 TB/s, the forward 4.4.
 #include <algorithm>
 
 #include "packed.hpp"
@@ -435,7 +436,7 @@ int fwd_tile(const PConvArgs& a, int v) {
   tile = tile < 8 ? 8 : (tile > 64 ? 64 : tile);
   return static_cast<int>(tile / 8 * 8);
 }
-// Tokens per tile of the backward, which computes as long as it reads: its waves on the busiest SIMD, times the rows that
+// Tokens per tile of the backward, where latency and arithmetic of a wave count: its waves on the busiest SIMD, times the rows that
 // each of them walks (the halo, and about 8 rows' worth of taps and partial sums, on top), as few as possible.  Measured
 // on 8191 tokens of the same rows (264 MB): 32, 48, 64 and 96 tokens (3, 2, 2 and 1 waves) 105, 87, 100 and 104 us.
 int bwd_tile(const PConvArgs& a, int v, int K) {

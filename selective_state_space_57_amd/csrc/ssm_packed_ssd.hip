@@ -16,15 +16,15 @@
 //
 // Precision: fp32 state and accumulation; x, B and C enter the matrix cores as they are.  The weighted x of the state
 // update is split into three bf16 parts, so the state keeps fp32 quality over long sequences (two parts, 2^-17, are 11 %
-// faster).  M (but for s = t, which is added in fp32) and the state that meets C only reach y: they are split into two,
+// faster when tried).  M (but for s = t, which is added in fp32) and the state that meets C only reach y: they are split into two,
 // which leave out 2^-16 of them at most, so that y is the 64-bit value rounded once but for 5e-5 of it in the 2-norm
-// (rounded to bf16 once each, they added 1.4e-3 to the rounding's own 1.66e-3; 16384 tokens of the 2.7B layer then took
-// 282 us instead of 337).
+// (rounded to bf16 once each, they added 1.4e-3 to the rounding's own 1.66e-3; on 16384 tokens of the 2.7B layer the
+// second part of M takes 24 us, that of the state 36).
 //
-// Measured on 16384 tokens of 80 heads, N = 128 (0.40 GB in and out, 43 GFLOP): 280 us, 200 of them this pass, 85 the walk
-// and its join.  VALU 42 % of the cycles, MFMA 19 %, the rest waits: leaving out a part saves 70 us (M x and C S^T),
-// 53 (the state's update), 19 (the stores) or 6 (C B^T).  The step kernel: 256 tokens of the same layer 250 us, 5.4 TB/s
-// of states.
+// Measured on 16384 tokens of 80 heads, N = 128 (0.40 GB in and out, 43 GFLOP): 340 us a call.  Under the profiler, where
+// every kernel is somewhat longer, this pass takes 272, the walk 89 and its join 23.  VALU 53 % of the cycles, MFMA 22 %,
+// the rest waits.  The kernel of N = 128 is over its 128 registers by 6 (28 bytes a lane in scratch memory).  The step
+// kernel: 256 tokens of the same layer 250 us, 5.4 TB/s of states.
 #include "packed_ssd.hpp"
 
 namespace ssm57 {

@@ -22,9 +22,10 @@
 // Two workgroups share a CU (N <= 128), so that one's barriers and loads run beside the other's products: with chunks of
 // 128 steps to a workgroup, which halve the saved states but recompute them in between, one filled the LDS and took
 // 790 us instead of 566 (2.7B layer, 16384 tokens, states in two bf16 parts each).
-// Measured on that layer: a call of 1249 us.
-// It reads 1.4 GB of states and 0.34 GB of inputs, MFMA and VALU are below half of the cycles: no single one is full, the
-// stages of a head and the barriers between them are its time.
+// Measured on that layer: 703 to 777 us under the profiler, in a call of 1250 us whose walks, joins and sums over heads are
+// the rest.  It reads 1.4 GB of states and 0.34 GB of inputs and writes 0.24 GB and what it spills; MFMA 13 % and VALU 45 % of
+// the cycles: no single one is full, the stages of a head and the barriers between them are its time.  The kernel of N = 128
+// is over its 128 registers by 18 (44 bytes a lane in scratch memory), that of 256 by 15.
 //
 // Precision: fp32 accumulation; the states are split into three bf16 parts, so that u, v and <G, S>, and with them dDelta
 // and dA, are good to fp32 quality.  G in dx, M = L Z phi and the head sum K (both but for s = t, which is added in fp32)
@@ -105,8 +106,8 @@ packed_ssd_bwd_kernel(BwdArgs a) {
   __shared__ alignas(16) uint16_t sG[N * kHead];       // G, transposed
   __shared__ ChunkScalars sc;
   __shared__ float sU[NW][kChunk], sV[NW][kChunk], sE[NW];
-  // of 8 waves, two have a second tile of K: it waits in LDS and not in a register of every wave, one of which the compiler
-  // would keep in scratch memory (16384 tokens, 2.7B layer: 642 us, else 690)
+  // of 8 waves, two have a second tile of K: it waits in LDS and not in four more registers of every wave, which would spill
+  // (16384 tokens, 2.7B layer, when tried: 642 us, else 690)
   constexpr int kHeld = NW == 8 ? 1 : kTiles;
   __shared__ pf4 sK2[kHeld < kTiles ? 2 : 1][64];
   __shared__ float sRow[10][16], sCol[10][16], sOwn[4][16], sDirect[4][16], sDiag[4], sTotal[10];

@@ -6,8 +6,9 @@
 // three bf16 parts, so states keep fp32 quality.  A sequence of several segments takes three launches: every segment from
 // zero, a join in order, and the walk proper, which saves the state entering every chunk.
 //
-// Measured on 16384 tokens of 80 heads, N = 128: the forward's first pass 85 us and its join 20; for the backward both first
-// passes 140 us, the joins 38 and both walks 360, in which they write 1.3 GB (3.7 TB/s): the saving is their bound.
+// Measured under the profiler on 16384 tokens of 80 heads, N = 128: the forward's first pass 89 us and its join 23; for the
+// backward both first passes 147 us, the joins 41 and both walks 378, in which they write 1.3 GB (3.6 TB/s): the saving is
+// their bound.
 #include "packed_ssd.hpp"
 
 namespace ssm57 {

@@ -374,8 +374,8 @@ def ssd_packed_bwd(x, dt, A, B, C, dy, cu_seqlens, dt_bias=None, Dskip=None, *, 
     float32, the gradient of the state each sequence starts from (want_dstate; by default when ``state`` or
     ``dstate_out`` is given).  ``out`` may hold dx, ddt, dB, dC to write into (rows of dx 16-byte, of dB and dC 8-byte
     aligned).  Rows outside every sequence are left as they are.  What is not finite in a sequence reaches the parameters'
-    gradients and may reach any gradient of that sequence, but no other one's.  The workspace holds the states and adjoint states of
-    every chunk of 64 steps: 512 H N bytes for each of about T / 64 + S chunks."""
+    gradients and may reach any gradient of that sequence, but no other one's.  The workspace holds the states and adjoint
+    states of every chunk of 64 steps: 512 H N bytes for each of about T / 64 + S chunks."""
     import torch
     T = x.shape[0]
     dev = _on_gpu(x, "x")
