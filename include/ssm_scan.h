@@ -56,7 +56,7 @@ typedef enum {
   SSM_ERR_HIP = 7           /* the HIP runtime refused a launch */
 } ssm_status;
 
-typedef enum { SSM_F32 = 0, SSM_BF16 = 1 } ssm_dtype;
+typedef enum { SSM_F32 = 0, SSM_BF16 = 1, SSM_E4M3 = 2 /* only where an entry point says so */ } ssm_dtype;
 
 typedef enum {
   SSM_DISC_EULER_B = 0, /* Abar = exp(Delta A), Bbar = Delta B (the tutorial's simplified selective SSM) */
@@ -433,6 +433,93 @@ size_t ssm_gated_norm_bwd_workspace_bytes(const ssm_gated_norm_params* p);
 ssm_status ssm_gated_norm_bwd(const ssm_gated_norm_params* p, const void* x, const void* z, const float* weight,
                               const float* bias, const void* dy, void* dx, void* dz, float* dweight, float* dbias,
                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The two ends of a block: the residual's addition with the norm in front of a projection, and projections in 8 bits.
+ *
+ * 8-bit arrays hold e4m3 values (4 exponent and 3 mantissa bits, largest 448, no infinities) and have an fp32 scale for
+ * each block of SSM57_BLOCK consecutive values of a row, or of SSM57_BLOCK rows and columns; the last block of a row or
+ * column may be cut short.  A value stands for code * scale.  scale = max(largest magnitude of the block, 2^-100) / 448,
+ * code = the value / scale rounded to nearest even.  A block that holds a NaN has a NaN scale; one that holds an infinity
+ * has an infinite scale, so that products with any of its values are NaN.
+ * Rows of 8-bit arrays have their length rounded up to a multiple of 16; what is added holds zeros.
+ */
+#define SSM57_BLOCK 128
+
+typedef struct {
+  int64_t ntokens;   /* rows, >= 1 and below 2^31 */
+  int64_t dim;       /* channels of a row, 1 to 16384 */
+  int64_t x_stride, residual_stride, h_stride, y_stride, scale_stride;   /* row strides; 0 = dense */
+  int64_t dy_stride, dh_stride, dx_stride, dresidual_stride;             /* of the backward's arrays (h_stride: h) */
+  float eps;         /* >= 0 */
+  int32_t io_dtype;  /* ssm_dtype of x, dy, dx */
+  int32_t res_dtype; /* ssm_dtype of residual, residual_out (h), dh, dresidual */
+  int32_t y_dtype;   /* ssm_dtype of y: io_dtype or SSM_E4M3 */
+  int32_t reserved;  /* must be 0 */
+} ssm_add_norm_params;
+
+/*
+ * Residual addition and root mean square norm of each row: h = x + residual, y = h weight / sqrt(mean(h^2) + eps).
+ * x [ntokens][dim] io_dtype; residual, residual_out [ntokens][dim] res_dtype or NULL (no residual: h = x; h is not kept);
+ * weight [dim] fp32; y [ntokens][dim] io_dtype, or with SSM_E4M3 [ntokens][dim rounded up to 16] e4m3 and
+ * y_scale [ntokens][ceil(dim / 128)] fp32 (8-bit rows 8-byte aligned).  The norm is that of the fp32 sum, also where
+ * residual_out is rounded to bf16.  residual_out may be residual (or x, where the types agree), y may be x.
+ */
+ssm_status ssm_add_norm_fwd(const ssm_add_norm_params* p, const void* x, const void* residual, const float* weight,
+                            void* residual_out, void* y, float* y_scale, void* stream);
+
+/* Bytes of device workspace ssm_add_norm_bwd needs (0 for invalid parameters). */
+size_t ssm_add_norm_bwd_workspace_bytes(const ssm_add_norm_params* p);
+
+/*
+ * Backward of ssm_add_norm_fwd for dy = dL/dy [ntokens][dim] io_dtype and, optionally, dh = dL/d(residual_out) res_dtype:
+ * h [ntokens][dim] res_dtype is the sum that the forward kept; statistics are recomputed.  Outputs, overwritten: the
+ * gradient of the sum, which is that of x and of the residual alike, as dx [ntokens][dim] io_dtype and / or dresidual
+ * [ntokens][dim] res_dtype (at least one); dweight [dim] fp32.  y_dtype is ignored (codes have no slope: the rounding to
+ * 8 bits counts as the identity).  dx may be dy, dresidual may be h or dh.  Deterministic.
+ */
+ssm_status ssm_add_norm_bwd(const ssm_add_norm_params* p, const void* h, const float* weight, const void* dy,
+                            const void* dh, void* dx, void* dresidual, float* dweight, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+typedef struct {
+  int64_t rows, cols;       /* of x, each >= 1 and below 2^30 */
+  int64_t x_stride;         /* row strides; 0 = dense (8-bit rows: the length rounded up to 16) */
+  int64_t q_stride, scale_stride, qt_stride, scale_t_stride;
+  int32_t io_dtype;         /* ssm_dtype of x */
+  int32_t square;           /* 0: blocks of 128 values of a row (of qt: of a column); 1: blocks of 128 rows and columns */
+  int32_t reserved[2];      /* must be 0 */
+} ssm_quantize_fp8_params;
+
+/*
+ * Quantisation of x [rows][cols] to 8 bits: q [rows][cols rounded up to 16] with scale [rows][ceil(cols / 128)], and / or
+ * qt [cols][rows rounded up to 16] of the transposed matrix with scale_t [cols][ceil(rows / 128)] (its blocks lie along
+ * the columns of x).  square: scale [ceil(rows / 128)][ceil(cols / 128)] and scale_t its transposed.  q and scale, and qt
+ * and scale_t, are given together or are NULL.  8-bit rows must be 16-byte aligned.
+ */
+ssm_status ssm_quantize_fp8(const ssm_quantize_fp8_params* p, const void* x, void* q, float* scale, void* qt,
+                            float* scale_t, void* stream);
+
+typedef struct {
+  int64_t m, n, k;          /* rows of a, rows of b, length of both; k a multiple of 16 */
+  int64_t a_stride, b_stride, out_stride, a_scale_stride, b_scale_stride;   /* row strides; 0 = dense; a, b: below 2^23 */
+  int32_t b_rows;           /* rows of b under one scale: 128 or 1 */
+  int32_t out_dtype;        /* SSM_F32 or SSM_BF16 */
+  int32_t splits;           /* 0: the library picks how many pieces of k are summed apart; s > 0 forces s (at most 64) */
+  int32_t reserved;         /* must be 0 */
+} ssm_matmul_fp8_params;
+
+/* Bytes of device workspace ssm_matmul_fp8 needs (0 when it needs none, and for invalid parameters). */
+size_t ssm_matmul_fp8_workspace_bytes(const ssm_matmul_fp8_params* p);
+
+/*
+ * Matrix product of 8-bit operands: out[i][j] = sum over blocks c of a_scale[i][c] b_scale[j / b_rows][c] times the sum
+ * over the block's k of a[i][k] b[j][k].  a [m][k], b [n][k] e4m3 (rows 16-byte aligned); a_scale [m][ceil(k / 128)],
+ * b_scale [ceil(n / b_rows)][ceil(k / 128)] fp32; out [m][n] out_dtype.  Products and sums are fp32; out is rounded once.
+ * The product of two scales has to be finite in fp32.  out must not overlap an input.  Deterministic.
+ */
+ssm_status ssm_matmul_fp8(const ssm_matmul_fp8_params* p, const void* a, const float* a_scale, const void* b,
+                          const float* b_scale, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Static description of a status code. */
 const char* ssm_status_str(ssm_status s);

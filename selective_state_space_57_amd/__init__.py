@@ -6,8 +6,10 @@ applied to x inside the kernels; ``complex_scan_fwd`` and ``complex_state_update
 ``ssd_fwd`` and ``ssd_state_update`` run the Mamba-2 SSD layer (scalar A per head, bf16 matrix cores).  The Mamba-2
 block over packed tokens (sequences of uneven length one behind the other, states in slots) is
 ``conv1d_packed_fwd`` / ``conv1d_slot_update`` / ``conv1d_packed_bwd``, ``ssd_packed_fwd`` / ``ssd_slot_update`` /
-``ssd_packed_bwd`` and ``gated_norm_fwd`` / ``gated_norm_bwd`` (module ``packed``).  The
-arithmetic runs entirely in the HIP kernels.  ``inputs`` generates the seeded
+``ssd_packed_bwd`` and ``gated_norm_fwd`` / ``gated_norm_bwd`` (module ``packed``).  Its two ends are
+``add_norm_fwd`` / ``add_norm_bwd`` (residual addition and norm, with an output in 8 bits), ``quantize_fp8`` /
+``quantize_fp8_blocks`` and ``matmul_fp8`` (projections in 8 bits with a scale for each block of 128; module
+``projection``).  The arithmetic runs entirely in the HIP kernels.  ``inputs`` generates the seeded
 synthetic workloads.
 """
 from __future__ import annotations
@@ -20,7 +22,8 @@ __all__ = ["scan_fwd", "scan_bwd", "state_update", "conv_scan_fwd", "conv_state_
            "complex_state_update", "conv1d_fwd", "conv1d_bwd", "ssd_fwd", "ssd_state_update", "ssd_workspace_bytes",
            "conv1d_packed_fwd", "conv1d_slot_update", "conv1d_packed_bwd", "ssd_packed_fwd", "ssd_packed_bwd",
            "ssd_slot_update",
-           "gated_norm_fwd", "gated_norm_bwd", "EULER_B", "ZOH", "SSMError",
+           "gated_norm_fwd", "gated_norm_bwd", "add_norm_fwd", "add_norm_bwd", "quantize_fp8", "quantize_fp8_blocks",
+           "matmul_fp8", "EULER_B", "ZOH", "SSMError",
            "Params", "make_params", "workspace_bytes", "bwd_workspace_bytes", "plan_segments", "io_code"]
 
 
@@ -436,3 +439,4 @@ def ssd_state_update(state, x, dt, A, B, C, dt_bias=None, Dskip=None, z=None, *,
 
 from .packed import (conv1d_packed_fwd, conv1d_slot_update, conv1d_packed_bwd, ssd_packed_fwd, ssd_packed_bwd,  # noqa: E402
                      ssd_slot_update, gated_norm_fwd, gated_norm_bwd)
+from .projection import add_norm_fwd, add_norm_bwd, quantize_fp8, quantize_fp8_blocks, matmul_fp8  # noqa: E402

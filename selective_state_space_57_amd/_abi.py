@@ -11,7 +11,7 @@ import os
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libssm57.so")
 
-SSM_F32, SSM_BF16 = 0, 1
+SSM_F32, SSM_BF16, SSM_E4M3 = 0, 1, 2
 EULER_B, ZOH = 0, 1
 STATUS = {0: "SSM_OK", 1: "SSM_ERR_NULL", 2: "SSM_ERR_SHAPE", 3: "SSM_ERR_DTYPE", 4: "SSM_ERR_UNSUPPORTED",
           5: "SSM_ERR_ALIGN", 6: "SSM_ERR_WORKSPACE", 7: "SSM_ERR_HIP"}
@@ -23,7 +23,8 @@ EXPORTS = ["ssm_scan_fwd_workspace_bytes", "ssm_scan_fwd", "ssm_state_update", "
            "ssm_conv1d_packed_bwd", "ssm_conv1d_packed_bwd_workspace_bytes", "ssm_ssd_packed_fwd",
            "ssm_ssd_packed_fwd_workspace_bytes", "ssm_ssd_packed_bwd", "ssm_ssd_packed_bwd_workspace_bytes",
            "ssm_ssd_slot_update", "ssm_gated_norm_fwd", "ssm_gated_norm_bwd",
-           "ssm_gated_norm_bwd_workspace_bytes"]
+           "ssm_gated_norm_bwd_workspace_bytes", "ssm_add_norm_fwd", "ssm_add_norm_bwd",
+           "ssm_add_norm_bwd_workspace_bytes", "ssm_quantize_fp8", "ssm_matmul_fp8", "ssm_matmul_fp8_workspace_bytes"]
 
 
 class Params(ctypes.Structure):
@@ -63,6 +64,25 @@ class GatedNormParams(ctypes.Structure):
                                               "dy_stride", "dx_stride", "dz_stride")] + \
                [("eps", ctypes.c_float)] + \
                [(n, ctypes.c_int32) for n in ("io_dtype", "gate_first", "center", "reserved")]
+
+
+class AddNormParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("ntokens", "dim", "x_stride", "residual_stride", "h_stride", "y_stride",
+                                              "scale_stride", "dy_stride", "dh_stride", "dx_stride", "dresidual_stride")] + \
+               [("eps", ctypes.c_float)] + \
+               [(n, ctypes.c_int32) for n in ("io_dtype", "res_dtype", "y_dtype", "reserved")]
+
+
+class QuantizeFp8Params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("rows", "cols", "x_stride", "q_stride", "scale_stride", "qt_stride",
+                                              "scale_t_stride")] + \
+               [("io_dtype", ctypes.c_int32), ("square", ctypes.c_int32), ("reserved", ctypes.c_int32 * 2)]
+
+
+class MatmulFp8Params(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("m", "n", "k", "a_stride", "b_stride", "out_stride", "a_scale_stride",
+                                              "b_scale_stride")] + \
+               [(n, ctypes.c_int32) for n in ("b_rows", "out_dtype", "splits", "reserved")]
 
 
 class SSMError(RuntimeError):
@@ -146,6 +166,19 @@ def lib():
         L.ssm_gated_norm_bwd_workspace_bytes.restype = S
         L.ssm_gated_norm_bwd.argtypes = [NP] + [P] * 9 + [P, S, P]
         L.ssm_gated_norm_bwd.restype = ctypes.c_int
+        AP, UP, MP = (ctypes.POINTER(c) for c in (AddNormParams, QuantizeFp8Params, MatmulFp8Params))
+        L.ssm_add_norm_fwd.argtypes = [AP] + [P] * 7
+        L.ssm_add_norm_fwd.restype = ctypes.c_int
+        L.ssm_add_norm_bwd_workspace_bytes.argtypes = [AP]
+        L.ssm_add_norm_bwd_workspace_bytes.restype = S
+        L.ssm_add_norm_bwd.argtypes = [AP] + [P] * 7 + [P, S, P]
+        L.ssm_add_norm_bwd.restype = ctypes.c_int
+        L.ssm_quantize_fp8.argtypes = [UP] + [P] * 6
+        L.ssm_quantize_fp8.restype = ctypes.c_int
+        L.ssm_matmul_fp8_workspace_bytes.argtypes = [MP]
+        L.ssm_matmul_fp8_workspace_bytes.restype = S
+        L.ssm_matmul_fp8.argtypes = [MP] + [P] * 5 + [P, S, P]
+        L.ssm_matmul_fp8.restype = ctypes.c_int
         L.ssm_status_str.argtypes = [ctypes.c_int]
         L.ssm_status_str.restype = ctypes.c_char_p
         L.ssm_last_error.argtypes = []

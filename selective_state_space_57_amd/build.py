@@ -11,7 +11,7 @@ ROOT = os.path.dirname(HERE)
 SRCS = [os.path.join(HERE, "csrc", f) for f in ("ssm_scan.hip", "ssm_conv_scan.hip", "ssm_complex_scan.hip",
                                                   "ssm_scan_bwd.hip", "ssm_ssd.hip", "ssm_packed_conv.hip",
                                                   "ssm_packed_ssd.hip", "ssm_packed_states.hip", "ssm_packed_ssd_bwd.hip",
-                                                  "ssm_gated_norm.hip")]
+                                                  "ssm_gated_norm.hip", "ssm_add_norm.hip", "ssm_quantize.hip", "ssm_matmul_fp8.hip")]
 INC = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libssm57.so")
 # the issue-rate probe that bench.py runs beside the scan (not part of the scan library's ABI)
