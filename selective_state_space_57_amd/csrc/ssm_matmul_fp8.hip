@@ -28,20 +28,22 @@ struct MatmulArgs {
   float* part;            // [splits][m][n]: the sums of each piece of k
   int64_t as, bs, os, sas, sbs;
   int m, n, k, blocks;    // blocks of 128 along k
-  int tiles_n;
+  int tiles_m, tiles_n;
   int splits, per;        // pieces of k, blocks of a piece
 };
 
-__device__ __forceinline__ v8i join(v4i lo, v4i hi) {
-  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-}
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) const v4i lds_v4i;
+typedef __attribute__((address_space(3))) const float lds_f32;
+typedef __attribute__((address_space(3))) const pf4 lds_pf4;
+
 __device__ __forceinline__ v8bf widen(int lo, int hi) {
   const pbf2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
   const pbf2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false), d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// A wave's 16 rows of a block: a lane's 32 codes, as they are or as bf16.
+// Half a block (64 k) of a wave's 32 rows: a lane's 32 codes, as they are or as bf16.
 template <bool WIDE>
 struct Frag {
   v8i v;
@@ -55,17 +57,16 @@ struct Frag<true> {
     for (int i = 0; i < 4; ++i) v[i] = widen(x[2 * i], x[2 * i + 1]);
   }
 };
-__device__ __forceinline__ pf4 mfma_block(const Frag<false>& b, const Frag<false>& a) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, pf4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+__device__ __forceinline__ v16f mfma_half(const Frag<false>& b, const Frag<false>& a, v16f d) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b.v, a.v, d, 0, 0, 0, 0, 0, 0);
 }
-__device__ __forceinline__ pf4 mfma_block(const Frag<true>& b, const Frag<true>& a) {
-  pf4 d{0.0f, 0.0f, 0.0f, 0.0f};
+__device__ __forceinline__ v16f mfma_half(const Frag<true>& b, const Frag<true>& a, v16f d) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[i], a.v[i], d, 0, 0, 0);
+  for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b.v[i], a.v[i], d, 0, 0, 0);
   return d;
 }
 
-// four neighbouring results, of which cnt are inside the row
+// Neighbouring results of a row, four (eight) of them, of which cnt are inside the row.
 template <typename TO>
 __device__ __forceinline__ void store4(TO* p, pf4 v, int cnt) {
   if constexpr (sizeof(TO) == 4) {
@@ -83,101 +84,299 @@ __device__ __forceinline__ void store4(TO* p, pf4 v, int cnt) {
         if (i < cnt) Elem<uint16_t>::st(p, i, v[i]);
   }
 }
+template <typename TO>
+__device__ __forceinline__ void store8(TO* p, pf4 v, pf4 w, int cnt) {
+  if (cnt >= 8 && sizeof(TO) == 2) {
+    *reinterpret_cast<pu4e*>(p) = pu4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3])};
+  } else {
+    store4<TO>(p, v, cnt);
+    store4<TO>(p + 4, w, cnt - 4);
+  }
+}
 
-// A workgroup's tile of BM x BN results; WM x WN waves.  BROWS: rows of b under one scale.  WIDE: bf16 products.
-template <int BM, int BN, int WM, int WN, int BROWS, bool WIDE, typename TO>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t bytes_rsrc(const void* base, uint32_t bytes) {   // at most 2^31
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0), static_cast<int>(bytes),
+                                           static_cast<int>(kRsrcWord3));
+}
+// Waits until at most N of this wave's memory operations are under way.
+template <int N = 0>
+__device__ __forceinline__ void wait_memory() {
+  static_assert(N < 64);
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4 << 14));
+}
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }      // lgkmcnt(0)
+
+// A workgroup's tiles of (32 TM WM) x (64 WN) results, one after the other; a wave has 32 TM x 64 of them.  BROWS: rows of b
+// under one scale.  WIDE: bf16 products.
+template <int TM, int WM, int WN, int BROWS, bool WIDE, typename TO>
 __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g) {
-  constexpr int NW = WM * WN, TM = BM / 16 / WM, TN = BN / 16 / WN;
-  constexpr int kLoads = (BM + BN) / 8;          // copies of 1 KB (8 rows of a block) in a stage
-  static_assert(kLoads % NW == 0 && BM / 8 % NW == 0);
-  struct Stage {
-    uint8_t rows[(BM + BN) * 128];
-    float scale[BM + (BROWS == 1 ? BN : 0)];
-  };
-  __shared__ __align__(1024) Stage stage[2];
+  constexpr int BM = 32 * TM * WM, BN = 64 * WN, NW = WM * WN, TN = 2;
+  constexpr int kA = BM / 8 / NW, kB = BN / 8 / NW;         // a wave's copies of 1 KB (8 rows of a block) in a stage
+  constexpr int kScales = BM / 64 + (BROWS == 1 ? BN / 64 : 1), kSlots = (kScales + NW - 1) / NW;
+  constexpr int kStores = TM * (sizeof(TO) == 2 ? 4 : 8);   // of a wave's results, where its tile is whole
+  constexpr int kStageA = BM * 128, kStageB = BN * 128, kStageS = 256 * kSlots * NW;
+  // A wave's copies of a stage are given out between its products: the first of them a block early, as soon as the stage is
+  // free, the others over the next block's first products.
+  constexpr int kCopies = kA + kB + kSlots, kSteps = 2 * TN * TM, kFree = 2 * TN;
+  constexpr int kPer = (kCopies + kSteps - 2) / (kSteps - 1), kEarly = kPer * kFree < kCopies ? kPer * kFree : kCopies;
+  static_assert(kEarly + kPer * (kSteps - kFree - 1) >= kCopies);
+  static_assert(BM / 8 % NW == 0 && BN / 8 % NW == 0 && NW % 2 == 0 && TM >= 2 && TM % 2 == 0);
+  __shared__ __align__(1024) uint8_t lds[2 * (kStageA + kStageB + kStageS)];   // two stages of a, of b, of scales
+  const uint32_t at_b = 2 * kStageA, at_s = 2 * (kStageA + kStageB);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM;
-  const int tile = blockIdx.x / g.splits, piece = blockIdx.x % g.splits;
-  const int m0 = tile / g.tiles_n * BM, n0 = tile % g.tiles_n * BN;
-  const int c0 = piece * g.per, c1 = min(c0 + g.per, g.blocks);
-  const int rows_m = min(BM, g.m - m0), rows_n = min(BN, g.n - n0);
-  const auto ra = make_rsrc(g.a + m0 * g.as, (rows_m - 1) * g.as + g.k);
-  const auto rb = make_rsrc(g.b + n0 * g.bs, (rows_n - 1) * g.bs + g.k);
-  const auto rsa = make_rsrc(g.sa + m0 * g.sas, (rows_m - 1) * g.sas + g.blocks);
-  const auto rsb = make_rsrc(g.sb + (BROWS == 1 ? n0 * g.sbs : 0), BROWS == 1 ? (rows_n - 1) * g.sbs + g.blocks : 0);
+  const int r32 = lane & 31, half = lane >> 5;
+
+  // Workgroups go to the 8 XCDs in turn: each XCD takes a run of tiles that walks along n four tiles of m at a time, so
+  // that the 32 tiles it has in work share 4 + 8 panels in its L2.
+  const int tiles = g.tiles_m * g.tiles_n, total = tiles * g.splits;
+  const int xcd = blockIdx.x & 7, each = total / 8, more = total % 8;
+  const int step = gridDim.x / 8 + (xcd < static_cast<int>(gridDim.x % 8) ? 1 : 0);
+  const int end = (xcd + 1) * each + min(xcd + 1, more);
+  struct Place {
+    int m0, n0, c, c1, piece;
+  };
+  auto place_of = [&](int id) {
+    const int piece = id / tiles, tile = id % tiles;
+    const int band = tile / (4 * g.tiles_n), in_band = tile % (4 * g.tiles_n), high = min(4, g.tiles_m - 4 * band);
+    return Place{(band * 4 + in_band % high) * BM, in_band / high * BN, piece * g.per, min(piece * g.per + g.per, g.blocks), piece};
+  };
 
   // A copy's lane has row lane / 8 of eight, and the unit of 16 bytes whose place in LDS is lane % 8: units are exchanged by
-  // row so that 8 rows' equal units lie in different banks.
-  const int unit = (lane & 7) ^ (lane >> 3);
-  const uint32_t voff_a = static_cast<uint32_t>(lane >> 3) * static_cast<uint32_t>(g.as) + 16u * unit;
-  const uint32_t voff_b = static_cast<uint32_t>(lane >> 3) * static_cast<uint32_t>(g.bs) + 16u * unit;
-  auto load = [&](int c, Stage& st) {
-    const bool in = c * 128 + unit * 16 < g.k;   // (past the end of k: zeros)
+  // bits 1 to 3 of the row, so that the rows that 16 lanes read at once lie in different banks.
+  const int unit = (lane & 7) ^ (lane >> 4) ^ ((wave & 1) << 2);
+  const uint32_t as = static_cast<uint32_t>(g.as), bs = static_cast<uint32_t>(g.bs);
+  const uint32_t first_a = (wave * 8 + (lane >> 3)) * as + unit * 16u, first_b = (wave * 8 + (lane >> 3)) * bs + unit * 16u;
+  // (a wave's scales are those of a or those of b: one place and one stride)
+  uint32_t first_s[kSlots];
 #pragma unroll
-    for (int i = 0; i < kLoads / NW; ++i) {
-      const int piece8 = wave + NW * i;          // eight rows
-      const bool is_a = NW * i < BM / 8;
-      const uint32_t row = is_a ? piece8 * 8 : (piece8 - BM / 8) * 8;
-      const uint32_t off = (is_a ? voff_a : voff_b) + row * static_cast<uint32_t>(is_a ? g.as : g.bs) + c * 128u;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb, (lds_mvoid*)(st.rows + piece8 * 1024), 16,
-                                               static_cast<int>(in ? off : kDropOffset), 0, 0, 0);
+  for (int i = 0; i < kSlots; ++i) {
+    const int p = wave + NW * i;
+    first_s[i] = p < BM / 64 ? 4u * (p * 64 + lane) * static_cast<uint32_t>(g.sas)
+                             : 4u * ((p - BM / 64) * 64 + lane) * static_cast<uint32_t>(g.sbs);
+  }
+  const uint8_t *pa = nullptr, *pb = nullptr;   // the block that is copied next, and bytes from there to the end of its rows
+  const float *psa = nullptr, *psb = nullptr;
+  uint32_t na = 0, nb = 0, nsa = 0, nsb = 0;
+  int lid = xcd * each + min(xcd, more) + (blockIdx.x >> 3);   // its tile
+  int left = 0, blocks = 0;                     // of k, and of the tile's blocks
+  auto enter = [&]() {
+    const Place t = place_of(lid);
+    const int rows_m = min(BM, g.m - t.m0), rows_n = min(BN, g.n - t.n0);
+    const int sb_rows = BROWS == 1 ? rows_n : min(BN / 128 + 1, (g.n - t.n0 / 128 * 128 + 127) / 128);
+    left = g.k - t.c * 128;
+    blocks = t.c1 - t.c;
+    pa = g.a + t.m0 * g.as + t.c * 128;
+    pb = g.b + t.n0 * g.bs + t.c * 128;
+    psa = g.sa + t.m0 * g.sas + t.c;
+    psb = g.sb + t.n0 / BROWS * g.sbs + t.c;
+    na = static_cast<uint32_t>((rows_m - 1) * g.as) + left;
+    nb = static_cast<uint32_t>((rows_n - 1) * g.bs) + left;
+    nsa = 4u * (static_cast<uint32_t>((rows_m - 1) * g.sas) + g.blocks - t.c);
+    nsb = 4u * (static_cast<uint32_t>((sb_rows - 1) * g.sbs) + g.blocks - t.c);
+  };
+  // copy i of a wave's copies of a stage
+  auto copy = [&](int s, int i) {
+    if (i < kA) {
+      const uint32_t o = unit * 16 < left ? first_a : kDropOffset;   // (past the end of k: zeros)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bytes_rsrc(pa, na), (lds_mvoid*)(lds + s * kStageA + (wave + NW * i) * 1024), 16,
+                                               static_cast<int>(o + i * NW * 8 * as), 0, 0, 0);
+    } else if (i < kA + kB) {
+      const uint32_t o = unit * 16 < left ? first_b : kDropOffset;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bytes_rsrc(pb, nb), (lds_mvoid*)(lds + at_b + s * kStageB + (wave + NW * (i - kA)) * 1024),
+                                               16, static_cast<int>(o + (i - kA) * NW * 8 * bs), 0, 0, 0);
+    } else {                                    // (rows behind the last one, and slots behind the last scale: zeros)
+      const int p = wave + NW * (i - kA - kB);
+      const bool of_a = p < BM / 64;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bytes_rsrc(of_a ? psa : psb, of_a ? nsa : nsb),
+                                               (lds_mvoid*)(lds + at_s + s * kStageS + p * 256), 4,
+                                               static_cast<int>(first_s[i - kA - kB]), 0, 0, 0);
     }
-    constexpr int kScales = BM / 64 + (BROWS == 1 ? BN / 64 : 0);
-#pragma unroll
-    for (int i = 0; i < (kScales + NW - 1) / NW; ++i) {
-      const int p = wave + NW * i;
-      if (p < kScales) {
-        const bool is_a = p < BM / 64;
-        const uint32_t row = (is_a ? p : p - BM / 64) * 64u + lane;
-        const uint32_t off = 4u * (row * static_cast<uint32_t>(is_a ? g.sas : g.sbs) + c);
-        if (is_a) __builtin_amdgcn_raw_ptr_buffer_load_lds(rsa, (lds_mvoid*)(st.scale + p * 64), 4, static_cast<int>(off), 0, 0, 0);
-        else __builtin_amdgcn_raw_ptr_buffer_load_lds(rsb, (lds_mvoid*)(st.scale + p * 64), 4, static_cast<int>(off), 0, 0, 0);
-      }
+  };
+  auto advance = [&]() {   // to the block behind the one that was copied last; behind the last of all there are zeros
+    if (--blocks > 0) {
+      pa += 128;
+      pb += 128;
+      psa += 1;
+      psb += 1;
+      na -= 128;
+      nb -= 128;
+      nsa -= 4;
+      nsb -= 4;
+      left -= 128;
+    } else if ((lid += step) < end) {
+      enter();
+    } else {
+      na = nb = nsa = nsb = 0;
+      lid = end;
     }
   };
 
-  pf4 acc[TM][TN] = {};
-  const int r16 = lane & 15, kg = lane >> 4;
-  const int u0 = ((2 * kg) ^ (r16 & 7)) * 16, u1 = ((2 * kg + 1) ^ (r16 & 7)) * 16;
-  const float* sb_row = g.sb + (n0 + wn * TN * 16) / 128 * g.sbs;
-  if (c0 < c1) load(c0, stage[0]);
-  for (int c = c0; c < c1; ++c) {
-    Stage& st = stage[(c - c0) & 1];
-    __syncthreads();
-    if (c + 1 < c1) load(c + 1, stage[(c + 1 - c0) & 1]);
-    Frag<WIDE> bf[TN];
-    pf4 sbn[TN];
+  // Where a lane reads in a stage: rows of a in order; rows of b such that a lane's 32 results are runs of 8 neighbours: the
+  // matrix instruction's row 8 q + 4 h + r of fragment j, which is register 4 q + r of the lanes with half h, is row
+  // 32 j + 16 (q / 2) + 8 h + 4 (q % 2) + r.
+  const int key_a = (r32 >> 1) & 7;
+  const int row_b = ((r32 >> 4) << 4) | (((r32 >> 2) & 1) << 3) | (((r32 >> 3) & 1) << 2) | (r32 & 3);
+  const int key_b = (row_b >> 1) & 7;
+  // (unit u of 16 bytes: half a block is units 4 kh + 2 half + 0, 1)
+  uint32_t a0 = (wm * TM * 32 + r32) * 128 + ((2 * half) ^ key_a) * 16;
+  uint32_t b0 = at_b + (wn * 64 + row_b) * 128 + ((2 * half) ^ key_b) * 16;
+  uint32_t s0 = at_s + (wm * TM * 32 + r32) * 4;
+  const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_mvoid*)lds));
+  a0 += base;
+  b0 += base;
+  s0 += base;
+  int cur = 0;
+  auto read_a = [&](int s, int i, int kh) {
+    const uint32_t p = a0 + s * kStageA;
+    return __builtin_shufflevector(*(lds_v4i*)((p ^ (kh * 64)) + i * 4096), *(lds_v4i*)((p ^ (kh * 64 + 16)) + i * 4096), 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+  auto read_b = [&](int s, int j, int kh) {
+    const uint32_t p = b0 + s * kStageB;
+    return __builtin_shufflevector(*(lds_v4i*)((p ^ (kh * 64)) + j * 4096), *(lds_v4i*)((p ^ (kh * 64 + 16)) + j * 4096), 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+
+  int id = lid;
+  if (id >= end) return;
+  enter();
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const uint8_t* p = st.rows + (BM + (wn * TN + j) * 16 + r16) * 128;
-      bf[j].set(join(*reinterpret_cast<const v4i*>(p + u0), *reinterpret_cast<const v4i*>(p + u1)));
-      if constexpr (BROWS == 1) sbn[j] = *reinterpret_cast<const pf4*>(st.scale + BM + (wn * TN + j) * 16 + kg * 4);
+  for (int i = 0; i < kCopies; ++i) copy(0, i);
+  advance();
+#pragma unroll
+  for (int i = 0; i < kEarly; ++i) copy(1, i);
+  wait_memory<kEarly>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+
+  Frag<WIDE> bf[TN][2];
+  v8i af[2][2];
+  float sa[2];
+  Place t = place_of(id);
+  bool stored = false, ahead = false;
+#pragma unroll
+  for (int kh = 0; kh < 2; ++kh) {
+    af[0][kh] = read_a(0, 0, kh);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) bf[j][kh].set(read_b(0, j, kh));
+  }
+  sa[0] = *(lds_f32*)(s0);
+  float sb = BROWS == 1 ? 1.0f : *(lds_f32*)(base + at_s + BM * 4 + (t.n0 % 128 + wn * 64) / 128 * 4);
+
+  while (true) {
+    v16f acc[TM][TN] = {};
+    v16f d[2];
+    float s[2] = {0.0f, 0.0f};
+    d[1] = v16f{};
+    // half (8 registers) of the product k (fragment k / 2 of a, k % 2 of b) goes into the sums
+    auto add = [&](int k, int h, const pf4* sbn) {
+      v16f& to = acc[k / TN][k % TN];
+#pragma unroll
+      for (int r = 8 * h; r < 8 * h + 8; ++r)
+        to[r] = fmaf(BROWS == 1 ? d[k & 1][r] * sbn[(r - 8 * h) / 4][r % 4] : d[k & 1][r], s[(k / TN) & 1], to[r]);
+      asm volatile("" : "+v"(to));   // (here, not at the end of the block)
+    };
+    auto scales_b = [&](int s, int k, int h, pf4* sbn) {
+      if constexpr (BROWS == 1) {
+        const uint32_t p = base + at_s + s * kStageS + BM * 4 + (wn * 64 + k % TN * 32 + h * 16 + half * 8) * 4;
+        sbn[0] = *(lds_pf4*)p;
+        sbn[1] = *(lds_pf4*)(p + 16);
+      }
+    };
+    pf4 sbl[4];   // of the block's last product, which goes into the sums in the next block
+    for (int c = t.c; c < t.c1; ++c) {
+      const int nx = cur ^ 1;
+      const bool last = c + 1 == t.c1;
+      const int n_next = last && id + step < end ? place_of(id + step).n0 : t.n0;
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        if (i == TM - 1) {
+          // All of this wave's reads of the stage are done, and its part of the next one has arrived: behind the barrier that
+          // holds for every wave, so the next block's fragments can be read and this stage filled again.  (Behind the last
+          // block what is copied and read is not used.)
+          if constexpr (BROWS == 1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) scales_b(cur, TM * TN - 1, h, sbl + 2 * h);
+          }
+          wait_lds();
+          if (stored) wait_memory<kStores>();   // (results on their way out were given to memory behind those copies)
+          else wait_memory();
+          stored = false;
+          __builtin_amdgcn_s_barrier();
+          asm volatile("" ::: "memory");
+        }
+        {
+          const int to = (i + 1) % 2, from = i == TM - 1 ? nx : cur, row = i == TM - 1 ? 0 : i + 1;
+#pragma unroll
+          for (int kh = 0; kh < 2; ++kh) af[to][kh] = read_a(from, row, kh);
+          sa[to] = *(lds_f32*)(s0 + from * kStageS + row * 128);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const int k = i * TN + j;
+#pragma unroll
+          for (int kh = 0; kh < 2; ++kh) {
+            Frag<WIDE> fa;
+            fa.set(af[i % 2][kh]);
+            d[k & 1] = mfma_half(bf[j][kh], fa, kh ? d[k & 1] : v16f{});
+            pf4 sbn[2];
+            if (k > 0) scales_b(cur, k - 1, kh, sbn);
+            if (k > 0) add(k - 1, kh, sbn);
+            else add(TM * TN - 1, kh, sbl + 2 * kh);
+            // Before results are stored all copies of a block are given out: they are waited for without those.
+            const int at = 2 * k + kh;
+            if (at < kSteps - kFree - 1) {
+              if (!ahead)
+#pragma unroll
+                for (int e = kEarly + kPer * at; e < min(kEarly + kPer * (at + 1), kCopies); ++e) copy(nx, e);
+            } else if (at == kSteps - kFree - 1) {
+              advance();
+            } else {
+              const int u = at - (kSteps - kFree);
+#pragma unroll
+              for (int e = kPer * u; e < min(kPer * (u + 1), kEarly); ++e) copy(cur, e);
+              if (u == kFree - 1) {
+                ahead = last;
+                if (last)
+#pragma unroll
+                  for (int e = kEarly; e < kCopies; ++e) copy(cur, e);
+              }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          if (j == 0) s[i & 1] = sa[i % 2] * sb;
+          if (i == TM - 1) {
+#pragma unroll
+            for (int kh = 0; kh < 2; ++kh) bf[j][kh].set(read_b(nx, j, kh));
+          }
+        }
+      }
+      if constexpr (BROWS != 1) sb = *(lds_f32*)(base + at_s + nx * kStageS + BM * 4 + (n_next % 128 + wn * 64) / 128 * 4);
+      cur = nx;
     }
-    const float sb = BROWS == 1 ? 1.0f : sb_row[c];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) add(TM * TN - 1, h, sbl + 2 * h);
+    TO* out = g.splits > 1 ? reinterpret_cast<TO*>(g.part + int64_t(t.piece) * g.m * g.n) : static_cast<TO*>(g.out);
+    const int64_t os = g.splits > 1 ? g.n : g.os;
+    const int col = t.n0 + wn * 64 + half * 8;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      const uint8_t* p = st.rows + ((wm * TM + i) * 16 + r16) * 128;
-      Frag<WIDE> af;
-      af.set(join(*reinterpret_cast<const v4i*>(p + u0), *reinterpret_cast<const v4i*>(p + u1)));
-      const float s = st.scale[(wm * TM + i) * 16 + r16] * sb;
+      const int row = t.m0 + (wm * TM + i) * 32 + r32;
+      if (row < g.m)
 #pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const pf4 d = mfma_block(bf[j], af);
+        for (int j = 0; j < TN; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(BROWS == 1 ? d[r] * sbn[j][r] : d[r], s, acc[i][j][r]);
-      }
+          for (int h = 0; h < 2; ++h) {
+            const v16f& v = acc[i][j];
+            const int e = col + 32 * j + 16 * h;
+            store8<TO>(out + row * os + e, pf4{v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]},
+                       pf4{v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]}, g.n - e);
+          }
     }
-  }
-  TO* out = g.splits > 1 ? reinterpret_cast<TO*>(g.part + int64_t(piece) * g.m * g.n) : static_cast<TO*>(g.out);
-  const int64_t os = g.splits > 1 ? g.n : g.os;
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int row = m0 + (wm * TM + i) * 16 + r16;
-#pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int col = n0 + (wn * TN + j) * 16 + kg * 4;
-      if (row < g.m) store4<TO>(out + row * os + col, acc[i][j], g.n - col);
-    }
+    stored = t.m0 + BM <= g.m && t.n0 + BN <= g.n;
+    id += step;
+    if (id >= end) return;
+    t = place_of(id);
   }
 }
 
@@ -201,16 +400,19 @@ __global__ void __launch_bounds__(256) matmul_join_kernel(MatmulArgs g) {
 }
 
 struct MatmulPlan {
-  int bm, bn, splits, per;
+  int bm, bn, slots, splits, per;    // slots: workgroups that run at a time
 };
 
 MatmulPlan plan_of(const ssm_matmul_fp8_params* p) {
-  MatmulPlan t{128, 128, 1, 0};
-  const int64_t blocks = blocks_of(p->k);
-  const int64_t tiles = ((p->m + t.bm - 1) / t.bm) * ((p->n + t.bn - 1) / t.bn);
-  int64_t s = p->splits > 0 ? p->splits : tiles >= 256 ? 1 : 512 / tiles;
+  const bool narrow = p->b_rows == kBlock && p->out_dtype == SSM_BF16;
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((p->m + bm - 1) / bm) * ((p->n + bn - 1) / bn); };
+  MatmulPlan t{narrow ? 256 : 128, 256, 256, 1, 0};
+  if (tiles(t.bm, t.bn) < 160) t.bn = t.bm = 128, t.slots = 512;
+  const int64_t blocks = blocks_of(p->k), all = tiles(t.bm, t.bn);
+  int64_t s = p->splits > 0 ? p->splits : all >= 128 ? 1 : t.slots / all;
+  if (p->splits == 0 && s > blocks / 4) s = blocks / 4;
   if (p->splits == 0 && s > 16) s = 16;
-  if (s > blocks) s = blocks;
+  s = s < 1 ? 1 : s > blocks ? blocks : s;
   t.per = static_cast<int>((blocks + s - 1) / s);
   t.splits = static_cast<int>((blocks + t.per - 1) / t.per);
   return t;
@@ -241,11 +443,23 @@ ssm_status check_matmul(const ssm_matmul_fp8_params* p) {
   return SSM_OK;
 }
 
-template <int BM, int BN, int WM, int WN, bool WIDE, typename TO>
-void launch_tile(const MatmulArgs& g, int brows, int64_t tiles, hipStream_t st) {
-  const dim3 grid(static_cast<uint32_t>(tiles * g.splits)), block(64 * WM * WN);
-  if (brows == 1) hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, WM, WN, 1, WIDE, TO>), grid, block, 0, st, g);
-  else hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, WM, WN, 128, WIDE, TO>), grid, block, 0, st, g);
+template <int TM, int WM, int WN, int BROWS, bool WIDE, typename TO>
+void launch_tile(const MatmulArgs& g, int64_t items, int slots, hipStream_t st) {
+  hipLaunchKernelGGL((matmul_tile_kernel<TM, WM, WN, BROWS, WIDE, TO>), dim3(static_cast<uint32_t>(items < slots ? items : slots)),
+                     dim3(64 * WM * WN), 0, st, g);
+}
+
+template <bool WIDE, typename TO>
+void launch_tiles(const MatmulArgs& g, const MatmulPlan& t, int brows, int64_t items, hipStream_t st) {
+  if (brows == 1) {
+    if (t.bn == 256) launch_tile<2, 2, 4, 1, WIDE, TO>(g, items, t.slots, st);
+    else launch_tile<2, 2, 2, 1, WIDE, TO>(g, items, t.slots, st);
+  } else if (t.bm == 128) {
+    if (t.bn == 256) launch_tile<2, 2, 4, kBlock, WIDE, TO>(g, items, t.slots, st);
+    else launch_tile<2, 2, 2, kBlock, WIDE, TO>(g, items, t.slots, st);
+  } else {
+    if constexpr (!WIDE) launch_tile<4, 2, 4, kBlock, false, TO>(g, items, t.slots, st);
+  }
 }
 
 }  // namespace
@@ -291,12 +505,14 @@ extern "C" ssm_status ssm_matmul_fp8(const ssm_matmul_fp8_params* p, const void*
   g.sbs = p->b_scale_stride ? p->b_scale_stride : g.blocks;
   g.splits = t.splits;
   g.per = t.per;
+  g.tiles_m = (g.m + t.bm - 1) / t.bm;
   g.tiles_n = (g.n + t.bn - 1) / t.bn;
-  const int64_t tiles = int64_t((g.m + t.bm - 1) / t.bm) * g.tiles_n;
+  const int64_t tiles = int64_t(g.tiles_m) * g.tiles_n;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (p->out_dtype == SSM_F32) launch_tile<128, 128, 2, 2, true, float>(g, p->b_rows, tiles, st);
-  else if (g.splits > 1) launch_tile<128, 128, 2, 2, false, float>(g, p->b_rows, tiles, st);
-  else launch_tile<128, 128, 2, 2, false, uint16_t>(g, p->b_rows, tiles, st);
+  const int64_t items = tiles * g.splits;
+  if (p->out_dtype == SSM_F32) launch_tiles<true, float>(g, t, p->b_rows, items, st);
+  else if (g.splits > 1) launch_tiles<false, float>(g, t, p->b_rows, items, st);
+  else launch_tiles<false, uint16_t>(g, t, p->b_rows, items, st);
   if (g.splits > 1) {
     const dim3 grid(static_cast<uint32_t>((int64_t(g.m) * ((g.n + 3) / 4) + 255) / 256));
     if (p->out_dtype == SSM_F32) hipLaunchKernelGGL((matmul_join_kernel<float>), grid, dim3(256), 0, st, g);
