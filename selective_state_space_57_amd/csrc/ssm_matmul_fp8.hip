@@ -30,6 +30,7 @@ struct MatmulArgs {
   int m, n, k, blocks;    // blocks of 128 along k
   int tiles_m, tiles_n;
   int splits, per;        // pieces of k, blocks of a piece
+  int whole, halved;      // tiles, and tiles in halves behind them
 };
 
 typedef float v16f __attribute__((ext_vector_type(16)));
@@ -98,6 +99,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t bytes_rsrc(const void* base, u
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0), static_cast<int>(bytes),
                                            static_cast<int>(kRsrcWord3));
 }
+// Values that are the same in a whole wave, in scalar registers.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+template <typename T>
+__device__ __forceinline__ T* uniform(T* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return reinterpret_cast<T*>(uint64_t(uniform(static_cast<uint32_t>(v >> 32))) << 32 | uniform(static_cast<uint32_t>(v)));
+}
 // Waits until at most N of this wave's memory operations are under way.
 template <int N = 0>
 __device__ __forceinline__ void wait_memory() {
@@ -106,10 +114,15 @@ __device__ __forceinline__ void wait_memory() {
 }
 __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }      // lgkmcnt(0)
 
-// A workgroup's tiles of (32 TM WM) x (64 WN) results, one after the other; a wave has 32 TM x 64 of them.  BROWS: rows of b
-// under one scale.  WIDE: bf16 products.
-template <int TM, int WM, int WN, int BROWS, bool WIDE, typename TO>
-__global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g) {
+template <int TM, int WM, int WN, int BROWS>
+constexpr int kTileLds = 2 * ((32 * TM * WM + 64 * WN) * 128 +
+                              256 * ((32 * TM * WM / 64 + (BROWS == 1 ? WN : 1) + WM * WN - 1) / (WM * WN)) * WM * WN);
+
+// A workgroup's tiles of (32 TM WM) x (64 WN) results, one after the other; a wave has 32 TM x 64 of them.  The tiles are
+// numbers first to first + count, or (PARTS > 1) the parts of that many rows of tiles that are PARTS times as high.
+// BROWS: rows of b under one scale.  WIDE: bf16 products.
+template <int TM, int WM, int WN, int BROWS, bool WIDE, int PARTS, typename TO>
+__device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, int first, int count) {
   constexpr int BM = 32 * TM * WM, BN = 64 * WN, NW = WM * WN, TN = 2;
   constexpr int kA = BM / 8 / NW, kB = BN / 8 / NW;         // a wave's copies of 1 KB (8 rows of a block) in a stage
   constexpr int kScales = BM / 64 + (BROWS == 1 ? BN / 64 : 1), kSlots = (kScales + NW - 1) / NW;
@@ -121,7 +134,7 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g)
   constexpr int kPer = (kCopies + kSteps - 2) / (kSteps - 1), kEarly = kPer * kFree < kCopies ? kPer * kFree : kCopies;
   static_assert(kEarly + kPer * (kSteps - kFree - 1) >= kCopies);
   static_assert(BM / 8 % NW == 0 && BN / 8 % NW == 0 && NW % 2 == 0 && TM >= 2 && TM % 2 == 0);
-  __shared__ __align__(1024) uint8_t lds[2 * (kStageA + kStageB + kStageS)];   // two stages of a, of b, of scales
+  static_assert(kTileLds<TM, WM, WN, BROWS> == 2 * (kStageA + kStageB + kStageS));   // two stages of a, of b, of scales
   const uint32_t at_b = 2 * kStageA, at_s = 2 * (kStageA + kStageB);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM;
@@ -129,7 +142,7 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g)
 
   // Workgroups go to the 8 XCDs in turn: each XCD takes a run of tiles that walks along n four tiles of m at a time, so
   // that the 32 tiles it has in work share 4 + 8 panels in its L2.
-  const int tiles = g.tiles_m * g.tiles_n, total = tiles * g.splits;
+  const int tiles = g.tiles_m * g.tiles_n, total = count * PARTS;
   const int xcd = blockIdx.x & 7, each = total / 8, more = total % 8;
   const int step = gridDim.x / 8 + (xcd < static_cast<int>(gridDim.x % 8) ? 1 : 0);
   const int end = (xcd + 1) * each + min(xcd + 1, more);
@@ -137,9 +150,9 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g)
     int m0, n0, c, c1, piece;
   };
   auto place_of = [&](int id) {
-    const int piece = id / tiles, tile = id % tiles;
+    const int whole = first + id / PARTS, piece = whole / tiles, tile = whole % tiles;
     const int band = tile / (4 * g.tiles_n), in_band = tile % (4 * g.tiles_n), high = min(4, g.tiles_m - 4 * band);
-    return Place{(band * 4 + in_band % high) * BM, in_band / high * BN, piece * g.per, min(piece * g.per + g.per, g.blocks), piece};
+    return Place{((band * 4 + in_band % high) * PARTS + id % PARTS) * BM, in_band / high * BN, piece * g.per, min(piece * g.per + g.per, g.blocks), piece};
   };
 
   // A copy's lane has row lane / 8 of eight, and the unit of 16 bytes whose place in LDS is lane % 8: units are exchanged by
@@ -156,24 +169,28 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g)
                              : 4u * ((p - BM / 64) * 64 + lane) * static_cast<uint32_t>(g.sbs);
   }
   const uint8_t *pa = nullptr, *pb = nullptr;   // the block that is copied next, and bytes from there to the end of its rows
-  const float *psa = nullptr, *psb = nullptr;
-  uint32_t na = 0, nb = 0, nsa = 0, nsb = 0;
+  const float* ps[kSlots] = {};
+  uint32_t na = 0, nb = 0, ns[kSlots] = {};
   int lid = xcd * each + min(xcd, more) + (blockIdx.x >> 3);   // its tile
   int left = 0, blocks = 0;                     // of k, and of the tile's blocks
   auto enter = [&]() {
     const Place t = place_of(lid);
-    const int rows_m = min(BM, g.m - t.m0), rows_n = min(BN, g.n - t.n0);
+    const int m0 = min(t.m0, g.m - 1);          // (a part may lie behind the last row: it reads that one, and writes nothing)
+    const int rows_m = min(BM, g.m - m0), rows_n = min(BN, g.n - t.n0);
     const int sb_rows = BROWS == 1 ? rows_n : min(BN / 128 + 1, (g.n - t.n0 / 128 * 128 + 127) / 128);
     left = g.k - t.c * 128;
     blocks = t.c1 - t.c;
-    pa = g.a + t.m0 * g.as + t.c * 128;
-    pb = g.b + t.n0 * g.bs + t.c * 128;
-    psa = g.sa + t.m0 * g.sas + t.c;
-    psb = g.sb + t.n0 / BROWS * g.sbs + t.c;
-    na = static_cast<uint32_t>((rows_m - 1) * g.as) + left;
-    nb = static_cast<uint32_t>((rows_n - 1) * g.bs) + left;
-    nsa = 4u * (static_cast<uint32_t>((rows_m - 1) * g.sas) + g.blocks - t.c);
-    nsb = 4u * (static_cast<uint32_t>((sb_rows - 1) * g.sbs) + g.blocks - t.c);
+    pa = uniform(g.a + m0 * g.as + t.c * 128);
+    pb = uniform(g.b + t.n0 * g.bs + t.c * 128);
+    na = uniform(static_cast<uint32_t>(rows_m - 1) * as + left);
+    nb = uniform(static_cast<uint32_t>(rows_n - 1) * bs + left);
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+      const bool of_a = wave + NW * i < BM / 64;
+      ps[i] = uniform(of_a ? g.sa + m0 * g.sas + t.c : g.sb + t.n0 / BROWS * g.sbs + t.c);
+      ns[i] = uniform(4u * ((of_a ? static_cast<uint32_t>(rows_m - 1) * static_cast<uint32_t>(g.sas)
+                                  : static_cast<uint32_t>(sb_rows - 1) * static_cast<uint32_t>(g.sbs)) + g.blocks - t.c));
+    }
   };
   // copy i of a wave's copies of a stage
   auto copy = [&](int s, int i) {
@@ -187,8 +204,7 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g)
                                                16, static_cast<int>(o + (i - kA) * NW * 8 * bs), 0, 0, 0);
     } else {                                    // (rows behind the last one, and slots behind the last scale: zeros)
       const int p = wave + NW * (i - kA - kB);
-      const bool of_a = p < BM / 64;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(bytes_rsrc(of_a ? psa : psb, of_a ? nsa : nsb),
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bytes_rsrc(ps[i - kA - kB], ns[i - kA - kB]),
                                                (lds_mvoid*)(lds + at_s + s * kStageS + p * 256), 4,
                                                static_cast<int>(first_s[i - kA - kB]), 0, 0, 0);
     }
@@ -197,17 +213,20 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g)
     if (--blocks > 0) {
       pa += 128;
       pb += 128;
-      psa += 1;
-      psb += 1;
       na -= 128;
       nb -= 128;
-      nsa -= 4;
-      nsb -= 4;
       left -= 128;
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) {
+        ps[i] += 1;
+        ns[i] -= 4;
+      }
     } else if ((lid += step) < end) {
       enter();
     } else {
-      na = nb = nsa = nsb = 0;
+      na = nb = 0;
+#pragma unroll
+      for (int i = 0; i < kSlots; ++i) ns[i] = 0;
       lid = end;
     }
   };
@@ -218,21 +237,18 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g)
   const int key_a = (r32 >> 1) & 7;
   const int row_b = ((r32 >> 4) << 4) | (((r32 >> 2) & 1) << 3) | (((r32 >> 3) & 1) << 2) | (r32 & 3);
   const int key_b = (row_b >> 1) & 7;
-  // (unit u of 16 bytes: half a block is units 4 kh + 2 half + 0, 1)
-  uint32_t a0 = (wm * TM * 32 + r32) * 128 + ((2 * half) ^ key_a) * 16;
-  uint32_t b0 = at_b + (wn * 64 + row_b) * 128 + ((2 * half) ^ key_b) * 16;
-  uint32_t s0 = at_s + (wm * TM * 32 + r32) * 4;
+  // (half a block kh of a row is units 4 kh + 2 half and the one behind it)
   const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_mvoid*)lds));
-  a0 += base;
-  b0 += base;
-  s0 += base;
+  const uint32_t at_frag_a = base + (wm * TM * 32 + r32) * 128 + ((2 * half) ^ key_a) * 16;
+  const uint32_t at_frag_b = base + at_b + (wn * 64 + row_b) * 128 + ((2 * half) ^ key_b) * 16;
+  const uint32_t at_scale = base + at_s + (wm * TM * 32 + r32) * 4;
   int cur = 0;
   auto read_a = [&](int s, int i, int kh) {
-    const uint32_t p = a0 + s * kStageA;
+    const uint32_t p = at_frag_a + s * kStageA;
     return __builtin_shufflevector(*(lds_v4i*)((p ^ (kh * 64)) + i * 4096), *(lds_v4i*)((p ^ (kh * 64 + 16)) + i * 4096), 0, 1, 2, 3, 4, 5, 6, 7);
   };
   auto read_b = [&](int s, int j, int kh) {
-    const uint32_t p = b0 + s * kStageB;
+    const uint32_t p = at_frag_b + s * kStageB;
     return __builtin_shufflevector(*(lds_v4i*)((p ^ (kh * 64)) + j * 4096), *(lds_v4i*)((p ^ (kh * 64 + 16)) + j * 4096), 0, 1, 2, 3, 4, 5, 6, 7);
   };
 
@@ -259,7 +275,7 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g)
 #pragma unroll
     for (int j = 0; j < TN; ++j) bf[j][kh].set(read_b(0, j, kh));
   }
-  sa[0] = *(lds_f32*)(s0);
+  sa[0] = *(lds_f32*)(at_scale);
   float sb = BROWS == 1 ? 1.0f : *(lds_f32*)(base + at_s + BM * 4 + (t.n0 % 128 + wn * 64) / 128 * 4);
 
   while (true) {
@@ -308,7 +324,7 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g)
           const int to = (i + 1) % 2, from = i == TM - 1 ? nx : cur, row = i == TM - 1 ? 0 : i + 1;
 #pragma unroll
           for (int kh = 0; kh < 2; ++kh) af[to][kh] = read_a(from, row, kh);
-          sa[to] = *(lds_f32*)(s0 + from * kStageS + row * 128);
+          sa[to] = *(lds_f32*)(at_scale + from * kStageS + row * 128);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -380,6 +396,20 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g)
   }
 }
 
+// The tiles of a product.  HALVES: those of the last turn are cut in two, so that as many workgroups again have work in it.
+template <int TM, int WM, int WN, int BROWS, bool WIDE, bool HALVES, typename TO>
+__global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g) {
+  __shared__ __align__(1024) uint8_t lds[kTileLds<TM, WM, WN, BROWS>];
+  matmul_tiles<TM, WM, WN, BROWS, WIDE, 1, TO>(g, lds, 0, g.whole);
+  if constexpr (HALVES) {
+    if (g.halved > 0) {
+      wait_memory();   // (the zeros that are copied behind the last block)
+      __syncthreads();
+      matmul_tiles<TM / 2, WM, WN, BROWS, WIDE, 2, TO>(g, lds, g.whole, g.halved);
+    }
+  }
+}
+
 // out: the sums of the pieces of k, in their order
 template <typename TO>
 __global__ void __launch_bounds__(256) matmul_join_kernel(MatmulArgs g) {
@@ -443,22 +473,25 @@ ssm_status check_matmul(const ssm_matmul_fp8_params* p) {
   return SSM_OK;
 }
 
-template <int TM, int WM, int WN, int BROWS, bool WIDE, typename TO>
-void launch_tile(const MatmulArgs& g, int64_t items, int slots, hipStream_t st) {
-  hipLaunchKernelGGL((matmul_tile_kernel<TM, WM, WN, BROWS, WIDE, TO>), dim3(static_cast<uint32_t>(items < slots ? items : slots)),
+template <int TM, int WM, int WN, int BROWS, bool WIDE, bool HALVES, typename TO>
+void launch_tile(MatmulArgs g, int64_t items, int slots, hipStream_t st) {
+  const int last = static_cast<int>(items % slots);
+  g.halved = HALVES && items > slots && last * 2 <= slots ? last : 0;
+  g.whole = static_cast<int>(items) - g.halved;
+  hipLaunchKernelGGL((matmul_tile_kernel<TM, WM, WN, BROWS, WIDE, HALVES, TO>), dim3(static_cast<uint32_t>(items < slots ? items : slots)),
                      dim3(64 * WM * WN), 0, st, g);
 }
 
 template <bool WIDE, typename TO>
 void launch_tiles(const MatmulArgs& g, const MatmulPlan& t, int brows, int64_t items, hipStream_t st) {
   if (brows == 1) {
-    if (t.bn == 256) launch_tile<2, 2, 4, 1, WIDE, TO>(g, items, t.slots, st);
-    else launch_tile<2, 2, 2, 1, WIDE, TO>(g, items, t.slots, st);
+    if (t.bn == 256) launch_tile<2, 2, 4, 1, WIDE, false, TO>(g, items, t.slots, st);
+    else launch_tile<2, 2, 2, 1, WIDE, false, TO>(g, items, t.slots, st);
   } else if (t.bm == 128) {
-    if (t.bn == 256) launch_tile<2, 2, 4, kBlock, WIDE, TO>(g, items, t.slots, st);
-    else launch_tile<2, 2, 2, kBlock, WIDE, TO>(g, items, t.slots, st);
+    if (t.bn == 256) launch_tile<2, 2, 4, kBlock, WIDE, false, TO>(g, items, t.slots, st);
+    else launch_tile<2, 2, 2, kBlock, WIDE, false, TO>(g, items, t.slots, st);
   } else {
-    if constexpr (!WIDE) launch_tile<4, 2, 4, kBlock, false, TO>(g, items, t.slots, st);
+    if constexpr (!WIDE) launch_tile<4, 2, 4, kBlock, false, true, TO>(g, items, t.slots, st);
   }
 }
 
