@@ -44,7 +44,7 @@ __device__ __forceinline__ v8bf widen(int lo, int hi) {
   return v8bf{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Half a block (64 k) of a wave's 32 rows: a lane's 32 codes, as they are or as bf16.
+// A lane's 32 codes of a row, as they are or as bf16: half a block (64 k) of 32 rows, or a block of 16.
 template <bool WIDE>
 struct Frag {
   v8i v;
@@ -66,6 +66,18 @@ __device__ __forceinline__ v16f mfma_half(const Frag<true>& b, const Frag<true>&
   for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b.v[i], a.v[i], d, 0, 0, 0);
   return d;
 }
+
+// A whole block of 16 rows.
+__device__ __forceinline__ pf4 mfma_block(const Frag<false>& b, const Frag<false>& a) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, pf4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
+}
+__device__ __forceinline__ pf4 mfma_block(const Frag<true>& b, const Frag<true>& a) {
+  pf4 d{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b.v[i], a.v[i], d, 0, 0, 0);
+  return d;
+}
+__device__ __forceinline__ v8i join(v4i lo, v4i hi) { return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7); }
 
 // Neighbouring results of a row, four (eight) of them, of which cnt are inside the row.
 template <typename TO>
@@ -410,6 +422,105 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g)
   }
 }
 
+// Few rows of a: 16 MT of them at most, bound by the reading of b.  A workgroup has 16 NT rows of b; its W waves take the
+// blocks of k in turn, each with a stage of its own in LDS that it alone fills and reads, so that no wave waits for another,
+// and the waves' sums are joined in LDS in a fixed order.  (Read straight into registers, 16 rows and half a line of each to
+// an instruction, the operands took 1.2 to 1.9 times as long.)
+// v_mfma_f32_16x16x128_f8f6f4: a lane has 32 codes of row lane % 16 of a and of b, and the result's four neighbouring j.
+template <int MT, int NT, int W, int BROWS, bool WIDE, typename TO>
+__global__ void __launch_bounds__(64 * W) matmul_few_kernel(MatmulArgs g) {
+  constexpr int kStage = (MT + NT) * 2048, kPart = MT * NT * 1024;
+  __shared__ __align__(1024) uint8_t lds[W * (kStage > kPart ? kStage : kPart)];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, kg = lane >> 4;
+  const int n0 = blockIdx.x * 16 * NT;
+  const int rows_n = min(16 * NT, g.n - n0);
+  const uint32_t as = static_cast<uint32_t>(g.as), bs = static_cast<uint32_t>(g.bs);
+  const auto ra = bytes_rsrc(g.a, static_cast<uint32_t>(g.m - 1) * as + g.k);
+  const auto rb = bytes_rsrc(g.b + n0 * g.bs, static_cast<uint32_t>(rows_n - 1) * bs + g.k);
+  const auto rsa = make_rsrc(g.sa, (g.m - 1) * g.sas + g.blocks);
+  const auto rsb = make_rsrc(g.sb + n0 / BROWS * g.sbs, BROWS == 1 ? (rows_n - 1) * g.sbs + g.blocks : g.blocks);
+  uint8_t* stage = lds + wave * kStage;          // rows of b, then of a
+  constexpr int kSa = (MT + 3) / 4;
+  float sa[kSa] = {}, sb = 0.0f;                 // of rows `lane`, `lane` + 64 of a; of row `lane` of b, or of its block
+  const int unit = (lane & 7) ^ (lane >> 4);     // as in the tiles; the second of two copies has it ^ 4
+  auto load = [&](int c) {
+    // (past the end of k, and behind the last row: zeros)
+#pragma unroll
+    for (int p = 0; p < 2 * (MT + NT); ++p) {
+      const int q = p < 2 * NT ? p : p - 2 * NT, at = (unit ^ (p % 2 * 4)) * 16;
+      const uint32_t o = (q * 8 + (lane >> 3)) * (p < 2 * NT ? bs : as) + c * 128u + at;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(p < 2 * NT ? rb : ra, (lds_mvoid*)(stage + p * 1024), 16,
+                                               static_cast<int>(at < g.k - c * 128 ? o : kDropOffset), 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kSa; ++i)
+      sa[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          rsa, static_cast<int>(4u * ((lane % (16 * MT) + 64 * i) * static_cast<uint32_t>(g.sas) + c)), 0, 0));
+    sb = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+        rsb, static_cast<int>(4u * ((BROWS == 1 ? (lane % (16 * NT)) * static_cast<uint32_t>(g.sbs) : 0u) + c)), 0, 0));
+  };
+  const uint8_t* frag = stage + r16 * 128 + (kg ^ (r16 >> 1)) * 16;
+  auto read = [&](int f) {                       // (units kg and kg + 4 of a row)
+    const uint8_t* p = frag + f * 2048;
+    const uint8_t* q = stage + r16 * 128 + (((kg ^ (r16 >> 1)) * 16) ^ 64) + f * 2048;
+    return join(*reinterpret_cast<const v4i*>(p), *reinterpret_cast<const v4i*>(q));
+  };
+  pf4 acc[MT][NT] = {};
+  int c = wave;
+  if (c < g.blocks) load(c);
+  for (; c < g.blocks; c += W) {
+    wait_memory();
+    asm volatile("" ::: "memory");
+    v8i va[MT], vb[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) vb[j] = read(j);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) va[i] = read(NT + i);
+    float sac[kSa];
+#pragma unroll
+    for (int i = 0; i < kSa; ++i) sac[i] = sa[i];
+    const float sbc = sb;
+    wait_lds();                                  // (the stage has been read)
+    asm volatile("" ::: "memory");
+    if (c + W < g.blocks) load(c + W);
+    Frag<WIDE> fb[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) fb[j].set(vb[j]);
+    float sbn[BROWS == 1 ? 4 * NT : 1] = {sbc};
+    if constexpr (BROWS == 1) {
+#pragma unroll
+      for (int q = 0; q < 4 * NT; ++q) sbn[q] = __shfl(sbc, q / 4 * 16 + kg * 4 + q % 4);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      Frag<WIDE> fa;
+      fa.set(va[i]);
+      const float s = MT == 1 ? sac[0] : __shfl(sac[i / 4], i % 4 * 16 + r16);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const pf4 d = mfma_block(fb[j], fa);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[r], s * sbn[BROWS == 1 ? 4 * j + r : 0], acc[i][j][r]);
+      }
+    }
+  }
+  __syncthreads();                               // (every stage has been read)
+  pf4* part = reinterpret_cast<pf4*>(lds);       // [W][MT NT][64]
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) part[(wave * MT * NT + i * NT + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+  for (int t = wave; t < MT * NT; t += W) {
+    pf4 sum = part[t * 64 + lane];
+#pragma unroll
+    for (int w = 1; w < W; ++w) sum += part[(w * MT * NT + t) * 64 + lane];
+    const int row = t / NT * 16 + r16, col = n0 + t % NT * 16 + kg * 4;
+    if (row < g.m) store4<TO>(static_cast<TO*>(g.out) + row * g.os + col, sum, g.n - col);
+  }
+}
+
 // out: the sums of the pieces of k, in their order
 template <typename TO>
 __global__ void __launch_bounds__(256) matmul_join_kernel(MatmulArgs g) {
@@ -429,14 +540,18 @@ __global__ void __launch_bounds__(256) matmul_join_kernel(MatmulArgs g) {
   store4<TO>(static_cast<TO*>(g.out) + row * g.os + col, sum, cnt);
 }
 
+constexpr int kFew = 128;             // rows of a
+
 struct MatmulPlan {
+  bool few;
   int bm, bn, slots, splits, per;    // slots: workgroups that run at a time
 };
 
 MatmulPlan plan_of(const ssm_matmul_fp8_params* p) {
   const bool narrow = p->b_rows == kBlock && p->out_dtype == SSM_BF16;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((p->m + bm - 1) / bm) * ((p->n + bn - 1) / bn); };
-  MatmulPlan t{narrow ? 256 : 128, 256, 256, 1, 0};
+  if (p->m <= kFew && p->splits <= 1) return {true, kFew, 16, 0, 1, 0};
+  MatmulPlan t{false, narrow ? 256 : 128, 256, 256, 1, 0};
   if (tiles(t.bm, t.bn) < 160) t.bn = t.bm = 128, t.slots = 512;
   const int64_t blocks = blocks_of(p->k), all = tiles(t.bm, t.bn);
   int64_t s = p->splits > 0 ? p->splits : all >= 128 ? 1 : t.slots / all;
@@ -480,6 +595,24 @@ void launch_tile(MatmulArgs g, int64_t items, int slots, hipStream_t st) {
   g.whole = static_cast<int>(items) - g.halved;
   hipLaunchKernelGGL((matmul_tile_kernel<TM, WM, WN, BROWS, WIDE, HALVES, TO>), dim3(static_cast<uint32_t>(items < slots ? items : slots)),
                      dim3(64 * WM * WN), 0, st, g);
+}
+
+template <int MT, int NT, int W, bool WIDE, typename TO>
+void launch_few(const MatmulArgs& g, int brows, hipStream_t st) {
+  const dim3 grid((g.n + 16 * NT - 1) / (16 * NT)), block(64 * W);
+  if (brows == 1) hipLaunchKernelGGL((matmul_few_kernel<MT, NT, W, 1, WIDE, TO>), grid, block, 0, st, g);
+  else hipLaunchKernelGGL((matmul_few_kernel<MT, NT, W, kBlock, WIDE, TO>), grid, block, 0, st, g);
+}
+
+// More rows of b to a workgroup read a less often, fewer make more workgroups (NT = 4 and 1, k = 2560 and 5120: 64 rows of a
+// 11.7 and 15.3 us at n = 10576, 13.0 and 8.9 us at 2560; 32 rows 9.6 and 11.1, 9.8 and 6.3).
+template <bool WIDE, typename TO>
+void launch_few_rows(const MatmulArgs& g, int brows, hipStream_t st) {
+  const bool many = g.n > 8192;
+  if (g.m <= 16) launch_few<1, 1, 8, WIDE, TO>(g, brows, st);
+  else if (g.m <= 32) many ? launch_few<2, 4, 8, WIDE, TO>(g, brows, st) : launch_few<2, 1, 8, WIDE, TO>(g, brows, st);
+  else if (g.m <= 64) many ? launch_few<4, 4, 8, WIDE, TO>(g, brows, st) : launch_few<4, 1, 8, WIDE, TO>(g, brows, st);
+  else many ? launch_few<8, 2, 4, WIDE, TO>(g, brows, st) : launch_few<8, 1, 8, WIDE, TO>(g, brows, st);
 }
 
 template <bool WIDE, typename TO>
@@ -543,7 +676,9 @@ extern "C" ssm_status ssm_matmul_fp8(const ssm_matmul_fp8_params* p, const void*
   const int64_t tiles = int64_t(g.tiles_m) * g.tiles_n;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const int64_t items = tiles * g.splits;
-  if (p->out_dtype == SSM_F32) launch_tiles<true, float>(g, t, p->b_rows, items, st);
+  if (t.few && p->out_dtype == SSM_F32) launch_few_rows<true, float>(g, p->b_rows, st);
+  else if (t.few) launch_few_rows<false, uint16_t>(g, p->b_rows, st);
+  else if (p->out_dtype == SSM_F32) launch_tiles<true, float>(g, t, p->b_rows, items, st);
   else if (g.splits > 1) launch_tiles<false, float>(g, t, p->b_rows, items, st);
   else launch_tiles<false, uint16_t>(g, t, p->b_rows, items, st);
   if (g.splits > 1) {
