@@ -118,17 +118,29 @@ __device__ __forceinline__ T* uniform(T* p) {
   const uint64_t v = reinterpret_cast<uint64_t>(p);
   return reinterpret_cast<T*>(uint64_t(uniform(static_cast<uint32_t>(v >> 32))) << 32 | uniform(static_cast<uint32_t>(v)));
 }
-// Waits until at most N of this wave's memory operations are under way.
+// Waits until at most N of this wave's memory operations, or none of its LDS operations, are under way.  (The empty asm
+// keeps the compiler from moving reads and copies over the wait.)
 template <int N = 0>
 __device__ __forceinline__ void wait_memory() {
   static_assert(N < 64);
+  asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4 << 14));
+  asm volatile("" ::: "memory");
 }
-__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }      // lgkmcnt(0)
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+}
 
 template <int TM, int WM, int WN, int BROWS>
-constexpr int kTileLds = 2 * ((32 * TM * WM + 64 * WN) * 128 +
-                              256 * ((32 * TM * WM / 64 + (BROWS == 1 ? WN : 1) + WM * WN - 1) / (WM * WN)) * WM * WN);
+constexpr int kTileLds = 2 * (32 * TM * WM + 64 * WN) * 128 +
+                         4 * 256 * ((32 * TM * WM / 64 + (BROWS == 1 ? WN : 1) + WM * WN - 1) / (WM * WN)) * WM * WN;
 
 // A workgroup's tiles of (32 TM WM) x (64 WN) results, one after the other; a wave has 32 TM x 64 of them.  The tiles are
 // numbers first to first + count, or (PARTS > 1) the parts of that many rows of tiles that are PARTS times as high.
@@ -145,8 +157,12 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
   constexpr int kCopies = kA + kB + kSlots, kSteps = 2 * TN * TM, kFree = 2 * TN;
   constexpr int kPer = (kCopies + kSteps - 2) / (kSteps - 1), kEarly = kPer * kFree < kCopies ? kPer * kFree : kCopies;
   static_assert(kEarly + kPer * (kSteps - kFree - 1) >= kCopies);
-  static_assert(BM / 8 % NW == 0 && BN / 8 % NW == 0 && NW % 2 == 0 && TM >= 2 && TM % 2 == 0);
-  static_assert(kTileLds<TM, WM, WN, BROWS> == 2 * (kStageA + kStageB + kStageS));   // two stages of a, of b, of scales
+  static_assert(BM / 8 % NW == 0 && BN / 8 % NW == 0 && NW % 2 == 0 && TM >= 2);
+  constexpr int kSlotsA = TM % 2 ? 3 : 2;                   // fragments of a in registers: the one in use and those ahead
+  static_assert(TM % kSlotsA == 0);
+  // Two stages of a and of b; four of scales, which are read until the end of a block, when the copies for the one behind
+  // the next may be under way.
+  static_assert(kTileLds<TM, WM, WN, BROWS> == 2 * (kStageA + kStageB) + 4 * kStageS);
   const uint32_t at_b = 2 * kStageA, at_s = 2 * (kStageA + kStageB);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM;
@@ -205,7 +221,7 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
     }
   };
   // copy i of a wave's copies of a stage
-  auto copy = [&](int s, int i) {
+  auto copy = [&](int s, int s4, int i) {
     if (i < kA) {
       const uint32_t o = unit * 16 < left ? first_a : kDropOffset;   // (past the end of k: zeros)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(bytes_rsrc(pa, na), (lds_mvoid*)(lds + s * kStageA + (wave + NW * i) * 1024), 16,
@@ -217,7 +233,7 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
     } else {                                    // (rows behind the last one, and slots behind the last scale: zeros)
       const int p = wave + NW * (i - kA - kB);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(bytes_rsrc(ps[i - kA - kB], ns[i - kA - kB]),
-                                               (lds_mvoid*)(lds + at_s + s * kStageS + p * 256), 4,
+                                               (lds_mvoid*)(lds + at_s + s4 * kStageS + p * 256), 4,
                                                static_cast<int>(first_s[i - kA - kB]), 0, 0, 0);
     }
   };
@@ -254,7 +270,7 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
   const uint32_t at_frag_a = base + (wm * TM * 32 + r32) * 128 + ((2 * half) ^ key_a) * 16;
   const uint32_t at_frag_b = base + at_b + (wn * 64 + row_b) * 128 + ((2 * half) ^ key_b) * 16;
   const uint32_t at_scale = base + at_s + (wm * TM * 32 + r32) * 4;
-  int cur = 0;
+  int cur = 0, cur4 = 0;
   auto read_a = [&](int s, int i, int kh) {
     const uint32_t p = at_frag_a + s * kStageA;
     return __builtin_shufflevector(*(lds_v4i*)((p ^ (kh * 64)) + i * 4096), *(lds_v4i*)((p ^ (kh * 64 + 16)) + i * 4096), 0, 1, 2, 3, 4, 5, 6, 7);
@@ -268,17 +284,16 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
   if (id >= end) return;
   enter();
 #pragma unroll
-  for (int i = 0; i < kCopies; ++i) copy(0, i);
+  for (int i = 0; i < kCopies; ++i) copy(0, 0, i);
   advance();
 #pragma unroll
-  for (int i = 0; i < kEarly; ++i) copy(1, i);
+  for (int i = 0; i < kEarly; ++i) copy(1, 1, i);
   wait_memory<kEarly>();
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+  barrier();
 
   Frag<WIDE> bf[TN][2];
-  v8i af[2][2];
-  float sa[2];
+  v8i af[kSlotsA][2];
+  float sa[kSlotsA];
   Place t = place_of(id);
   bool stored = false, ahead = false;
 #pragma unroll
@@ -303,40 +318,34 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
         to[r] = fmaf(BROWS == 1 ? d[k & 1][r] * sbn[(r - 8 * h) / 4][r % 4] : d[k & 1][r], s[(k / TN) & 1], to[r]);
       asm volatile("" : "+v"(to));   // (here, not at the end of the block)
     };
-    auto scales_b = [&](int s, int k, int h, pf4* sbn) {
+    auto scales_b = [&](int s4, int k, int h, pf4* sbn) {
       if constexpr (BROWS == 1) {
-        const uint32_t p = base + at_s + s * kStageS + BM * 4 + (wn * 64 + k % TN * 32 + h * 16 + half * 8) * 4;
+        const uint32_t p = base + at_s + s4 * kStageS + BM * 4 + (wn * 64 + k % TN * 32 + h * 16 + half * 8) * 4;
         sbn[0] = *(lds_pf4*)p;
         sbn[1] = *(lds_pf4*)(p + 16);
       }
     };
-    pf4 sbl[4];   // of the block's last product, which goes into the sums in the next block
     for (int c = t.c; c < t.c1; ++c) {
-      const int nx = cur ^ 1;
+      const int nx = cur ^ 1, nx4 = (cur4 + 1) & 3;
       const bool last = c + 1 == t.c1;
       const int n_next = last && id + step < end ? place_of(id + step).n0 : t.n0;
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
         if (i == TM - 1) {
-          // All of this wave's reads of the stage are done, and its part of the next one has arrived: behind the barrier that
+          // All of this wave's reads of the stage (but scales) are done, and its part of the next one has arrived: behind the barrier that
           // holds for every wave, so the next block's fragments can be read and this stage filled again.  (Behind the last
           // block what is copied and read is not used.)
-          if constexpr (BROWS == 1) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) scales_b(cur, TM * TN - 1, h, sbl + 2 * h);
-          }
           wait_lds();
           if (stored) wait_memory<kStores>();   // (results on their way out were given to memory behind those copies)
           else wait_memory();
           stored = false;
-          __builtin_amdgcn_s_barrier();
-          asm volatile("" ::: "memory");
+          barrier();
         }
         {
-          const int to = (i + 1) % 2, from = i == TM - 1 ? nx : cur, row = i == TM - 1 ? 0 : i + 1;
+          const int to = (i + 1) % kSlotsA, from = i == TM - 1 ? nx : cur, row = i == TM - 1 ? 0 : i + 1;
 #pragma unroll
           for (int kh = 0; kh < 2; ++kh) af[to][kh] = read_a(from, row, kh);
-          sa[to] = *(lds_f32*)(at_scale + from * kStageS + row * 128);
+          sa[to] = *(lds_f32*)(at_scale + (i == TM - 1 ? nx4 : cur4) * kStageS + row * 128);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -345,45 +354,55 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
 #pragma unroll
           for (int kh = 0; kh < 2; ++kh) {
             Frag<WIDE> fa;
-            fa.set(af[i % 2][kh]);
+            fa.set(af[i % kSlotsA][kh]);
             d[k & 1] = mfma_half(bf[j][kh], fa, kh ? d[k & 1] : v16f{});
             pf4 sbn[2];
-            if (k > 0) scales_b(cur, k - 1, kh, sbn);
-            if (k > 0) add(k - 1, kh, sbn);
-            else add(TM * TN - 1, kh, sbl + 2 * kh);
+            // (the block's last product goes into the sums in the next one)
+            if (k > 0) {
+              scales_b(cur4, k - 1, kh, sbn);
+              add(k - 1, kh, sbn);
+            } else if (BROWS != 1 || c > t.c) {
+              scales_b((cur4 + 3) & 3, TM * TN - 1, kh, sbn);
+              add(TM * TN - 1, kh, sbn);
+            }
             // Before results are stored all copies of a block are given out: they are waited for without those.
             const int at = 2 * k + kh;
             if (at < kSteps - kFree - 1) {
               if (!ahead)
 #pragma unroll
-                for (int e = kEarly + kPer * at; e < min(kEarly + kPer * (at + 1), kCopies); ++e) copy(nx, e);
+                for (int e = kEarly + kPer * at; e < min(kEarly + kPer * (at + 1), kCopies); ++e) copy(nx, nx4, e);
             } else if (at == kSteps - kFree - 1) {
               advance();
             } else {
               const int u = at - (kSteps - kFree);
 #pragma unroll
-              for (int e = kPer * u; e < min(kPer * (u + 1), kEarly); ++e) copy(cur, e);
+              for (int e = kPer * u; e < min(kPer * (u + 1), kEarly); ++e) copy(cur, (cur4 + 2) & 3, e);
               if (u == kFree - 1) {
                 ahead = last;
                 if (last)
 #pragma unroll
-                  for (int e = kEarly; e < kCopies; ++e) copy(cur, e);
+                  for (int e = kEarly; e < kCopies; ++e) copy(cur, (cur4 + 2) & 3, e);
               }
             }
             __builtin_amdgcn_sched_barrier(0);
           }
-          if (j == 0) s[i & 1] = sa[i % 2] * sb;
+          if (j == 0) s[i & 1] = sa[i % kSlotsA] * sb;
           if (i == TM - 1) {
 #pragma unroll
             for (int kh = 0; kh < 2; ++kh) bf[j][kh].set(read_b(nx, j, kh));
           }
         }
       }
-      if constexpr (BROWS != 1) sb = *(lds_f32*)(base + at_s + nx * kStageS + BM * 4 + (n_next % 128 + wn * 64) / 128 * 4);
+      if constexpr (BROWS != 1) sb = *(lds_f32*)(base + at_s + nx4 * kStageS + BM * 4 + (n_next % 128 + wn * 64) / 128 * 4);
       cur = nx;
+      cur4 = nx4;
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) add(TM * TN - 1, h, sbl + 2 * h);
+    for (int h = 0; h < 2; ++h) {
+      pf4 sbn[2];
+      scales_b((cur4 + 3) & 3, TM * TN - 1, h, sbn);
+      add(TM * TN - 1, h, sbn);
+    }
     TO* out = g.splits > 1 ? reinterpret_cast<TO*>(g.part + int64_t(t.piece) * g.m * g.n) : static_cast<TO*>(g.out);
     const int64_t os = g.splits > 1 ? g.n : g.os;
     const int col = t.n0 + wn * 64 + half * 8;
@@ -403,9 +422,10 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
     }
     stored = t.m0 + BM <= g.m && t.n0 + BN <= g.n;
     id += step;
-    if (id >= end) return;
+    if (id >= end) break;
     t = place_of(id);
   }
+  wait_memory();   // (the zeros that were copied behind the last block: LDS is given up only now)
 }
 
 // The tiles of a product.  HALVES: those of the last turn are cut in two, so that as many workgroups again have work in it.
@@ -415,7 +435,6 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g)
   matmul_tiles<TM, WM, WN, BROWS, WIDE, 1, TO>(g, lds, 0, g.whole);
   if constexpr (HALVES) {
     if (g.halved > 0) {
-      wait_memory();   // (the zeros that are copied behind the last block)
       __syncthreads();
       matmul_tiles<TM / 2, WM, WN, BROWS, WIDE, 2, TO>(g, lds, g.whole, g.halved);
     }
@@ -471,7 +490,6 @@ __global__ void __launch_bounds__(64 * W) matmul_few_kernel(MatmulArgs g) {
   if (c < g.blocks) load(c);
   for (; c < g.blocks; c += W) {
     wait_memory();
-    asm volatile("" ::: "memory");
     v8i va[MT], vb[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) vb[j] = read(j);
@@ -482,7 +500,6 @@ __global__ void __launch_bounds__(64 * W) matmul_few_kernel(MatmulArgs g) {
     for (int i = 0; i < kSa; ++i) sac[i] = sa[i];
     const float sbc = sb;
     wait_lds();                                  // (the stage has been read)
-    asm volatile("" ::: "memory");
     if (c + W < g.blocks) load(c + W);
     Frag<WIDE> fb[NT];
 #pragma unroll
@@ -551,7 +568,14 @@ MatmulPlan plan_of(const ssm_matmul_fp8_params* p) {
   const bool narrow = p->b_rows == kBlock && p->out_dtype == SSM_BF16;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((p->m + bm - 1) / bm) * ((p->n + bn - 1) / bn); };
   if (p->m <= kFew && p->splits <= 1) return {true, kFew, 16, 0, 1, 0};
-  MatmulPlan t{false, narrow ? 256 : 128, 256, 256, 1, 0};
+  MatmulPlan t{false, 128, 256, 256, 1, 0};
+  if (narrow) {
+    // Turns of 256 workgroups, in hundredths of one of 256 x 256 tiles: the last of those in halves where they fit, or all
+    // of 192 x 256.  (A turn at k = 8192: 256 rows 125 to 129 us, 192 rows 98 to 112, 128 rows 90.)
+    const int64_t whole = tiles(256, 256), last = whole % 256, low = tiles(192, 256);
+    const int64_t cost = whole / 256 * 100 + (last == 0 ? 0 : whole > 256 && last <= 128 ? 70 : 100);
+    t.bm = (low + 255) / 256 * 80 < cost ? 192 : 256;
+  }
   if (tiles(t.bm, t.bn) < 160) t.bn = t.bm = 128, t.slots = 512;
   const int64_t blocks = blocks_of(p->k), all = tiles(t.bm, t.bn);
   int64_t s = p->splits > 0 ? p->splits : all >= 128 ? 1 : t.slots / all;
@@ -623,8 +647,9 @@ void launch_tiles(const MatmulArgs& g, const MatmulPlan& t, int brows, int64_t i
   } else if (t.bm == 128) {
     if (t.bn == 256) launch_tile<2, 2, 4, kBlock, WIDE, false, TO>(g, items, t.slots, st);
     else launch_tile<2, 2, 2, kBlock, WIDE, false, TO>(g, items, t.slots, st);
-  } else {
-    if constexpr (!WIDE) launch_tile<4, 2, 4, kBlock, false, true, TO>(g, items, t.slots, st);
+  } else if constexpr (!WIDE) {
+    if (t.bm == 192) launch_tile<3, 2, 4, kBlock, false, false, TO>(g, items, t.slots, st);
+    else launch_tile<4, 2, 4, kBlock, false, true, TO>(g, items, t.slots, st);
   }
 }
 

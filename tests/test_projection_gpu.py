@@ -366,6 +366,27 @@ def test_matmul_of_whole_numbers(M, N, K, b_rows, out):
         assert torch.equal(ssm().matmul_fp8(a, sa, b, sb, out_dtype=out, splits=splits), want.to(out))
 
 
+# Every plan of a launch: tiles of 256 rows, whole and with the last turn in halves, of 192 rows, of 128; cut columns and rows.
+@pytest.mark.parametrize("M,N,K,b_rows,out", [
+    (4100, 4001, 144, 128, BF), (4099, 2560, 400, 128, BF), (8191, 2561, 272, 128, BF), (16389, 10576, 144, 128, BF),
+    (8192, 8193, 1040, 128, BF), (4099, 3001, 272, 1, BF), (4099, 3001, 272, 1, F32), (4099, 3001, 272, 128, F32), (2000, 2100, 272, 1, F32),
+    (16000, 200, 272, 128, BF), (200, 20001, 272, 1, BF), (1030, 1000, 2064, 128, BF), (129, 4100, 1040, 128, F32)])
+def test_matmul_plans(M, N, K, b_rows, out):
+    """Small whole numbers under scales that are powers of two, so that fp32 products are exact; every element is checked."""
+    r = Rand(M + N)
+    blocks = (K + 127) // 128
+    a = torch.randint(-3, 4, (M, K), generator=r.g, device="cuda").float().to(F8)
+    b = torch.randint(-3, 4, (N, K), generator=r.g, device="cuda").float().to(F8)
+    sa = torch.exp2(torch.randint(-2, 3, (M, blocks), generator=r.g, device="cuda").float())
+    sb = torch.exp2(torch.randint(-2, 3, (-(-N // b_rows), blocks), generator=r.g, device="cuda").float())
+    want = (a.float() * R.spread(sa, 1, a.shape)) @ (b.float() * R.spread(sb, b_rows, b.shape)).t()
+    base = torch.full((M + 1, N + 2), 5.0, dtype=out, device="cuda")
+    for _ in range(2):
+        got = ssm().matmul_fp8(a, sa, b, sb, out=base[:M, :N])
+        assert torch.equal(got, want.to(out))
+    assert (base[M:] == 5.0).all() and (base[:, N:] == 5.0).all()
+
+
 @pytest.mark.parametrize("out", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("M,N,K", [(1, 37, 144), (30, 200, 272), (300, 400, 272)])
 def test_matmul_strides(M, N, K, out):
