@@ -505,12 +505,8 @@ typedef struct {
   int64_t a_stride, b_stride, out_stride, a_scale_stride, b_scale_stride;   /* row strides; 0 = dense; a, b: below 2^23 */
   int32_t b_rows;           /* rows of b under one scale: 128 or 1 */
   int32_t out_dtype;        /* SSM_F32 or SSM_BF16 */
-  int32_t splits;           /* 0: the library picks how many pieces of k are summed apart; s > 0 forces s (at most 64) */
-  int32_t reserved;         /* must be 0 */
+  int32_t reserved[2];      /* must be 0 */
 } ssm_matmul_fp8_params;
-
-/* Bytes of device workspace ssm_matmul_fp8 needs (0 when it needs none, and for invalid parameters). */
-size_t ssm_matmul_fp8_workspace_bytes(const ssm_matmul_fp8_params* p);
 
 /*
  * Matrix product of 8-bit operands: out[i][j] = sum over blocks c of a_scale[i][c] b_scale[j / b_rows][c] times the sum
@@ -519,7 +515,7 @@ size_t ssm_matmul_fp8_workspace_bytes(const ssm_matmul_fp8_params* p);
  * The product of two scales has to be finite in fp32.  out must not overlap an input.  Deterministic.
  */
 ssm_status ssm_matmul_fp8(const ssm_matmul_fp8_params* p, const void* a, const float* a_scale, const void* b,
-                          const float* b_scale, void* out, void* workspace, size_t workspace_bytes, void* stream);
+                          const float* b_scale, void* out, void* stream);
 
 /* Static description of a status code. */
 const char* ssm_status_str(ssm_status s);

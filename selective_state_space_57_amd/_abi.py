@@ -24,7 +24,7 @@ EXPORTS = ["ssm_scan_fwd_workspace_bytes", "ssm_scan_fwd", "ssm_state_update", "
            "ssm_ssd_packed_fwd_workspace_bytes", "ssm_ssd_packed_bwd", "ssm_ssd_packed_bwd_workspace_bytes",
            "ssm_ssd_slot_update", "ssm_gated_norm_fwd", "ssm_gated_norm_bwd",
            "ssm_gated_norm_bwd_workspace_bytes", "ssm_add_norm_fwd", "ssm_add_norm_bwd",
-           "ssm_add_norm_bwd_workspace_bytes", "ssm_quantize_fp8", "ssm_matmul_fp8", "ssm_matmul_fp8_workspace_bytes"]
+           "ssm_add_norm_bwd_workspace_bytes", "ssm_quantize_fp8", "ssm_matmul_fp8"]
 
 
 class Params(ctypes.Structure):
@@ -82,7 +82,7 @@ class QuantizeFp8Params(ctypes.Structure):
 class MatmulFp8Params(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int64) for n in ("m", "n", "k", "a_stride", "b_stride", "out_stride", "a_scale_stride",
                                               "b_scale_stride")] + \
-               [(n, ctypes.c_int32) for n in ("b_rows", "out_dtype", "splits", "reserved")]
+               [("b_rows", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32 * 2)]
 
 
 class SSMError(RuntimeError):
@@ -175,9 +175,7 @@ def lib():
         L.ssm_add_norm_bwd.restype = ctypes.c_int
         L.ssm_quantize_fp8.argtypes = [UP] + [P] * 6
         L.ssm_quantize_fp8.restype = ctypes.c_int
-        L.ssm_matmul_fp8_workspace_bytes.argtypes = [MP]
-        L.ssm_matmul_fp8_workspace_bytes.restype = S
-        L.ssm_matmul_fp8.argtypes = [MP] + [P] * 5 + [P, S, P]
+        L.ssm_matmul_fp8.argtypes = [MP] + [P] * 6
         L.ssm_matmul_fp8.restype = ctypes.c_int
         L.ssm_status_str.argtypes = [ctypes.c_int]
         L.ssm_status_str.restype = ctypes.c_char_p

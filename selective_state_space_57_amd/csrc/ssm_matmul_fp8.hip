@@ -25,11 +25,9 @@ struct MatmulArgs {
   const float* sa;
   const float* sb;
   void* out;
-  float* part;            // [splits][m][n]: the sums of each piece of k
   int64_t as, bs, os, sas, sbs;
   int m, n, k, blocks;    // blocks of 128 along k
   int tiles_m, tiles_n;
-  int splits, per;        // pieces of k, blocks of a piece
   int whole, halved;      // tiles, and tiles in halves behind them
 };
 
@@ -150,13 +148,12 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
   constexpr int BM = 32 * TM * WM, BN = 64 * WN, NW = WM * WN, TN = 2;
   constexpr int kA = BM / 8 / NW, kB = BN / 8 / NW;         // a wave's copies of 1 KB (8 rows of a block) in a stage
   constexpr int kScales = BM / 64 + (BROWS == 1 ? BN / 64 : 1), kSlots = (kScales + NW - 1) / NW;
+  // A wave's copies of a stage are given out between its products: the first of them a block early, as soon as the stage is
+  // free, the others over the next block's first products.  (All at once they hold up the products behind them.)
+  constexpr int kCopies = kA + kB + kSlots, kPer = (kCopies + TM * TN - 1) / (TM * TN), kEarly = kPer * TN;
+  static_assert(kEarly <= kCopies);
   constexpr int kStores = TM * (sizeof(TO) == 2 ? 4 : 8);   // of a wave's results, where its tile is whole
   constexpr int kStageA = BM * 128, kStageB = BN * 128, kStageS = 256 * kSlots * NW;
-  // A wave's copies of a stage are given out between its products: the first of them a block early, as soon as the stage is
-  // free, the others over the next block's first products.
-  constexpr int kCopies = kA + kB + kSlots, kSteps = 2 * TN * TM, kFree = 2 * TN;
-  constexpr int kPer = (kCopies + kSteps - 2) / (kSteps - 1), kEarly = kPer * kFree < kCopies ? kPer * kFree : kCopies;
-  static_assert(kEarly + kPer * (kSteps - kFree - 1) >= kCopies);
   static_assert(BM / 8 % NW == 0 && BN / 8 % NW == 0 && NW % 2 == 0 && TM >= 2);
   constexpr int kSlotsA = TM % 2 ? 3 : 2;                   // fragments of a in registers: the one in use and those ahead
   static_assert(TM % kSlotsA == 0);
@@ -170,17 +167,17 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
 
   // Workgroups go to the 8 XCDs in turn: each XCD takes a run of tiles that walks along n four tiles of m at a time, so
   // that the 32 tiles it has in work share 4 + 8 panels in its L2.
-  const int tiles = g.tiles_m * g.tiles_n, total = count * PARTS;
+  const int total = count * PARTS;
   const int xcd = blockIdx.x & 7, each = total / 8, more = total % 8;
   const int step = gridDim.x / 8 + (xcd < static_cast<int>(gridDim.x % 8) ? 1 : 0);
   const int end = (xcd + 1) * each + min(xcd + 1, more);
   struct Place {
-    int m0, n0, c, c1, piece;
+    int m0, n0;
   };
   auto place_of = [&](int id) {
-    const int whole = first + id / PARTS, piece = whole / tiles, tile = whole % tiles;
+    const int tile = first + id / PARTS;
     const int band = tile / (4 * g.tiles_n), in_band = tile % (4 * g.tiles_n), high = min(4, g.tiles_m - 4 * band);
-    return Place{((band * 4 + in_band % high) * PARTS + id % PARTS) * BM, in_band / high * BN, piece * g.per, min(piece * g.per + g.per, g.blocks), piece};
+    return Place{((band * 4 + in_band % high) * PARTS + id % PARTS) * BM, in_band / high * BN};
   };
 
   // A copy's lane has row lane / 8 of eight, and the unit of 16 bytes whose place in LDS is lane % 8: units are exchanged by
@@ -196,66 +193,48 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
     first_s[i] = p < BM / 64 ? 4u * (p * 64 + lane) * static_cast<uint32_t>(g.sas)
                              : 4u * ((p - BM / 64) * 64 + lane) * static_cast<uint32_t>(g.sbs);
   }
-  const uint8_t *pa = nullptr, *pb = nullptr;   // the block that is copied next, and bytes from there to the end of its rows
-  const float* ps[kSlots] = {};
-  uint32_t na = 0, nb = 0, ns[kSlots] = {};
-  int lid = xcd * each + min(xcd, more) + (blockIdx.x >> 3);   // its tile
-  int left = 0, blocks = 0;                     // of k, and of the tile's blocks
+  // The ranges of the tile that is copied next begin at its first block and end with its last row; the block is an offset that
+  // the check of the range may or may not count: rows behind the last one are out of range either way.
+  __amdgpu_buffer_rsrc_t ra, rb, rs[kSlots];
+  int lid = xcd * each + min(xcd, more) + (blockIdx.x >> 3);   // the tile's number
+  int block = 0, left = 0;                      // the block in it, and what is left of k
   auto enter = [&]() {
     const Place t = place_of(lid);
     const int m0 = min(t.m0, g.m - 1);          // (a part may lie behind the last row: it reads that one, and writes nothing)
     const int rows_m = min(BM, g.m - m0), rows_n = min(BN, g.n - t.n0);
     const int sb_rows = BROWS == 1 ? rows_n : min(BN / 128 + 1, (g.n - t.n0 / 128 * 128 + 127) / 128);
-    left = g.k - t.c * 128;
-    blocks = t.c1 - t.c;
-    pa = uniform(g.a + m0 * g.as + t.c * 128);
-    pb = uniform(g.b + t.n0 * g.bs + t.c * 128);
-    na = uniform(static_cast<uint32_t>(rows_m - 1) * as + left);
-    nb = uniform(static_cast<uint32_t>(rows_n - 1) * bs + left);
+    block = 0;
+    left = g.k;
+    ra = bytes_rsrc(uniform(g.a + m0 * g.as), uniform(static_cast<uint32_t>(rows_m - 1) * as + g.k));
+    rb = bytes_rsrc(uniform(g.b + t.n0 * g.bs), uniform(static_cast<uint32_t>(rows_n - 1) * bs + g.k));
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) {
       const bool of_a = wave + NW * i < BM / 64;
-      ps[i] = uniform(of_a ? g.sa + m0 * g.sas + t.c : g.sb + t.n0 / BROWS * g.sbs + t.c);
-      ns[i] = uniform(4u * ((of_a ? static_cast<uint32_t>(rows_m - 1) * static_cast<uint32_t>(g.sas)
-                                  : static_cast<uint32_t>(sb_rows - 1) * static_cast<uint32_t>(g.sbs)) + g.blocks - t.c));
+      rs[i] = bytes_rsrc(uniform(of_a ? g.sa + m0 * g.sas : g.sb + t.n0 / BROWS * g.sbs),
+                         uniform(4u * ((of_a ? static_cast<uint32_t>(rows_m - 1) * static_cast<uint32_t>(g.sas)
+                                             : static_cast<uint32_t>(sb_rows - 1) * static_cast<uint32_t>(g.sbs)) + g.blocks)));
     }
   };
-  // copy i of a wave's copies of a stage
-  auto copy = [&](int s, int s4, int i) {
-    if (i < kA) {
-      const uint32_t o = unit * 16 < left ? first_a : kDropOffset;   // (past the end of k: zeros)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(bytes_rsrc(pa, na), (lds_mvoid*)(lds + s * kStageA + (wave + NW * i) * 1024), 16,
-                                               static_cast<int>(o + i * NW * 8 * as), 0, 0, 0);
-    } else if (i < kA + kB) {
-      const uint32_t o = unit * 16 < left ? first_b : kDropOffset;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(bytes_rsrc(pb, nb), (lds_mvoid*)(lds + at_b + s * kStageB + (wave + NW * (i - kA)) * 1024),
-                                               16, static_cast<int>(o + (i - kA) * NW * 8 * bs), 0, 0, 0);
-    } else {                                    // (rows behind the last one, and slots behind the last scale: zeros)
-      const int p = wave + NW * (i - kA - kB);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(bytes_rsrc(ps[i - kA - kB], ns[i - kA - kB]),
-                                               (lds_mvoid*)(lds + at_s + s4 * kStageS + p * 256), 4,
-                                               static_cast<int>(first_s[i - kA - kB]), 0, 0, 0);
-    }
+  // copy i of a wave's copies of a stage (past the end of k, behind the last row, and in slots behind the last scale: zeros)
+  auto copy = [&](int s, int ss, int i) {
+    const bool in = unit * 16 < left;
+    if (i < kA)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_mvoid*)(lds + s * kStageA + (wave + NW * i) * 1024), 16,
+                                               static_cast<int>((in ? first_a : kDropOffset) + i * NW * 8 * as), block * 128, 0, 0);
+    else if (i < kA + kB)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_mvoid*)(lds + at_b + s * kStageB + (wave + NW * (i - kA)) * 1024), 16,
+                                               static_cast<int>((in ? first_b : kDropOffset) + (i - kA) * NW * 8 * bs), block * 128, 0, 0);
+    else
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs[i - kA - kB], (lds_mvoid*)(lds + at_s + ss * kStageS + (wave + NW * (i - kA - kB)) * 256),
+                                               4, static_cast<int>(left > 0 ? first_s[i - kA - kB] : kDropOffset), block * 4, 0, 0);
   };
   auto advance = [&]() {   // to the block behind the one that was copied last; behind the last of all there are zeros
-    if (--blocks > 0) {
-      pa += 128;
-      pb += 128;
-      na -= 128;
-      nb -= 128;
-      left -= 128;
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i) {
-        ps[i] += 1;
-        ns[i] -= 4;
-      }
-    } else if ((lid += step) < end) {
-      enter();
-    } else {
-      na = nb = 0;
-#pragma unroll
-      for (int i = 0; i < kSlots; ++i) ns[i] = 0;
-      lid = end;
+    ++block;
+    left -= 128;
+    if (left <= 0) {
+      lid += step;
+      if (lid < end) enter();
+      else lid = end, left = 0;
     }
   };
 
@@ -270,7 +249,7 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
   const uint32_t at_frag_a = base + (wm * TM * 32 + r32) * 128 + ((2 * half) ^ key_a) * 16;
   const uint32_t at_frag_b = base + at_b + (wn * 64 + row_b) * 128 + ((2 * half) ^ key_b) * 16;
   const uint32_t at_scale = base + at_s + (wm * TM * 32 + r32) * 4;
-  int cur = 0, cur4 = 0;
+  int cur = 0, cur_s = 0;
   auto read_a = [&](int s, int i, int kh) {
     const uint32_t p = at_frag_a + s * kStageA;
     return __builtin_shufflevector(*(lds_v4i*)((p ^ (kh * 64)) + i * 4096), *(lds_v4i*)((p ^ (kh * 64 + 16)) + i * 4096), 0, 1, 2, 3, 4, 5, 6, 7);
@@ -310,101 +289,92 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
     v16f d[2];
     float s[2] = {0.0f, 0.0f};
     d[1] = v16f{};
-    // half (8 registers) of the product k (fragment k / 2 of a, k % 2 of b) goes into the sums
-    auto add = [&](int k, int h, const pf4* sbn) {
+    // the product k (fragment k / 2 of a, k % 2 of b) of the block with its scales in stage ss goes into the sums
+    auto add = [&](int k, int ss) {
       v16f& to = acc[k / TN][k % TN];
 #pragma unroll
-      for (int r = 8 * h; r < 8 * h + 8; ++r)
-        to[r] = fmaf(BROWS == 1 ? d[k & 1][r] * sbn[(r - 8 * h) / 4][r % 4] : d[k & 1][r], s[(k / TN) & 1], to[r]);
+      for (int h = 0; h < 2; ++h) {
+        pf4 sbn[2];
+        if constexpr (BROWS == 1) {
+          const uint32_t p = base + at_s + ss * kStageS + BM * 4 + (wn * 64 + k % TN * 32 + h * 16 + half * 8) * 4;
+          sbn[0] = *(lds_pf4*)p;
+          sbn[1] = *(lds_pf4*)(p + 16);
+        }
+#pragma unroll
+        for (int r = 8 * h; r < 8 * h + 8; ++r)
+          to[r] = fmaf(BROWS == 1 ? d[k & 1][r] * sbn[(r - 8 * h) / 4][r % 4] : d[k & 1][r], s[(k / TN) & 1], to[r]);
+      }
       asm volatile("" : "+v"(to));   // (here, not at the end of the block)
     };
-    auto scales_b = [&](int s4, int k, int h, pf4* sbn) {
-      if constexpr (BROWS == 1) {
-        const uint32_t p = base + at_s + s4 * kStageS + BM * 4 + (wn * 64 + k % TN * 32 + h * 16 + half * 8) * 4;
-        sbn[0] = *(lds_pf4*)p;
-        sbn[1] = *(lds_pf4*)(p + 16);
-      }
-    };
-    for (int c = t.c; c < t.c1; ++c) {
-      const int nx = cur ^ 1, nx4 = (cur4 + 1) & 3;
-      const bool last = c + 1 == t.c1;
-      const int n_next = last && id + step < end ? place_of(id + step).n0 : t.n0;
+    for (int c = 0; c < g.blocks; ++c) {
+      const int nx = cur ^ 1, nx_s = (cur_s + 1) & 3;
+      const int n_next = c + 1 == g.blocks && id + step < end ? place_of(id + step).n0 : t.n0;
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
-        if (i == TM - 1) {
-          // All of this wave's reads of the stage (but scales) are done, and its part of the next one has arrived: behind the barrier that
-          // holds for every wave, so the next block's fragments can be read and this stage filled again.  (Behind the last
-          // block what is copied and read is not used.)
-          wait_lds();
-          if (stored) wait_memory<kStores>();   // (results on their way out were given to memory behind those copies)
-          else wait_memory();
-          stored = false;
-          barrier();
-        }
-        {
-          const int to = (i + 1) % kSlotsA, from = i == TM - 1 ? nx : cur, row = i == TM - 1 ? 0 : i + 1;
+        if (i + 1 < TM) {
+          const int to = (i + 1) % kSlotsA;
 #pragma unroll
-          for (int kh = 0; kh < 2; ++kh) af[to][kh] = read_a(from, row, kh);
-          sa[to] = *(lds_f32*)(at_scale + (i == TM - 1 ? nx4 : cur4) * kStageS + row * 128);
+          for (int kh = 0; kh < 2; ++kh) af[to][kh] = read_a(cur, i + 1, kh);
+          sa[to] = *(lds_f32*)(at_scale + cur_s * kStageS + (i + 1) * 128);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
           const int k = i * TN + j;
+          // A product's two instructions, then the sums of the one before it: as many instructions lie between a result and its
+          // use as the matrix cores need, and they work on this product meanwhile.
 #pragma unroll
           for (int kh = 0; kh < 2; ++kh) {
             Frag<WIDE> fa;
             fa.set(af[i % kSlotsA][kh]);
             d[k & 1] = mfma_half(bf[j][kh], fa, kh ? d[k & 1] : v16f{});
-            pf4 sbn[2];
-            // (the block's last product goes into the sums in the next one)
-            if (k > 0) {
-              scales_b(cur4, k - 1, kh, sbn);
-              add(k - 1, kh, sbn);
-            } else if (BROWS != 1 || c > t.c) {
-              scales_b((cur4 + 3) & 3, TM * TN - 1, kh, sbn);
-              add(TM * TN - 1, kh, sbn);
-            }
-            // Before results are stored all copies of a block are given out: they are waited for without those.
-            const int at = 2 * k + kh;
-            if (at < kSteps - kFree - 1) {
-              if (!ahead)
-#pragma unroll
-                for (int e = kEarly + kPer * at; e < min(kEarly + kPer * (at + 1), kCopies); ++e) copy(nx, nx4, e);
-            } else if (at == kSteps - kFree - 1) {
-              advance();
-            } else {
-              const int u = at - (kSteps - kFree);
-#pragma unroll
-              for (int e = kPer * u; e < min(kPer * (u + 1), kEarly); ++e) copy(cur, (cur4 + 2) & 3, e);
-              if (u == kFree - 1) {
-                ahead = last;
-                if (last)
-#pragma unroll
-                  for (int e = kEarly; e < kCopies; ++e) copy(cur, (cur4 + 2) & 3, e);
-              }
-            }
-            __builtin_amdgcn_sched_barrier(0);
           }
+          __builtin_amdgcn_sched_barrier(0);
+          if (i == TM - 1 && j == 0) {
+            // All of this wave's reads of the stage (but scales) are done, and its part of the next one has arrived: behind the
+            // barrier that holds for every wave, so the next block's fragments can be read and this stage filled again.
+            // (Behind the last block what is copied and read is not used.)
+            wait_lds();
+            if (stored) wait_memory<kStores>();   // (results on their way out were given to memory behind those copies)
+            else wait_memory();
+            stored = false;
+            barrier();
+#pragma unroll
+            for (int kh = 0; kh < 2; ++kh) af[0][kh] = read_a(nx, 0, kh);
+            sa[0] = *(lds_f32*)(at_scale + nx_s * kStageS);
+          }
+          if (i == TM - 1) {
+#pragma unroll
+            for (int e = kPer * j; e < kPer * (j + 1); ++e) copy(cur, (cur_s + 2) & 3, e);
+            if (j == TN - 1) {
+              ahead = c + 1 == g.blocks;   // (before results are stored all of them: they are waited for without those)
+              if (ahead)
+#pragma unroll
+                for (int e = kEarly; e < kCopies; ++e) copy(cur, (cur_s + 2) & 3, e);
+            }
+          } else if (kEarly + kPer * k < kCopies) {
+            if (!ahead)
+#pragma unroll
+              for (int e = kEarly + kPer * k; e < min(kEarly + kPer * (k + 1), kCopies); ++e) copy(nx, nx_s, e);
+          }
+          if (k == TN * (TM - 1) - 1) advance();
+          // (the block's last product goes into the sums in the next one)
+          if (k > 0) add(k - 1, cur_s);
+          else if (BROWS != 1 || c > 0) add(TM * TN - 1, (cur_s + 3) & 3);
           if (j == 0) s[i & 1] = sa[i % kSlotsA] * sb;
           if (i == TM - 1) {
 #pragma unroll
             for (int kh = 0; kh < 2; ++kh) bf[j][kh].set(read_b(nx, j, kh));
           }
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
-      if constexpr (BROWS != 1) sb = *(lds_f32*)(base + at_s + nx4 * kStageS + BM * 4 + (n_next % 128 + wn * 64) / 128 * 4);
+      if constexpr (BROWS != 1) sb = *(lds_f32*)(base + at_s + nx_s * kStageS + BM * 4 + (n_next % 128 + wn * 64) / 128 * 4);
       cur = nx;
-      cur4 = nx4;
+      cur_s = nx_s;
     }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      pf4 sbn[2];
-      scales_b((cur4 + 3) & 3, TM * TN - 1, h, sbn);
-      add(TM * TN - 1, h, sbn);
-    }
-    TO* out = g.splits > 1 ? reinterpret_cast<TO*>(g.part + int64_t(t.piece) * g.m * g.n) : static_cast<TO*>(g.out);
-    const int64_t os = g.splits > 1 ? g.n : g.os;
+    add(TM * TN - 1, (cur_s + 3) & 3);
+    TO* out = static_cast<TO*>(g.out);
     const int col = t.n0 + wn * 64 + half * 8;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -416,7 +386,7 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
           for (int h = 0; h < 2; ++h) {
             const v16f& v = acc[i][j];
             const int e = col + 32 * j + 16 * h;
-            store8<TO>(out + row * os + e, pf4{v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]},
+            store8<TO>(out + row * g.os + e, pf4{v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]},
                        pf4{v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]}, g.n - e);
           }
     }
@@ -430,7 +400,7 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
 
 // The tiles of a product.  HALVES: those of the last turn are cut in two, so that as many workgroups again have work in it.
 template <int TM, int WM, int WN, int BROWS, bool WIDE, bool HALVES, typename TO>
-__global__ void __launch_bounds__(64 * WM * WN) matmul_tile_kernel(MatmulArgs g) {
+__global__ void __launch_bounds__(64 * WM * WN, 2) matmul_tile_kernel(MatmulArgs g) {
   __shared__ __align__(1024) uint8_t lds[kTileLds<TM, WM, WN, BROWS>];
   matmul_tiles<TM, WM, WN, BROWS, WIDE, 1, TO>(g, lds, 0, g.whole);
   if constexpr (HALVES) {
@@ -452,12 +422,12 @@ __global__ void __launch_bounds__(64 * W) matmul_few_kernel(MatmulArgs g) {
   __shared__ __align__(1024) uint8_t lds[W * (kStage > kPart ? kStage : kPart)];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, kg = lane >> 4;
-  const int n0 = blockIdx.x * 16 * NT;
-  const int rows_n = min(16 * NT, g.n - n0);
+  const int m0 = static_cast<int>(blockIdx.x) % g.tiles_m * 16 * MT, n0 = static_cast<int>(blockIdx.x) / g.tiles_m * 16 * NT;
+  const int rows_m = min(16 * MT, g.m - m0), rows_n = min(16 * NT, g.n - n0);
   const uint32_t as = static_cast<uint32_t>(g.as), bs = static_cast<uint32_t>(g.bs);
-  const auto ra = bytes_rsrc(g.a, static_cast<uint32_t>(g.m - 1) * as + g.k);
+  const auto ra = bytes_rsrc(g.a + m0 * g.as, static_cast<uint32_t>(rows_m - 1) * as + g.k);
   const auto rb = bytes_rsrc(g.b + n0 * g.bs, static_cast<uint32_t>(rows_n - 1) * bs + g.k);
-  const auto rsa = make_rsrc(g.sa, (g.m - 1) * g.sas + g.blocks);
+  const auto rsa = make_rsrc(g.sa + m0 * g.sas, (rows_m - 1) * g.sas + g.blocks);
   const auto rsb = make_rsrc(g.sb + n0 / BROWS * g.sbs, BROWS == 1 ? (rows_n - 1) * g.sbs + g.blocks : g.blocks);
   uint8_t* stage = lds + wave * kStage;          // rows of b, then of a
   constexpr int kSa = (MT + 3) / 4;
@@ -533,69 +503,48 @@ __global__ void __launch_bounds__(64 * W) matmul_few_kernel(MatmulArgs g) {
     pf4 sum = part[t * 64 + lane];
 #pragma unroll
     for (int w = 1; w < W; ++w) sum += part[(w * MT * NT + t) * 64 + lane];
-    const int row = t / NT * 16 + r16, col = n0 + t % NT * 16 + kg * 4;
+    const int row = m0 + t / NT * 16 + r16, col = n0 + t % NT * 16 + kg * 4;
     if (row < g.m) store4<TO>(static_cast<TO*>(g.out) + row * g.os + col, sum, g.n - col);
   }
 }
 
-// out: the sums of the pieces of k, in their order
-template <typename TO>
-__global__ void __launch_bounds__(256) matmul_join_kernel(MatmulArgs g) {
-  const int64_t quads = (int64_t(g.n) + 3) / 4, id = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  if (id >= quads * g.m) return;
-  const int64_t row = id / quads;
-  const int col = static_cast<int>(id % quads) * 4, cnt = min(4, g.n - col);
-  pf4 sum = {};
-  for (int s = 0; s < g.splits; ++s) {
-    const float* p = g.part + (int64_t(s) * g.m + row) * g.n + col;
-    if (cnt == 4) sum += *reinterpret_cast<const pf4u*>(p);
-    else
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
-        if (i < cnt) sum[i] += p[i];
-  }
-  store4<TO>(static_cast<TO*>(g.out) + row * g.os + col, sum, cnt);
-}
-
-constexpr int kFew = 128;             // rows of a
-
 struct MatmulPlan {
   bool few;
-  int bm, bn, slots, splits, per;    // slots: workgroups that run at a time
+  int bm, bn, slots;    // slots: workgroups that run at a time
 };
 
 MatmulPlan plan_of(const ssm_matmul_fp8_params* p) {
   const bool narrow = p->b_rows == kBlock && p->out_dtype == SSM_BF16;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((p->m + bm - 1) / bm) * ((p->n + bn - 1) / bn); };
-  if (p->m <= kFew && p->splits <= 1) return {true, kFew, 16, 0, 1, 0};
-  MatmulPlan t{false, 128, 256, 256, 1, 0};
+  // Fewer tiles than would keep the CUs busy: workgroups that share a tile's k among their waves (512 x 2560 x 2560, 80 tiles:
+  // 18 us; 256 x 10576 x 2560, 166 tiles: 31 us, and 21 in tiles).
+  if (p->m <= 64 || tiles(128, 128) < 160) return {true, 64, 64, 0};
+  // Tiles of 128 x 128, two workgroups to a CU, which wait for their own copies only.  Where a lane has one scale of b for all
+  // of its results and the products are 8-bit, the sums of 256 x 256 or 192 x 256 fit the registers of one, and large products
+  // are faster so: what the turns of all workgroups take is counted in hundredths of one of 256 x 256 tiles, with the last of
+  // those in halves where they fit.  (A turn at k = 8192: 256 rows 125 to 129 us, 192 rows 98 to 112, 128 rows 90, 512 tiles of
+  // 128 x 128 82 to 85.  2800 x 2560 x 2560 takes 39, 35 and 29 us in tiles of 256, 192 and 128 rows, 3600 x 2560 x 2560 39, 36
+  // and 42.  With a scale for each row of b 10576 x 2560 x 8192 takes 347 us in tiles of 128 x 128 and 407 in tiles of
+  // 128 x 256, as fp32 503 and 571.)
+  MatmulPlan t{false, 128, 128, 512};
   if (narrow) {
-    // Turns of 256 workgroups, in hundredths of one of 256 x 256 tiles: the last of those in halves where they fit, or all
-    // of 192 x 256.  (A turn at k = 8192: 256 rows 125 to 129 us, 192 rows 98 to 112, 128 rows 90.)
-    const int64_t whole = tiles(256, 256), last = whole % 256, low = tiles(192, 256);
+    const int64_t whole = tiles(256, 256), last = whole % 256, small = tiles(128, 128), rest = small % 512;
     const int64_t cost = whole / 256 * 100 + (last == 0 ? 0 : whole > 256 && last <= 128 ? 70 : 100);
-    t.bm = (low + 255) / 256 * 80 < cost ? 192 : 256;
+    const int64_t low = (tiles(192, 256) + 255) / 256 * 80;
+    const int64_t least = small / 512 * 68 + (rest == 0 ? 0 : rest <= 256 ? 45 : 68);
+    if (least > (low < cost ? low : cost)) t = {false, low < cost ? 192 : 256, 256, 256};
   }
-  if (tiles(t.bm, t.bn) < 160) t.bn = t.bm = 128, t.slots = 512;
-  const int64_t blocks = blocks_of(p->k), all = tiles(t.bm, t.bn);
-  int64_t s = p->splits > 0 ? p->splits : all >= 128 ? 1 : t.slots / all;
-  if (p->splits == 0 && s > blocks / 4) s = blocks / 4;
-  if (p->splits == 0 && s > 16) s = 16;
-  s = s < 1 ? 1 : s > blocks ? blocks : s;
-  t.per = static_cast<int>((blocks + s - 1) / s);
-  t.splits = static_cast<int>((blocks + t.per - 1) / t.per);
   return t;
 }
 
 ssm_status check_matmul(const ssm_matmul_fp8_params* p) {
   if (!p) return fail(SSM_ERR_NULL, "params is NULL");
-  if (p->reserved != 0) return fail(SSM_ERR_UNSUPPORTED, "reserved must be 0");
+  if (p->reserved[0] != 0 || p->reserved[1] != 0) return fail(SSM_ERR_UNSUPPORTED, "reserved must be 0");
   if (p->m < 1 || p->n < 1 || p->k < 1) return fail(SSM_ERR_SHAPE, "m, n and k must be >= 1");
   if (p->m >= (int64_t(1) << 30) || p->n >= (int64_t(1) << 30)) return fail(SSM_ERR_SHAPE, "m and n must be below 2^30");
   if (p->k % 16) return fail(SSM_ERR_SHAPE, "k (%lld) must be a multiple of 16", (long long)p->k);
   if (p->b_rows != 1 && p->b_rows != kBlock) return fail(SSM_ERR_UNSUPPORTED, "b_rows must be 1 or %d", kBlock);
   if (p->out_dtype != SSM_F32 && p->out_dtype != SSM_BF16) return fail(SSM_ERR_DTYPE, "unknown out_dtype %d", p->out_dtype);
-  if (p->splits < 0 || p->splits > 64) return fail(SSM_ERR_UNSUPPORTED, "splits must be 0 to 64");
   const int64_t blocks = blocks_of(p->k);
   const struct { int64_t stride, row, most; } rows[] = {{p->a_stride, p->k, 1 << 23}, {p->b_stride, p->k, 1 << 23},
                                                         {p->a_scale_stride, blocks, 1 << 20}, {p->b_scale_stride, blocks, 1 << 20},
@@ -605,9 +554,8 @@ ssm_status check_matmul(const ssm_matmul_fp8_params* p) {
     if (r.stride != 0 && (r.stride < r.row || r.stride >= r.most))
       return fail(SSM_ERR_SHAPE, "a row stride of %lld: at least a row of %lld, below %lld", (long long)r.stride,
                   (long long)r.row, (long long)r.most);
-  const MatmulPlan t = plan_of(p);
-  const int64_t tiles = ((p->m + t.bm - 1) / t.bm) * ((p->n + t.bn - 1) / t.bn);
-  if (!fits_launch(tiles * t.splits, 512) || !fits_launch(p->m * ((p->n + 3) / 4) / 256 + 1, 256))
+  // (the numbers of tiles are 32-bit; the workgroups that share a tile's k have 16 columns at least)
+  if (((p->m + 127) / 128) * ((p->n + 127) / 128) >= (int64_t(1) << 30) || !fits_launch((p->n + 15) / 16, 512))
     return fail(SSM_ERR_SHAPE, "a product of %lld x %lld does not fit a launch", (long long)p->m, (long long)p->n);
   return SSM_OK;
 }
@@ -622,31 +570,32 @@ void launch_tile(MatmulArgs g, int64_t items, int slots, hipStream_t st) {
 }
 
 template <int MT, int NT, int W, bool WIDE, typename TO>
-void launch_few(const MatmulArgs& g, int brows, hipStream_t st) {
-  const dim3 grid((g.n + 16 * NT - 1) / (16 * NT)), block(64 * W);
+void launch_few(MatmulArgs g, int brows, hipStream_t st) {
+  g.tiles_m = (g.m + 16 * MT - 1) / (16 * MT);
+  const dim3 grid(g.tiles_m * ((g.n + 16 * NT - 1) / (16 * NT))), block(64 * W);
   if (brows == 1) hipLaunchKernelGGL((matmul_few_kernel<MT, NT, W, 1, WIDE, TO>), grid, block, 0, st, g);
   else hipLaunchKernelGGL((matmul_few_kernel<MT, NT, W, kBlock, WIDE, TO>), grid, block, 0, st, g);
 }
 
 // More rows of b to a workgroup read a less often, fewer make more workgroups (NT = 4 and 1, k = 2560 and 5120: 64 rows of a
-// 11.7 and 15.3 us at n = 10576, 13.0 and 8.9 us at 2560; 32 rows 9.6 and 11.1, 9.8 and 6.3).
+// 11.7 and 15.3 us at n = 10576, 13.0 and 8.9 us at 2560; 32 rows 9.6 and 11.1, 9.8 and 6.3; NT = 4 and 2: 128 rows 21.3 and
+// 22.1, 13.5 and 10.9; 256 rows 31.4 and 38.9, 15.7 and 20.9).
 template <bool WIDE, typename TO>
 void launch_few_rows(const MatmulArgs& g, int brows, hipStream_t st) {
   const bool many = g.n > 8192;
   if (g.m <= 16) launch_few<1, 1, 8, WIDE, TO>(g, brows, st);
   else if (g.m <= 32) many ? launch_few<2, 4, 8, WIDE, TO>(g, brows, st) : launch_few<2, 1, 8, WIDE, TO>(g, brows, st);
-  else if (g.m <= 64) many ? launch_few<4, 4, 8, WIDE, TO>(g, brows, st) : launch_few<4, 1, 8, WIDE, TO>(g, brows, st);
-  else many ? launch_few<8, 2, 4, WIDE, TO>(g, brows, st) : launch_few<8, 1, 8, WIDE, TO>(g, brows, st);
+  else if (g.m <= 64 && !many) launch_few<4, 1, 8, WIDE, TO>(g, brows, st);
+  else if (g.m <= 128 && !many) launch_few<4, 2, 8, WIDE, TO>(g, brows, st);
+  else launch_few<4, 4, 8, WIDE, TO>(g, brows, st);
 }
 
 template <bool WIDE, typename TO>
 void launch_tiles(const MatmulArgs& g, const MatmulPlan& t, int brows, int64_t items, hipStream_t st) {
   if (brows == 1) {
-    if (t.bn == 256) launch_tile<2, 2, 4, 1, WIDE, false, TO>(g, items, t.slots, st);
-    else launch_tile<2, 2, 2, 1, WIDE, false, TO>(g, items, t.slots, st);
+    launch_tile<2, 2, 2, 1, WIDE, false, TO>(g, items, t.slots, st);
   } else if (t.bm == 128) {
-    if (t.bn == 256) launch_tile<2, 2, 4, kBlock, WIDE, false, TO>(g, items, t.slots, st);
-    else launch_tile<2, 2, 2, kBlock, WIDE, false, TO>(g, items, t.slots, st);
+    launch_tile<2, 2, 2, kBlock, WIDE, false, TO>(g, items, t.slots, st);
   } else if constexpr (!WIDE) {
     if (t.bm == 192) launch_tile<3, 2, 4, kBlock, false, false, TO>(g, items, t.slots, st);
     else launch_tile<4, 2, 4, kBlock, false, true, TO>(g, items, t.slots, st);
@@ -658,15 +607,8 @@ void launch_tiles(const MatmulArgs& g, const MatmulPlan& t, int brows, int64_t i
 
 using namespace ssm57;
 
-extern "C" size_t ssm_matmul_fp8_workspace_bytes(const ssm_matmul_fp8_params* p) {
-  if (check_matmul(p) != SSM_OK) return 0;
-  const MatmulPlan t = plan_of(p);
-  return t.splits > 1 ? size_t(t.splits) * p->m * p->n * 4 : 0;
-}
-
 extern "C" ssm_status ssm_matmul_fp8(const ssm_matmul_fp8_params* p, const void* a, const float* a_scale, const void* b,
-                                     const float* b_scale, void* out, void* workspace, size_t workspace_bytes,
-                                     void* stream) {
+                                     const float* b_scale, void* out, void* stream) {
   g_err[0] = 0;
   if (ssm_status s = check_matmul(p); s != SSM_OK) return s;
   if (!a || !a_scale || !b || !b_scale || !out) return fail(SSM_ERR_NULL, "a, a_scale, b, b_scale and out are required");
@@ -675,16 +617,12 @@ extern "C" ssm_status ssm_matmul_fp8(const ssm_matmul_fp8_params* p, const void*
   if (!aligned(a, 16) || !aligned(b, 16) || p->a_stride % 16 || p->b_stride % 16)
     return fail(SSM_ERR_ALIGN, "rows of a and b must be 16-byte aligned");
   const MatmulPlan t = plan_of(p);
-  const size_t need = t.splits > 1 ? size_t(t.splits) * p->m * p->n * 4 : 0;
-  if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
-    return fail(SSM_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu at %p", need, workspace_bytes, workspace);
   MatmulArgs g{};
   g.a = static_cast<const uint8_t*>(a);
   g.b = static_cast<const uint8_t*>(b);
   g.sa = a_scale;
   g.sb = b_scale;
   g.out = out;
-  g.part = static_cast<float*>(workspace);
   g.m = static_cast<int>(p->m);
   g.n = static_cast<int>(p->n);
   g.k = static_cast<int>(p->k);
@@ -694,23 +632,14 @@ extern "C" ssm_status ssm_matmul_fp8(const ssm_matmul_fp8_params* p, const void*
   g.os = p->out_stride ? p->out_stride : p->n;
   g.sas = p->a_scale_stride ? p->a_scale_stride : g.blocks;
   g.sbs = p->b_scale_stride ? p->b_scale_stride : g.blocks;
-  g.splits = t.splits;
-  g.per = t.per;
   g.tiles_m = (g.m + t.bm - 1) / t.bm;
   g.tiles_n = (g.n + t.bn - 1) / t.bn;
   const int64_t tiles = int64_t(g.tiles_m) * g.tiles_n;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  const int64_t items = tiles * g.splits;
   if (t.few && p->out_dtype == SSM_F32) launch_few_rows<true, float>(g, p->b_rows, st);
   else if (t.few) launch_few_rows<false, uint16_t>(g, p->b_rows, st);
-  else if (p->out_dtype == SSM_F32) launch_tiles<true, float>(g, t, p->b_rows, items, st);
-  else if (g.splits > 1) launch_tiles<false, float>(g, t, p->b_rows, items, st);
-  else launch_tiles<false, uint16_t>(g, t, p->b_rows, items, st);
-  if (g.splits > 1) {
-    const dim3 grid(static_cast<uint32_t>((int64_t(g.m) * ((g.n + 3) / 4) + 255) / 256));
-    if (p->out_dtype == SSM_F32) hipLaunchKernelGGL((matmul_join_kernel<float>), grid, dim3(256), 0, st, g);
-    else hipLaunchKernelGGL((matmul_join_kernel<uint16_t>), grid, dim3(256), 0, st, g);
-  }
+  else if (p->out_dtype == SSM_F32) launch_tiles<true, float>(g, t, p->b_rows, tiles, st);
+  else launch_tiles<false, uint16_t>(g, t, p->b_rows, tiles, st);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SSM_OK : fail(SSM_ERR_HIP, "matmul launch: %s", hipGetErrorString(e));
 }

@@ -228,11 +228,12 @@ def quantize_fp8_blocks(w, *, rows=True, columns=False, q=None, scale=None, qt=N
 # ---------------------------------------------------------------------------------------------------------------
 # product
 
-def matmul_fp8(a, a_scale, b, b_scale, *, out_dtype=None, out=None, splits=0, workspace=None, stream=None):
+def matmul_fp8(a, a_scale, b, b_scale, *, out_dtype=None, out=None, stream=None):
     """Matrix product of 8-bit operands: out (M, N) = a b^T for a (M, K), b (N, K) float8_e4m3fn, K a multiple of 16, with
     a_scale (M, ceil(K / 128)) and b_scale (ceil(N / 128), ceil(K / 128)), or (N, ceil(K / 128)) with a scale for each row,
-    float32.  out is bfloat16 (default) or float32; sums are fp32, rounded once.  splits: pieces of K that are summed apart
-    (0: the library's choice; results agree within rounding).  The product of two scales has to be finite in fp32."""
+    float32.  out is bfloat16 (default) or float32, rounded once; the product of two scales has to be finite in fp32.
+    float32 results are sums in fp32.  For bfloat16 ones the matrix cores drop what lies below about 2^-12 of the largest
+    product of a block (1e-5 to 5e-5 of the result, whose rounding is 1.7e-3)."""
     import torch
     M, K = a.shape
     dev = _on_gpu(a, "a")
@@ -259,15 +260,9 @@ def matmul_fp8(a, a_scale, b, b_scale, *, out_dtype=None, out=None, splits=0, wo
     os_ = _rows("out", out, (M, N), out_dtype, dev, optional=True)
     if out is not None:
         _apart(out, "out", ("a", a), ("a_scale", a_scale), ("b", b), ("b_scale", b_scale))
-    with _launch(dev, stream, a, a_scale, b, b_scale, out, workspace) as st:
+    with _launch(dev, stream, a, a_scale, b, b_scale, out) as st:
         if out is None:
             out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        p = _abi.MatmulFp8Params(M, N, K, sa, sb, os_, sas, sbs, b_rows, _abi.SSM_F32 if out_dtype == f32 else _abi.SSM_BF16,
-                                 int(splits), 0)
-        if workspace is None:
-            need = int(_abi.lib().ssm_matmul_fp8_workspace_bytes(ctypes.byref(p)))
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        _abi.check(_abi.lib().ssm_matmul_fp8(ctypes.byref(p), _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(out),
-                                             _ptr(workspace), _space(workspace, dev), st))
+        p = _abi.MatmulFp8Params(M, N, K, sa, sb, os_, sas, sbs, b_rows, _abi.SSM_F32 if out_dtype == f32 else _abi.SSM_BF16)
+        _abi.check(_abi.lib().ssm_matmul_fp8(ctypes.byref(p), _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(out), st))
     return out

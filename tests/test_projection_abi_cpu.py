@@ -39,7 +39,7 @@ ENTRIES = {
     "ssm_add_norm_fwd": (norm_params, "x residual weight residual_out y y_scale", "x weight y", False),
     "ssm_add_norm_bwd": (norm_params, "h weight dy dh dx dresidual dweight", "h weight dy dresidual dweight", True),
     "ssm_quantize_fp8": (quant_params, "x q scale qt scale_t", "x q scale", False),
-    "ssm_matmul_fp8": (matmul_params, "a a_scale b b_scale out", "a a_scale b b_scale out", True),
+    "ssm_matmul_fp8": (matmul_params, "a a_scale b b_scale out", "a a_scale b b_scale out", False),
 }
 
 
@@ -73,8 +73,8 @@ BAD = {
     "ssm_matmul_fp8": [(dict(m=0), SHAPE), (dict(n=0), SHAPE), (dict(k=0), SHAPE), (dict(k=24), SHAPE), (dict(m=1 << 30), SHAPE),
                        (dict(n=1 << 30), SHAPE), (dict(k=1 << 23), SHAPE), (dict(a_stride=240), SHAPE), (dict(b_stride=1 << 23), SHAPE),
                        (dict(out_stride=199), SHAPE), (dict(a_scale_stride=1), SHAPE), (dict(b_scale_stride=1 << 20), SHAPE),
-                       (dict(b_rows=2), UNSUPPORTED), (dict(out_dtype=2), DTYPE), (dict(splits=-1), UNSUPPORTED),
-                       (dict(splits=65), UNSUPPORTED), (dict(reserved=1), UNSUPPORTED), (dict(m=(1 << 30) - 1, n=1 << 20), SHAPE)],
+                       (dict(b_rows=2), UNSUPPORTED), (dict(out_dtype=2), DTYPE), (dict(reserved=(ctypes.c_int32 * 2)(0, 1)), UNSUPPORTED),
+                       (dict(m=(1 << 30) - 1, n=1 << 20), SHAPE), (dict(n=(1 << 30) - 1, m=1), SHAPE)],
 }
 BAD["ssm_add_norm_bwd"] = [(kw, code) for kw, code in BAD["ssm_add_norm_fwd"] if kw.get("y_dtype") != 0]
 
@@ -117,8 +117,7 @@ def test_scales_go_with_their_codes(lib):
     assert call(lib, "ssm_quantize_fp8", quant_params(), q=0, scale=0) == NULL
 
 
-@pytest.mark.parametrize("name,kw", [("ssm_add_norm_bwd", {}), ("ssm_add_norm_bwd", dict(ntokens=70000, dim=5120)),
-                                     ("ssm_matmul_fp8", dict(k=2560, splits=4))])
+@pytest.mark.parametrize("name,kw", [("ssm_add_norm_bwd", {}), ("ssm_add_norm_bwd", dict(ntokens=70000, dim=5120))])
 def test_workspace(lib, name, kw):
     p = ENTRIES[name][0](**kw)
     need = getattr(lib, name + "_workspace_bytes")(ctypes.byref(p))
@@ -127,12 +126,6 @@ def test_workspace(lib, name, kw):
     assert call(lib, name, p, ws=FAKE, ws_bytes=need - 1) == WORKSPACE
     assert call(lib, name, p, ws=0, ws_bytes=need) == WORKSPACE
     assert call(lib, name, p, ws=FAKE + 2, ws_bytes=need) == WORKSPACE
-
-
-def test_large_products_need_no_workspace(lib):
-    size = lib.ssm_matmul_fp8_workspace_bytes
-    assert size(ctypes.byref(matmul_params(m=1 << 20, n=1 << 16, k=2560))) == 0
-    assert size(ctypes.byref(matmul_params(splits=1))) == 0
 
 
 def test_python_forms_want_the_gpu():
