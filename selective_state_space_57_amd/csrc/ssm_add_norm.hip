@@ -231,19 +231,27 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) add_norm_bwd_kernel(A
   }
 }
 
-// dw: the partial sums of a channel, 16 interleaved runs, joined in a fixed order
-__global__ void __launch_bounds__(256) add_norm_reduce_kernel(AddNormArgs a) {
-  __shared__ float sum[16][17];
-  const int cl = threadIdx.x & 15, r = threadIdx.x >> 4;
-  const int c = blockIdx.x * 16 + cl;
+// dw: the partial sums of a channel, 32 interleaved runs of them (eight loads at once), joined in a fixed order
+__global__ void __launch_bounds__(1024) add_norm_reduce_kernel(AddNormArgs a) {
+  __shared__ float sum[32][33];
+  const int cl = threadIdx.x & 31, r = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + cl;
   float v = 0.0f;
-  if (c < a.D)
-    for (int i = r; i < a.nb; i += 16) v += a.part[int64_t(i) * a.D + c];
+  if (c < a.D) {
+    for (int i = r; i < a.nb; i += 256) {
+      float t[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) t[u] = i + 32 * u < a.nb ? a.part[int64_t(i + 32 * u) * a.D + c] : 0.0f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v += t[u];
+    }
+  }
   sum[r][cl] = v;
   __syncthreads();
   if (r == 0 && c < a.D) {
     float t = 0.0f;
-    for (int i = 0; i < 16; ++i) t += sum[i][cl];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t += sum[i][cl];
     a.dw[c] = t;
   }
 }
@@ -287,7 +295,9 @@ AddNormShape shape_of(const ssm_add_norm_params* p, bool bwd) {
       break;
     }
   const int64_t waves = s.team < 256 ? 4 : s.team / 64;
-  int64_t nb = (bwd ? 2048 : 16384) / waves;
+  // 16 waves for each SIMD in the forward; in the backward, whose partial sums grow with the workgroups, two workgroups of
+  // four waves to a CU or one of 16 (8001 rows of 1001 23.4 us; twice as many 27.1; 2000 rows of 16384 112 us, half as many 143)
+  int64_t nb = bwd ? (s.team == 1024 ? 256 : 512) : 16384 / waves;
   const int64_t teams = s.team < 256 ? 256 / s.team : 1, rows = (p->ntokens + teams - 1) / teams;
   s.nb = static_cast<int>(nb > rows ? rows : nb);
   return s;
@@ -326,7 +336,7 @@ ssm_status dispatch_add_norm(const ssm_add_norm_params* p, AddNormArgs& a, hipSt
   else if (xb) go(uint16_t{}, float{});
   else if (rb) go(float{}, uint16_t{});
   else go(float{}, float{});
-  if constexpr (BWD) hipLaunchKernelGGL(add_norm_reduce_kernel, dim3((a.D + 15) / 16), dim3(256), 0, st, a);
+  if constexpr (BWD) hipLaunchKernelGGL(add_norm_reduce_kernel, dim3((a.D + 31) / 32), dim3(1024), 0, st, a);
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SSM_OK : fail(SSM_ERR_HIP, "add norm launch: %s", hipGetErrorString(e));
 }

@@ -32,9 +32,12 @@ struct MatmulArgs {
 };
 
 typedef float v16f __attribute__((ext_vector_type(16)));
-typedef __attribute__((address_space(3))) const v4i lds_v4i;
-typedef __attribute__((address_space(3))) const float lds_f32;
-typedef __attribute__((address_space(3))) const pf4 lds_pf4;
+
+// what lies at an address of LDS
+template <typename T>
+__device__ __forceinline__ T from_lds(uint32_t at) {
+  return *reinterpret_cast<__attribute__((address_space(3))) const T*>(static_cast<uintptr_t>(at));
+}
 
 __device__ __forceinline__ v8bf widen(int lo, int hi) {
   const pbf2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false), b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
@@ -252,11 +255,11 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
   int cur = 0, cur_s = 0;
   auto read_a = [&](int s, int i, int kh) {
     const uint32_t p = at_frag_a + s * kStageA;
-    return __builtin_shufflevector(*(lds_v4i*)((p ^ (kh * 64)) + i * 4096), *(lds_v4i*)((p ^ (kh * 64 + 16)) + i * 4096), 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_shufflevector(from_lds<v4i>((p ^ (kh * 64)) + i * 4096), from_lds<v4i>((p ^ (kh * 64 + 16)) + i * 4096), 0, 1, 2, 3, 4, 5, 6, 7);
   };
   auto read_b = [&](int s, int j, int kh) {
     const uint32_t p = at_frag_b + s * kStageB;
-    return __builtin_shufflevector(*(lds_v4i*)((p ^ (kh * 64)) + j * 4096), *(lds_v4i*)((p ^ (kh * 64 + 16)) + j * 4096), 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_shufflevector(from_lds<v4i>((p ^ (kh * 64)) + j * 4096), from_lds<v4i>((p ^ (kh * 64 + 16)) + j * 4096), 0, 1, 2, 3, 4, 5, 6, 7);
   };
 
   int id = lid;
@@ -281,8 +284,8 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
 #pragma unroll
     for (int j = 0; j < TN; ++j) bf[j][kh].set(read_b(0, j, kh));
   }
-  sa[0] = *(lds_f32*)(at_scale);
-  float sb = BROWS == 1 ? 1.0f : *(lds_f32*)(base + at_s + BM * 4 + (t.n0 % 128 + wn * 64) / 128 * 4);
+  sa[0] = from_lds<float>(at_scale);
+  float sb = BROWS == 1 ? 1.0f : from_lds<float>(base + at_s + BM * 4 + (t.n0 % 128 + wn * 64) / 128 * 4);
 
   while (true) {
     v16f acc[TM][TN] = {};
@@ -297,8 +300,8 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
         pf4 sbn[2];
         if constexpr (BROWS == 1) {
           const uint32_t p = base + at_s + ss * kStageS + BM * 4 + (wn * 64 + k % TN * 32 + h * 16 + half * 8) * 4;
-          sbn[0] = *(lds_pf4*)p;
-          sbn[1] = *(lds_pf4*)(p + 16);
+          sbn[0] = from_lds<pf4>(p);
+          sbn[1] = from_lds<pf4>(p + 16);
         }
 #pragma unroll
         for (int r = 8 * h; r < 8 * h + 8; ++r)
@@ -315,7 +318,7 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
           const int to = (i + 1) % kSlotsA;
 #pragma unroll
           for (int kh = 0; kh < 2; ++kh) af[to][kh] = read_a(cur, i + 1, kh);
-          sa[to] = *(lds_f32*)(at_scale + cur_s * kStageS + (i + 1) * 128);
+          sa[to] = from_lds<float>(at_scale + cur_s * kStageS + (i + 1) * 128);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -341,7 +344,7 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
             barrier();
 #pragma unroll
             for (int kh = 0; kh < 2; ++kh) af[0][kh] = read_a(nx, 0, kh);
-            sa[0] = *(lds_f32*)(at_scale + nx_s * kStageS);
+            sa[0] = from_lds<float>(at_scale + nx_s * kStageS);
           }
           if (i == TM - 1) {
 #pragma unroll
@@ -369,7 +372,7 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
           __builtin_amdgcn_sched_barrier(0);
         }
       }
-      if constexpr (BROWS != 1) sb = *(lds_f32*)(base + at_s + nx_s * kStageS + BM * 4 + (n_next % 128 + wn * 64) / 128 * 4);
+      if constexpr (BROWS != 1) sb = from_lds<float>(base + at_s + nx_s * kStageS + BM * 4 + (n_next % 128 + wn * 64) / 128 * 4);
       cur = nx;
       cur_s = nx_s;
     }

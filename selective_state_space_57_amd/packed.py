@@ -107,7 +107,8 @@ class _launch:
         if self.stream is None:
             if self.device.index != torch.cuda.current_device():
                 self._enter(torch.cuda.device(self.device))
-            return torch.cuda.current_stream(self.device).cuda_stream
+            # (the handle alone: torch.cuda.current_stream makes an object around it, 1.9 of a call's 10 us)
+            return torch._C._cuda_getCurrentRawStream(self.device.index)
         if self.stream.device != self.device:
             raise ValueError("stream: expected one of %s, got %s" % (self.device, self.stream.device))
         self._enter(torch.cuda.device(self.device))

@@ -170,7 +170,16 @@ def add_norm_bwd(h, weight, dy, dh=None, *, eps=1e-5, dx=None, dresidual=None, w
 # ---------------------------------------------------------------------------------------------------------------
 # quantisation
 
-def _quantize(x, square, rows, columns, out, stream):
+def _output(name, t, shape, dtype, dev, *ins):
+    """Checks an output that is given, which may not overlap ``ins``, and returns the stride between its rows."""
+    if t is None:
+        return 0
+    stride = _rows(name, t, shape, dtype, dev)
+    _apart(t, name, *ins)
+    return stride
+
+
+def _quantize(x, square, rows, columns, q, scale, qt, scale_t, stream):
     import torch
     T, D = x.shape
     dev = _on_gpu(x, "x")
@@ -178,51 +187,46 @@ def _quantize(x, square, rows, columns, out, stream):
     f8, f32 = torch.float8_e4m3fn, torch.float32
     if not rows and not columns:
         raise ValueError("rows or columns: at least one is required")
-    given = {k: v for k, v in out.items() if v is not None}
-    per, per_t = (_blocks(T), _blocks(D)) if square else (T, D)
-    shapes = {}
-    if rows:
-        shapes.update(q=((T, _up16(D)), f8), scale=((per, _blocks(D)), f32))
-    if columns:
-        shapes.update(qt=((D, _up16(T)), f8), scale_t=((per_t, _blocks(T)), f32))
-    for k in given:
-        if k not in shapes:
-            raise ValueError("%s: not an output of this call" % k)
+    if not rows and (q is not None or scale is not None):
+        raise ValueError("q and scale: no output of this call without rows")
+    if not columns and (qt is not None or scale_t is not None):
+        raise ValueError("qt and scale_t: no output of this call without columns")
+    tb, db = _blocks(T), _blocks(D)
+    of_rows, of_columns = ((tb, db), (db, tb)) if square else ((T, db), (D, tb))
     xs = _rows("x", x, (T, D), x.dtype, dev)
-    strides = dict.fromkeys(("q", "scale", "qt", "scale_t"), 0)
-    if given:
-        ins = [("x", x)]
-        for k, v in given.items():
-            strides[k] = _rows(k, v, shapes[k][0], shapes[k][1], dev)
-            _apart(v, k, *ins)
-            ins.append((k, v))
-    with _launch(dev, stream, x, *given.values()) as st:
-        o = {"q": None, "scale": None, "qt": None, "scale_t": None}
-        for k, (shape, dtype) in shapes.items():
-            if k in given:
-                o[k] = given[k]
-            elif dtype == f8:
-                o[k] = _codes(shape[0], shape[1], dev)
-                strides[k] = o[k].stride(0)
-            else:
-                o[k] = torch.empty(shape, dtype=dtype, device=dev)
-        p = _abi.QuantizeFp8Params(T, D, xs, strides["q"], strides["scale"], strides["qt"], strides["scale_t"], io, square)
-        _abi.check(_abi.lib().ssm_quantize_fp8(ctypes.byref(p), _ptr(x), _ptr(o["q"]), _ptr(o["scale"]), _ptr(o["qt"]),
-                                               _ptr(o["scale_t"]), st))
-    return o
+    qs = _output("q", q, (T, _up16(D)), f8, dev, ("x", x))
+    ss = _output("scale", scale, of_rows, f32, dev, ("x", x), ("q", q))
+    qts = _output("qt", qt, (D, _up16(T)), f8, dev, ("x", x), ("q", q), ("scale", scale))
+    sts = _output("scale_t", scale_t, of_columns, f32, dev, ("x", x), ("q", q), ("scale", scale), ("qt", qt))
+    with _launch(dev, stream, x, q, scale, qt, scale_t) as st:
+        if rows:
+            if q is None:
+                q = _codes(T, D, dev)
+                qs = q.stride(0)
+            if scale is None:
+                scale = torch.empty(of_rows, dtype=f32, device=dev)
+        if columns:
+            if qt is None:
+                qt = _codes(D, T, dev)
+                qts = qt.stride(0)
+            if scale_t is None:
+                scale_t = torch.empty(of_columns, dtype=f32, device=dev)
+        p = _abi.QuantizeFp8Params(T, D, xs, qs, ss, qts, sts, io, square)
+        _abi.check(_abi.lib().ssm_quantize_fp8(ctypes.byref(p), _ptr(x), _ptr(q), _ptr(scale), _ptr(qt), _ptr(scale_t), st))
+    return {"q": q, "scale": scale, "qt": qt, "scale_t": scale_t}
 
 
 def quantize_fp8(x, *, rows=True, columns=False, q=None, scale=None, qt=None, scale_t=None, stream=None):
     """x (T, D) float32 or bfloat16 to 8 bits with a scale for each block of 128 along the rows, the columns or both.
     Returns dict q (T, D rounded up to 16) and scale (T, ceil(D / 128)) with ``rows``, qt (D, T rounded up to 16), the codes
     of the transposed matrix, and scale_t (D, ceil(T / 128)) with ``columns``; the others are None.  Outputs may be given."""
-    return _quantize(x, 0, rows, columns, {"q": q, "scale": scale, "qt": qt, "scale_t": scale_t}, stream)
+    return _quantize(x, 0, rows, columns, q, scale, qt, scale_t, stream)
 
 
 def quantize_fp8_blocks(w, *, rows=True, columns=False, q=None, scale=None, qt=None, scale_t=None, stream=None):
     """w (N, K) float32 or bfloat16 to 8 bits with a scale for each block of 128 rows and 128 columns: the form of a
     weight.  Returns dict as quantize_fp8, with scale (ceil(N / 128), ceil(K / 128)) and scale_t its transposed."""
-    return _quantize(w, 1, rows, columns, {"q": q, "scale": scale, "qt": qt, "scale_t": scale_t}, stream)
+    return _quantize(w, 1, rows, columns, q, scale, qt, scale_t, stream)
 
 
 # ---------------------------------------------------------------------------------------------------------------
