@@ -502,7 +502,8 @@ ssm_status ssm_quantize_fp8(const ssm_quantize_fp8_params* p, const void* x, voi
 
 typedef struct {
   int64_t m, n, k;          /* rows of a, rows of b, length of both; k a multiple of 16 */
-  int64_t a_stride, b_stride, out_stride, a_scale_stride, b_scale_stride;   /* row strides; 0 = dense; a, b: below 2^23 */
+  int64_t a_stride, b_stride, out_stride;   /* row strides; 0 = dense; of a and b below 2^23 */
+  int64_t a_scale_stride, b_scale_stride;   /* below 2^20 */
   int32_t b_rows;           /* rows of b under one scale: 128 or 1 */
   int32_t out_dtype;        /* SSM_F32 or SSM_BF16 */
   int32_t reserved[2];      /* must be 0 */
@@ -511,8 +512,10 @@ typedef struct {
 /*
  * Matrix product of 8-bit operands: out[i][j] = sum over blocks c of a_scale[i][c] b_scale[j / b_rows][c] times the sum
  * over the block's k of a[i][k] b[j][k].  a [m][k], b [n][k] e4m3 (rows 16-byte aligned); a_scale [m][ceil(k / 128)],
- * b_scale [ceil(n / b_rows)][ceil(k / 128)] fp32; out [m][n] out_dtype.  Products and sums are fp32; out is rounded once.
- * The product of two scales has to be finite in fp32.  out must not overlap an input.  Deterministic.
+ * b_scale [ceil(n / b_rows)][ceil(k / 128)] fp32; out [m][n] out_dtype, rounded once.  The sums over blocks are fp32, and for
+ * an fp32 out those inside a block too; for a bf16 out the 8-bit matrix instructions drop what lies below about 2^-12 of the
+ * largest products of a block (1e-5 to 5e-5 of the result's 2-norm; the rounding to bf16 is 1.7e-3).  k below 2^23, n below
+ * 2^27.  The product of two scales has to be finite in fp32.  out must not overlap an input.  Deterministic.
  */
 ssm_status ssm_matmul_fp8(const ssm_matmul_fp8_params* p, const void* a, const float* a_scale, const void* b,
                           const float* b_scale, void* out, void* stream);

@@ -1,14 +1,28 @@
 // Matrix product of e4m3 operands with an fp32 scale for each block of 128 along k:
 //   out[i][j] = sum over blocks c of sa[i][c] sb[j / b_rows][c] (sum over the block's k of a[i][k] b[j][k])
 //
-// v_mfma_f32_16x16x128_f8f6f4 takes a whole block of 128 k at once: its result is the block's inner sum, which goes into
-// the fp32 sums times the two scales.  b is the first operand, so that a lane's four results are four neighbouring j of
-// one i: one scale of a for them all, and one store.
+// A block's inner sum is matrix instructions' work (two v_mfma_f32_32x32x64_f8f6f4 for 32 x 32 results in large products,
+// one v_mfma_f32_16x16x128_f8f6f4 for 16 x 16 where a has few rows); it goes into the fp32 sums times the two scales, one fma for
+// each result and block.  b is the first operand, so that a lane's results are of one row of a, with one scale of a for them all,
+// and neighbours in it, for wide stores.
 //
 // Inside, the 8-bit matrix instructions (of every shape) align their products to the largest of a group and drop what lies
 // below about 2^-12 of it: measured 1.4e-5 of the result's 2-norm for values of a normal distribution, 5e-5 for codes drawn
 // evenly.  A bf16 result, whose own rounding is 1.7e-3, is computed with them.  An fp32 result (a weight gradient) is not:
-// its codes become bf16, which holds them exactly, on the way into v_mfma_f32_16x16x32_bf16, which sums in fp32.
+// its codes become bf16, which holds them exactly, on the way into the bf16 matrix instructions, which sum in fp32 (1.5e-7).
+//
+// Large products are bound by the matrix cores, the fmas that apply the scales (a quarter of the vector unit's cycles: with
+// instructions of 16 x 16 x 128, whose results come twice as often for the same work, a loop without memory reached 3562 TF,
+// with these 4015) and, above all, by the copies into LDS that run beside them: 8192^3 takes 540 us, without the copies 440.
+// Measured, bf16 results and one scale for 128 rows of b: 16384 x 10576 x 2560 437 us (2030 TF; the matrix cores are busy 57 % of
+// the time; a library product with one scale for each whole tensor takes 392 to 470), 4099 x 2560 x 5120 58 us; rows of b with
+// scales of their own, fp32 results: 10576 x 2560 x 8191 470 us (945 TF), bound by the conversions and by two vector operations
+// for each result and block.  Few rows are bound by the reading of b: 1 row at 10576 x 2560 7.8 us (3.5 TB/s with the launch).
+//
+// Tried and not kept, for the large products: four waves of 128 x 128 results each (their sums move between register files:
+// 801 us at 8192^3), lines touched ahead of their copies (5 to 10 % slower), all of a stage's copies at once (3 % slower), raised
+// priority around the matrix instructions (15 % slower); for few tiles: three or four stages in LDS (256 x 10576 x 2560 20.1 to
+// 20.8 us for 21.5, on one workgroup to a CU), k split over workgroups with a join (512 x 2560 x 2560 24.9 us for 18.5).
 #include "fp8.hpp"
 
 namespace ssm57 {

@@ -4,8 +4,8 @@
 rows and columns (weights); a value stands for code times scale.  scale = max(largest magnitude of the block, 2^-100) / 448
 and the code is value / scale, rounded to nearest even.  Rows of 8-bit tensors that are made here have their length rounded
 up to a multiple of 16, with zeros behind the end, so that any of them can go into a product, and begin at a multiple of 128
-bytes where they are long.  A block that holds a NaN or
-an infinity makes every result of its row (its rows and columns) that it meets NaN.
+bytes where they are long.  A block that holds a NaN or an infinity makes every result of its row (its rows and columns) that
+it meets NaN.
 
 A projection y = x W^T and its gradients are
 
@@ -105,11 +105,12 @@ def add_norm_fwd(x, weight, residual=None, *, eps=1e-5, y_dtype=None, residual_d
     ss = _rows("y_scale", y_scale, (T, _blocks(D)), torch.float32, dev, optional=True)
     if residual_out is not None:
         ins = (("x", x), ("residual", residual))
-        _apart(residual_out, "residual_out", *ins, may_be=_alias(residual_out, *ins))
+        _apart(residual_out, "residual_out", ("weight", weight), *ins, may_be=_alias(residual_out, *ins))
     if y is not None:
-        _apart(y, "y", ("x", x), ("residual", residual), ("residual_out", residual_out), may_be=_alias(y, ("x", x)))
+        _apart(y, "y", ("x", x), ("weight", weight), ("residual", residual), ("residual_out", residual_out),
+               may_be=_alias(y, ("x", x)))
     if y_scale is not None:
-        _apart(y_scale, "y_scale", ("x", x), ("residual", residual), ("residual_out", residual_out), ("y", y))
+        _apart(y_scale, "y_scale", ("x", x), ("weight", weight), ("residual", residual), ("residual_out", residual_out), ("y", y))
     with _launch(dev, stream, x, weight, residual, y, y_scale, residual_out) as st:
         if y is None:
             y = _codes(T, D, dev) if eight else torch.empty((T, D), dtype=y_dtype, device=dev)
@@ -144,9 +145,11 @@ def add_norm_bwd(h, weight, dy, dh=None, *, eps=1e-5, dx=None, dresidual=None, w
     drs = _rows("dresidual", dresidual, (T, D), h.dtype, dev, optional=True)
     ins = (("h", h), ("dy", dy), ("dh", dh))
     if dx is not None:
-        _apart(dx, "dx", *ins, ("dresidual", dresidual), may_be=_alias(dx, *ins))
+        _apart(dx, "dx", *ins, ("weight", weight), ("dresidual", dresidual), may_be=_alias(dx, *ins))
     if dresidual is not None:
-        _apart(dresidual, "dresidual", *ins, may_be=_alias(dresidual, *ins))
+        _apart(dresidual, "dresidual", *ins, ("weight", weight), may_be=_alias(dresidual, *ins))
+    if workspace is not None:
+        _apart(workspace, "workspace", *ins, ("weight", weight), ("dx", dx), ("dresidual", dresidual))
     with _launch(dev, stream, h, weight, dy, dh, dx, dresidual, workspace) as st:
         one = io == rio and (dx is None or dresidual is None)
         if one:
@@ -249,8 +252,8 @@ def matmul_fp8(a, a_scale, b, b_scale, *, out_dtype=None, out=None, stream=None)
     sb = _rows("b", b, (N, K), f8, dev)
     kb = _blocks(K)
     sas = _rows("a_scale", a_scale, (M, kb), f32, dev)
-    if b_scale is None:
-        raise ValueError("b_scale is required")
+    if b_scale is None or b_scale.dim() != 2:
+        raise ValueError("b_scale: expected shape (%d, %d) or (%d, %d)" % (_blocks(N), kb, N, kb))
     b_rows = 1 if b_scale.shape[0] == N and N > 1 else BLOCK
     sbs = _rows("b_scale", b_scale, (N if b_rows == 1 else _blocks(N), kb), f32, dev)
     if out is not None:

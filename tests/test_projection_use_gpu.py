@@ -285,3 +285,33 @@ def test_refusals():
               lambda: qz(x, q=odd[:, :256])):
         with pytest.raises(E):
             f()
+
+
+def test_more_rows_than_a_launch():
+    """A row more than 2^23 workgroups of four rows: every one is quantised, the last like the first."""
+    rows = (1 << 25) + 3
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB")
+    x = torch.arange(rows, device="cuda", dtype=torch.float32)[:, None].remainder(1000).add(1.0) * torch.tensor(
+        [1.0, -0.5, 0.25], device="cuda")
+    all_, few = ssm().quantize_fp8(x), ssm().quantize_fp8(x[-1000:])
+    for name in ("q", "scale"):
+        assert torch.equal(all_[name][-1000:].view(torch.uint8), few[name].view(torch.uint8))
+    peak, scale = x[:, :1].double(), all_["scale"].double()
+    # (a quotient in 32 bits: half a step)
+    assert bool(((scale * 448 - peak).abs() <= 2.0 ** -24 * peak).all())
+    for c, code in enumerate((448.0, -224.0, 112.0)):
+        assert bool((all_["q"][:, c].float() == code).all())
+
+
+def test_refusals_of_shared_memory():
+    """Outputs and workspaces over the weight or another tensor of the call, and scales of a wrong number of axes."""
+    r = Rand(83)
+    x, w, dy = r(1, 256), r(256), r(1, 256)
+    n, g, mm = ssm().add_norm_fwd, ssm().add_norm_bwd, ssm().matmul_fp8
+    q, s, b = r.codes(6, 256), r.scales(6, 2), r.codes(300, 256)
+    for f in (lambda: n(x, w, y=w[None]), lambda: n(x, w, residual_out=w[None]), lambda: n(x, w, y_dtype=F8, y_scale=w[None, 2:4]),
+              lambda: g(x, w, dy, dx=w[None]), lambda: g(x, w, dy, dresidual=w[None]), lambda: g(x, w, dy, workspace=w),
+              lambda: g(x, w, dy, workspace=dy.view(torch.uint8)), lambda: mm(q, s, b, s[0]), lambda: mm(q, s, b, s[0, 0])):
+        with pytest.raises(ValueError):
+            f()
