@@ -428,27 +428,34 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) matmul_tile_kernel(MatmulArgs
   }
 }
 
-// Few rows of a: 16 MT of them at most, bound by the reading of b.  A workgroup has 16 NT rows of b; its W waves take the
-// blocks of k in turn, each with a stage of its own in LDS that it alone fills and reads, so that no wave waits for another,
-// and the waves' sums are joined in LDS in a fixed order.  (Read straight into registers, 16 rows and half a line of each to
-// an instruction, the operands took 1.2 to 1.9 times as long.)
+// Few rows of a, or few tiles: a workgroup has 16 MT rows of a and 16 NT of b and is bound by the reading of them.  Its W waves
+// take the blocks of k in turn, each with a stage of its own in LDS that it alone fills and reads, so that no wave waits for
+// another, and the waves' sums are joined in LDS in a fixed order.  (Read straight into registers, 16 rows and half a line of
+// each to an instruction, the operands took 1.05 to 1.8 times as long.)
 // v_mfma_f32_16x16x128_f8f6f4: a lane has 32 codes of row lane % 16 of a and of b, and the result's four neighbouring j.
 template <int MT, int NT, int W, int BROWS, bool WIDE, typename TO>
 __global__ void __launch_bounds__(64 * W) matmul_few_kernel(MatmulArgs g) {
   constexpr int kStage = (MT + NT) * 2048, kPart = MT * NT * 1024;
-  __shared__ __align__(1024) uint8_t lds[W * (kStage > kPart ? kStage : kPart)];
+  // sums that need more memory than the stages are joined in two steps
+  constexpr int kParts = kPart > kStage ? W / 2 : W;
+  static_assert(kParts * kPart <= W * kStage);
+  __shared__ __align__(1024) uint8_t lds[W * kStage];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, kg = lane >> 4;
-  const int m0 = static_cast<int>(blockIdx.x) % g.tiles_m * 16 * MT, n0 = static_cast<int>(blockIdx.x) / g.tiles_m * 16 * NT;
+  // (as in the tiles the workgroups that share rows of b are neighbours on one XCD: 512 x 2560 x 2560 11.8 us, and 15.9 without)
+  const int xcd = blockIdx.x & 7, id = xcd * (gridDim.x / 8) + min(xcd, static_cast<int>(gridDim.x % 8)) + (blockIdx.x >> 3);
+  const int m0 = id % g.tiles_m * 16 * MT, n0 = id / g.tiles_m * 16 * NT;
   const int rows_m = min(16 * MT, g.m - m0), rows_n = min(16 * NT, g.n - n0);
   const uint32_t as = static_cast<uint32_t>(g.as), bs = static_cast<uint32_t>(g.bs);
   const auto ra = bytes_rsrc(g.a + m0 * g.as, static_cast<uint32_t>(rows_m - 1) * as + g.k);
   const auto rb = bytes_rsrc(g.b + n0 * g.bs, static_cast<uint32_t>(rows_n - 1) * bs + g.k);
   const auto rsa = make_rsrc(g.sa + m0 * g.sas, (rows_m - 1) * g.sas + g.blocks);
-  const auto rsb = make_rsrc(g.sb + n0 / BROWS * g.sbs, BROWS == 1 ? (rows_n - 1) * g.sbs + g.blocks : g.blocks);
+  const auto rsb = make_rsrc(g.sb + n0 / BROWS * g.sbs, (BROWS == 1 ? rows_n - 1 : (n0 % 128 + rows_n - 1) / 128) * g.sbs + g.blocks);
   uint8_t* stage = lds + wave * kStage;          // rows of b, then of a
-  constexpr int kSa = (MT + 3) / 4;
-  float sa[kSa] = {}, sb = 0.0f;                 // of rows `lane`, `lane` + 64 of a; of row `lane` of b, or of its block
+  constexpr int kSa = (MT + 3) / 4, kSb = BROWS == 1 ? (NT + 3) / 4 : 1;
+  float sa[kSa] = {}, sb[kSb] = {};              // of rows `lane`, `lane` + 64 of a and of b; or of the block of 16 rows `lane` of b
+  const uint32_t at_sb = BROWS == 1 ? lane * static_cast<uint32_t>(g.sbs)
+                                    : (n0 % 128 + lane % NT * 16) / 128 * static_cast<uint32_t>(g.sbs);
   const int unit = (lane & 7) ^ (lane >> 4);     // as in the tiles; the second of two copies has it ^ 4
   auto load = [&](int c) {
     // (past the end of k, and behind the last row: zeros)
@@ -463,8 +470,10 @@ __global__ void __launch_bounds__(64 * W) matmul_few_kernel(MatmulArgs g) {
     for (int i = 0; i < kSa; ++i)
       sa[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
           rsa, static_cast<int>(4u * ((lane % (16 * MT) + 64 * i) * static_cast<uint32_t>(g.sas) + c)), 0, 0));
-    sb = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-        rsb, static_cast<int>(4u * ((BROWS == 1 ? (lane % (16 * NT)) * static_cast<uint32_t>(g.sbs) : 0u) + c)), 0, 0));
+#pragma unroll
+    for (int i = 0; i < kSb; ++i)
+      sb[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+          rsb, static_cast<int>(4u * (at_sb + 64 * i * static_cast<uint32_t>(g.sbs) + c)), 0, 0));
   };
   const uint8_t* frag = stage + r16 * 128 + (kg ^ (r16 >> 1)) * 16;
   auto read = [&](int f) {                       // (units kg and kg + 4 of a row)
@@ -485,16 +494,26 @@ __global__ void __launch_bounds__(64 * W) matmul_few_kernel(MatmulArgs g) {
     float sac[kSa];
 #pragma unroll
     for (int i = 0; i < kSa; ++i) sac[i] = sa[i];
-    const float sbc = sb;
+    float sbc[kSb];
+#pragma unroll
+    for (int i = 0; i < kSb; ++i) sbc[i] = sb[i];
     wait_lds();                                  // (the stage has been read)
     if (c + W < g.blocks) load(c + W);
     Frag<WIDE> fb[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) fb[j].set(vb[j]);
-    float sbn[BROWS == 1 ? 4 * NT : 1] = {sbc};
-    if constexpr (BROWS == 1) {
+    constexpr bool kOne = BROWS != 1 && 128 % (16 * NT) == 0;   // all rows of b here are under one scale
+    float sbn[kOne ? 1 : BROWS == 1 ? 4 * NT : NT] = {sbc[0]};
+    if constexpr (!kOne) {
 #pragma unroll
-      for (int q = 0; q < 4 * NT; ++q) sbn[q] = __shfl(sbc, q / 4 * 16 + kg * 4 + q % 4);
+      for (int j = 0; j < NT; ++j) {
+        if constexpr (BROWS == 1) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sbn[4 * j + r] = __shfl(sbc[j / 4], j % 4 * 16 + kg * 4 + r);
+        } else {
+          sbn[j] = __shfl(sbc[0], j);
+        }
+      }
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -505,37 +524,70 @@ __global__ void __launch_bounds__(64 * W) matmul_few_kernel(MatmulArgs g) {
       for (int j = 0; j < NT; ++j) {
         const pf4 d = mfma_block(fb[j], fa);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[r], s * sbn[BROWS == 1 ? 4 * j + r : 0], acc[i][j][r]);
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(d[r], s * sbn[kOne ? 0 : BROWS == 1 ? 4 * j + r : j], acc[i][j][r]);
       }
     }
   }
   __syncthreads();                               // (every stage has been read)
-  pf4* part = reinterpret_cast<pf4*>(lds);       // [W][MT NT][64]
+  pf4* part = reinterpret_cast<pf4*>(lds);       // [kParts][MT NT][64]
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int step = W / kParts - 1; step >= 0; --step) {
+    if (wave / kParts == step) {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) part[(wave * MT * NT + i * NT + j) * 64 + lane] = acc[i][j];
-  __syncthreads();
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          pf4& to = part[(wave % kParts * MT * NT + i * NT + j) * 64 + lane];
+          to = step + 1 < W / kParts ? acc[i][j] + to : acc[i][j];
+        }
+    }
+    __syncthreads();
+  }
   for (int t = wave; t < MT * NT; t += W) {
     pf4 sum = part[t * 64 + lane];
 #pragma unroll
-    for (int w = 1; w < W; ++w) sum += part[(w * MT * NT + t) * 64 + lane];
+    for (int w = 1; w < kParts; ++w) sum += part[(w * MT * NT + t) * 64 + lane];
     const int row = m0 + t / NT * 16 + r16, col = n0 + t % NT * 16 + kg * 4;
     if (row < g.m) store4<TO>(static_cast<TO*>(g.out) + row * g.os + col, sum, g.n - col);
   }
 }
 
 struct MatmulPlan {
-  bool few;
+  int few;              // fragments of 16 rows of b to a workgroup that shares k among its waves; 0: tiles
   int bm, bn, slots;    // slots: workgroups that run at a time
 };
+
+int few_rows(int64_t m) { return m <= 16 ? 1 : m <= 32 ? 2 : 4; }   // fragments of 16 rows of a to a workgroup
+
+struct FewWidth {
+  int nt;
+  int64_t cost;
+};
+// Fragments of b to a workgroup that has mt of a: with more of them a is read less often, with fewer there are more workgroups.
+// What counts is the fragments that the busiest CU reads.  (Width 1, 2, 3, 4 and 6 in us, k = 2560: 16 rows at n = 10576 8.7,
+// 9.1, 7.7, 8.1, -, at 5120 5.1, 4.6, 5.1, 5.6, -; 64 rows at 10576 15.7, 15.8, 11.0, 11.7, 14.7, at 16384 19.1, 16.0, 18.5,
+// 12.8, 15.2; 128 rows at 10576 25.2, 21.6, 18.3, 20.5, 14.9; 512 rows at 2560 -, 16.5, 14.2, 15.5, 11.8.)  With bf16 products
+// four fragments of a and six of b do not fit the registers (512 rows at 2560: 16.0 us with three of b, 17.2 with six).
+FewWidth few_width(const ssm_matmul_fp8_params* p) {
+  const int mt = few_rows(p->m);
+  FewWidth best{};
+  for (int nt : {1, 2, 3, 4, 6}) {
+    if (nt == 6 && mt == 4 && p->out_dtype == SSM_F32) continue;
+    const int64_t groups = ((p->m + 16 * mt - 1) / (16 * mt)) * ((p->n + 16 * nt - 1) / (16 * nt));
+    const int64_t cost = (groups + 255) / 256 * (mt + nt);
+    if (best.nt == 0 || cost < best.cost) best = {nt, cost};
+  }
+  return best;
+}
 
 MatmulPlan plan_of(const ssm_matmul_fp8_params* p) {
   const bool narrow = p->b_rows == kBlock && p->out_dtype == SSM_BF16;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((p->m + bm - 1) / bm) * ((p->n + bn - 1) / bn); };
-  // Fewer tiles than would keep the CUs busy: workgroups that share a tile's k among their waves (512 x 2560 x 2560, 80 tiles:
-  // 18 us; 256 x 10576 x 2560, 166 tiles: 31 us, and 21 in tiles).
-  if (p->m <= 64 || tiles(128, 128) < 160) return {true, 64, 64, 0};
+  // Workgroups that share a tile's k among their waves, where a CU reads no more than it would for one tile of 128 x 128 (16
+  // fragments: 512 x 2560 x 2560 11.8 us and 21.0 in tiles, 640 x 2560 x 2560 15.4 and 21.3, 768 x 768 x 8192 17.6 and 56.5;
+  // with more 256 x 10576 x 2560 takes 25.5 and 20.3, 512 x 5120 x 2560 22.4 and 21.4), and for few rows at any n.
+  const FewWidth few = few_width(p);
+  if (p->m <= 64 || few.cost <= 16) return {few.nt, 0, 0, 0};
   // Tiles of 128 x 128, two workgroups to a CU, which wait for their own copies only.  Where a lane has one scale of b for all
   // of its results and the products are 8-bit, the sums of 256 x 256 or 192 x 256 fit the registers of one, and large products
   // are faster so: what the turns of all workgroups take is counted in hundredths of one of 256 x 256 tiles, with the last of
@@ -543,13 +595,13 @@ MatmulPlan plan_of(const ssm_matmul_fp8_params* p) {
   // 128 x 128 82 to 85.  2800 x 2560 x 2560 takes 39, 35 and 29 us in tiles of 256, 192 and 128 rows, 3600 x 2560 x 2560 39, 36
   // and 42.  With a scale for each row of b 10576 x 2560 x 8192 takes 347 us in tiles of 128 x 128 and 407 in tiles of
   // 128 x 256, as fp32 503 and 571.)
-  MatmulPlan t{false, 128, 128, 512};
+  MatmulPlan t{0, 128, 128, 512};
   if (narrow) {
     const int64_t whole = tiles(256, 256), last = whole % 256, small = tiles(128, 128), rest = small % 512;
     const int64_t cost = whole / 256 * 100 + (last == 0 ? 0 : whole > 256 && last <= 128 ? 70 : 100);
     const int64_t low = (tiles(192, 256) + 255) / 256 * 80;
     const int64_t least = small / 512 * 68 + (rest == 0 ? 0 : rest <= 256 ? 45 : 68);
-    if (least > (low < cost ? low : cost)) t = {false, low < cost ? 192 : 256, 256, 256};
+    if (least > (low < cost ? low : cost)) t = {0, low < cost ? 192 : 256, 256, 256};
   }
   return t;
 }
@@ -594,17 +646,21 @@ void launch_few(MatmulArgs g, int brows, hipStream_t st) {
   else hipLaunchKernelGGL((matmul_few_kernel<MT, NT, W, kBlock, WIDE, TO>), grid, block, 0, st, g);
 }
 
-// More rows of b to a workgroup read a less often, fewer make more workgroups (NT = 4 and 1, k = 2560 and 5120: 64 rows of a
-// 11.7 and 15.3 us at n = 10576, 13.0 and 8.9 us at 2560; 32 rows 9.6 and 11.1, 9.8 and 6.3; NT = 4 and 2: 128 rows 21.3 and
-// 22.1, 13.5 and 10.9; 256 rows 31.4 and 38.9, 15.7 and 20.9).
+template <int MT, bool WIDE, typename TO>
+void launch_few_width(const MatmulArgs& g, int nt, int brows, hipStream_t st) {
+  if (nt == 1) launch_few<MT, 1, 8, WIDE, TO>(g, brows, st);
+  else if (nt == 2) launch_few<MT, 2, 8, WIDE, TO>(g, brows, st);
+  else if (nt == 3) launch_few<MT, 3, 8, WIDE, TO>(g, brows, st);
+  else if (nt == 4) launch_few<MT, 4, 8, WIDE, TO>(g, brows, st);
+  else if constexpr (!WIDE || MT < 4) launch_few<MT, 6, 8, WIDE, TO>(g, brows, st);
+}
+
 template <bool WIDE, typename TO>
-void launch_few_rows(const MatmulArgs& g, int brows, hipStream_t st) {
-  const bool many = g.n > 8192;
-  if (g.m <= 16) launch_few<1, 1, 8, WIDE, TO>(g, brows, st);
-  else if (g.m <= 32) many ? launch_few<2, 4, 8, WIDE, TO>(g, brows, st) : launch_few<2, 1, 8, WIDE, TO>(g, brows, st);
-  else if (g.m <= 64 && !many) launch_few<4, 1, 8, WIDE, TO>(g, brows, st);
-  else if (g.m <= 128 && !many) launch_few<4, 2, 8, WIDE, TO>(g, brows, st);
-  else launch_few<4, 4, 8, WIDE, TO>(g, brows, st);
+void launch_few_rows(const MatmulArgs& g, int nt, int brows, hipStream_t st) {
+  const int mt = few_rows(g.m);
+  if (mt == 1) launch_few_width<1, WIDE, TO>(g, nt, brows, st);
+  else if (mt == 2) launch_few_width<2, WIDE, TO>(g, nt, brows, st);
+  else launch_few_width<4, WIDE, TO>(g, nt, brows, st);
 }
 
 template <bool WIDE, typename TO>
@@ -649,14 +705,17 @@ extern "C" ssm_status ssm_matmul_fp8(const ssm_matmul_fp8_params* p, const void*
   g.os = p->out_stride ? p->out_stride : p->n;
   g.sas = p->a_scale_stride ? p->a_scale_stride : g.blocks;
   g.sbs = p->b_scale_stride ? p->b_scale_stride : g.blocks;
-  g.tiles_m = (g.m + t.bm - 1) / t.bm;
-  g.tiles_n = (g.n + t.bn - 1) / t.bn;
-  const int64_t tiles = int64_t(g.tiles_m) * g.tiles_n;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  if (t.few && p->out_dtype == SSM_F32) launch_few_rows<true, float>(g, p->b_rows, st);
-  else if (t.few) launch_few_rows<false, uint16_t>(g, p->b_rows, st);
-  else if (p->out_dtype == SSM_F32) launch_tiles<true, float>(g, t, p->b_rows, tiles, st);
-  else launch_tiles<false, uint16_t>(g, t, p->b_rows, tiles, st);
+  if (t.few) {
+    if (p->out_dtype == SSM_F32) launch_few_rows<true, float>(g, t.few, p->b_rows, st);
+    else launch_few_rows<false, uint16_t>(g, t.few, p->b_rows, st);
+  } else {
+    g.tiles_m = (g.m + t.bm - 1) / t.bm;
+    g.tiles_n = (g.n + t.bn - 1) / t.bn;
+    const int64_t tiles = int64_t(g.tiles_m) * g.tiles_n;
+    if (p->out_dtype == SSM_F32) launch_tiles<true, float>(g, t, p->b_rows, tiles, st);
+    else launch_tiles<false, uint16_t>(g, t, p->b_rows, tiles, st);
+  }
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? SSM_OK : fail(SSM_ERR_HIP, "matmul launch: %s", hipGetErrorString(e));
 }

@@ -373,6 +373,22 @@ def test_matmul_plans(M, N, K, b_rows, out):
     assert (base[M:] == 5.0).all() and (base[:, N:] == 5.0).all()
 
 
+# Workgroups that share k: 16, 32 and 64 rows of a to one, and each width that n gives them (16, 32, 48, 64 and 96 rows of b);
+# more blocks of k than waves, and fewer.
+@pytest.mark.parametrize("out,b_rows", [(BF, 128), (BF, 1), (F32, 128), (F32, 1)], ids=["bf16-128", "bf16-1", "f32-128", "f32-1"])
+@pytest.mark.parametrize("N", [2551, 5103, 10571, 16381, 24573])
+@pytest.mark.parametrize("M,K", [(13, 1168), (29, 272), (61, 1168)])
+def test_matmul_widths(M, N, K, out, b_rows):
+    test_matmul_plans(M, N, K, b_rows, out)
+
+
+@pytest.mark.parametrize("M,N,K,b_rows,out", [
+    (127, 10571, 1168, 128, BF), (127, 10571, 272, 1, BF), (510, 2557, 2320, 128, BF), (510, 2557, 400, 128, F32), (250, 2557, 400, 1, F32),
+    (640, 2560, 272, 128, BF), (767, 769, 4112, 1, F32), (4000, 100, 272, 128, BF), (20001, 61, 144, 1, BF)])
+def test_matmul_few_tiles(M, N, K, b_rows, out):
+    test_matmul_plans(M, N, K, b_rows, out)
+
+
 @pytest.mark.parametrize("out", [BF, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("M,N,K", [(1, 37, 144), (30, 200, 272), (300, 400, 272)])
 def test_matmul_strides(M, N, K, out):
