@@ -434,13 +434,13 @@ __global__ void __launch_bounds__(64 * WM * WN, 2) matmul_tile_kernel(MatmulArgs
 // 128 x 128 as above, of 128 x 64 20.9, and the same with operands in the L2: a block took as long as its copies' way.  Five
 // stages 13.3; 1000 x 2560 x 2560 in 216 tiles of 128 x 96 by 12 waves 14.9, by four with three fragments each 19.2.)
 // Lanes, swizzle and fragments are those of matmul_tiles.
-template <int TM, int TN, int WM, int WN, int S, int BROWS>
-__global__ void __launch_bounds__(64 * WM * WN) matmul_deep_kernel(MatmulArgs g) {
-  constexpr int BM = 32 * TM * WM, BN = 32 * TN * WN, NW = WM * WN;
+template <int TM, int WM, int WN, int BROWS>
+__global__ void __launch_bounds__(64 * WM * WN) matmul_own_kernel(MatmulArgs g) {
+  constexpr int BM = 32 * TM * WM, BN = 32 * WN, NW = WM * WN, S = 3;
   // A stage's copies, given to the waves in turn: 1 KB each of a and of b (8 rows of a block), then the scales of 64 rows each.
   constexpr int kA = BM / 8, kAB = (BM + BN) / 8, kSB = kAB + BM / 64, kAll = kSB + (BROWS == 1 ? (BN + 63) / 64 : 1);
   constexpr int kCopies = (kAll + NW - 1) / NW, kStage = (BM + BN) * 128 + 256 * (kCopies * NW - kAB);
-  static_assert(BM % 64 == 0 && BN % 32 == 0 && NW % 2 == 0 && S >= 3 && S * kStage <= 163840);
+  static_assert(BM % 64 == 0 && BN % 32 == 0 && NW % 2 == 0 && S * kStage <= 163840);
   __shared__ __align__(1024) uint8_t lds[S * kStage];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % WM, wn = wave / WM, r32 = lane & 31, half = lane >> 5;
@@ -485,48 +485,41 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_deep_kernel(MatmulArgs g)
   const int key_b = (row_b >> 1) & 7;
   const uint32_t base = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_mvoid*)lds));
   const uint32_t at_a = base + (wm * TM * 32 + r32) * 128 + ((2 * half) ^ key_a) * 16;
-  const uint32_t at_b = base + BM * 128 + (wn * TN * 32 + row_b) * 128 + ((2 * half) ^ key_b) * 16;
+  const uint32_t at_b = base + BM * 128 + (wn * 32 + row_b) * 128 + ((2 * half) ^ key_b) * 16;
   const uint32_t at_sa = base + (BM + BN) * 128 + (wm * TM * 32 + r32) * 4, at_sb = base + (BM + BN) * 128 + BM * 4;
-  v16f acc[TM][TN] = {};
+  v16f acc[TM] = {};
   int s = 0;
   for (int c = 0; c < g.blocks; ++c) {
     wait_memory<(S - 2) * kCopies>();
     barrier();   // (block c has arrived, and every wave has read block c - 1)
     copy(c + S - 1, s == 0 ? S - 1 : s - 1);
     const uint32_t o = s * kStage;
-    Frag<false> fa[TM][2], fb[TN][2];
-    float sa[TM], sb[TN];
+    Frag<false> fa[TM][2], fb[2];
+    float sa[TM], sb = 1.0f;
+    pf4 sbn[4];
 #pragma unroll
     for (int kh = 0; kh < 2; ++kh) {
-#pragma unroll
-      for (int j = 0; j < TN; ++j)
-        fb[j][kh].set(join(from_lds<v4i>(((at_b + o) ^ (kh * 64)) + j * 4096), from_lds<v4i>(((at_b + o) ^ (kh * 64 + 16)) + j * 4096)));
+      fb[kh].set(join(from_lds<v4i>((at_b + o) ^ (kh * 64)), from_lds<v4i>((at_b + o) ^ (kh * 64 + 16))));
 #pragma unroll
       for (int i = 0; i < TM; ++i)
         fa[i][kh].set(join(from_lds<v4i>(((at_a + o) ^ (kh * 64)) + i * 4096), from_lds<v4i>(((at_a + o) ^ (kh * 64 + 16)) + i * 4096)));
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i) sa[i] = from_lds<float>(at_sa + o + i * 128);
-    if constexpr (BROWS != 1) {
+    if constexpr (BROWS == 1) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j) sb[j] = from_lds<float>(at_sb + o + (n0 % 128 + (wn * TN + j) * 32) / 128 * 4);
+      for (int h = 0; h < 4; ++h) sbn[h] = from_lds<pf4>(at_sb + o + (wn * 32 + h / 2 * 16 + half * 8 + h % 2 * 4) * 4);
+    } else {
+      sb = from_lds<float>(at_sb + o + (n0 % 128 + wn * 32) / 128 * 4);
     }
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      pf4 sbn[4];
-      if constexpr (BROWS == 1) {
+    for (int i = 0; i < TM; ++i) {
+      v16f d{};
 #pragma unroll
-        for (int h = 0; h < 4; ++h) sbn[h] = from_lds<pf4>(at_sb + o + ((wn * TN + j) * 32 + h / 2 * 16 + half * 8 + h % 2 * 4) * 4);
-      }
+      for (int kh = 0; kh < 2; ++kh) d = mfma_half(fb[kh], fa[i][kh], d);
+      const float t = sa[i] * sb;
 #pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        v16f d{};
-#pragma unroll
-        for (int kh = 0; kh < 2; ++kh) d = mfma_half(fb[j][kh], fa[i][kh], d);
-        const float t = BROWS == 1 ? sa[i] : sa[i] * sb[j];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(BROWS == 1 ? d[r] * sbn[r / 4][r % 4] : d[r], t, acc[i][j][r]);
-      }
+      for (int r = 0; r < 16; ++r) acc[i][r] = fmaf(BROWS == 1 ? d[r] * sbn[r / 4][r % 4] : d[r], t, acc[i][r]);
     }
     wait_lds();
     s = s + 1 == S ? 0 : s + 1;
@@ -537,14 +530,12 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_deep_kernel(MatmulArgs g)
     const int row = m0 + (wm * TM + i) * 32 + r32;
     if (row < g.m)
 #pragma unroll
-      for (int j = 0; j < TN; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const v16f& v = acc[i][j];
-          const int e = n0 + (wn * TN + j) * 32 + 16 * h + half * 8;
-          store8<uint16_t>(out + row * g.os + e, pf4{v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]},
-                           pf4{v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]}, g.n - e);
-        }
+      for (int h = 0; h < 2; ++h) {
+        const v16f& v = acc[i];
+        const int e = n0 + wn * 32 + 16 * h + half * 8;
+        store8<uint16_t>(out + row * g.os + e, pf4{v[8 * h], v[8 * h + 1], v[8 * h + 2], v[8 * h + 3]},
+                         pf4{v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]}, g.n - e);
+      }
   }
   wait_memory();   // (the zeros that were copied behind the last block: LDS is given up only now)
 }
@@ -675,8 +666,8 @@ __global__ void __launch_bounds__(64 * W) matmul_few_kernel(MatmulArgs g) {
 
 struct MatmulPlan {
   int few;              // fragments of 16 rows of b to a workgroup that shares k among its waves; 0: tiles
-  int deep;             // fragments of 32 rows of b to a tile of 128 rows that has a CU to itself; 0: others
-  int bm, bn, slots;    // slots: workgroups that run at a time
+  int bm, bn;
+  int slots;            // workgroups that run at a time; 0: of the tiles that have a CU to themselves, which all do
 };
 
 int few_rows(int64_t m) { return m <= 16 ? 1 : m <= 32 ? 2 : 4; }   // fragments of 16 rows of a to a workgroup
@@ -705,18 +696,25 @@ FewWidth few_width(const ssm_matmul_fp8_params* p) {
 MatmulPlan plan_of(const ssm_matmul_fp8_params* p) {
   const bool narrow = p->b_rows == kBlock && p->out_dtype == SSM_BF16;
   auto tiles = [&](int64_t bm, int64_t bn) { return ((p->m + bm - 1) / bm) * ((p->n + bn - 1) / bn); };
-  // Small products take as long as their busiest CU reads.  Where one tile of 128 rows to a CU is enough for all of them, the
-  // narrowest such tile, or workgroups that share a tile's k among their waves, whichever has a CU read less (us, shared k and
-  // tiles: 512 x 2560 x 2560 11.8, 11.4; 640 x 2560 15.4, 12.1; 256 x 10576 25.5, 18.0; 512 x 5120 22.4, 16.3; 128 x 10576 14.9,
-  // 16.3; 768 x 768 x 8192 17.6, 47).  With fp32 results, whose tiles are only those of 128 x 128 for a turn of two, shared k as
-  // far as 16 fragments (512 x 2560 x 2560 16.0 and 29.1 us, 192 x 10576 x 2560 24.0 and 30.4).
+  // Small products take as long as their busiest CU reads.  Where one tile to a CU is enough for all of them, the smallest such
+  // tile, or workgroups that share a tile's k among their waves, whichever has a CU read less (us, shared k and tiles:
+  // 512 x 2560 x 2560 11.8, 11.4; 640 x 2560 15.4, 12.1; 256 x 10576 25.5, 18.0; 512 x 5120 22.4, 16.3; 128 x 10576 14.9, 16.3;
+  // 768 x 768 x 8192 17.6, 47; 256 x 96 and two tiles of 128 x 128 to a CU: 1024 x 5120 x 2560 22.7, 26.0, 2048 x 2560 x 5120
+  // 43.2, 46.7; 192 x 256, 256 x 128 and others of that kind are no faster than the tiles below).  With fp32 results, whose
+  // tiles are only those of 128 x 128 below, shared k as far as 16 fragments (512 x 2560 x 2560 16.0 and 29.1 us,
+  // 192 x 10576 x 2560 24.0 and 30.4).
   const FewWidth few = few_width(p);
-  int deep = 0;
-  if (p->out_dtype == SSM_BF16)
-    for (int nt : {4, 3, 2})
-      if (tiles(128, 32 * nt) <= 256) deep = nt;
-  if (p->m <= 64 || few.cost <= (deep ? 8 + 2 * deep : 16)) return {few.nt, 0, 0, 0, 0};
-  if (deep) return {0, deep, 128, 32 * deep, 0};
+  MatmulPlan own{};
+  if (p->out_dtype == SSM_BF16) {
+    static const int sizes[][2] = {{128, 64}, {128, 96}, {128, 128}, {256, 96}};
+    for (const auto& c : sizes)
+      if (tiles(c[0], c[1]) <= 256) {
+        own = {0, c[0], c[1], 0};
+        break;
+      }
+  }
+  if (p->m <= 64 || few.cost <= (own.bm ? (own.bm + own.bn) / 16 : 16)) return {few.nt, 0, 0, 0};
+  if (own.bm) return own;
   // Tiles of 128 x 128, two workgroups to a CU, which wait for their own copies only.  Where a lane has one scale of b for all
   // of its results and the products are 8-bit, the sums of 256 x 256 or 192 x 256 fit the registers of one, and large products
   // are faster so: what the turns of all workgroups take is counted in hundredths of one of 256 x 256 tiles, with the last of
@@ -724,13 +722,13 @@ MatmulPlan plan_of(const ssm_matmul_fp8_params* p) {
   // 128 x 128 82 to 85.  2800 x 2560 x 2560 takes 39, 35 and 29 us in tiles of 256, 192 and 128 rows, 3600 x 2560 x 2560 39, 36
   // and 42.  With a scale for each row of b 10576 x 2560 x 8192 takes 347 us in tiles of 128 x 128 and 407 in tiles of
   // 128 x 256, as fp32 503 and 571.)
-  MatmulPlan t{0, 0, 128, 128, 512};
+  MatmulPlan t{0, 128, 128, 512};
   if (narrow) {
     const int64_t whole = tiles(256, 256), last = whole % 256, small = tiles(128, 128), rest = small % 512;
     const int64_t cost = whole / 256 * 100 + (last == 0 ? 0 : whole > 256 && last <= 128 ? 70 : 100);
     const int64_t low = (tiles(192, 256) + 255) / 256 * 80;
     const int64_t least = small / 512 * 68 + (rest == 0 ? 0 : rest <= 256 ? 45 : 68);
-    if (least > (low < cost ? low : cost)) t = {0, 0, low < cost ? 192 : 256, 256, 256};
+    if (least > (low < cost ? low : cost)) t = {0, low < cost ? 192 : 256, 256, 256};
   }
   return t;
 }
@@ -793,10 +791,10 @@ void launch_few_rows(const MatmulArgs& g, int nt, int brows, hipStream_t st) {
 }
 
 template <int TM, int WM, int WN>
-void launch_deep(const MatmulArgs& g, int brows, hipStream_t st) {
+void launch_own(const MatmulArgs& g, int brows, hipStream_t st) {
   const dim3 grid(g.tiles_m * g.tiles_n), block(64 * WM * WN);
-  if (brows == 1) hipLaunchKernelGGL((matmul_deep_kernel<TM, 1, WM, WN, 3, 1>), grid, block, 0, st, g);
-  else hipLaunchKernelGGL((matmul_deep_kernel<TM, 1, WM, WN, 3, kBlock>), grid, block, 0, st, g);
+  if (brows == 1) hipLaunchKernelGGL((matmul_own_kernel<TM, WM, WN, 1>), grid, block, 0, st, g);
+  else hipLaunchKernelGGL((matmul_own_kernel<TM, WM, WN, kBlock>), grid, block, 0, st, g);
 }
 
 template <bool WIDE, typename TO>
@@ -849,9 +847,10 @@ extern "C" ssm_status ssm_matmul_fp8(const ssm_matmul_fp8_params* p, const void*
     g.tiles_m = (g.m + t.bm - 1) / t.bm;
     g.tiles_n = (g.n + t.bn - 1) / t.bn;
     const int64_t tiles = int64_t(g.tiles_m) * g.tiles_n;
-    if (t.deep == 2) launch_deep<1, 4, 2>(g, p->b_rows, st);
-    else if (t.deep == 3) launch_deep<1, 4, 3>(g, p->b_rows, st);
-    else if (t.deep == 4) launch_deep<2, 2, 4>(g, p->b_rows, st);
+    if (t.slots == 0 && t.bm == 256) launch_own<2, 4, 3>(g, p->b_rows, st);
+    else if (t.slots == 0 && t.bn == 64) launch_own<1, 4, 2>(g, p->b_rows, st);
+    else if (t.slots == 0 && t.bn == 96) launch_own<1, 4, 3>(g, p->b_rows, st);
+    else if (t.slots == 0) launch_own<2, 2, 4>(g, p->b_rows, st);
     else if (p->out_dtype == SSM_F32) launch_tiles<true, float>(g, t, p->b_rows, tiles, st);
     else launch_tiles<false, uint16_t>(g, t, p->b_rows, tiles, st);
   }

@@ -389,11 +389,12 @@ def test_matmul_few_tiles(M, N, K, b_rows, out):
     test_matmul_plans(M, N, K, b_rows, out)
 
 
-# Tiles that have a CU to themselves: 64, 96 and 128 rows of b; one block of k, fewer and more than the stages; cut rows and
+# Tiles that have a CU to themselves: 64, 96 and 128 rows of b, and 256 of a; one block of k, fewer and more than the stages; cut rows and
 # columns, rows of b under one scale that begin inside a tile.
 @pytest.mark.parametrize("b_rows", [128, 1])
 @pytest.mark.parametrize("K", [112, 144, 400, 1168])
-@pytest.mark.parametrize("M,N", [(767, 2557), (730, 2560), (1000, 2555), (250, 10571), (1001, 4090), (129, 16001)])
+@pytest.mark.parametrize("M,N", [(767, 2557), (730, 2560), (1000, 2555), (250, 10571), (1001, 4090), (129, 16001), (2001, 2550),
+                                 (510, 10571)])
 def test_matmul_single_turn(M, N, K, b_rows):
     test_matmul_plans(M, N, K, b_rows, BF)
 
