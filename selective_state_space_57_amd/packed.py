@@ -38,7 +38,7 @@ def _dtype_code(t, name):
 def _rows(name, t, shape, dtype, device, optional=False):
     """Checks a tensor of rows and returns the stride between them (0 for an absent tensor)."""
     if t is not None and t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
-        return t.numel() // max(shape[0], 1)
+        return shape[1] if len(shape) == 2 else t.numel() // max(shape[0], 1)
     if t is None:
         if not optional:
             raise ValueError("%s is required" % name)
@@ -105,7 +105,7 @@ class _launch:
     def __enter__(self):
         import torch
         if self.stream is None:
-            if self.device.index != torch.cuda.current_device():
+            if self.device.index != torch._C._cuda_getDevice():
                 self._enter(torch.cuda.device(self.device))
             # (the handle alone: torch.cuda.current_stream makes an object around it, 1.9 of a call's 10 us)
             return torch._C._cuda_getCurrentRawStream(self.device.index)

@@ -39,10 +39,10 @@ def _codes(rows, cols, device):
     """Memory for codes (rows, cols rounded up to 16).  Rows of several cache lines begin with one: the product of rows that
     do not reads every line twice (8191 x 2560 x 10576: 320 and 287 us)."""
     import torch
-    n, line = _up16(cols), (cols + 127) // 128 * 128
-    if n == line or n < 512:
-        return torch.empty((rows, n), dtype=torch.float8_e4m3fn, device=device)
-    return torch.empty((rows, line), dtype=torch.float8_e4m3fn, device=device)[:, :n]
+    n = (cols + 15) // 16 * 16
+    if n % 128 == 0 or n < 512:
+        return torch.empty(rows, n, dtype=torch.float8_e4m3fn, device=device)
+    return torch.empty(rows, (n + 127) // 128 * 128, dtype=torch.float8_e4m3fn, device=device)[:, :n]
 
 
 def _blocks(n):
@@ -96,14 +96,17 @@ def add_norm_fwd(x, weight, residual=None, *, eps=1e-5, y_dtype=None, residual_d
     keep = residual_dtype is not None
     _whole("weight", weight, (D,), torch.float32, dev, optional=False)
     xs = _rows("x", x, (T, D), x.dtype, dev)
-    rs = _rows("residual", residual, (T, D), residual_dtype, dev, optional=True)
-    hs = _rows("residual_out", residual_out, (T, D), residual_dtype, dev, optional=True)
-    width = _up16(D) if eight else D
-    ys = _rows("y", y, (T, width), y_dtype, dev, optional=True)
-    if y_scale is not None and not eight:
-        raise ValueError("y_scale without an 8-bit y")
-    ss = _rows("y_scale", y_scale, (T, _blocks(D)), torch.float32, dev, optional=True)
+    rs = hs = ys = ss = 0
+    if residual is not None:
+        rs = _rows("residual", residual, (T, D), residual_dtype, dev)
+    if y_scale is not None:
+        if not eight:
+            raise ValueError("y_scale without an 8-bit y")
+        ss = _rows("y_scale", y_scale, (T, _blocks(D)), torch.float32, dev)
+    if y is not None:
+        ys = _rows("y", y, (T, _up16(D) if eight else D), y_dtype, dev)
     if residual_out is not None:
+        hs = _rows("residual_out", residual_out, (T, D), residual_dtype, dev)
         ins = (("x", x), ("residual", residual))
         _apart(residual_out, "residual_out", ("weight", weight), *ins, may_be=_alias(residual_out, *ins))
     if y is not None:
@@ -113,12 +116,12 @@ def add_norm_fwd(x, weight, residual=None, *, eps=1e-5, y_dtype=None, residual_d
         _apart(y_scale, "y_scale", ("x", x), ("weight", weight), ("residual", residual), ("residual_out", residual_out), ("y", y))
     with _launch(dev, stream, x, weight, residual, y, y_scale, residual_out) as st:
         if y is None:
-            y = _codes(T, D, dev) if eight else torch.empty((T, D), dtype=y_dtype, device=dev)
+            y = _codes(T, D, dev) if eight else torch.empty(T, D, dtype=y_dtype, device=dev)
             ys = y.stride(0)
         if eight and y_scale is None:
-            y_scale = torch.empty((T, _blocks(D)), dtype=torch.float32, device=dev)
+            y_scale = torch.empty(T, _blocks(D), dtype=torch.float32, device=dev)
         if keep and residual_out is None:
-            residual_out = torch.empty((T, D), dtype=residual_dtype, device=dev)
+            residual_out = torch.empty(T, D, dtype=residual_dtype, device=dev)
         p = _abi.AddNormParams(T, D, xs, rs, hs, ys, ss, 0, 0, 0, 0, float(eps), io, rio, _abi.SSM_E4M3 if eight else io, 0)
         _abi.check(_abi.lib().ssm_add_norm_fwd(ctypes.byref(p), _ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out),
                                                _ptr(y), _ptr(y_scale), st))
@@ -141,12 +144,13 @@ def add_norm_bwd(h, weight, dy, dh=None, *, eps=1e-5, dx=None, dresidual=None, w
     hs = _rows("h", h, (T, D), h.dtype, dev)
     dys = _rows("dy", dy, (T, D), dy.dtype, dev)
     dhs = _rows("dh", dh, (T, D), h.dtype, dev, optional=True)
-    dxs = _rows("dx", dx, (T, D), dy.dtype, dev, optional=True)
-    drs = _rows("dresidual", dresidual, (T, D), h.dtype, dev, optional=True)
+    dxs = drs = 0
     ins = (("h", h), ("dy", dy), ("dh", dh))
     if dx is not None:
+        dxs = _rows("dx", dx, (T, D), dy.dtype, dev)
         _apart(dx, "dx", *ins, ("weight", weight), ("dresidual", dresidual), may_be=_alias(dx, *ins))
     if dresidual is not None:
+        drs = _rows("dresidual", dresidual, (T, D), h.dtype, dev)
         _apart(dresidual, "dresidual", *ins, ("weight", weight), may_be=_alias(dresidual, *ins))
     if workspace is not None:
         _apart(workspace, "workspace", *ins, ("weight", weight), ("dx", dx), ("dresidual", dresidual))
@@ -154,12 +158,12 @@ def add_norm_bwd(h, weight, dy, dh=None, *, eps=1e-5, dx=None, dresidual=None, w
         one = io == rio and (dx is None or dresidual is None)
         if one:
             dx = dresidual = dx if dx is not None else dresidual if dresidual is not None else torch.empty(
-                (T, D), dtype=h.dtype, device=dev)
+                T, D, dtype=h.dtype, device=dev)
             dxs = drs = dxs or drs
         else:
-            dx = torch.empty((T, D), dtype=dy.dtype, device=dev) if dx is None else dx
-            dresidual = torch.empty((T, D), dtype=h.dtype, device=dev) if dresidual is None else dresidual
-        dweight = torch.empty((D,), dtype=torch.float32, device=dev)
+            dx = torch.empty(T, D, dtype=dy.dtype, device=dev) if dx is None else dx
+            dresidual = torch.empty(T, D, dtype=h.dtype, device=dev) if dresidual is None else dresidual
+        dweight = torch.empty(D, dtype=torch.float32, device=dev)
         p = _abi.AddNormParams(T, D, 0, 0, hs, 0, 0, dys, dhs, dxs, drs, float(eps), io, rio, io, 0)
         if workspace is None:
             need = int(_abi.lib().ssm_add_norm_bwd_workspace_bytes(ctypes.byref(p)))
@@ -174,9 +178,7 @@ def add_norm_bwd(h, weight, dy, dh=None, *, eps=1e-5, dx=None, dresidual=None, w
 # quantisation
 
 def _output(name, t, shape, dtype, dev, *ins):
-    """Checks an output that is given, which may not overlap ``ins``, and returns the stride between its rows."""
-    if t is None:
-        return 0
+    """Checks an output, which may not overlap ``ins``, and returns the stride between its rows."""
     stride = _rows(name, t, shape, dtype, dev)
     _apart(t, name, *ins)
     return stride
@@ -194,26 +196,31 @@ def _quantize(x, square, rows, columns, q, scale, qt, scale_t, stream):
         raise ValueError("q and scale: no output of this call without rows")
     if not columns and (qt is not None or scale_t is not None):
         raise ValueError("qt and scale_t: no output of this call without columns")
-    tb, db = _blocks(T), _blocks(D)
+    tb, db = (T + 127) // 128, (D + 127) // 128
     of_rows, of_columns = ((tb, db), (db, tb)) if square else ((T, db), (D, tb))
     xs = _rows("x", x, (T, D), x.dtype, dev)
-    qs = _output("q", q, (T, _up16(D)), f8, dev, ("x", x))
-    ss = _output("scale", scale, of_rows, f32, dev, ("x", x), ("q", q))
-    qts = _output("qt", qt, (D, _up16(T)), f8, dev, ("x", x), ("q", q), ("scale", scale))
-    sts = _output("scale_t", scale_t, of_columns, f32, dev, ("x", x), ("q", q), ("scale", scale), ("qt", qt))
+    qs = ss = qts = sts = 0
+    if q is not None:
+        qs = _output("q", q, (T, _up16(D)), f8, dev, ("x", x))
+    if scale is not None:
+        ss = _output("scale", scale, of_rows, f32, dev, ("x", x), ("q", q))
+    if qt is not None:
+        qts = _output("qt", qt, (D, _up16(T)), f8, dev, ("x", x), ("q", q), ("scale", scale))
+    if scale_t is not None:
+        sts = _output("scale_t", scale_t, of_columns, f32, dev, ("x", x), ("q", q), ("scale", scale), ("qt", qt))
     with _launch(dev, stream, x, q, scale, qt, scale_t) as st:
         if rows:
             if q is None:
                 q = _codes(T, D, dev)
                 qs = q.stride(0)
             if scale is None:
-                scale = torch.empty(of_rows, dtype=f32, device=dev)
+                scale = torch.empty(*of_rows, dtype=f32, device=dev)
         if columns:
             if qt is None:
                 qt = _codes(D, T, dev)
                 qts = qt.stride(0)
             if scale_t is None:
-                scale_t = torch.empty(of_columns, dtype=f32, device=dev)
+                scale_t = torch.empty(*of_columns, dtype=f32, device=dev)
         p = _abi.QuantizeFp8Params(T, D, xs, qs, ss, qts, sts, io, square)
         _abi.check(_abi.lib().ssm_quantize_fp8(ctypes.byref(p), _ptr(x), _ptr(q), _ptr(scale), _ptr(qt), _ptr(scale_t), st))
     return {"q": q, "scale": scale, "qt": qt, "scale_t": scale_t}
@@ -250,12 +257,12 @@ def matmul_fp8(a, a_scale, b, b_scale, *, out_dtype=None, out=None, stream=None)
     N = b.shape[0]
     sa = _rows("a", a, (M, K), f8, dev)
     sb = _rows("b", b, (N, K), f8, dev)
-    kb = _blocks(K)
+    kb = (K + 127) // 128
     sas = _rows("a_scale", a_scale, (M, kb), f32, dev)
     if b_scale is None or b_scale.dim() != 2:
         raise ValueError("b_scale: expected shape (%d, %d) or (%d, %d)" % (_blocks(N), kb, N, kb))
     b_rows = 1 if b_scale.shape[0] == N and N > 1 else BLOCK
-    sbs = _rows("b_scale", b_scale, (N if b_rows == 1 else _blocks(N), kb), f32, dev)
+    sbs = _rows("b_scale", b_scale, (N if b_rows == 1 else (N + 127) // 128, kb), f32, dev)
     if out is not None:
         if out_dtype is not None and out_dtype != out.dtype:
             raise TypeError("out_dtype %s does not match the given out (%s)" % (out_dtype, out.dtype))
@@ -264,12 +271,13 @@ def matmul_fp8(a, a_scale, b, b_scale, *, out_dtype=None, out=None, stream=None)
         out_dtype = torch.bfloat16
     if out_dtype != torch.bfloat16 and out_dtype != f32:
         raise TypeError("out: unsupported dtype %s (float32 or bfloat16)" % out_dtype)
-    os_ = _rows("out", out, (M, N), out_dtype, dev, optional=True)
+    os_ = 0
     if out is not None:
+        os_ = _rows("out", out, (M, N), out_dtype, dev)
         _apart(out, "out", ("a", a), ("a_scale", a_scale), ("b", b), ("b_scale", b_scale))
     with _launch(dev, stream, a, a_scale, b, b_scale, out) as st:
         if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+            out = torch.empty(M, N, dtype=out_dtype, device=dev)
         p = _abi.MatmulFp8Params(M, N, K, sa, sb, os_, sas, sbs, b_rows, _abi.SSM_F32 if out_dtype == f32 else _abi.SSM_BF16)
         _abi.check(_abi.lib().ssm_matmul_fp8(ctypes.byref(p), _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale), _ptr(out), st))
     return out
