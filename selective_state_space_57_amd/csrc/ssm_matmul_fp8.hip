@@ -14,15 +14,17 @@
 // Large products are bound by the matrix cores, the fmas that apply the scales (a quarter of the vector unit's cycles: with
 // instructions of 16 x 16 x 128, whose results come twice as often for the same work, a loop without memory reached 3562 TF,
 // with these 4015) and, above all, by the copies into LDS that run beside them: 8192^3 takes 540 us, without the copies 440.
-// Measured, bf16 results and one scale for 128 rows of b: 16384 x 10576 x 2560 437 us (2030 TF; the matrix cores are busy 57 % of
-// the time; a library product with one scale for each whole tensor takes 392 to 470), 4099 x 2560 x 5120 58 us; rows of b with
-// scales of their own, fp32 results: 10576 x 2560 x 8191 470 us (945 TF), bound by the conversions and by two vector operations
-// for each result and block.  Few rows are bound by the reading of b: 1 row at 10576 x 2560 7.8 us (3.5 TB/s with the launch).
+// Measured, bf16 results and one scale for 128 rows of b: 16384 x 10576 x 2560 437 to 452 us (2030 TF; the matrix cores are busy
+// 57 % of the time, the clock falls to 1.9 GHz under the power limit; a library product with one scale for each whole tensor takes
+// 392 to 470), 4099 x 2560 x 5120 58 to 60 us; rows of b with scales of their own, fp32 results: 10576 x 2560 x 8191 470 to
+// 490 us (945 TF), bound by the conversions, two vector operations for each result and block, and power.  Products of one turn
+// are bound by a CU's copies (about 45 B/ns): 256 x 10576 x 2560 15 us, 1000 x 2560 x 2560 15.8 (library 15.7 for 1024).  Few
+// rows are bound by the reading of b: 1 row at 10576 x 2560 7.6 us (3.6 TB/s with the launch).
 //
 // Tried and not kept, for the large products: four waves of 128 x 128 results each (their sums move between register files:
 // 801 us at 8192^3), lines touched ahead of their copies (5 to 10 % slower), all of a stage's copies at once (3 % slower), raised
-// priority around the matrix instructions (15 % slower); for few tiles: three or four stages in LDS (256 x 10576 x 2560 20.1 to
-// 20.8 us for 21.5, on one workgroup to a CU), k split over workgroups with a join (512 x 2560 x 2560 24.9 us for 18.5).
+// priority around the matrix instructions (15 % slower), 12 or 16 waves over 192 x 256 (4099 x 2560 x 5120 65.7 us for 62.5);
+// for few tiles k split over workgroups with a join (512 x 2560 x 2560 24.9 us; 11.8 now).
 #include "fp8.hpp"
 
 namespace ssm57 {
