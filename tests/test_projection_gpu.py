@@ -455,3 +455,24 @@ def test_matmul_range_of_scales():
     sb = torch.exp2(torch.randint(-30, 30, (1, 2), generator=r.g, device="cuda").float())
     want, size = R.product(a, sa, b, sb, 128)
     inside(ssm().matmul_fp8(a, sa, b, sb, out_dtype=F32), want, tolerance(a, sa, b, sb, 128, F32, want, size))
+
+
+# The same for tiles: with a CU to themselves (64, 96 and 128 rows of b, 256 of a), of 128, 192 and 256 rows.
+TILES = [(767, 2557, 272, BF), (250, 10571, 144, BF), (1001, 4090, 272, BF), (2001, 2550, 400, BF), (2750, 2560, 144, BF),
+         (4099, 2560, 272, BF), (5100, 5120, 144, BF), (2100, 2600, 272, F32)]
+
+
+@pytest.mark.parametrize("M,N,K,out", TILES)
+def test_matmul_strides_of_tiles(M, N, K, out):
+    test_matmul_strides(M, N, K, out)
+
+
+@pytest.mark.parametrize("M,N,K,out", TILES)
+def test_matmul_not_finite_of_tiles(M, N, K, out):
+    test_matmul_not_finite(M, N, K, out)
+
+
+@pytest.mark.parametrize("b_rows", [128, 1], ids=["blocks", "rows"])
+@pytest.mark.parametrize("M,N,K,out", TILES)
+def test_matmul_of_tiles(M, N, K, out, b_rows):
+    test_matmul(M, N, K, b_rows, out)
