@@ -439,9 +439,10 @@ ssm_status ssm_gated_norm_bwd(const ssm_gated_norm_params* p, const void* x, con
  *
  * 8-bit arrays hold e4m3 values (4 exponent and 3 mantissa bits, largest 448, no infinities) and have an fp32 scale for
  * each block of SSM57_BLOCK consecutive values of a row, or of SSM57_BLOCK rows and columns; the last block of a row or
- * column may be cut short.  A value stands for code * scale.  scale = max(largest magnitude of the block, 2^-100) / 448,
- * code = the value / scale rounded to nearest even.  A block that holds a NaN has a NaN scale; one that holds an infinity
- * has an infinite scale, so that products with any of its values are NaN.
+ * column may be cut short.  A value stands for code * scale.  scale = max(largest magnitude of the block, 2^-100) / 448 and
+ * the quotient value / scale are fp32, rounded to nearest even, and the code is the e4m3 value nearest to that quotient,
+ * halves to the even one.  A block that holds a NaN has a NaN scale; one that holds an infinity has an infinite scale, so that
+ * products with any of its values are NaN.
  * Rows of 8-bit arrays have their length rounded up to a multiple of 16; what is added holds zeros.
  */
 #define SSM57_BLOCK 128

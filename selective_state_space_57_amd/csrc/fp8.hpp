@@ -1,5 +1,5 @@
-// Device helpers shared by the kernels that write 8-bit values with a scale for each block of 128 (ssm_add_norm.hip,
-// ssm_quantize.hip): eight consecutive elements of a row at any alignment, magnitudes, codes.
+// Device helpers of the kernels at a block's ends (ssm_add_norm.hip, ssm_quantize.hip, ssm_matmul_fp8.hip): eight consecutive
+// elements of a row at any alignment; magnitudes, scales and codes of 8-bit values with a scale for each block of 128.
 #pragma once
 
 #include "packed.hpp"
@@ -96,8 +96,28 @@ __device__ __forceinline__ uint32_t codes(float a, float b, float c, float d) {
   int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
   return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
 }
-__device__ __forceinline__ pu2 codes8(const float* v, float inv) {
-  return pu2{codes(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv), codes(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv)};
+// Codes of eight values of a block: their fp32 quotients by the scale, rounded to nearest, then to the nearest code.  bf16
+// values often lie halfway between two codes, where a product with the rounded reciprocal went to the wrong side (5 codes in
+// 10,000), so the quotient's remainder, which a fma has exactly, corrects it: two more operations for a code, with the same
+// codes as a division for each (tried on the host at every border between codes for every divisor's mantissa).  Measured
+// beside the product alone: 8191 x 5120 bf16, rows and columns, 42.9 us and 39.6; 16384 rows of 2560 of the norm 86.6 and 84.9.
+__device__ __forceinline__ pu2 codes8(const float* v, float scale) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = v[i];
+  if (scale < 0x1p-90f) {   // (remainders would be subnormal)
+    scale *= 0x1p64f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] *= 0x1p64f;
+  }
+  const float inv = 1.0f / scale;
+  const float s = scale < __builtin_inff() ? scale : 0.0f;   // (of a block with an infinity: finite values have code 0)
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float near = q[i] * inv;
+    q[i] = fmaf(-fmaf(near, s, -q[i]), inv, near);
+  }
+  return pu2{codes(q[0], q[1], q[2], q[3]), codes(q[4], q[5], q[6], q[7])};
 }
 
 inline int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(TEAM < 256 ? 256 : TEAM) add_norm_fwd_kernel(A
           for (int v = 0; v < 8; ++v) o[v] = v < cnt[j] ? o[v] : 0.0f;
         }
         const float scale = scale_of(row_largest(FULL && cnt[j] <= 0 ? 0u : largest(o)));
-        pu2 c = codes8(o, 1.0f / scale);
+        pu2 c = codes8(o, scale);
         if constexpr (!FULL) {
           if (cnt[j] < 8) {
             uint64_t bits = __builtin_bit_cast(uint64_t, c);

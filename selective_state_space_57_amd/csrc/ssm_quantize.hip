@@ -27,8 +27,8 @@ struct QuantArgs {
 };
 
 // codes of eight values, zeros from the cnt-th on
-__device__ __forceinline__ pu2 codes8_part(const float* v, float inv, int cnt) {
-  pu2 c = codes8(v, inv);
+__device__ __forceinline__ pu2 codes8_part(const float* v, float scale, int cnt) {
+  pu2 c = codes8(v, scale);
   if (cnt < 8) {
     uint64_t bits = __builtin_bit_cast(uint64_t, c);
     bits = cnt <= 0 ? 0 : bits & ((uint64_t(1) << (8 * cnt)) - 1);
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(QuantArgs a) {
     float v[8];
     e.get(v);
     const float scale = scale_of(row_largest(largest(v)));
-    if (at < a.cols16) *reinterpret_cast<pu2e*>(a.q + row * a.qs + at) = codes8_part(v, 1.0f / scale, a.cols - at);
+    if (at < a.cols16) *reinterpret_cast<pu2e*>(a.q + row * a.qs + at) = codes8_part(v, scale, a.cols - at);
     if ((lane & 15) == 0 && at < a.cols) a.s[row * a.ss + at / kBlock] = scale;
   }
 }
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(QuantArgs a) {
       e[i].get(v);
       const float scale = SQUARE ? whole : scale_of(row_largest(rm[i]));
       if (i < rcnt) {
-        if (col < a.cols16) *reinterpret_cast<pu2e*>(a.q + int64_t(row + i) * a.qs + col) = codes8_part(v, 1.0f / scale, ccnt);
+        if (col < a.cols16) *reinterpret_cast<pu2e*>(a.q + int64_t(row + i) * a.qs + col) = codes8_part(v, scale, ccnt);
         if (!SQUARE && cl == 0) a.s[int64_t(row + i) * a.ss + ct] = scale;
       }
     }
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(256) quantize_tile_kernel(QuantArgs a) {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = t[i][j];
-    const pu2 c = codes8_part(v, 1.0f / scale, rcnt);
+    const pu2 c = codes8_part(v, scale, rcnt);
     slot[(cl * 8 + j) * 16 + (rg ^ cl)] = uint2{c[0], c[1]};
   }
   __syncthreads();

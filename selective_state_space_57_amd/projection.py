@@ -2,7 +2,8 @@
 
 8-bit tensors are ``torch.float8_e4m3fn`` with an fp32 scale for each block of 128 consecutive values of a row, or of 128
 rows and columns (weights); a value stands for code times scale.  scale = max(largest magnitude of the block, 2^-100) / 448
-and the code is value / scale, rounded to nearest even.  Rows of 8-bit tensors that are made here have their length rounded
+and value / scale are fp32, and the code is the nearest to that quotient, halves to the even one: ``(x / scale).to(
+torch.float8_e4m3fn)`` of finite fp32 tensors, bit for bit.  Rows of 8-bit tensors that are made here have their length rounded
 up to a multiple of 16, with zeros behind the end, so that any of them can go into a product, and begin at a multiple of 128
 bytes where they are long.  A block that holds a NaN or an infinity makes every result of its row (its rows and columns) that
 it meets NaN.
