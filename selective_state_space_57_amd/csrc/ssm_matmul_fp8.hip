@@ -2,8 +2,9 @@
 //   out[i][j] = sum over blocks c of sa[i][c] sb[j / b_rows][c] (sum over the block's k of a[i][k] b[j][k])
 //
 // A block's inner sum is matrix instructions' work (two v_mfma_f32_32x32x64_f8f6f4 for 32 x 32 results in large products,
-// one v_mfma_f32_16x16x128_f8f6f4 for 16 x 16 where a has few rows); it goes into the fp32 sums times the two scales, one fma for
-// each result and block.  b is the first operand, so that a lane's results are of one row of a, with one scale of a for them all,
+// one v_mfma_f32_16x16x128_f8f6f4 for 16 x 16 where a has few rows); it goes into the fp32 sums times the product of the two
+// scales, one fma for each result and block.  (The scales meet first in every kernel: an inner sum, 2^24 at most, times one of
+// them may be out of range where their product is an ordinary number.)  b is the first operand, so that a lane's results are of one row of a, with one scale of a for them all,
 // and neighbours in it, for wide stores.
 //
 // Inside, the 8-bit matrix instructions (of every shape) align their products to the largest of a group and drop what lies
@@ -321,7 +322,7 @@ __device__ __forceinline__ void matmul_tiles(const MatmulArgs& g, uint8_t* lds, 
         }
 #pragma unroll
         for (int r = 8 * h; r < 8 * h + 8; ++r)
-          to[r] = fmaf(BROWS == 1 ? d[k & 1][r] * sbn[(r - 8 * h) / 4][r % 4] : d[k & 1][r], s[(k / TN) & 1], to[r]);
+          to[r] = fmaf(d[k & 1][r], BROWS == 1 ? sbn[(r - 8 * h) / 4][r % 4] * s[(k / TN) & 1] : s[(k / TN) & 1], to[r]);
       }
       asm volatile("" : "+v"(to));   // (here, not at the end of the block)
     };
@@ -521,7 +522,7 @@ __global__ void __launch_bounds__(64 * WM * WN) matmul_own_kernel(MatmulArgs g) 
       for (int kh = 0; kh < 2; ++kh) d = mfma_half(fb[kh], fa[i][kh], d);
       const float t = sa[i] * sb;
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][r] = fmaf(BROWS == 1 ? d[r] * sbn[r / 4][r % 4] : d[r], t, acc[i][r]);
+      for (int r = 0; r < 16; ++r) acc[i][r] = fmaf(d[r], BROWS == 1 ? sbn[r / 4][r % 4] * t : t, acc[i][r]);
     }
     wait_lds();
     s = s + 1 == S ? 0 : s + 1;

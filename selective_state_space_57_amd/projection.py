@@ -246,7 +246,8 @@ def quantize_fp8_blocks(w, *, rows=True, columns=False, q=None, scale=None, qt=N
 def matmul_fp8(a, a_scale, b, b_scale, *, out_dtype=None, out=None, stream=None):
     """Matrix product of 8-bit operands: out (M, N) = a b^T for a (M, K), b (N, K) float8_e4m3fn, K a multiple of 16, with
     a_scale (M, ceil(K / 128)) and b_scale (ceil(N / 128), ceil(K / 128)), or (N, ceil(K / 128)) with a scale for each row,
-    float32.  out is bfloat16 (default) or float32, rounded once; the product of two scales has to be finite in fp32.
+    float32.  out is bfloat16 (default) or float32, rounded once.  Two scales are multiplied in fp32: their product has to be
+    finite, and below 2^-126 it is rounded to a multiple of 2^-149.
     float32 results are sums in fp32.  For bfloat16 ones the matrix cores drop what lies below about 2^-12 of the largest
     product of a block (1e-5 to 5e-5 of the result, whose rounding is 1.7e-3)."""
     import torch
