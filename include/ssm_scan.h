@@ -476,8 +476,9 @@ size_t ssm_add_norm_bwd_workspace_bytes(const ssm_add_norm_params* p);
  * Backward of ssm_add_norm_fwd for dy = dL/dy [ntokens][dim] io_dtype and, optionally, dh = dL/d(residual_out) res_dtype:
  * h [ntokens][dim] res_dtype is the sum that the forward kept; statistics are recomputed.  Outputs, overwritten: the
  * gradient of the sum, which is that of x and of the residual alike, as dx [ntokens][dim] io_dtype and / or dresidual
- * [ntokens][dim] res_dtype (at least one); dweight [dim] fp32.  y_dtype is ignored (codes have no slope: the rounding to
- * 8 bits counts as the identity).  dx may be dy, dresidual may be h or dh.  Deterministic.
+ * [ntokens][dim] res_dtype (at least one); dweight [dim] fp32.  p may be the forward's: y_dtype, y_stride and scale_stride
+ * are refused where the forward refuses them, and change nothing (codes have no slope: the rounding to 8 bits counts as the
+ * identity).  dx may be dy, dresidual may be h or dh.  Deterministic.
  */
 ssm_status ssm_add_norm_bwd(const ssm_add_norm_params* p, const void* h, const float* weight, const void* dy,
                             const void* dh, void* dx, void* dresidual, float* dweight, void* workspace,
