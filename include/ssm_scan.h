@@ -464,7 +464,8 @@ typedef struct {
  * x [ntokens][dim] io_dtype; residual, residual_out [ntokens][dim] res_dtype or NULL (no residual: h = x; h is not kept);
  * weight [dim] fp32; y [ntokens][dim] io_dtype, or with SSM_E4M3 [ntokens][dim rounded up to 16] e4m3 and
  * y_scale [ntokens][ceil(dim / 128)] fp32 (8-bit rows 8-byte aligned).  The norm is that of the fp32 sum, also where
- * residual_out is rounded to bf16.  residual_out may be residual (or x, where the types agree), y may be x.
+ * residual_out is rounded to bf16, and of rows of any finite size.  residual_out may be residual (or x, where the types agree),
+ * y may be x.
  */
 ssm_status ssm_add_norm_fwd(const ssm_add_norm_params* p, const void* x, const void* residual, const float* weight,
                             void* residual_out, void* y, float* y_scale, void* stream);

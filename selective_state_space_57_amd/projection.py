@@ -66,7 +66,8 @@ def add_norm_fwd(x, weight, residual=None, *, eps=1e-5, y_dtype=None, residual_d
     (y, residual_out, y_scale).  y has x's type, or with ``y_dtype`` (or a given y of) float8_e4m3fn it holds codes
     (T, D rounded up to 16) and y_scale (T, ceil(D / 128)) their scales; without, y_scale is None.  residual_out is h in the
     residual's type; without a residual it is kept (h = x) when ``residual_dtype`` or ``residual_out`` is given, else None.
-    The norm is that of the fp32 sum.  residual_out may be the residual or x, y may be x (of one type with it)."""
+    The norm is that of the fp32 sum, of rows of any finite size.  residual_out may be the residual or x, y may be x (of one
+    type with it)."""
     import torch
     T, D = x.shape
     dev = _on_gpu(x, "x")

@@ -1,4 +1,4 @@
-"""The norm over more rows than a launch has workgroups, and in place: against 64 bits, with the
+"""The norm over rows of any finite size, over more rows than a launch has workgroups, and in place: against 64 bits, with the
 tolerances of the other tests of the norm (additions in a row; u = 2^-24).
 """
 import pytest
@@ -54,6 +54,60 @@ def test_more_rows_than_workgroups(T, D, dtype, res):
 def test_gradients_of_more_rows_than_workgroups(T, D, dtype, htype, rows):
     r = Rand(T + D)
     check_backward(r(T, D, scale=2.0, dtype=htype), 1 + r(D, scale=0.2), r(T, D, dtype=dtype, wide=2), r(T, D, dtype=htype), 1e-5, rows)
+
+
+# Channels of one, four and sixteen waves, cut chunks and whole ones.
+SIZES = [1, 64, 520, 1001, 2560, 8192, 16379]
+
+
+@pytest.mark.parametrize("power", [126, 90, 63, 55, 40, -40])
+@pytest.mark.parametrize("D", SIZES)
+def test_rows_of_any_size(D, power):
+    """Rows whose squares leave fp32's range, between rows of ordinary ones."""
+    r = Rand(D + power)
+    T = 9
+    size = torch.ones(T, 1, device="cuda", dtype=torch.float64)
+    size[1::3] = 2.0 ** power
+    w = 1 + r(D, scale=0.2)
+    for dtype in (BF, F32):
+        x = (r(T, D).clamp(-1.9, 1.9).double() * size).to(dtype)
+        check_forward(x, w, None, 1e-5)
+        check_forward(x, w, (x.double() * 0.5).float(), 1e-5)
+        for htype in (BF, F32):
+            dy = r(T, D, dtype=dtype)
+            check_backward(x.to(htype), w, dy, None, 1e-5, 3)
+            check_backward(x.to(htype), w, dy, r(T, D, dtype=htype), 1e-5, 3)
+
+
+@pytest.mark.parametrize("power", [-60, -75, -100])
+@pytest.mark.parametrize("D", SIZES)
+def test_small_rows_without_eps(D, power):
+    """eps = 0 and rows whose squares are below fp32's range."""
+    r = Rand(D - power)
+    T = 9
+    size = torch.ones(T, 1, device="cuda", dtype=torch.float64)
+    size[1::3] = 2.0 ** power
+    w = 1 + r(D, scale=0.2)
+    for dtype in (BF, F32):
+        x = (r(T, D).double() * size).to(dtype)
+        check_forward(x, w, None, 0.0)
+        # (of one channel the gradient is the difference of two equal numbers, 1 / h in size)
+        check_backward(x, w, (r(T, D).double() * size).to(dtype), None, 0.0, 3)
+
+
+def test_largest_values():
+    """The largest finite value of either type, in one channel and in all of them."""
+    w = torch.ones(2560, device="cuda")
+    for dtype in (BF, F32):
+        top = torch.finfo(dtype).max
+        x = torch.zeros(3, 2560, device="cuda", dtype=dtype)
+        x[0, 7], x[1], x[2] = -top, top, 1.0
+        y, _, _ = ssm().add_norm_fwd(x, w)
+        want = R.add_norm(x, None, w, 1e-5)[1]
+        inside(y, want, (HALF[dtype] + additions(2560) * u) * want.abs())
+        big = torch.full((3, 2560), 3.0e38, device="cuda")
+        y, h, _ = ssm().add_norm_fwd(big, w, big)                # the sum itself is out of range: infinite, and no norm
+        assert h.isinf().all() and y.isnan().all()
 
 
 def test_in_place_of_x():
