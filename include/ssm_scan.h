@@ -517,8 +517,9 @@ typedef struct {
  * over the block's k of a[i][k] b[j][k].  a [m][k], b [n][k] e4m3 (rows 16-byte aligned); a_scale [m][ceil(k / 128)],
  * b_scale [ceil(n / b_rows)][ceil(k / 128)] fp32; out [m][n] out_dtype, rounded once.  The sums over blocks are fp32, and for
  * an fp32 out those inside a block too; for a bf16 out the 8-bit matrix instructions drop what lies below about 2^-12 of the
- * largest products of a block (1e-5 to 5e-5 of the result's 2-norm; the rounding to bf16 is 1.7e-3).  k below 2^23, n below
- * 2^27.  Two scales are multiplied in fp32, whatever the sizes: their product has to be finite, and below 2^-126 it is rounded
+ * largest products of a block (1e-5 to 5e-5 of the result's 2-norm; the rounding to bf16 is 1.7e-3).  Where large products
+ * of a block cancel, what is left below that is lost for a bf16 out and kept for an fp32 one.  k below 2^23, n below 2^27.
+ * Two scales are multiplied in fp32, whatever the sizes: their product has to be finite, and below 2^-126 it is rounded
  * to a multiple of 2^-149.  out must not overlap an input.  Deterministic.
  */
 ssm_status ssm_matmul_fp8(const ssm_matmul_fp8_params* p, const void* a, const float* a_scale, const void* b,

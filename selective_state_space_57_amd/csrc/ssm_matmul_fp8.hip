@@ -9,8 +9,10 @@
 //
 // Inside, the 8-bit matrix instructions (of every shape) align their products to the largest of a group and drop what lies
 // below about 2^-12 of it: measured 1.4e-5 of the result's 2-norm for values of a normal distribution, 5e-5 for codes drawn
-// evenly.  A bf16 result, whose own rounding is 1.7e-3, is computed with them.  An fp32 result (a weight gradient) is not:
-// its codes become bf16, which holds them exactly, on the way into the bf16 matrix instructions, which sum in fp32 (1.5e-7).
+// evenly (3.1e-4 to 5.6e-4 between the rounded results and the correctly rounded ones).  A bf16 result, whose own rounding is
+// 1.7e-3, is computed with them: the bf16 instructions, which drop nothing, have half their rate.  An fp32 result (a weight
+// gradient) is not: its codes become bf16, which holds them exactly, on the way into the bf16 matrix instructions, which sum in
+// fp32 (1.5e-7).
 //
 // Large products are bound by the matrix cores, the fmas that apply the scales (a quarter of the vector unit's cycles: with
 // instructions of 16 x 16 x 128, whose results come twice as often for the same work, a loop without memory reached 3562 TF,

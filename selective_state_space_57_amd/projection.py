@@ -250,7 +250,8 @@ def matmul_fp8(a, a_scale, b, b_scale, *, out_dtype=None, out=None, stream=None)
     float32.  out is bfloat16 (default) or float32, rounded once.  Two scales are multiplied in fp32: their product has to be
     finite, and below 2^-126 it is rounded to a multiple of 2^-149.
     float32 results are sums in fp32.  For bfloat16 ones the matrix cores drop what lies below about 2^-12 of the largest
-    product of a block (1e-5 to 5e-5 of the result, whose rounding is 1.7e-3)."""
+    product of a block (1e-5 to 5e-5 of the results' 2-norm, whose rounding is 1.7e-3); where large products of a block cancel,
+    float32 results keep what is left below that."""
     import torch
     M, K = a.shape
     dev = _on_gpu(a, "a")
