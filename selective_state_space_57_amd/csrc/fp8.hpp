@@ -97,7 +97,7 @@ __device__ __forceinline__ uint32_t codes(float a, float b, float c, float d) {
   return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
 }
 // Codes of eight values of a block: their fp32 quotients by the scale, rounded to nearest, then to the nearest code.  bf16
-// values often lie halfway between two codes, where a product with the rounded reciprocal went to the wrong side (5 codes in
+// values often lie halfway between two codes, where a product with the rounded reciprocal went to the wrong side (6 codes in
 // 10,000), so the quotient's remainder, which a fma has exactly, corrects it: two more operations for a code, with the same
 // codes as a division for each (tried on the host at every border between codes for every divisor's mantissa).  Measured
 // beside the product alone: 8191 x 5120 bf16, rows and columns, 42.9 us and 39.6; 16384 rows of 2560 of the norm 86.6 and 84.9.

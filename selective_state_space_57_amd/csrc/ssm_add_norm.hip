@@ -13,7 +13,7 @@
 //
 // Measured (a large copy reaches 5.1 TB/s): 16384 rows of 2560, bf16 with an fp32 residual and 8-bit output, 461 MB, 88 us
 // (5.2 TB/s); 4099 rows 25 us; 64 rows 3.6 us, all but a little of it latency: load, two barriers, store.  Backward, 8191 rows
-// of 2560, 336 MB, 63 us (5.3 TB/s) and 4 for the join.
+// of 2560, 336 MB, 64 to 66 us (5.2 TB/s) and 4 for the join.
 #include "fp8.hpp"
 
 namespace ssm57 {

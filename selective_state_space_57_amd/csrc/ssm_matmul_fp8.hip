@@ -4,8 +4,8 @@
 // A block's inner sum is matrix instructions' work (two v_mfma_f32_32x32x64_f8f6f4 for 32 x 32 results in large products,
 // one v_mfma_f32_16x16x128_f8f6f4 for 16 x 16 where a has few rows); it goes into the fp32 sums times the product of the two
 // scales, one fma for each result and block.  (The scales meet first in every kernel: an inner sum, 2^24 at most, times one of
-// them may be out of range where their product is an ordinary number.)  b is the first operand, so that a lane's results are of one row of a, with one scale of a for them all,
-// and neighbours in it, for wide stores.
+// them may be out of range where their product is an ordinary number.)  b is the first operand, so that a lane's results are of
+// one row of a, with one scale of a for them all, and neighbours in it, for wide stores.
 //
 // Inside, the 8-bit matrix instructions (of every shape) align their products to the largest of a group and drop what lies
 // below about 2^-12 of it: measured 1.4e-5 of the result's 2-norm for values of a normal distribution, 5e-5 for codes drawn
@@ -17,12 +17,13 @@
 // Large products are bound by the matrix cores, the fmas that apply the scales (a quarter of the vector unit's cycles: with
 // instructions of 16 x 16 x 128, whose results come twice as often for the same work, a loop without memory reached 3562 TF,
 // with these 4015) and, above all, by the copies into LDS that run beside them: 8192^3 takes 540 us, without the copies 440.
-// Measured, bf16 results and one scale for 128 rows of b: 16384 x 10576 x 2560 437 to 452 us (2030 TF; the matrix cores are busy
-// 57 % of the time, the clock falls to 1.9 GHz under the power limit; a library product with one scale for each whole tensor takes
-// 392 to 470), 4099 x 2560 x 5120 58 to 60 us; rows of b with scales of their own, fp32 results: 10576 x 2560 x 8191 470 to
-// 490 us (945 TF), bound by the conversions, two vector operations for each result and block, and power.  Products of one turn
-// are bound by a CU's copies (about 45 B/ns): 256 x 10576 x 2560 15 us, 1000 x 2560 x 2560 15.8 (library 15.7 for 1024).  Few
-// rows are bound by the reading of b: 1 row at 10576 x 2560 7.6 us (3.6 TB/s with the launch).
+// Measured, bf16 results and one scale for 128 rows of b: 16384 x 10576 x 2560 437 to 468 us (2030 to 1900 TF; the matrix cores
+// are busy 57 % of the time, the clock falls to 1.9 GHz under the power limit; a library product with one scale for each whole
+// tensor takes 392 to 470), 4099 x 2560 x 5120 58 to 62 us; rows of b with scales of their own: 10576 x 2560 x 8192 344 to 370
+// us (tiles of 128 x 128, whose copies are twice those of 256 x 256 for the same products, and two vector operations for each
+// result and block), with fp32 results 470 to 510 (945 to 870 TF), bound by the conversions, those operations and power.
+// Products of one turn are bound by a CU's copies (about 45 B/ns): 256 x 10576 x 2560 15 us, 1000 x 2560 x 2560 15.8 (library
+// 15.7 for 1024).  Few rows are bound by the reading of b: 1 row at 10576 x 2560 7.6 us (3.6 TB/s with the launch).
 //
 // Tried and not kept, for the large products: four waves of 128 x 128 results each (their sums move between register files:
 // 801 us at 8192^3), lines touched ahead of their copies (5 to 10 % slower), all of a stage's copies at once (3 % slower), raised

@@ -8,8 +8,9 @@
 // LDS, and the transposed codes go through LDS (16 KB, slots of 8 bytes exchanged by column so that neither side's accesses
 // meet in a bank) so that they leave in runs of 128 bytes.  A tile's elements stay in registers from the maxima to the codes.
 //
-// Measured (a large copy reaches 5.1 TB/s): 8191 x 5120 bf16, rows and columns, 168 MB, 38 us (4.4 TB/s); rows alone 27; blocks
-// of 10576 x 2560 fp32, both layouts, 162 MB, 31 us (5.2 TB/s); 256 rows of 5120 3.0 us, latency.
+// Measured (a large copy reaches 5.1 TB/s): 8191 x 5120 bf16, rows and columns, 168 MB, 40 us (4.2 TB/s); rows or columns
+// alone, 126 MB, 26 and 27; blocks of 10576 x 2560 fp32, both layouts, 162 MB, 33 us (5.0 TB/s); 256 rows of 5120 3.1 us,
+// latency.
 #include "fp8.hpp"
 
 namespace ssm57 {
